@@ -68,7 +68,10 @@ typedef enum {
     HPC_ERR_CUDA = -4         /* a CUDA runtime/driver call failed (launch, tensor map) */
 } hpc_status;
 
-typedef enum { HPC_KV_BF16 = 0, HPC_KV_FP8_E4M3 = 1 } hpc_kv_dtype;
+/* HPC_KV_E4M3_BLOCK: E4M3 codes with one scale for each 16 tokens and head
+ * (see "Block-scaled 8-bit cache"); only the calls that take d_kv_scale and
+ * hpc_decode_num_ctas accept it. */
+typedef enum { HPC_KV_BF16 = 0, HPC_KV_FP8_E4M3 = 1, HPC_KV_E4M3_BLOCK = 2 } hpc_kv_dtype;
 
 /* Device-side error bits, OR-ed into meta[3]. */
 #define HPC_FLAG_BAD_SEQLEN 1u   /* a seqlen < 0 or > 64 * max_pages_per_req; clamped */
@@ -80,6 +83,7 @@ typedef enum { HPC_KV_BF16 = 0, HPC_KV_FP8_E4M3 = 1 } hpc_kv_dtype;
 #define HPC_PAGE_SIZE 64
 #define HPC_MAX_GROUP 16
 #define HPC_MAX_BATCH 16384
+#define HPC_SCALE_BLOCK 16 /* tokens that share a scale in a block-scaled cache */
 #define HPC_MAX_QUERY_ROWS 16 /* multi-query decode: q_len * G query rows per KV head at most */
 
 /*
@@ -98,8 +102,10 @@ typedef enum { HPC_KV_BF16 = 0, HPC_KV_FP8_E4M3 = 1 } hpc_kv_dtype;
  *               left zero by every attention launch.
  * cap_desc, cap_bins and cap_units give the sizes of desc (entries of four
  * int32), bin_ptr and chunk_count / chunk_off, and are set by the caller.
- * B, Hkv, num_ctas (the number of bins), persistent, min_tiles and
- * max_pages (the planner's arguments) are written by the planners (the
+ * B, Hkv, num_ctas (the number of bins), persistent (0 for a static map, odd
+ * for a load-balanced one; a windowed plan keeps a tag of its window above
+ * bit 0), min_tiles and max_pages (the planner's arguments) are written by
+ * the planners (the
  * host-side struct is updated) and read by hpc_decode_attn /
  * hpc_decode_combine, which check B and Hkv against their own arguments.
  * The attention kernel of a persistent map re-derives each CTA's first
@@ -605,6 +611,152 @@ hpc_status hpc_prefill_attn(const void *d_q, const void *d_k_cache, const void *
                             int32_t max_pages_per_req, const int32_t *d_seqlens, int32_t B,
                             int32_t Hq, int32_t Hkv, int32_t head_dim, int32_t q_len,
                             float sm_scale, void *d_out, int32_t *d_flags, hpc_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Windowed attention with sinks.  A query at position p of its request sees
+ * token j <= p when j > p - window (the last `window` tokens, itself among
+ * them) or j < sinks (the request's first tokens stay visible).  window = 0
+ * means every token up to the query and needs sinks = 0; window and sinks
+ * are below 2^30, and so is 64 * max_pages_per_req (HPC_ERR_UNSUPPORTED).
+ * A query that sees no token gets a zero row.  Pages without a token that
+ * some query of the request sees are neither looked up in the block table
+ * nor read, so a serving runtime may free them and leave any entry there;
+ * tokens that no query of the request sees may hold anything (NaN included).
+ * A token that one query of the request sees has to be finite for all of
+ * them: the others multiply its value by a zero weight.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * hpc_decode_plan for a window: the tiles of a request are its sink tiles
+ * and those from its first query's window on, numbered through (descriptor
+ * tile t is the request's tile t below ceil(sinks / 64), else t plus the
+ * tiles left out).  q_len, window and sinks have to be those of the attention
+ * calls that use the map: they are checked against it (HPC_ERR_ARG), and the
+ * calls without a window refuse a windowed map.  window = 0 is
+ * hpc_decode_plan.  Other arguments as there; 1 <= q_len <= 16.
+ */
+hpc_status hpc_decode_plan_win(const int32_t *d_seqlens, int32_t B, int32_t Hkv,
+                               int32_t max_pages_per_req, int32_t num_ctas,
+                               int32_t min_tiles_per_cta, int32_t q_len, int32_t window,
+                               int32_t sinks, hpc_task_map *map, hpc_stream_t stream);
+
+/*
+ * hpc_decode_attn_combine_mq (d_unit_done and d_out given) or
+ * hpc_decode_attn_mq (both NULL: partials only, to be merged by
+ * hpc_decode_combine_mq) with a window and for every cache type.
+ *   d_kv_scale  block scales, device fp32 [num_pages, Hkv, 2, 4], 16-byte
+ *               aligned, for HPC_KV_E4M3_BLOCK; NULL for the others.  Scores
+ *               then use q_scale * the block's K scale, values its V scale,
+ *               and k_scale and v_scale are ignored.  The scales of blocks
+ *               that hold a visible token are finite and not negative; the
+ *               others may be anything.
+ * Other arguments as in those calls.
+ */
+hpc_status hpc_decode_attn_win(const void *d_q, const float *d_q_scale, const void *d_k_cache,
+                               const void *d_v_cache, int32_t num_pages, float k_scale,
+                               float v_scale, const float *d_kv_scale, hpc_kv_dtype kv_dtype,
+                               const int32_t *d_block_table, int32_t max_pages_per_req,
+                               const int32_t *d_seqlens, int32_t B, int32_t Hq, int32_t Hkv,
+                               int32_t head_dim, int32_t q_len, int32_t window, int32_t sinks,
+                               float sm_scale, const hpc_task_map *map, float *d_part_o,
+                               float *d_part_lse, int32_t *d_unit_done, void *d_out,
+                               hpc_stream_t stream);
+
+/*
+ * One whole decode step of one layer: hpc_decode_plan_win, then the fused
+ * attention (d_unit_done != NULL) or attention and hpc_decode_combine_mq
+ * (d_unit_done == NULL), all on `stream`.
+ */
+hpc_status hpc_decode_step_win(const void *d_q, const float *d_q_scale, const void *d_k_cache,
+                               const void *d_v_cache, int32_t num_pages, float k_scale,
+                               float v_scale, const float *d_kv_scale, hpc_kv_dtype kv_dtype,
+                               const int32_t *d_block_table, int32_t max_pages_per_req,
+                               const int32_t *d_seqlens, int32_t B, int32_t Hq, int32_t Hkv,
+                               int32_t head_dim, int32_t q_len, int32_t window, int32_t sinks,
+                               float sm_scale, int32_t num_ctas, int32_t min_tiles_per_cta,
+                               hpc_task_map *map, float *d_part_o, float *d_part_lse,
+                               int32_t *d_unit_done, void *d_out, hpc_stream_t stream);
+
+/*
+ * hpc_prefill_attn with a window: the request's last q_len live tokens are
+ * the queries, over a paged BF16 cache.  window = 0 is hpc_prefill_attn.
+ * Other arguments as there.
+ */
+hpc_status hpc_prefill_attn_win(const void *d_q, const void *d_k_cache, const void *d_v_cache,
+                                int32_t num_pages, const int32_t *d_block_table,
+                                int32_t max_pages_per_req, const int32_t *d_seqlens, int32_t B,
+                                int32_t Hq, int32_t Hkv, int32_t head_dim, int32_t q_len,
+                                int32_t window, int32_t sinks, float sm_scale, void *d_out,
+                                int32_t *d_flags, hpc_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Block-scaled 8-bit cache: the codes are laid out as in an FP8 cache
+ * ([num_pages, 64, Hkv, 128] E4M3, K and V apart), and kv_scale, fp32
+ * [num_pages, Hkv, 2, 4], holds for each page and head the scales of K's
+ * four blocks of 16 tokens and then of V's: value = code * scale.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * The fused prologue (hpc_rope_norm) writing into a block-scaled cache.  A
+ * run is what one call writes into one block: the tokens of one request
+ * whose positions share position / 16.  They have to be neighbours in the
+ * call's token list (as a request's consecutive tokens are); tokens of one
+ * block in several places of the list leave that block's contents
+ * unspecified.  Where a run holds a position twice, the later token stays.
+ * For each head, and for K and V apart:
+ *   a  = the largest finite |y| over the run's rows,
+ *   s* = the smallest power of two >= 2^-126 with a <= 448 s*,
+ *   a run that holds the block's first position starts the block afresh:
+ *   s = s*, and the block's other slots hold nothing until they are written;
+ *   any other run appends: s = max(s_old, s*) (an s_old that is not positive
+ *   and finite counts as 0), and if s > s_old the codes of the block's other
+ *   slots become E4M3(code * s_old / s);
+ *   codes = E4M3(y / s), round to nearest even, saturating (an infinite y
+ *   becomes +-448, NaN stays NaN).
+ * With powers of two the quotients are exact and a growing scale re-rounds
+ * only codes that leave E4M3's normal range.
+ *   d_kv_scale     device fp32 [num_pages, Hkv, 2, 4], read and written
+ *   d_q_out        BF16 [num_tokens, Hq, 128] (d_q_scale_out NULL: what
+ *                  hpc_prefill_attn_win takes) or E4M3 with d_q_scale_out
+ *                  [num_tokens, Hq] (what hpc_decode_attn_win takes)
+ * Other arguments, flags and stream order as in hpc_rope_norm; d_kv_scale is
+ * 16-byte aligned like the other pointers.
+ */
+hpc_status hpc_rope_norm_block(const void *d_qkv, int64_t qkv_row_stride, const void *d_q_norm_w,
+                               const void *d_k_norm_w, const int32_t *d_positions,
+                               const int32_t *d_token_req, int32_t num_tokens, int32_t Hq,
+                               int32_t Hkv, int32_t head_dim, const int32_t *d_block_table,
+                               int32_t max_pages_per_req, int32_t B, void *d_k_cache,
+                               void *d_v_cache, float *d_kv_scale, int32_t num_pages,
+                               void *d_q_out, float *d_q_scale_out, int32_t *d_flags,
+                               const hpc_rope_norm_params *params, hpc_stream_t stream);
+
+/*
+ * Reads a block-scaled cache back as BF16 pages (what hpc_prefill_attn and
+ * hpc_prefill_attn_win take): tokens d_starts[r] .. d_seqlens[r] - 1 of every
+ * request r (from 0 with d_starts NULL), value = BF16(code * scale).  Token t
+ * goes to page out_block_table[r, t / 64], slot t % 64; nothing else is
+ * written.  The output pages may not overlap the cache; where two tokens name
+ * one output slot either one's row is left there.
+ *   d_block_table      device int32 [B, max_pages_per_req], the cache's
+ *   d_k_out, d_v_out   device bf16 [out_num_pages, 64, Hkv, 128]
+ *   d_out_block_table  device int32 [B, out_max_pages_per_req]
+ *   d_flags            device int32 or NULL: HPC_FLAG_BAD_SEQLEN for a length
+ *                      outside [0, 64 * the smaller row length] (clamped) or a
+ *                      start below 0 (taken as 0); HPC_FLAG_BAD_PAGE for an
+ *                      entry outside either cache (that page is left out)
+ * Pointers to caches, outputs and scales are 16-byte aligned.  B <=
+ * HPC_MAX_BATCH.  Asynchronous on `stream`; reads nothing before the previous
+ * kernel on the stream has finished.
+ */
+hpc_status hpc_kv_read_block(const void *d_k_cache, const void *d_v_cache,
+                             const float *d_kv_scale, int32_t num_pages,
+                             const int32_t *d_block_table, int32_t max_pages_per_req,
+                             const int32_t *d_starts, const int32_t *d_seqlens, int32_t B,
+                             int32_t Hkv, int32_t head_dim, void *d_k_out, void *d_v_out,
+                             int32_t out_num_pages, const int32_t *d_out_block_table,
+                             int32_t out_max_pages_per_req, int32_t *d_flags,
+                             hpc_stream_t stream);
 
 /*
  * Synchronises `stream` and copies map->meta into host_meta[4]

@@ -10,11 +10,14 @@ router GEMM with a BF16 hi/lo split of FP32 weights.  This package
 holds the build step, the ctypes binding and the seeded workload generators.
 """
 
-from .binding import (EXPORTS, HPC_KV_BF16, HPC_KV_FP8_E4M3, HPC_ROPE_HALVES,
+from .binding import (EXPORTS, HPC_KV_BF16, HPC_KV_E4M3_BLOCK, HPC_KV_FP8_E4M3, HPC_ROPE_HALVES,
                       HPC_ROPE_INTERLEAVED, HpcError, TaskMap, Workspace, hpc_decode_attn,
                       hpc_decode_attn_combine, hpc_decode_attn_combine_mq, hpc_decode_attn_mq,
+                      hpc_decode_attn_win,
                       hpc_decode_combine, hpc_decode_combine_mq, hpc_decode_desc_capacity,
                       hpc_decode_num_ctas, hpc_decode_plan, hpc_decode_plan_static,
+                      hpc_decode_plan_win, hpc_decode_step_win, hpc_kv_read_block,
+                      hpc_prefill_attn_win, hpc_rope_norm_block,
                       hpc_decode_read_meta, hpc_decode_static_capacity, hpc_decode_step,
                       hpc_decode_step_mq,
                       hpc_decode_packed_layout, hpc_decode_step_host,
@@ -24,11 +27,13 @@ from .binding import (EXPORTS, HPC_KV_BF16, HPC_KV_FP8_E4M3, HPC_ROPE_HALVES,
                       kv_dtype_of, lib)
 
 __all__ = [
-    "EXPORTS", "HPC_KV_BF16", "HPC_KV_FP8_E4M3", "HPC_ROPE_HALVES", "HPC_ROPE_INTERLEAVED",
+    "EXPORTS", "HPC_KV_BF16", "HPC_KV_E4M3_BLOCK", "HPC_KV_FP8_E4M3", "HPC_ROPE_HALVES", "HPC_ROPE_INTERLEAVED",
     "HpcError", "TaskMap", "Workspace", "hpc_decode_attn", "hpc_decode_attn_combine",
     "hpc_decode_attn_combine_mq", "hpc_decode_attn_mq", "hpc_decode_combine",
     "hpc_decode_combine_mq", "hpc_decode_desc_capacity", "hpc_decode_num_ctas",
     "hpc_decode_plan", "hpc_decode_plan_static", "hpc_decode_read_meta",
+    "hpc_decode_attn_win", "hpc_decode_plan_win", "hpc_decode_step_win", "hpc_kv_read_block",
+    "hpc_prefill_attn_win", "hpc_rope_norm_block",
     "hpc_decode_packed_layout", "hpc_decode_static_capacity", "hpc_decode_step",
     "hpc_decode_step_host", "hpc_decode_step_host_packed", "hpc_decode_step_mq",
     "hpc_decode_version", "hpc_prefill_attn", "hpc_rope_frequencies", "hpc_rope_norm", "hpc_router_gemm",

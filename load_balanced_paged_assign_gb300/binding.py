@@ -16,9 +16,10 @@ import torch
 from . import _build
 
 HPC_OK, HPC_ERR_ARG, HPC_ERR_UNSUPPORTED, HPC_ERR_WORKSPACE, HPC_ERR_CUDA = 0, -1, -2, -3, -4
-HPC_KV_BF16, HPC_KV_FP8_E4M3 = 0, 1
+HPC_KV_BF16, HPC_KV_FP8_E4M3, HPC_KV_E4M3_BLOCK = 0, 1, 2
 HPC_FLAG_BAD_SEQLEN, HPC_FLAG_DESC_OVERFLOW, HPC_FLAG_BAD_PAGE, HPC_FLAG_TIMEOUT = 1, 2, 4, 8
 HEAD_DIM, PAGE_SIZE, MAX_GROUP, MAX_QUERY_ROWS = 128, 64, 16, 16
+SCALE_BLOCK = 16
 HPC_ROPE_HALVES, HPC_ROPE_INTERLEAVED = 0, 1
 
 # Every symbol the header declares; the CPU tests check the library exports them all.
@@ -31,6 +32,8 @@ EXPORTS = (
     "hpc_selftest_wait_timeout", "hpc_router_split", "hpc_router_workspace_bytes", "hpc_router_plan",
     "hpc_router_gemm", "hpc_prefill_attn",
     "hpc_decode_packed_layout", "hpc_decode_step_host_packed",
+    "hpc_decode_plan_win", "hpc_decode_attn_win", "hpc_decode_step_win", "hpc_prefill_attn_win",
+    "hpc_rope_norm_block", "hpc_kv_read_block",
 )
 
 
@@ -129,6 +132,21 @@ def lib():
         "hpc_rope_norm": (ctypes.c_int, [vp, i64, vp, vp, vp, vp, i32, i32, i32, i32, vp, i32,
                                          i32, vp, vp, i32, ctypes.c_int, f32, f32, vp, vp, vp,
                                          ctypes.POINTER(hpc_rope_norm_params), vp]),
+        "hpc_decode_plan_win": (ctypes.c_int, [vp, i32, i32, i32, i32, i32, i32, i32, i32, tm,
+                                               vp]),
+        "hpc_decode_attn_win": (ctypes.c_int, [vp, vp, vp, vp, i32, f32, f32, vp, ctypes.c_int,
+                                               vp, i32, vp, i32, i32, i32, i32, i32, i32, i32,
+                                               f32, tm, vp, vp, vp, vp, vp]),
+        "hpc_decode_step_win": (ctypes.c_int, [vp, vp, vp, vp, i32, f32, f32, vp, ctypes.c_int,
+                                               vp, i32, vp, i32, i32, i32, i32, i32, i32, i32,
+                                               f32, i32, i32, tm, vp, vp, vp, vp, vp]),
+        "hpc_prefill_attn_win": (ctypes.c_int, [vp, vp, vp, i32, vp, i32, vp, i32, i32, i32, i32,
+                                                i32, i32, i32, f32, vp, vp, vp]),
+        "hpc_rope_norm_block": (ctypes.c_int, [vp, i64, vp, vp, vp, vp, i32, i32, i32, i32, vp,
+                                               i32, i32, vp, vp, vp, i32, vp, vp, vp,
+                                               ctypes.POINTER(hpc_rope_norm_params), vp]),
+        "hpc_kv_read_block": (ctypes.c_int, [vp, vp, vp, i32, vp, i32, vp, vp, i32, i32, i32, vp,
+                                             vp, i32, vp, i32, vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -165,6 +183,29 @@ def kv_dtype_of(t: torch.Tensor) -> int:
     if t.dtype == torch.float8_e4m3fn:
         return HPC_KV_FP8_E4M3
     raise TypeError(f"unsupported KV cache dtype {t.dtype}")
+
+
+def _dense(fn: str, dev: int, **tensors):
+    """Raises ValueError for a tensor that the call cannot take as a plain row-major
+    array of its type on the device `dev`: {name: (tensor or None, dtype)}."""
+    for name, (t, dtype) in tensors.items():
+        if t is None:
+            continue
+        if t.dtype is not dtype:
+            raise ValueError(f"{fn}: {name} is {t.dtype}, not {dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} is not contiguous")
+        if t.get_device() != dev:
+            raise ValueError(f"{fn}: {name} is on {t.device}, not on the current device")
+
+
+def _shape(fn: str, name: str, t, want: tuple):
+    if tuple(t.shape) != want:
+        raise ValueError(f"{fn}: {name} is {tuple(t.shape)}, not {want}")
+
+
+def _current_device() -> int:
+    return torch.cuda.current_device() if torch.cuda.is_available() else -1
 
 
 class TaskMap:
@@ -453,6 +494,177 @@ def hpc_rope_norm(qkv, q_norm_w, k_norm_w, positions, token_req, Hq, Hkv, block_
         int(block_table.shape[1]), int(block_table.shape[0]), _ptr(k_cache), _ptr(v_cache),
         int(k_cache.shape[0]), kv_dtype_of(k_cache), float(k_scale), float(v_scale), _ptr(q_out),
         _ptr(q_scale_out), _ptr(flags), ctypes.byref(params), _stream(stream)))
+
+
+def hpc_decode_plan_win(seqlens, Hkv, max_pages_per_req, num_ctas, min_tiles_per_cta,
+                        tmap: TaskMap, *, q_len=1, window=0, sinks=0, stream=None):
+    """hpc_decode_plan for queries that see the last `window` tokens and the
+    first `sinks` ones (window = 0: every token)."""
+    _dense("hpc_decode_plan_win", _current_device(), seqlens=(seqlens, torch.int32))
+    _check("hpc_decode_plan_win", lib().hpc_decode_plan_win(
+        _ptr(seqlens), int(seqlens.numel()), int(Hkv), int(max_pages_per_req), int(num_ctas),
+        int(min_tiles_per_cta), int(q_len), int(window), int(sinks), ctypes.byref(tmap.c),
+        _stream(stream)))
+
+
+def _win_args(fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, Hq, Hkv, q_len,
+              part_o, part_lse, out, unit_done):
+    """The checks of the windowed decode calls; returns the KV dtype."""
+    block = kv_scale is not None
+    kv = torch.float8_e4m3fn if block else k_cache.dtype
+    f32, i32, B = torch.float32, torch.int32, int(seqlens.numel())
+    _dense(fn, _current_device(), q=(q, kv), q_scale=(q_scale, f32), k_cache=(k_cache, kv),
+           v_cache=(v_cache, kv), kv_scale=(kv_scale, f32), block_table=(block_table, i32),
+           seqlens=(seqlens, i32), part_o=(part_o, f32), part_lse=(part_lse, f32),
+           out=(out, torch.bfloat16), unit_done=(unit_done, i32))
+    pages, rows = int(k_cache.shape[0]), B * int(q_len) * int(Hq)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _shape(fn, name, t, (pages, PAGE_SIZE, int(Hkv), HEAD_DIM))
+    if block:
+        _shape(fn, "kv_scale", kv_scale, (pages, int(Hkv), 2, PAGE_SIZE // SCALE_BLOCK))
+    if block_table.dim() != 2 or block_table.shape[0] < B:
+        raise ValueError(f"{fn}: block_table has not a row for each of the {B} requests")
+    if q.numel() != rows * HEAD_DIM or (out is not None and out.numel() < rows * HEAD_DIM):
+        raise ValueError(f"{fn}: q or out does not hold {B} x {q_len} x {Hq} rows")
+    if q_scale is not None and q_scale.numel() != rows:
+        raise ValueError(f"{fn}: q_scale does not hold {B} x {q_len} x {Hq} scales")
+    return HPC_KV_E4M3_BLOCK if block else kv_dtype_of(k_cache)
+
+
+def _split_args(fn, tmap, part_o, part_lse, unit_done, B, Hq, Hkv, q_len):
+    """Room in the split buffer and the counters for what the map may hold."""
+    rows = tmap.cap_desc * int(q_len) * (int(Hq) // max(int(Hkv), 1))
+    if part_o.numel() < rows * HEAD_DIM or part_lse.numel() < rows:
+        raise ValueError(f"{fn}: part_o or part_lse is smaller than the map's {tmap.cap_desc} "
+                         f"descriptors need")
+    if unit_done is not None and unit_done.numel() < B * int(Hkv):
+        raise ValueError(f"{fn}: unit_done holds fewer than {B} x {Hkv} counters")
+
+
+def hpc_decode_attn_win(q, q_scale, k_cache, v_cache, k_scale, v_scale, kv_scale, block_table,
+                        seqlens, Hq, Hkv, q_len, window, sinks, sm_scale, tmap: TaskMap, part_o,
+                        part_lse, out=None, unit_done=None, stream=None):
+    """Attention over a window with sinks (window = 0: every token) on a map from
+    hpc_decode_plan_win.  kv_scale: the block scales [num_pages, Hkv, 2, 4] of a
+    block-scaled cache, else None.  out and unit_done given: combine fused in;
+    both None: partials only."""
+    fn, B = "hpc_decode_attn_win", int(seqlens.numel())
+    dtype = _win_args(fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, Hq, Hkv,
+                      q_len, part_o, part_lse, out, unit_done)
+    _split_args(fn, tmap, part_o, part_lse, unit_done, B, Hq, Hkv, q_len)
+    _check(fn, lib().hpc_decode_attn_win(
+        _ptr(q), _ptr(q_scale), _ptr(k_cache), _ptr(v_cache), int(k_cache.shape[0]),
+        float(k_scale), float(v_scale), _ptr(kv_scale), dtype, _ptr(block_table),
+        int(block_table.shape[1]), _ptr(seqlens), B, int(Hq), int(Hkv), HEAD_DIM, int(q_len),
+        int(window), int(sinks), float(sm_scale), ctypes.byref(tmap.c), _ptr(part_o),
+        _ptr(part_lse), _ptr(unit_done), _ptr(out), _stream(stream)))
+
+
+def hpc_decode_step_win(q, q_scale, k_cache, v_cache, k_scale, v_scale, kv_scale, block_table,
+                        seqlens, Hq, Hkv, q_len, window, sinks, sm_scale, num_ctas,
+                        min_tiles_per_cta, tmap: TaskMap, part_o, part_lse, out, unit_done=None,
+                        stream=None):
+    """hpc_decode_plan_win and hpc_decode_attn_win in one call (unit_done None:
+    with the separate combine kernel)."""
+    fn, B = "hpc_decode_step_win", int(seqlens.numel())
+    dtype = _win_args(fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, Hq, Hkv,
+                      q_len, part_o, part_lse, out, unit_done)
+    _split_args(fn, tmap, part_o, part_lse, unit_done, B, Hq, Hkv, q_len)
+    _check(fn, lib().hpc_decode_step_win(
+        _ptr(q), _ptr(q_scale), _ptr(k_cache), _ptr(v_cache), int(k_cache.shape[0]),
+        float(k_scale), float(v_scale), _ptr(kv_scale), dtype, _ptr(block_table),
+        int(block_table.shape[1]), _ptr(seqlens), B, int(Hq), int(Hkv), HEAD_DIM, int(q_len),
+        int(window), int(sinks), float(sm_scale), int(num_ctas), int(min_tiles_per_cta),
+        ctypes.byref(tmap.c), _ptr(part_o), _ptr(part_lse), _ptr(unit_done), _ptr(out),
+        _stream(stream)))
+
+
+def hpc_prefill_attn_win(q, k_cache, v_cache, block_table, seqlens, Hq, Hkv, q_len, window, sinks,
+                         sm_scale, out, flags=None, stream=None):
+    """hpc_prefill_attn with a window and sinks (window = 0: plain causal)."""
+    fn, B, bf16, i32 = "hpc_prefill_attn_win", int(seqlens.numel()), torch.bfloat16, torch.int32
+    _dense(fn, _current_device(), q=(q, bf16), k_cache=(k_cache, bf16), v_cache=(v_cache, bf16),
+           block_table=(block_table, i32), seqlens=(seqlens, i32), out=(out, bf16),
+           flags=(flags, i32))
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _shape(fn, name, t, (int(k_cache.shape[0]), PAGE_SIZE, int(Hkv), HEAD_DIM))
+    n = B * int(q_len) * int(Hq) * HEAD_DIM
+    if block_table.dim() != 2 or block_table.shape[0] < B:
+        raise ValueError(f"{fn}: block_table has not a row for each of the {B} requests")
+    if q.numel() != n or out.numel() < n:
+        raise ValueError(f"{fn}: q or out does not hold {B} x {q_len} x {Hq} rows")
+    _check(fn, lib().hpc_prefill_attn_win(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), int(k_cache.shape[0]), _ptr(block_table),
+        int(block_table.shape[1]), _ptr(seqlens), B, int(Hq), int(Hkv), HEAD_DIM, int(q_len),
+        int(window), int(sinks), float(sm_scale), _ptr(out), _ptr(flags), _stream(stream)))
+
+
+def hpc_rope_norm_block(qkv, q_norm_w, k_norm_w, positions, token_req, Hq, Hkv, block_table,
+                        k_cache, v_cache, kv_scale, q_out, q_scale_out=None, flags=None, *,
+                        eps=1e-6, rope_base=1e6, rope_layout=HPC_ROPE_HALVES, norm_first=True,
+                        freq=None, stream=None):
+    """hpc_rope_norm writing into a block-scaled cache (E4M3 k_cache, v_cache and
+    kv_scale [num_pages, Hkv, 2, 4]).  q_scale_out given: E4M3 queries, else BF16."""
+    fn, f32, i32, e4m3 = "hpc_rope_norm_block", torch.float32, torch.int32, torch.float8_e4m3fn
+    N, pages = int(positions.numel()), int(k_cache.shape[0])
+    _dense(fn, _current_device(), q_norm_w=(q_norm_w, torch.bfloat16),
+           k_norm_w=(k_norm_w, torch.bfloat16), positions=(positions, i32),
+           token_req=(token_req, i32), block_table=(block_table, i32), k_cache=(k_cache, e4m3),
+           v_cache=(v_cache, e4m3), kv_scale=(kv_scale, f32),
+           q_out=(q_out, torch.bfloat16 if q_scale_out is None else e4m3),
+           q_scale_out=(q_scale_out, f32), flags=(flags, i32), freq=(freq, torch.float64))
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _shape(fn, name, t, (pages, PAGE_SIZE, int(Hkv), HEAD_DIM))
+    _shape(fn, "kv_scale", kv_scale, (pages, int(Hkv), 2, PAGE_SIZE // SCALE_BLOCK))
+    if qkv.dtype is not torch.bfloat16 or qkv.dim() != 2 or (N and qkv.stride(1) != 1) or \
+            qkv.shape[0] < N or qkv.shape[1] < (Hq + 2 * Hkv) * HEAD_DIM:
+        raise ValueError(f"{fn}: qkv is not a BF16 matrix of {N} rows of {Hq} + 2 x {Hkv} heads")
+    if qkv.get_device() != k_cache.get_device():
+        raise ValueError(f"{fn}: qkv is on {qkv.device}, not on the current device")
+    if q_norm_w.numel() != HEAD_DIM or k_norm_w.numel() != HEAD_DIM or \
+            (freq is not None and freq.numel() != HEAD_DIM // 2):
+        raise ValueError(f"{fn}: norm weights hold {HEAD_DIM} values, freq {HEAD_DIM // 2}")
+    if q_out.numel() < N * Hq * HEAD_DIM or (q_scale_out is not None and
+                                             q_scale_out.numel() < N * Hq):
+        raise ValueError(f"{fn}: q_out or q_scale_out does not hold {N} x {Hq} rows")
+    if block_table.dim() != 2 or (token_req is not None and token_req.numel() != N):
+        raise ValueError(f"{fn}: block_table is no matrix or token_req has not {N} entries")
+    # a stride says nothing where there are not two rows
+    stride = int(qkv.stride(0)) if qkv.shape[0] > 1 else int(qkv.shape[1])
+    params = hpc_rope_norm_params(float(eps), float(rope_base), int(rope_layout),
+                                  1 if norm_first else 0,
+                                  None if freq is None else freq.data_ptr())
+    _check(fn, lib().hpc_rope_norm_block(
+        _ptr(qkv), stride, _ptr(q_norm_w), _ptr(k_norm_w), _ptr(positions), _ptr(token_req), N,
+        int(Hq), int(Hkv), HEAD_DIM, _ptr(block_table), int(block_table.shape[1]),
+        int(block_table.shape[0]), _ptr(k_cache), _ptr(v_cache), _ptr(kv_scale), pages,
+        _ptr(q_out), _ptr(q_scale_out), _ptr(flags), ctypes.byref(params), _stream(stream)))
+
+
+def hpc_kv_read_block(k_cache, v_cache, kv_scale, block_table, starts, seqlens, Hkv, k_out, v_out,
+                      out_block_table, flags=None, stream=None):
+    """Tokens starts[r] .. seqlens[r] - 1 (starts None: from 0) of a block-scaled
+    cache as BF16 into the pages out_block_table names."""
+    fn, f32, i32, e4m3 = "hpc_kv_read_block", torch.float32, torch.int32, torch.float8_e4m3fn
+    B, pages, out_pages = int(seqlens.numel()), int(k_cache.shape[0]), int(k_out.shape[0])
+    _dense(fn, _current_device(), k_cache=(k_cache, e4m3), v_cache=(v_cache, e4m3),
+           kv_scale=(kv_scale, f32), block_table=(block_table, i32), starts=(starts, i32),
+           seqlens=(seqlens, i32), k_out=(k_out, torch.bfloat16), v_out=(v_out, torch.bfloat16),
+           out_block_table=(out_block_table, i32), flags=(flags, i32))
+    for name, t, n in (("k_cache", k_cache, pages), ("v_cache", v_cache, pages),
+                       ("k_out", k_out, out_pages), ("v_out", v_out, out_pages)):
+        _shape(fn, name, t, (n, PAGE_SIZE, int(Hkv), HEAD_DIM))
+    _shape(fn, "kv_scale", kv_scale, (pages, int(Hkv), 2, PAGE_SIZE // SCALE_BLOCK))
+    for name, t in (("block_table", block_table), ("out_block_table", out_block_table)):
+        if t.dim() != 2 or t.shape[0] < B:
+            raise ValueError(f"{fn}: {name} has not a row for each of the {B} requests")
+    if starts is not None and starts.numel() != B:
+        raise ValueError(f"{fn}: starts has not {B} entries")
+    _check(fn, lib().hpc_kv_read_block(
+        _ptr(k_cache), _ptr(v_cache), _ptr(kv_scale), pages, _ptr(block_table),
+        int(block_table.shape[1]), _ptr(starts), _ptr(seqlens), B, int(Hkv), HEAD_DIM,
+        _ptr(k_out), _ptr(v_out), out_pages, _ptr(out_block_table),
+        int(out_block_table.shape[1]), _ptr(flags), _stream(stream)))
 
 
 class Workspace:

@@ -104,9 +104,12 @@ hpc_status make_cache_map(CUtensorMap *m, const void *base, int32_t num_pages, i
     return r == CUDA_SUCCESS ? HPC_OK : HPC_ERR_CUDA;
 }
 
-// Resident CTAs of the attention kernel per device and variant (KV dtype x
-// row blocks; cached).
-std::atomic<int> g_capacity[kMaxDevices][4];
+// Kernel variants: {BF16, FP8, windowed BF16, windowed FP8, block-scaled E4M3}
+// x row blocks.
+constexpr int kAttnVariants = 10;
+
+// Resident CTAs of the attention kernel per device and variant (cached).
+std::atomic<int> g_capacity[kMaxDevices][kAttnVariants];
 
 int resident_ctas(const AttnConfig &cfg, int which) {
     int dev = 0;
@@ -125,14 +128,50 @@ int resident_ctas(const AttnConfig &cfg, int which) {
     return c;
 }
 
-// Kernel variant: KV dtype x row blocks (nb = 1: up to 8 query rows per KV
-// head, 2: up to 16).
-int variant_of(hpc_kv_dtype dt, int nb) { return (dt == HPC_KV_FP8_E4M3 ? 1 : 0) + 2 * (nb - 1); }
+// Kernel variant: KV dtype, windowed or not, row blocks (nb = 1: up to 8
+// query rows per KV head, 2: up to 16).  A block-scaled cache has one form:
+// without a window it runs the windowed one with a window that hides nothing.
+int variant_of(hpc_kv_dtype dt, int nb, bool win = false) {
+    const int kind = dt == HPC_KV_E4M3_BLOCK ? 4 : (dt == HPC_KV_FP8_E4M3 ? 1 : 0) + (win ? 2 : 0);
+    return 2 * kind + (nb - 1);
+}
 
-const AttnConfig &config_for(hpc_kv_dtype dt, int nb = 1) {
-    static const AttnConfig cfg[4] = {attn_config_bf16(1), attn_config_fp8(1),
-                                      attn_config_bf16(2), attn_config_fp8(2)};
-    return cfg[variant_of(dt, nb)];
+const AttnConfig &config_for(hpc_kv_dtype dt, int nb = 1, bool win = false) {
+    static const AttnConfig cfg[kAttnVariants] = {
+        attn_config_bf16(1),     attn_config_bf16(2),     attn_config_fp8(1),
+        attn_config_fp8(2),      attn_config_win_bf16(1), attn_config_win_bf16(2),
+        attn_config_win_fp8(1),  attn_config_win_fp8(2),  attn_config_block(1),
+        attn_config_block(2)};
+    return cfg[variant_of(dt, nb, win)];
+}
+
+// The window and the block scales of the hpc_decode_*_win calls; the other
+// calls have neither.
+struct AttnForm {
+    int32_t window = 0, sinks = 0;  // window 0: every token up to the query
+    const float *kv_scale = nullptr;
+};
+
+int32_t sink_tiles_of(int32_t sinks) { return (int32_t)(((int64_t)sinks + kTile - 1) / kTile); }
+
+// What map->persistent holds beside bit 0 for a windowed plan: a value
+// derived from the query count, window and sinks it was planned for (0
+// without a window), so that a call with others is refused.
+int32_t window_tag(int32_t q_len, const AttnForm &f) {
+    if (f.window <= 0) return 0;
+    uint64_t x = ((uint64_t)(uint32_t)f.window << 34) ^ ((uint64_t)(uint32_t)f.sinks << 4) ^
+                 (uint64_t)(uint32_t)(q_len - 1);
+    x *= 0x9E3779B97F4A7C15ull;  // 2^64 / golden ratio: spreads every bit upwards
+    return (int32_t)(x >> 34) | 1;
+}
+
+// Limits of the hpc_decode_*_win and hpc_prefill_attn_win arguments.
+hpc_status check_window(int32_t window, int32_t sinks, int32_t max_pages) {
+    if (window < 0 || sinks < 0 || (window == 0 && sinks != 0)) return HPC_ERR_ARG;
+    if (window >= kNoWindow || sinks >= kNoWindow) return HPC_ERR_UNSUPPORTED;
+    // token indices plus a window must stay in int32
+    if ((int64_t)max_pages * HPC_PAGE_SIZE >= (int64_t)1 << 30) return HPC_ERR_UNSUPPORTED;
+    return HPC_OK;
 }
 
 // Shared body of hpc_decode_attn (unit_done == out == nullptr: partials only)
@@ -144,13 +183,17 @@ hpc_status launch_attention(const void *d_q, const float *d_q_scale, const void 
                             int32_t Hq, int32_t Hkv, int32_t head_dim, float sm_scale,
                             const hpc_task_map *map, float *d_part_o, float *d_part_lse,
                             int32_t *d_unit_done, void *d_out, bool after_plan, int32_t q_len,
-                            hpc_stream_t stream) {
+                            hpc_stream_t stream, const AttnForm &form = AttnForm()) {
     hpc_status st = check_shapes(B, Hq, Hkv, head_dim, max_pages_per_req);
     if (st != HPC_OK) return st;
     if (q_len < 1) return HPC_ERR_ARG;
-    if (q_len * (Hq / Hkv) > HPC_MAX_QUERY_ROWS) return HPC_ERR_UNSUPPORTED;
-    if (kv_dtype != HPC_KV_BF16 && kv_dtype != HPC_KV_FP8_E4M3) return HPC_ERR_ARG;
-    const bool fp8 = kv_dtype == HPC_KV_FP8_E4M3;
+    if (q_len > HPC_MAX_QUERY_ROWS || q_len * (Hq / Hkv) > HPC_MAX_QUERY_ROWS)
+        return HPC_ERR_UNSUPPORTED;
+    const bool block = kv_dtype == HPC_KV_E4M3_BLOCK && form.kv_scale;
+    if (kv_dtype != HPC_KV_BF16 && kv_dtype != HPC_KV_FP8_E4M3 && !block) return HPC_ERR_ARG;
+    const bool fp8 = kv_dtype != HPC_KV_BF16;
+    if (block) k_scale = v_scale = 1.f;  // the block scales stand in for them
+    if (!aligned16(form.kv_scale)) return HPC_ERR_ARG;
     if (num_pages <= 0 || !d_k_cache || !d_v_cache || !d_part_o || !d_part_lse)
         return HPC_ERR_ARG;
     if (B > 0 && (!d_q || !d_block_table || !d_seqlens)) return HPC_ERR_ARG;
@@ -164,6 +207,8 @@ hpc_status launch_attention(const void *d_q, const float *d_q_scale, const void 
     if (st != HPC_OK) return st;
     if (map->B != B || map->Hkv != Hkv || map->num_ctas < 1 || map->num_ctas >= map->cap_bins)
         return HPC_ERR_ARG;
+    // planned for this window (the tag is 0 without one)
+    if (map->persistent >> 1 != window_tag(q_len, form)) return HPC_ERR_ARG;
 
     CUtensorMap tk, tv;
     st = make_cache_map(&tk, d_k_cache, num_pages, Hkv, fp8);
@@ -194,14 +239,20 @@ hpc_status launch_attention(const void *d_q, const float *d_q_scale, const void 
     p.R = q_len * p.G;
     p.score_scale = sm_scale * kLog2eF * (fp8 ? k_scale : 1.f);
     p.v_scale = fp8 ? v_scale : 1.f;
+    const bool win = form.window > 0;
+    p.window = win ? form.window : kNoWindow;
+    p.sinks = win ? form.sinks : 0;
+    p.sink_tiles = sink_tiles_of(p.sinks);
+    p.kv_scale = form.kv_scale;
 
     const int nb = p.R > 8 ? 2 : 1;
-    const AttnConfig &cfg = config_for(kv_dtype, nb);
-    cudaError_t e = prepare_kernel(cfg, variant_of(kv_dtype, nb));
+    const int variant = variant_of(kv_dtype, nb, win);
+    const AttnConfig &cfg = config_for(kv_dtype, nb, win);
+    cudaError_t e = prepare_kernel(cfg, variant);
     if (e != cudaSuccess) return HPC_ERR_CUDA;
     int grid = map->num_ctas;  // static map: one CTA per bin
     if (map->persistent) {     // persistent: resident CTAs, extra bins pulled dynamically
-        const int cap = resident_ctas(cfg, variant_of(kv_dtype, nb));
+        const int cap = resident_ctas(cfg, variant);
         if (cap < 1) return HPC_ERR_CUDA;
         grid = std::min(grid, cap);
     }
@@ -222,7 +273,13 @@ hpc_status launch_attention(const void *d_q, const float *d_q_scale, const void 
                 ? 1
                 : 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    e = fp8 ? launch_attn_fp8(nb, tk, tv, p, grid, s) : launch_attn_bf16(nb, tk, tv, p, grid, s);
+    if (block) e = launch_attn_block(nb, tk, tv, p, grid, s);
+    else if (win)
+        e = fp8 ? launch_attn_win_fp8(nb, tk, tv, p, grid, s)
+                : launch_attn_win_bf16(nb, tk, tv, p, grid, s);
+    else
+        e = fp8 ? launch_attn_fp8(nb, tk, tv, p, grid, s)
+                : launch_attn_bf16(nb, tk, tv, p, grid, s);
     return cuda_status(e);
 }
 
@@ -234,7 +291,7 @@ hpc_status attn_combine(const void *d_q, const float *d_q_scale, const void *d_k
                         int32_t Hq, int32_t Hkv, int32_t head_dim, float sm_scale,
                         const hpc_task_map *map, float *d_part_o, float *d_part_lse,
                         int32_t *d_unit_done, void *d_out, bool after_plan, int32_t q_len,
-                        hpc_stream_t stream) {
+                        hpc_stream_t stream, const AttnForm &form = AttnForm()) {
     if (B > 0 && (!d_unit_done || !d_out)) return HPC_ERR_ARG;
     if (!aligned16(d_out)) return HPC_ERR_ARG;
     if (!map || !map->chunk_count || !map->chunk_off) return HPC_ERR_ARG;
@@ -242,7 +299,7 @@ hpc_status attn_combine(const void *d_q, const float *d_q_scale, const void *d_k
     return launch_attention(d_q, d_q_scale, d_k_cache, d_v_cache, num_pages, k_scale, v_scale,
                             kv_dtype, d_block_table, max_pages_per_req, d_seqlens, B, Hq, Hkv,
                             head_dim, sm_scale, map, d_part_o, d_part_lse, d_unit_done, d_out,
-                            after_plan, q_len, stream);
+                            after_plan, q_len, stream, form);
 }
 
 // hpc_decode_combine_mq's checks and launch.
@@ -353,13 +410,14 @@ int64_t hpc_decode_static_capacity(int32_t B, int32_t Hkv, int32_t num_splits) {
 }
 
 int32_t hpc_decode_num_ctas(int32_t device, hpc_kv_dtype kv_dtype) {
-    if (kv_dtype != HPC_KV_BF16 && kv_dtype != HPC_KV_FP8_E4M3) return HPC_ERR_ARG;
+    if (kv_dtype != HPC_KV_BF16 && kv_dtype != HPC_KV_FP8_E4M3 && kv_dtype != HPC_KV_E4M3_BLOCK)
+        return HPC_ERR_ARG;
     int prev = 0, sms = 0, per_sm = 0;
     if (cudaGetDevice(&prev) != cudaSuccess) return HPC_ERR_CUDA;
     if (device != prev && cudaSetDevice(device) != cudaSuccess) return HPC_ERR_CUDA;
     const AttnConfig &cfg = config_for(kv_dtype);
     cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
-    if (e == cudaSuccess) e = prepare_kernel(cfg, kv_dtype == HPC_KV_FP8_E4M3 ? 1 : 0);
+    if (e == cudaSuccess) e = prepare_kernel(cfg, variant_of(kv_dtype, 1));
     if (e == cudaSuccess)
         e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, cfg.kernel, cfg.threads,
                                                           cfg.smem_bytes);
@@ -373,7 +431,8 @@ namespace {
 // warmed in L2 by the assign kernel for the attention grid that follows.
 hpc_status plan_impl(const int32_t *d_seqlens, int32_t B, int32_t Hkv, int32_t max_pages_per_req,
                      int32_t num_ctas, int32_t min_tiles_per_cta, hpc_task_map *map,
-                     hpc_stream_t stream, const int32_t *bt_prefetch) {
+                     hpc_stream_t stream, const int32_t *bt_prefetch, int32_t q_len = 1,
+                     const AttnForm &form = AttnForm()) {
     if (B < 0 || Hkv <= 0 || max_pages_per_req <= 0 || num_ctas < 1 || min_tiles_per_cta < 0)
         return HPC_ERR_ARG;
     if (min_tiles_per_cta >= (1 << 29)) return HPC_ERR_ARG;
@@ -389,12 +448,15 @@ hpc_status plan_impl(const int32_t *d_seqlens, int32_t B, int32_t Hkv, int32_t m
     m.B = B;
     m.Hkv = Hkv;
     m.num_ctas = num_ctas;
-    m.persistent = 1;
+    const int32_t tag = window_tag(q_len, form);
+    m.persistent = 1 | (tag << 1);
     m.min_tiles = min_tiles_per_cta;
     m.max_pages = max_pages_per_req;
+    PlanWindow win;
+    if (form.window > 0) win = {q_len, form.window, sink_tiles_of(form.sinks)};
     st = cuda_status(launch_assign(d_seqlens, B, Hkv, max_pages_per_req, num_ctas,
                                    min_tiles_per_cta, m, static_cast<cudaStream_t>(stream),
-                                   bt_prefetch));
+                                   bt_prefetch, win));
     if (st == HPC_OK) *map = m;
     return st;
 }
@@ -545,6 +607,86 @@ hpc_status hpc_decode_step(const void *d_q, const float *d_q_scale, const void *
                               kv_dtype, d_block_table, max_pages_per_req, d_seqlens, B, Hq, Hkv,
                               head_dim, 1, sm_scale, num_ctas, min_tiles_per_cta, num_splits,
                               map, d_part_o, d_part_lse, d_unit_done, d_out, stream);
+}
+
+hpc_status hpc_decode_plan_win(const int32_t *d_seqlens, int32_t B, int32_t Hkv,
+                               int32_t max_pages_per_req, int32_t num_ctas,
+                               int32_t min_tiles_per_cta, int32_t q_len, int32_t window,
+                               int32_t sinks, hpc_task_map *map, hpc_stream_t stream) {
+    if (q_len < 1) return HPC_ERR_ARG;
+    if (q_len > HPC_MAX_QUERY_ROWS) return HPC_ERR_UNSUPPORTED;
+    hpc_status st = check_window(window, sinks, max_pages_per_req);
+    if (st != HPC_OK) return st;
+    AttnForm form;
+    form.window = window;
+    form.sinks = sinks;
+    return plan_impl(d_seqlens, B, Hkv, max_pages_per_req, num_ctas, min_tiles_per_cta, map,
+                     stream, nullptr, q_len, form);
+}
+
+hpc_status hpc_decode_attn_win(const void *d_q, const float *d_q_scale, const void *d_k_cache,
+                               const void *d_v_cache, int32_t num_pages, float k_scale,
+                               float v_scale, const float *d_kv_scale, hpc_kv_dtype kv_dtype,
+                               const int32_t *d_block_table, int32_t max_pages_per_req,
+                               const int32_t *d_seqlens, int32_t B, int32_t Hq, int32_t Hkv,
+                               int32_t head_dim, int32_t q_len, int32_t window, int32_t sinks,
+                               float sm_scale, const hpc_task_map *map, float *d_part_o,
+                               float *d_part_lse, int32_t *d_unit_done, void *d_out,
+                               hpc_stream_t stream) {
+    hpc_status st = check_window(window, sinks, max_pages_per_req);
+    if (st != HPC_OK) return st;
+    if ((kv_dtype == HPC_KV_E4M3_BLOCK) != (d_kv_scale != nullptr)) return HPC_ERR_ARG;
+    if ((d_unit_done == nullptr) != (d_out == nullptr)) return HPC_ERR_ARG;
+    AttnForm form;
+    form.window = window;
+    form.sinks = sinks;
+    form.kv_scale = d_kv_scale;
+    if (d_unit_done)
+        return attn_combine(d_q, d_q_scale, d_k_cache, d_v_cache, num_pages, k_scale, v_scale,
+                            kv_dtype, d_block_table, max_pages_per_req, d_seqlens, B, Hq, Hkv,
+                            head_dim, sm_scale, map, d_part_o, d_part_lse, d_unit_done, d_out,
+                            false, q_len, stream, form);
+    return launch_attention(d_q, d_q_scale, d_k_cache, d_v_cache, num_pages, k_scale, v_scale,
+                            kv_dtype, d_block_table, max_pages_per_req, d_seqlens, B, Hq, Hkv,
+                            head_dim, sm_scale, map, d_part_o, d_part_lse, nullptr, nullptr,
+                            false, q_len, stream, form);
+}
+
+hpc_status hpc_decode_step_win(const void *d_q, const float *d_q_scale, const void *d_k_cache,
+                               const void *d_v_cache, int32_t num_pages, float k_scale,
+                               float v_scale, const float *d_kv_scale, hpc_kv_dtype kv_dtype,
+                               const int32_t *d_block_table, int32_t max_pages_per_req,
+                               const int32_t *d_seqlens, int32_t B, int32_t Hq, int32_t Hkv,
+                               int32_t head_dim, int32_t q_len, int32_t window, int32_t sinks,
+                               float sm_scale, int32_t num_ctas, int32_t min_tiles_per_cta,
+                               hpc_task_map *map, float *d_part_o, float *d_part_lse,
+                               int32_t *d_unit_done, void *d_out, hpc_stream_t stream) {
+    hpc_status st = check_shapes(B, Hq, Hkv, head_dim, max_pages_per_req);
+    if (st == HPC_OK) st = check_window(window, sinks, max_pages_per_req);
+    if (st != HPC_OK) return st;
+    if (q_len < 1) return HPC_ERR_ARG;
+    if (q_len > HPC_MAX_QUERY_ROWS || q_len * (Hq / Hkv) > HPC_MAX_QUERY_ROWS)
+        return HPC_ERR_UNSUPPORTED;
+    if ((kv_dtype == HPC_KV_E4M3_BLOCK) != (d_kv_scale != nullptr)) return HPC_ERR_ARG;
+    AttnForm form;
+    form.window = window;
+    form.sinks = sinks;
+    form.kv_scale = d_kv_scale;
+    st = plan_impl(d_seqlens, B, Hkv, max_pages_per_req, num_ctas, min_tiles_per_cta, map, stream,
+                   d_block_table, q_len, form);
+    if (st != HPC_OK) return st;
+    // the attention grid follows the assign kernel directly (after_plan)
+    if (d_unit_done)
+        return attn_combine(d_q, d_q_scale, d_k_cache, d_v_cache, num_pages, k_scale, v_scale,
+                            kv_dtype, d_block_table, max_pages_per_req, d_seqlens, B, Hq, Hkv,
+                            head_dim, sm_scale, map, d_part_o, d_part_lse, d_unit_done, d_out,
+                            true, q_len, stream, form);
+    st = launch_attention(d_q, d_q_scale, d_k_cache, d_v_cache, num_pages, k_scale, v_scale,
+                          kv_dtype, d_block_table, max_pages_per_req, d_seqlens, B, Hq, Hkv,
+                          head_dim, sm_scale, map, d_part_o, d_part_lse, nullptr, nullptr, true,
+                          q_len, stream, form);
+    if (st != HPC_OK) return st;
+    return combine_impl(d_part_o, d_part_lse, map, B, Hq, Hkv, head_dim, q_len, d_out, stream);
 }
 
 hpc_status hpc_decode_step_host(const void *h_q, const float *h_q_scale, const int32_t *h_seqlens,

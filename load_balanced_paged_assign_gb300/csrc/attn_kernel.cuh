@@ -45,6 +45,20 @@
 //    every K/V fragment feeds NB MMAs and each KV tile is read once for all
 //    rows.  Query token i sees tokens below L - q_len + 1 + i (per-column
 //    limits in the softmax); NB = 1, q_len = 1 is plain decode.
+//  * windowed form (WIN): query position p sees token j <= p when j > p - W or
+//    j < S.  The map then counts a request's visible tiles only: its sink
+//    tiles, followed by the tiles from its first query's window on (tile t of
+//    a descriptor is physical tile t below sink_tiles, else t + skip), so no
+//    page in between is looked up or read.  Tokens no query of the request
+//    sees are treated like those past its length: no score, a zero V row.
+//  * block-scaled form (BLK, FP8): a page brings its 4 + 4 block scales (one
+//    for 16 tokens of K, one of V) as one 32-byte bulk copy beside its tiles.
+//    A consumer warp's 16 tokens are exactly one block, so K's scale is one
+//    more factor of its score scale.  V's scale v_s enters the weights in the
+//    log2 domain: beside the softmax's running maximum m of the scores x, M is
+//    the running maximum of x + log2 v_s, the f16 weights are 2^(x + log2 v_s
+//    - M) <= 1 whatever the scales' range, and O (in units of 2^M) is brought
+//    to the units of 2^m once, when the state is handed over.
 //  * the kernel is launched as a programmatic dependent of the assign kernel:
 //    it sets up its barriers, prefetches the block table into L2, derives its
 //    first descriptor from the sequence lengths and starts streaming while
@@ -62,7 +76,7 @@ namespace hpc {
 struct StageInfo {
     int kv_head, req, tile0, ntiles;  // tiles tile0 .. tile0 + ntiles - 1 of request req
     int flags, seqlen, desc_idx, count;  // count: chunks of the unit
-    int chunk_off, pad0, pad1, pad2;
+    int chunk_off, skip, pad1, pad2;  // skip: tiles between the sinks and the window (WIN)
     int pad3[4];
     float qscale[kMaxRows];  // FP8: scale of query row rho
 };
@@ -96,7 +110,20 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     return mbar_wait_warp(bar, parity, abort);
 }
 
-template <bool FP8, int STAGES, int TPS, int NB>
+// Clamped length of a request, and its length in the map's tiles: without
+// the ones a windowed map leaves out.
+__device__ __forceinline__ int clamp_len(const AttnParams &p, int L) {
+    return L < 0 ? 0 : min(L, p.max_pages * kTile);
+}
+
+template <bool WIN>
+__device__ __forceinline__ int planned_len(const AttnParams &p, int L) {
+    L = clamp_len(p, L);
+    if (WIN) L -= kTile * window_skip(L, p.q_len, p.window, p.sink_tiles);
+    return L;
+}
+
+template <bool FP8, int STAGES, int TPS, int NB, bool WIN = false, bool BLK = false>
 struct AttnTraits {
     static constexpr int kConsumers = kConsumerWarps * TPS;          // consumer warps
     static constexpr int kThreads = 32 * (2 + kConsumers);           // + producer, combiner
@@ -106,11 +133,13 @@ struct AttnTraits {
     static constexpr int kStageKV = TPS * kTileBytes;               // K (or V) bytes per stage
     static constexpr int kRows = 8 * NB;                             // query rows held per stage
     static constexpr int kQBytes = kRows * kHeadDim * kElem;        // Q slot per stage
+    static constexpr int kScaleBytes = BLK ? TPS * kPageScales * 4 : 0;  // block scales per stage
     static constexpr int kState = kStateRegs * NB;                   // state floats per lane
     static constexpr int kSlotFloats = kConsumers * kState * 32;     // one hand-off slot
     // Shared memory of the layout below with `slots` hand-off slots.
     static constexpr int bytes_with(int slots) {
-        return 2 * STAGES * kStageKV + STAGES * kQBytes + STAGES * (int)sizeof(StageInfo) +
+        return 2 * STAGES * kStageKV + STAGES * kQBytes + STAGES * kScaleBytes +
+               STAGES * (int)sizeof(StageInfo) +
                slots * kSlotFloats * 4 + kRows * kStageStride * 4 +
                slots * (int)sizeof(SlotInfo) + (kMaxLast + 1) * (int)sizeof(SlotInfo) +
                (2 * STAGES + 2 * slots + 1) * 8 + 16 + 1024;
@@ -121,7 +150,8 @@ struct AttnTraits {
     static constexpr int kOffK = 0;
     static constexpr int kOffV = kOffK + STAGES * kStageKV;
     static constexpr int kOffQ = kOffV + STAGES * kStageKV;
-    static constexpr int kOffInfo = kOffQ + STAGES * kQBytes;
+    static constexpr int kOffScale = kOffQ + STAGES * kQBytes;
+    static constexpr int kOffInfo = kOffScale + STAGES * kScaleBytes;
     static constexpr int kOffComb = kOffInfo + STAGES * (int)sizeof(StageInfo);
     static constexpr int kOffStage = kOffComb + kSlots * kSlotFloats * 4;
     static constexpr int kOffSlotInfo = kOffStage + kRows * kStageStride * 4;
@@ -155,15 +185,15 @@ __device__ __forceinline__ void wait_for_map(ProducerState &ps) {
 // Hkv * sum n_r, budget = max(ceil(T / bins), floor, 1), bin c = global tiles
 // [c * budget, ...), units head-major).  Returns false when the batch is too
 // large to scan here; te == tb means the bin is empty.
+template <bool WIN>
 __device__ __forceinline__ bool first_descriptor(const AttnParams &p, int c, int &h, int &r,
                                                  int &tb, int &te) {
     if (p.B > kFlyMaxBatch) return false;
-    const int lane = threadIdx.x & 31, cap = p.max_pages * kTile;
+    const int lane = threadIdx.x & 31;
     int N = 0;
     for (int base = 0; base < p.B; base += 32) {
         const int rr = base + lane;
-        int L = rr < p.B ? p.seqlens[rr] : 0;
-        L = L < 0 ? 0 : min(L, cap);
+        const int L = planned_len<WIN>(p, rr < p.B ? p.seqlens[rr] : 0);
         N += __reduce_add_sync(kFullMask, (L + kTile - 1) / kTile);
     }
     const long long T = (long long)p.Hkv * N;
@@ -176,8 +206,7 @@ __device__ __forceinline__ bool first_descriptor(const AttnParams &p, int c, int
     int carry = 0;
     for (int base = 0; base < p.B; base += 32) {
         const int rr = base + lane;
-        int L = rr < p.B ? p.seqlens[rr] : 0;
-        L = L < 0 ? 0 : min(L, cap);
+        const int L = planned_len<WIN>(p, rr < p.B ? p.seqlens[rr] : 0);
         const int n = (L + kTile - 1) / kTile;
         int incl = n;  // inclusive prefix of n over this chunk
 #pragma unroll
@@ -262,12 +291,11 @@ __device__ __forceinline__ void walk_base(const AttnParams &p, FlyWalk &w) {
     w.base = w.c + inner;
 }
 
+template <bool WIN>
 __device__ __forceinline__ void walk_init(const AttnParams &p, int c, FlyWalk &w) {
-    const int lane = threadIdx.x & 31, cap = p.max_pages * kTile;
-    int L0 = lane < p.B ? p.seqlens[lane] : 0;
-    int L1 = lane + 32 < p.B ? p.seqlens[lane + 32] : 0;
-    L0 = L0 < 0 ? 0 : min(L0, cap);
-    L1 = L1 < 0 ? 0 : min(L1, cap);
+    const int lane = threadIdx.x & 31;
+    const int L0 = planned_len<WIN>(p, lane < p.B ? p.seqlens[lane] : 0);
+    const int L1 = planned_len<WIN>(p, lane + 32 < p.B ? p.seqlens[lane + 32] : 0);
     w.n0 = (L0 + kTile - 1) / kTile;
     w.n1 = (L1 + kTile - 1) / kTile;
     w.N = __reduce_add_sync(kFullMask, w.n0 + w.n1);
@@ -350,13 +378,13 @@ __device__ __forceinline__ void walk_chunk(const AttnParams &p, FlyWalk &w, int 
 // which case its last stage's copies are issued before the map is waited for
 // (the stage is released once the layout is written), so the wait overlaps
 // the stage's transfer.  Returns false after a timeout.
-template <bool FP8, int STAGES, int TPS, int NB>
+template <bool FP8, int STAGES, int TPS, int NB, bool WIN = false, bool BLK = false>
 __device__ __forceinline__ bool stream_desc(const CUtensorMap *tmap_k, const CUtensorMap *tmap_v,
                                             const AttnParams &p, uint8_t *smem, int h, int r,
                                             int tb, int te, int desc_idx, int bin,
                                             FlyWalk *walk, int bin_pos, ProducerState &ps,
                                             uint64_t policy, volatile int *abort) {
-    using Tr = AttnTraits<FP8, STAGES, TPS, NB>;
+    using Tr = AttnTraits<FP8, STAGES, TPS, NB, WIN, BLK>;
     const int lane = threadIdx.x & 31;
     StageInfo *info = reinterpret_cast<StageInfo *>(smem + Tr::kOffInfo);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Tr::kOffBar);
@@ -367,7 +395,11 @@ __device__ __forceinline__ bool stream_desc(const CUtensorMap *tmap_k, const CUt
     const uint32_t q_bytes = q_group * (uint32_t)p.q_len;
     const size_t q_token_stride = (size_t)p.Hq * kHeadDim * Tr::kElem;
     if (tb >= te) return true;  // empty split of the static schedule
-    const int L = p.seqlens[r];
+    int L = p.seqlens[r], skip = 0;
+    if (WIN) {
+        L = clamp_len(p, L);
+        skip = window_skip(L, p.q_len, p.window, p.sink_tiles);
+    }
     const int u = h * p.B + r;
     float qs = 1.f;
     if (FP8 && lane < p.R) {
@@ -382,8 +414,13 @@ __device__ __forceinline__ bool stream_desc(const CUtensorMap *tmap_k, const CUt
     // only after the first stage's copies are issued: the consumers need
     // them once the stage has landed, so their load (from DRAM after a
     // flush, where the block table is warm in L2) does not hold up the copies
+    // block-table entry of the descriptor's tile t (a windowed map planned for
+    // other lengths must not lead past the row)
+    auto entry = [&](int t) {
+        return WIN ? min(t < p.sink_tiles ? t : t + skip, p.max_pages - 1) : t;
+    };
     int page0 = 0;
-    if (lane < min(32, te - tb)) page0 = bt_row[tb + lane];
+    if (lane < min(32, te - tb)) page0 = bt_row[entry(tb + lane)];
     float qsg[Tr::kRows];
 #pragma unroll
     for (int g = 0; g < Tr::kRows; ++g) qsg[g] = 1.f;
@@ -393,7 +430,7 @@ __device__ __forceinline__ bool stream_desc(const CUtensorMap *tmap_k, const CUt
         const int nt = min(32, te - t0);
         int page = 0;
         if (lane < nt) {
-            page = t0 == tb ? page0 : bt_row[t0 + lane];
+            page = t0 == tb ? page0 : bt_row[entry(t0 + lane)];
             if (page < 0 || page >= p.num_pages) {
                 ps.late_flags |= HPC_FLAG_BAD_PAGE;
                 page = 0;  // stay inside the cache; the result is flagged as invalid
@@ -437,11 +474,13 @@ __device__ __forceinline__ bool stream_desc(const CUtensorMap *tmap_k, const CUt
                 si.desc_idx = idx;
                 si.count = count;
                 si.chunk_off = chunk_off;
+                if (WIN) si.skip = skip;
                 if (!late_q) {
 #pragma unroll
                     for (int g = 0; g < Tr::kRows; ++g) si.qscale[g] = qsg[g];
                 }
-                const uint32_t bytes = 2u * ns * Tr::kTileBytes + (first ? q_bytes : 0u);
+                const uint32_t bytes = 2u * ns * Tr::kTileBytes + (first ? q_bytes : 0u) +
+                                       (BLK ? ns * kPageScales * 4u : 0u);
                 if (defer || late_q) mbar_expect_tx(&full[stage], bytes);  // arrives below
                 else mbar_arrive_expect_tx(&full[stage], bytes);
 #pragma unroll
@@ -452,6 +491,11 @@ __device__ __forceinline__ bool stream_desc(const CUtensorMap *tmap_k, const CUt
                     if (FP8) {
                         tma_load_4d(sk, tmap_k, &full[stage], 0, h, 0, pg[s], policy);
                         tma_load_4d(sv, tmap_v, &full[stage], 0, h, 0, pg[s], policy);
+                        if (BLK)
+                            bulk_load(smem + Tr::kOffScale + stage * Tr::kScaleBytes +
+                                          s * kPageScales * 4,
+                                      p.kv_scale + ((size_t)pg[s] * p.Hkv + h) * kPageScales,
+                                      kPageScales * 4, &full[stage]);
                     } else {
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
@@ -499,11 +543,11 @@ __device__ __forceinline__ bool stream_desc(const CUtensorMap *tmap_k, const CUt
     return true;
 }
 
-template <bool FP8, int STAGES, int TPS, int NB>
+template <bool FP8, int STAGES, int TPS, int NB, bool WIN = false, bool BLK = false>
 __device__ __forceinline__ void attn_producer(const CUtensorMap *tmap_k, const CUtensorMap *tmap_v,
                                               const AttnParams &p, uint8_t *smem,
                                               volatile int *abort) {
-    using Tr = AttnTraits<FP8, STAGES, TPS, NB>;
+    using Tr = AttnTraits<FP8, STAGES, TPS, NB, WIN, BLK>;
     const int lane = threadIdx.x & 31;
     StageInfo *info = reinterpret_cast<StageInfo *>(smem + Tr::kOffInfo);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Tr::kOffBar);
@@ -527,11 +571,11 @@ __device__ __forceinline__ void attn_producer(const CUtensorMap *tmap_k, const C
     bool walked = false;  // the whole first bin came from the walk (the map is not needed)
     if (p.fly && p.B <= kWalkMaxBatch) {
         FlyWalk w;
-        walk_init(p, blockIdx.x, w);
+        walk_init<WIN>(p, blockIdx.x, w);
         int streamed = 0;
         while (ok && w.te > w.tb) {
             const bool derive = streamed + (w.te - w.tb) < kWalkTiles;
-            ok = stream_desc<FP8, STAGES, TPS, NB>(tmap_k, tmap_v, p, smem, w.h, w.r, w.tb, w.te,
+            ok = stream_desc<FP8, STAGES, TPS, NB, WIN, BLK>(tmap_k, tmap_v, p, smem, w.h, w.r, w.tb, w.te,
                                                -1, blockIdx.x, derive ? &w : nullptr, w.k, ps,
                                                policy, abort);
             ++skip;
@@ -542,8 +586,8 @@ __device__ __forceinline__ void attn_producer(const CUtensorMap *tmap_k, const C
         walked = ok && w.te == w.tb && !ps.waited && !dynamic;
     } else if (p.fly) {
         int h, r, tb, te;
-        if (first_descriptor(p, blockIdx.x, h, r, tb, te) && te > tb) {
-            ok = stream_desc<FP8, STAGES, TPS, NB>(tmap_k, tmap_v, p, smem, h, r, tb, te, -1,
+        if (first_descriptor<WIN>(p, blockIdx.x, h, r, tb, te) && te > tb) {
+            ok = stream_desc<FP8, STAGES, TPS, NB, WIN, BLK>(tmap_k, tmap_v, p, smem, h, r, tb, te, -1,
                                                blockIdx.x, nullptr, 0, ps, policy, abort);
             skip = 1;
         }
@@ -561,7 +605,7 @@ __device__ __forceinline__ void attn_producer(const CUtensorMap *tmap_k, const C
         const int d_end = p.bin_ptr[bin + 1];
         for (int d = d_begin; d < d_end && ok; ++d) {
             const int4 ds = p.desc[d];
-            ok = stream_desc<FP8, STAGES, TPS, NB>(tmap_k, tmap_v, p, smem, ds.x, ds.y, ds.z, ds.w, d,
+            ok = stream_desc<FP8, STAGES, TPS, NB, WIN, BLK>(tmap_k, tmap_v, p, smem, ds.x, ds.y, ds.z, ds.w, d,
                                                bin, nullptr, 0, ps, policy, abort);
         }
         if (!dynamic) break;
@@ -749,10 +793,10 @@ __device__ __forceinline__ int stage_col(int dim) { return dim ^ (((dim >> 4) & 
 
 // Merges the consumers' states of each finished descriptor and writes the
 // result; counts chunks of split units.  Returns false after a timeout.
-template <bool FP8, int STAGES, int TPS, int NB>
+template <bool FP8, int STAGES, int TPS, int NB, bool WIN = false, bool BLK = false>
 __device__ __forceinline__ bool attn_combiner(const AttnParams &p, uint8_t *smem,
                                               volatile int *abort) {
-    using Tr = AttnTraits<FP8, STAGES, TPS, NB>;
+    using Tr = AttnTraits<FP8, STAGES, TPS, NB, WIN, BLK>;
     constexpr int NC = Tr::kConsumers;
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const float *comb = reinterpret_cast<const float *>(smem + Tr::kOffComb);
@@ -881,10 +925,10 @@ __device__ __forceinline__ bool attn_combiner(const AttnParams &p, uint8_t *smem
 }
 
 // ------------------------------------------------------------------ consumer
-template <bool FP8, int STAGES, int TPS, int NB>
+template <bool FP8, int STAGES, int TPS, int NB, bool WIN = false, bool BLK = false>
 __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem,
                                               volatile int *abort) {
-    using Tr = AttnTraits<FP8, STAGES, TPS, NB>;
+    using Tr = AttnTraits<FP8, STAGES, TPS, NB, WIN, BLK>;
     const int lane = threadIdx.x & 31, cw = (threadIdx.x >> 5) - 2;
     const int g = lane >> 2, t4 = lane & 3;
     const int slot = cw >> 2;  // which tile of the stage this warp works on
@@ -908,13 +952,14 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
     // (rows) 8 nb + 2 t4 + c, c = 0, 1 of every block.
     float o[NB][8][4];
     float m[NB][2], l[NB][2], sc[NB][2];
+    float mw[NB][2];  // BLK: running maximum of score + log2 of the V scale (O's reference)
     int lim[NB][2];  // tokens visible to the lane's rows: t < lim (causal for q_len > 1)
     uint32_t qf[NB][8][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            m[nb][c] = kNegInf;
+            m[nb][c] = mw[nb][c] = kNegInf;
             l[nb][c] = sc[nb][c] = 0.f;
             lim[nb][c] = 0;
         }
@@ -960,7 +1005,7 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
                         sc[nb][c] = p.score_scale * info[stage].qscale[rho];
                         // query token i = rho / G sees tokens below L - q_len + 1 + i
                         lim[nb][c] = rho < p.R ? L - p.q_len + 1 + rho / p.G : L;
-                        m[nb][c] = kNegInf;
+                        m[nb][c] = mw[nb][c] = kNegInf;
                         l[nb][c] = 0.f;
                     }
 #pragma unroll
@@ -969,9 +1014,26 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
                 }
             }
 
-            if (slot < ntiles) {
+            int tile = tile0 + slot;
+            if (WIN && tile >= p.sink_tiles) tile += info[stage].skip;
+            const int tok0 = tile * kTile + 16 * sub;  // first token of this warp's slice
+            // WIN: the first token of the window of the request's first query;
+            // a token below it that is no sink is dead, like one past L
+            const int lo0 = WIN ? L - p.q_len + 1 - p.window : 0;
+            auto live = [&](int t) { return t < L && (!WIN || t >= lo0 || t < p.sinks); };
+            // a slice without a live token changes nothing (and its block may
+            // hold anything, its scales among it)
+            const bool any_live = !(WIN || BLK) ||
+                                  (tok0 < L && (!WIN || tok0 + 15 >= lo0 || tok0 < p.sinks));
+            if (slot < ntiles && any_live) {
                 const uint32_t sK = sK0 + stage * Tr::kStageKV, sV = sV0 + stage * Tr::kStageKV;
-                const int tile = tile0 + slot;
+                float kf = 1.f, lv = 0.f;  // BLK: the block's K scale, log2 of its V scale
+                if (BLK) {
+                    const float *bs = reinterpret_cast<const float *>(
+                        smem + Tr::kOffScale + stage * Tr::kScaleBytes + slot * kPageScales * 4);
+                    kf = bs[sub];
+                    lv = lg2(bs[kPageScales / 2 + sub]);
+                }
 
                 // ---- S^T = K . Q^T for this warp's 16 tokens x 8 NB rows
                 float s4[NB][4];
@@ -1025,7 +1087,7 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
                     for (int q = 0; q < 4; ++q) {
                         const int tok = 16 * sub + 2 * t4 + (q & 1) + (q >> 1) * 8;
                         Rv[q] = lds128(sV + tok * 128 + ((g ^ (tok & 7)) << 4));
-                        if (tile * kTile + tok >= L) Rv[q] = make_uint4(0u, 0u, 0u, 0u);
+                        if (!live(tile * kTile + tok)) Rv[q] = make_uint4(0u, 0u, 0u, 0u);
                     }
                     const uint32_t wA[4] = {Rv[0].x, Rv[0].y, Rv[0].z, Rv[0].w};
                     const uint32_t wB[4] = {Rv[1].x, Rv[1].y, Rv[1].z, Rv[1].w};
@@ -1040,15 +1102,20 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
                 }
                 // ---- online softmax (log2 domain); a token at or past a row's
                 // limit is masked for that row
-                const int tok0 = tile * kTile + 16 * sub;  // first token of this warp's slice
+                // (WIN: or before its window, unless it is a sink)
                 const int ta = tok0 + g, tb_ = tok0 + g + 8;
+                auto sees = [&](int t, int limit) {
+                    return t < limit && (!WIN || t + p.window >= limit || t < p.sinks);
+                };
                 float x[NB][4], mx[NB][2];
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
-                    x[nb][0] = ta < lim[nb][0] ? s4[nb][0] * sc[nb][0] : kNegInf;
-                    x[nb][1] = ta < lim[nb][1] ? s4[nb][1] * sc[nb][1] : kNegInf;
-                    x[nb][2] = tb_ < lim[nb][0] ? s4[nb][2] * sc[nb][0] : kNegInf;
-                    x[nb][3] = tb_ < lim[nb][1] ? s4[nb][3] * sc[nb][1] : kNegInf;
+                    const float s0 = BLK ? sc[nb][0] * kf : sc[nb][0];
+                    const float s1 = BLK ? sc[nb][1] * kf : sc[nb][1];
+                    x[nb][0] = sees(ta, lim[nb][0]) ? s4[nb][0] * s0 : kNegInf;
+                    x[nb][1] = sees(ta, lim[nb][1]) ? s4[nb][1] * s1 : kNegInf;
+                    x[nb][2] = sees(tb_, lim[nb][0]) ? s4[nb][2] * s0 : kNegInf;
+                    x[nb][3] = sees(tb_, lim[nb][1]) ? s4[nb][3] * s1 : kNegInf;
                     mx[nb][0] = fmaxf(x[nb][0], x[nb][2]);
                     mx[nb][1] = fmaxf(x[nb][1], x[nb][3]);
                 }
@@ -1064,19 +1131,35 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
                 uint32_t b0[NB], b1[NB];
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
-                    float ms[2];
+                    float ms[2], wf[2];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const float mn = fmaxf(m[nb][c], mx[nb][c]);
                         ms[c] = mn == kNegInf ? 0.f : mn;
                         al[nb][c] = ex2(m[nb][c] - ms[c]);
                         m[nb][c] = mn;
+                        if (BLK) {
+                            // l keeps the reference m; O moves to M, and p to the
+                            // weight p 2^(log2 v_s + m - M) <= 1 (the exponent is
+                            // capped so that p = 0 stays 0 for any scales)
+                            l[nb][c] *= al[nb][c];
+                            const float wn = fmaxf(mw[nb][c], mx[nb][c] + lv);
+                            const float wr = wn == kNegInf ? 0.f : wn;
+                            al[nb][c] = ex2(mw[nb][c] - wr);
+                            wf[c] = wn == kNegInf ? 0.f : ex2(fminf(lv + ms[c] - wr, 126.f));
+                            mw[nb][c] = wn;
+                        }
                         rescale |= al[nb][c] != 1.f;
                     }
                     const float p0 = ex2(x[nb][0] - ms[0]), p1 = ex2(x[nb][1] - ms[1]);
                     const float p2 = ex2(x[nb][2] - ms[0]), p3 = ex2(x[nb][3] - ms[1]);
                     uint32_t pk01, pk23;
-                    if (FP8) {
+                    if (BLK) {
+                        pk01 = pack_f16x2(p0 * wf[0], p1 * wf[1]);
+                        pk23 = pack_f16x2(p2 * wf[0], p3 * wf[1]);
+                        l[nb][0] += p0 + p2;
+                        l[nb][1] += p1 + p3;
+                    } else if (FP8) {
                         pk01 = pack_f16x2(p0, p1);
                         pk23 = pack_f16x2(p2, p3);
                         const float2 r01 = f16x2_to_f32x2(pk01), r23 = f16x2_to_f32x2(pk23);
@@ -1114,9 +1197,9 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
                 } else {
                     const int tv = tok0 + 2 * t4;  // tokens of a0/a1 halves; +8 for a2/a3
                     const uint32_t mk01 =
-                        (tv < L ? 0x0000ffffu : 0u) | (tv + 1 < L ? 0xffff0000u : 0u);
+                        (live(tv) ? 0x0000ffffu : 0u) | (live(tv + 1) ? 0xffff0000u : 0u);
                     const uint32_t mk23 =
-                        (tv + 8 < L ? 0x0000ffffu : 0u) | (tv + 9 < L ? 0xffff0000u : 0u);
+                        (live(tv + 8) ? 0x0000ffffu : 0u) | (live(tv + 9) ? 0xffff0000u : 0u);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const int chunk = (2 * j + (mi & 1)) & 7;
@@ -1139,6 +1222,19 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
             const int k = handed % Tr::kSlots;
             if (!warp_wait(&slot_empty[k], ((handed / Tr::kSlots) & 1u) ^ 1u, abort))
                 return false;
+            if (BLK && (flags & kLast)) {  // O from units of 2^M to units of 2^m, l's
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float f = mw[nb][c] == kNegInf ? 0.f : ex2(mw[nb][c] - m[nb][c]);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            o[nb][j][c] *= f;
+                            o[nb][j][c + 2] *= f;
+                        }
+                    }
+            }
             if (flags & kLast) {  // lane-major: 9 NB float4 per lane, conflict-free
                 float4 *dst = reinterpret_cast<float4 *>(
                     comb + ((k * Tr::kConsumers + cw) * 32 + lane) * Tr::kState);
@@ -1162,11 +1258,11 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
 }
 
 // ------------------------------------------------------------------ kernel
-template <bool FP8, int STAGES, int TPS, int NB>
-__global__ void __launch_bounds__(AttnTraits<FP8, STAGES, TPS, NB>::kThreads, 1)
+template <bool FP8, int STAGES, int TPS, int NB, bool WIN = false, bool BLK = false>
+__global__ void __launch_bounds__(AttnTraits<FP8, STAGES, TPS, NB, WIN, BLK>::kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const __grid_constant__ CUtensorMap tmap_v, const AttnParams p) {
-    using Tr = AttnTraits<FP8, STAGES, TPS, NB>;
+    using Tr = AttnTraits<FP8, STAGES, TPS, NB, WIN, BLK>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Tr::kOffBar);
@@ -1209,7 +1305,7 @@ __global__ void __launch_bounds__(AttnTraits<FP8, STAGES, TPS, NB>::kThreads, 1)
     __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) {
-        attn_producer<FP8, STAGES, TPS, NB>(&tmap_k, &tmap_v, p, smem, abort);
+        attn_producer<FP8, STAGES, TPS, NB, WIN, BLK>(&tmap_k, &tmap_v, p, smem, abort);
         return;
     }
     // Every global write of this grid (outputs, partials, counters) comes
@@ -1225,8 +1321,8 @@ __global__ void __launch_bounds__(AttnTraits<FP8, STAGES, TPS, NB>::kThreads, 1)
             for (int i = lane; i < row_vec; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
         }
     }
-    bool ok = warp == 1 ? attn_combiner<FP8, STAGES, TPS, NB>(p, smem, abort)
-                        : attn_consumer<FP8, STAGES, TPS, NB>(p, smem, abort);
+    bool ok = warp == 1 ? attn_combiner<FP8, STAGES, TPS, NB, WIN, BLK>(p, smem, abort)
+                        : attn_consumer<FP8, STAGES, TPS, NB, WIN, BLK>(p, smem, abort);
     if (!ok) {
         grid_dependency_wait();  // meta[3] is written by the assign kernel
         if (lane == 0) atomicOr(p.meta + 3, (int)HPC_FLAG_TIMEOUT);
@@ -1273,5 +1369,31 @@ __global__ void __launch_bounds__(AttnTraits<FP8, STAGES, TPS, NB>::kThreads, 1)
             merge_unit_head<NB == 1 ? 16 : 8>(p, last[1 + item / p.R].di, item % p.R);
     }
 }
+
+// Launches one instantiation as a programmatic dependent of the previous
+// kernel in the stream (the assign kernel): its prologue overlaps that
+// kernel's tail.
+template <bool FP8, int STAGES, int TPS, int NB, bool WIN, bool BLK>
+struct AttnVariant {
+    using Tr = AttnTraits<FP8, STAGES, TPS, NB, WIN, BLK>;
+    static AttnConfig config() {
+        return {reinterpret_cast<const void *>(&attn_kernel<FP8, STAGES, TPS, NB, WIN, BLK>),
+                Tr::kSmemBytes, Tr::kThreads};
+    }
+    static cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const AttnParams &p,
+                              int grid, cudaStream_t s) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(grid);
+        cfg.blockDim = dim3(Tr::kThreads);
+        cfg.dynamicSmemBytes = Tr::kSmemBytes;
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, attn_kernel<FP8, STAGES, TPS, NB, WIN, BLK>, tk, tv, p);
+    }
+};
 
 }  // namespace hpc

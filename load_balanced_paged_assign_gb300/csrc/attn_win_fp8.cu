@@ -1,0 +1,18 @@
+// Windowed form of the persistent attention kernel over an FP8-E4M3 cache.
+#include "attn_kernel.cuh"
+
+namespace hpc {
+
+// The plain form's pipeline shapes: two tiles per stage (eight consumer
+// warps), four stages.
+using One = AttnVariant<true, 4, 2, 1, true, false>;  // up to 8 query rows per KV head
+using Two = AttnVariant<true, 4, 2, 2, true, false>;  // up to 16
+
+AttnConfig attn_config_win_fp8(int nb) { return nb == 2 ? Two::config() : One::config(); }
+
+cudaError_t launch_attn_win_fp8(int nb, const CUtensorMap &tk, const CUtensorMap &tv,
+                             const AttnParams &p, int grid, cudaStream_t s) {
+    return nb == 2 ? Two::launch(tk, tv, p, grid, s) : One::launch(tk, tv, p, grid, s);
+}
+
+}  // namespace hpc

@@ -67,7 +67,8 @@ __global__ void __launch_bounds__(kPlanThreads)
     assign_kernel(const int32_t *__restrict__ seqlens, int B, int Hkv, int max_pages,
                   int num_ctas, int floor, int4 *__restrict__ desc, int32_t *__restrict__ bin_ptr,
                   int32_t *__restrict__ chunk_count, int32_t *__restrict__ chunk_off,
-                  int32_t *__restrict__ meta, int cap_desc, const int32_t *bt_prefetch) {
+                  int32_t *__restrict__ meta, int cap_desc, const int32_t *bt_prefetch,
+                  const PlanWindow win) {
     extern __shared__ int s_end[];  // [B] inclusive prefix of tiles per request
     __shared__ int s_scan[32];
     __shared__ unsigned s_flags;
@@ -86,11 +87,16 @@ __global__ void __launch_bounds__(kPlanThreads)
     if (tid == 0) s_flags = 0;
     unsigned flags = 0;
 
-    // a1: tiles per request, n_r = ceil(L_r / 64), and their running sum.
+    // a1: tiles per request, n_r = ceil(L_r / 64) less the tiles that no query's
+    // window reaches, and their running sum.
     int carry = 0;
     for (int base = 0; base < B; base += blockDim.x) {
         const int r = base + tid;
-        const int n = r < B ? tiles_of(live_len(seqlens, r, max_pages, flags)) : 0;
+        int n = 0;
+        if (r < B) {
+            const int L = live_len(seqlens, r, max_pages, flags);
+            n = tiles_of(L) - window_skip(L, win.q_len, win.window, win.sink_tiles);
+        }
         int chunk_total;
         const int incl = block_inclusive_scan(n, s_scan, chunk_total);
         if (r < B) s_end[r] = carry + incl;
@@ -220,7 +226,7 @@ static int plan_threads(int B, int Hkv, int num_ctas) {
 
 cudaError_t launch_assign(const int32_t *seqlens, int B, int Hkv, int max_pages, int num_ctas,
                           int floor, const hpc_task_map &map, cudaStream_t s,
-                          const int32_t *bt_prefetch) {
+                          const int32_t *bt_prefetch, const PlanWindow &win) {
     const int smem = assign_smem_bytes(B);
     if (smem > 48 * 1024) {
         cudaError_t e = cudaFuncSetAttribute(assign_kernel,
@@ -239,7 +245,7 @@ cudaError_t launch_assign(const int32_t *seqlens, int B, int Hkv, int max_pages,
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, assign_kernel, seqlens, B, Hkv, max_pages, num_ctas, floor,
                               reinterpret_cast<int4 *>(map.desc), map.bin_ptr, map.chunk_count,
-                              map.chunk_off, map.meta, map.cap_desc, bt_prefetch);
+                              map.chunk_off, map.meta, map.cap_desc, bt_prefetch, win);
 }
 
 cudaError_t launch_static_plan(const int32_t *seqlens, int B, int Hkv, int max_pages,
