@@ -745,7 +745,7 @@ hpc_status hpc_rope_norm_block(const void *d_qkv, int64_t qkv_row_stride, const 
  *                      outside [0, 64 * the smaller row length] (clamped) or a
  *                      start below 0 (taken as 0); HPC_FLAG_BAD_PAGE for an
  *                      entry outside either cache (that page is left out)
- * Pointers to caches, outputs and scales are 16-byte aligned.  B <=
+ * Caches and scales are 16-byte aligned, the outputs 32-byte.  B <=
  * HPC_MAX_BATCH.  Asynchronous on `stream`; reads nothing before the previous
  * kernel on the stream has finished.
  */

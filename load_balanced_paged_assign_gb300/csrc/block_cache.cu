@@ -132,8 +132,10 @@ __device__ __forceinline__ void quotient8(float (&x)[8], float s) {
 }
 
 // One run's rows of one KV head, K or V: half-warp `half` holds rows 2 i +
-// half of the run, all of them in registers, so that the block's maximum is
-// known before the first code is written and each row is read once.
+// half of the run, all of them in registers as the BF16 words they came in, so
+// each row is read once; K's norm and rotation are computed for the block's
+// maximum and again for the codes (a tenth of a prompt's rows; the fp32 values
+// would take twice the registers and cost a resident CTA).
 template <int LAYOUT, bool NF, bool KEY>
 __device__ __forceinline__ void write_run(const BlockWriteArgs &a, const BlockWriteShared &sh,
                                           int t0, const RunInfo run, int head, int lane) {
@@ -162,19 +164,23 @@ __device__ __forceinline__ void write_run(const BlockWriteArgs &a, const BlockWr
     const bool fresh = written & 1u;
     const bool twice = __popc(written) < run.len;  // a position comes twice: the later one stays
 
-    float x[kRowPairs][8], w[8];
+    float w[8];
     if constexpr (KEY) unpack8(load_words<LAYOUT>(reinterpret_cast<const char *>(a.k_w), s), w);
+    auto row = [&](int i, float (&x)[8]) {
+        unpack8(v[i], x);
+        if constexpr (KEY) {
+            float c[4], sn[4], nsn[4];
+            load_angles(sh.ang + min(run.first + 2 * i + half, kBwTokens - 1) * 128, s, c, sn, nsn);
+            norm_rope<LAYOUT, NF>(x, w, c, sn, nsn, a.eps);
+        }
+    };
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < kRowPairs; ++i) {
         if (2 * i >= run.len) continue;
-        unpack8(v[i], x[i]);
-        if constexpr (KEY) {
-            float c[4], sn[4], nsn[4];
-            load_angles(sh.ang + min(run.first + 2 * i + half, kBwTokens - 1) * 128, s, c, sn, nsn);
-            norm_rope<LAYOUT, NF>(x[i], w, c, sn, nsn, a.eps);
-        }
-        if (2 * i + half < run.len) amax = fmaxf(amax, absmax8_finite(x[i]));
+        float x[8];
+        row(i, x);
+        if (2 * i + half < run.len) amax = fmaxf(amax, absmax8_finite(x));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, o));
@@ -215,8 +221,10 @@ __device__ __forceinline__ void write_run(const BlockWriteArgs &a, const BlockWr
         if (twice)
             for (int k = j + 1; k < run.len; ++k)
                 store &= (int)(sh.slot[run.first + k] % kScaleBlock) != off;
-        quotient8(x[i], sc);
-        if (store) store_e4m3<kHeld>(reinterpret_cast<char *>(base + off * step), s, x[i]);
+        float x[8];
+        row(i, x);
+        quotient8(x, sc);
+        if (store) store_e4m3<kHeld>(reinterpret_cast<char *>(base + off * step), s, x);
     }
 }
 
@@ -265,8 +273,11 @@ __device__ __forceinline__ void write_queries(const BlockWriteArgs &a, const flo
 // (a run's rows of one head, K or V; 8 query rows of a token) go round the
 // eight warps.  Each row is read once, straight into registers (16 bytes a
 // lane, 4 to 8 rows in flight per half-warp).
+#ifndef HPC_BW_CTAS
+#define HPC_BW_CTAS 3  // resident CTAs per SM the register budget must allow
+#endif
 template <int LAYOUT, bool NF, bool Q8>
-__global__ void __launch_bounds__(kBwThreads, 2) rope_norm_block_kernel(const BlockWriteArgs a) {
+__global__ void __launch_bounds__(kBwThreads, HPC_BW_CTAS) rope_norm_block_kernel(const BlockWriteArgs a) {
     __shared__ __align__(16) BlockWriteShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dependency_wait();  // everything read may come from the kernel before
@@ -380,8 +391,8 @@ __device__ __forceinline__ int2 read_range(const BlockReadArgs &a, int r, unsign
     return make_int2(st, L);
 }
 
-// 16 codes at scale f as 16 BF16 values.
-__device__ __forceinline__ void widen16(uint4 q, float f, uint4 &lo, uint4 &hi) {
+// 16 codes at scale f as 16 BF16 values, stored by one 32-byte instruction.
+__device__ __forceinline__ void widen16(uint4 q, float f, uint4 *dst) {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
     uint32_t o[8];
 #pragma unroll
@@ -392,17 +403,19 @@ __device__ __forceinline__ void widen16(uint4 q, float f, uint4 &lo, uint4 &hi) 
         o[2 * k] = pack_bf16x2(a.x * f, a.y * f);
         o[2 * k + 1] = pack_bf16x2(b.x * f, b.y * f);
     }
-    lo = make_uint4(o[0], o[1], o[2], o[3]);
-    hi = make_uint4(o[4], o[5], o[6], o[7]);
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(o[0]),
+                 "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                 : "memory");
 }
 
-// The requests' pages, numbered through, go round the persistent CTAs (each
-// finds the page's request in a prefix sum over the requests, built once per
-// CTA), so a batch of very different lengths loads the SMs evenly.  A page's
-// tokens are contiguous for all heads: a thread takes 16 codes (16 bytes in,
-// 32 out) of K and the same of V at a time.
+// The requests' blocks of 16 tokens, numbered through, go round the persistent
+// CTAs (each finds a block's request in a prefix sum over the requests, built
+// once per CTA), so a batch of very different lengths, or one request alone,
+// loads the SMs evenly.  A block's tokens are contiguous for all heads: a
+// thread takes 16 codes (16 bytes in, 32 out) of K and the same of V at a
+// time, two of each in flight.
 __global__ void __launch_bounds__(kRdThreads) kv_read_block_kernel(const BlockReadArgs a) {
-    extern __shared__ int s_end[];  // [B] pages of the requests up to and with r
+    extern __shared__ int s_end[];  // [B] blocks of the requests up to and with r
     __shared__ int s_scan[kRdThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dependency_wait();
@@ -413,7 +426,7 @@ __global__ void __launch_bounds__(kRdThreads) kv_read_block_kernel(const BlockRe
         int n = 0;
         if (r < a.B) {
             const int2 x = read_range(a, r, bad);
-            n = x.y > x.x ? (x.y - 1) / kTile - x.x / kTile + 1 : 0;
+            n = x.y > x.x ? (x.y - 1) / kScaleBlock - x.x / kScaleBlock + 1 : 0;
         }
         int v = n;
 #pragma unroll
@@ -434,8 +447,9 @@ __global__ void __launch_bounds__(kRdThreads) kv_read_block_kernel(const BlockRe
         __syncthreads();
     }
     if (bad && blockIdx.x == 0 && a.flags) atomicOr(a.flags, (int)bad);
+    const int per_token = a.Hkv * (kHeadDim / 16);  // 16-code vectors
     for (int p = blockIdx.x; p < total; p += gridDim.x) {
-        int lo = 0, hi = a.B - 1;  // the first request whose pages end past p
+        int lo = 0, hi = a.B - 1;  // the first request whose blocks end past p
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
             if (s_end[mid] > p) hi = mid;
@@ -443,37 +457,44 @@ __global__ void __launch_bounds__(kRdThreads) kv_read_block_kernel(const BlockRe
         }
         unsigned ignored = 0;
         const int2 x = read_range(a, lo, ignored);
-        const int tile = x.x / kTile + p - (lo ? s_end[lo - 1] : 0);
+        const int block = x.x / kScaleBlock + p - (lo ? s_end[lo - 1] : 0);
+        const int tile = block / (kTile / kScaleBlock), sub = block % (kTile / kScaleBlock);
         const int src = a.block_table[(size_t)lo * a.max_pages + tile];
         const int dst = a.out_table[(size_t)lo * a.out_max_pages + tile];
         if (src < 0 || src >= a.num_pages || dst < 0 || dst >= a.out_num_pages) {
             if (tid == 0 && a.flags) atomicOr(a.flags, (int)HPC_FLAG_BAD_PAGE);
             continue;
         }
-        const int per_token = a.Hkv * (kHeadDim / 16);  // 16-code vectors
-        const int from = max(x.x - tile * kTile, 0) * per_token;
-        const int to = min(x.y - tile * kTile, kTile) * per_token;
-        const size_t in0 = (size_t)src * kTile * per_token, out0 = (size_t)dst * kTile * per_token;
-        const float *sc = a.kv_scale + (size_t)src * a.Hkv * kPageScales;
+        const int first = block * kScaleBlock;  // the block's first token
+        const int from = max(x.x - first, 0) * per_token;
+        const int to = min(x.y - first, kScaleBlock) * per_token;
+        const size_t in0 = ((size_t)src * kTile + sub * kScaleBlock) * per_token;
+        const size_t out0 = ((size_t)dst * kTile + sub * kScaleBlock) * per_token;
+        const float *sc = a.kv_scale + (size_t)src * a.Hkv * kPageScales + sub;
         const uint4 *kc = reinterpret_cast<const uint4 *>(a.k_cache) + in0;
         const uint4 *vc = reinterpret_cast<const uint4 *>(a.v_cache) + in0;
         uint4 *ko = reinterpret_cast<uint4 *>(a.k_out) + 2 * out0;
         uint4 *vo = reinterpret_cast<uint4 *>(a.v_out) + 2 * out0;
-        for (int i = from + tid; i < to; i += kRdThreads) {
-            const int token = i / per_token, h = (i - token * per_token) / (kHeadDim / 16);
-            const float *s = sc + h * kPageScales + token / kScaleBlock;
-            const uint4 kq = kc[i], vq = vc[i];
-            uint4 l, u;
-            widen16(kq, s[0], l, u);
-            ko[2 * i] = l;
-            ko[2 * i + 1] = u;
-            widen16(vq, s[kPageScales / 2], l, u);
-            vo[2 * i] = l;
-            vo[2 * i + 1] = u;
+        for (int i = from + tid; i < to; i += 2 * kRdThreads) {
+            const int j = i + kRdThreads;
+            const bool two = j < to;
+            const float *si = sc + (i / (kHeadDim / 16)) % a.Hkv * kPageScales;
+            const float *sj = sc + (j / (kHeadDim / 16)) % a.Hkv * kPageScales;
+            const uint4 k0 = kc[i], v0 = vc[i];
+            const uint4 k1 = two ? kc[j] : k0, v1 = two ? vc[j] : v0;
+            const float fk0 = si[0], fv0 = si[kPageScales / 2];
+            const float fk1 = sj[0], fv1 = sj[kPageScales / 2];
+            widen16(k0, fk0, ko + 2 * i);
+            widen16(v0, fv0, vo + 2 * i);
+            if (two) {
+                widen16(k1, fk1, ko + 2 * j);
+                widen16(v1, fv1, vo + 2 * j);
+            }
         }
     }
 }
 
+bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int sm_count() {
@@ -594,14 +615,14 @@ extern "C" hpc_status hpc_kv_read_block(const void *d_k_cache, const void *d_v_c
     if (head_dim != HPC_HEAD_DIM || B > HPC_MAX_BATCH || Hkv > (1 << 16))
         return HPC_ERR_UNSUPPORTED;
     const int64_t pages = std::min(max_pages_per_req, out_max_pages_per_req);
-    if (pages * HPC_PAGE_SIZE >= (int64_t)1 << 30 || pages * B >= (int64_t)1 << 30)
+    if (pages * HPC_PAGE_SIZE >= (int64_t)1 << 30 || pages * B >= (int64_t)1 << 28)
         return HPC_ERR_UNSUPPORTED;
     if (B == 0) return HPC_OK;
     if (!d_k_cache || !d_v_cache || !d_kv_scale || !d_block_table || !d_seqlens || !d_k_out ||
         !d_v_out || !d_out_block_table)
         return HPC_ERR_ARG;
     if (!aligned16(d_k_cache) || !aligned16(d_v_cache) || !aligned16(d_kv_scale) ||
-        !aligned16(d_k_out) || !aligned16(d_v_out))
+        !aligned32(d_k_out) || !aligned32(d_v_out))
         return HPC_ERR_ARG;
     BlockReadArgs a;
     a.k_cache = static_cast<const uint8_t *>(d_k_cache);
@@ -627,7 +648,8 @@ extern "C" hpc_status hpc_kv_read_block(const void *d_k_cache, const void *d_v_c
         return HPC_ERR_CUDA;
     const int sms = sm_count();
     if (sms < 1) return HPC_ERR_CUDA;
-    const int grid = (int)std::min<int64_t>(pages * B, (int64_t)sms * (smem > 24 * 1024 ? 2 : 8));
+    const int grid = (int)std::min<int64_t>(pages * (HPC_PAGE_SIZE / kScaleBlock) * B,
+                                            (int64_t)sms * (smem > 24 * 1024 ? 2 : 8));
     return launch_dependent(kv_read_block_kernel, grid, kRdThreads, smem,
                             static_cast<cudaStream_t>(stream), a) == cudaSuccess
                ? HPC_OK

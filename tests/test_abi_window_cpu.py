@@ -153,7 +153,7 @@ def test_read_refusals():
     assert call(D=64) == UNS and call(B=20000) == UNS
     assert call(mp=1 << 24, omp=1 << 24) == UNS
     assert call(k=None) == ARG and call(kvs=None) == ARG and call(sl=None) == ARG
-    assert call(k=FAKE + 8) == ARG and call(ko=FAKE + 8) == ARG and call(kvs=FAKE + 4) == ARG
+    assert call(k=FAKE + 8) == ARG and call(ko=FAKE + 16) == ARG and call(kvs=FAKE + 4) == ARG
 
 
 # ---------------------------------------------------------------- binding
