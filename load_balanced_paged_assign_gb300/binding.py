@@ -185,18 +185,20 @@ def kv_dtype_of(t: torch.Tensor) -> int:
     raise TypeError(f"unsupported KV cache dtype {t.dtype}")
 
 
-def _dense(fn: str, dev: int, **tensors):
-    """Raises ValueError for a tensor that the call cannot take as a plain row-major
-    array of its type on the device `dev`: {name: (tensor or None, dtype)}."""
-    for name, (t, dtype) in tensors.items():
-        if t is None:
-            continue
-        if t.dtype is not dtype:
-            raise ValueError(f"{fn}: {name} is {t.dtype}, not {dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{fn}: {name} is not contiguous")
-        if t.get_device() != dev:
-            raise ValueError(f"{fn}: {name} is on {t.device}, not on the current device")
+def _bad(fn: str, name: str, t, dtype, dev: int):
+    """ValueError saying why `t` is no dense array of `dtype` on the device `dev`."""
+    why = f"{t.dtype}, not {dtype}" if t.dtype is not dtype else \
+        "not contiguous" if not t.is_contiguous() else f"on {t.device}, not on the current device"
+    raise ValueError(f"{fn}: {name} is {why}")
+
+
+def _dense(fn: str, dev: int, names: str, dtype, *tensors):
+    """Checks that each tensor (or None) is a row-major array of `dtype` on the device
+    `dev`, as the pointers handed to the library are taken to be."""
+    for i, t in enumerate(tensors):
+        if t is not None and (t.dtype is not dtype or not t.is_contiguous() or
+                              t.get_device() != dev):
+            _bad(fn, names.split()[i], t, dtype, dev)
 
 
 def _shape(fn: str, name: str, t, want: tuple):
@@ -204,8 +206,27 @@ def _shape(fn: str, name: str, t, want: tuple):
         raise ValueError(f"{fn}: {name} is {tuple(t.shape)}, not {want}")
 
 
+_HAS_CUDA = None
+
+
 def _current_device() -> int:
-    return torch.cuda.current_device() if torch.cuda.is_available() else -1
+    """The current CUDA device, or -1 (the device number of CPU tensors) without one."""
+    global _HAS_CUDA
+    if _HAS_CUDA is None:
+        _HAS_CUDA = torch.cuda.is_available()
+    return torch.cuda.current_device() if _HAS_CUDA else -1
+
+
+def _raw_stream(dev: int, stream):
+    """The stream's handle; None: the current stream of `dev`."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else None
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _adr(t):
+    """A tensor's address as ctypes takes it (None for no tensor)."""
+    return None if t is None else t.data_ptr()
 
 
 class TaskMap:
@@ -500,23 +521,25 @@ def hpc_decode_plan_win(seqlens, Hkv, max_pages_per_req, num_ctas, min_tiles_per
                         tmap: TaskMap, *, q_len=1, window=0, sinks=0, stream=None):
     """hpc_decode_plan for queries that see the last `window` tokens and the
     first `sinks` ones (window = 0: every token)."""
-    _dense("hpc_decode_plan_win", _current_device(), seqlens=(seqlens, torch.int32))
+    dev = _current_device()
+    _dense("hpc_decode_plan_win", dev, "seqlens", torch.int32, seqlens)
     _check("hpc_decode_plan_win", lib().hpc_decode_plan_win(
-        _ptr(seqlens), int(seqlens.numel()), int(Hkv), int(max_pages_per_req), int(num_ctas),
+        _adr(seqlens), int(seqlens.numel()), int(Hkv), int(max_pages_per_req), int(num_ctas),
         int(min_tiles_per_cta), int(q_len), int(window), int(sinks), ctypes.byref(tmap.c),
-        _stream(stream)))
+        _raw_stream(dev, stream)))
 
 
 def _win_args(fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, Hq, Hkv, q_len,
               part_o, part_lse, out, unit_done):
-    """The checks of the windowed decode calls; returns the KV dtype."""
+    """The checks of the windowed decode calls; returns (KV dtype, device)."""
     block = kv_scale is not None
     kv = torch.float8_e4m3fn if block else k_cache.dtype
-    f32, i32, B = torch.float32, torch.int32, int(seqlens.numel())
-    _dense(fn, _current_device(), q=(q, kv), q_scale=(q_scale, f32), k_cache=(k_cache, kv),
-           v_cache=(v_cache, kv), kv_scale=(kv_scale, f32), block_table=(block_table, i32),
-           seqlens=(seqlens, i32), part_o=(part_o, f32), part_lse=(part_lse, f32),
-           out=(out, torch.bfloat16), unit_done=(unit_done, i32))
+    B, dev = seqlens.numel(), _current_device()
+    _dense(fn, dev, "q k_cache v_cache", kv, q, k_cache, v_cache)
+    _dense(fn, dev, "q_scale kv_scale part_o part_lse", torch.float32, q_scale, kv_scale, part_o,
+           part_lse)
+    _dense(fn, dev, "block_table seqlens unit_done", torch.int32, block_table, seqlens, unit_done)
+    _dense(fn, dev, "out", torch.bfloat16, out)
     pages, rows = int(k_cache.shape[0]), B * int(q_len) * int(Hq)
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
         _shape(fn, name, t, (pages, PAGE_SIZE, int(Hkv), HEAD_DIM))
@@ -528,7 +551,7 @@ def _win_args(fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, 
         raise ValueError(f"{fn}: q or out does not hold {B} x {q_len} x {Hq} rows")
     if q_scale is not None and q_scale.numel() != rows:
         raise ValueError(f"{fn}: q_scale does not hold {B} x {q_len} x {Hq} scales")
-    return HPC_KV_E4M3_BLOCK if block else kv_dtype_of(k_cache)
+    return HPC_KV_E4M3_BLOCK if block else kv_dtype_of(k_cache), dev
 
 
 def _split_args(fn, tmap, part_o, part_lse, unit_done, B, Hq, Hkv, q_len):
@@ -549,15 +572,15 @@ def hpc_decode_attn_win(q, q_scale, k_cache, v_cache, k_scale, v_scale, kv_scale
     block-scaled cache, else None.  out and unit_done given: combine fused in;
     both None: partials only."""
     fn, B = "hpc_decode_attn_win", int(seqlens.numel())
-    dtype = _win_args(fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, Hq, Hkv,
-                      q_len, part_o, part_lse, out, unit_done)
+    dtype, dev = _win_args(fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, Hq,
+                           Hkv, q_len, part_o, part_lse, out, unit_done)
     _split_args(fn, tmap, part_o, part_lse, unit_done, B, Hq, Hkv, q_len)
     _check(fn, lib().hpc_decode_attn_win(
-        _ptr(q), _ptr(q_scale), _ptr(k_cache), _ptr(v_cache), int(k_cache.shape[0]),
-        float(k_scale), float(v_scale), _ptr(kv_scale), dtype, _ptr(block_table),
-        int(block_table.shape[1]), _ptr(seqlens), B, int(Hq), int(Hkv), HEAD_DIM, int(q_len),
-        int(window), int(sinks), float(sm_scale), ctypes.byref(tmap.c), _ptr(part_o),
-        _ptr(part_lse), _ptr(unit_done), _ptr(out), _stream(stream)))
+        _adr(q), _adr(q_scale), _adr(k_cache), _adr(v_cache), int(k_cache.shape[0]),
+        float(k_scale), float(v_scale), _adr(kv_scale), dtype, _adr(block_table),
+        int(block_table.shape[1]), _adr(seqlens), B, int(Hq), int(Hkv), HEAD_DIM, int(q_len),
+        int(window), int(sinks), float(sm_scale), ctypes.byref(tmap.c), _adr(part_o),
+        _adr(part_lse), _adr(unit_done), _adr(out), _raw_stream(dev, stream)))
 
 
 def hpc_decode_step_win(q, q_scale, k_cache, v_cache, k_scale, v_scale, kv_scale, block_table,
@@ -567,25 +590,25 @@ def hpc_decode_step_win(q, q_scale, k_cache, v_cache, k_scale, v_scale, kv_scale
     """hpc_decode_plan_win and hpc_decode_attn_win in one call (unit_done None:
     with the separate combine kernel)."""
     fn, B = "hpc_decode_step_win", int(seqlens.numel())
-    dtype = _win_args(fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, Hq, Hkv,
-                      q_len, part_o, part_lse, out, unit_done)
+    dtype, dev = _win_args(fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, Hq,
+                           Hkv, q_len, part_o, part_lse, out, unit_done)
     _split_args(fn, tmap, part_o, part_lse, unit_done, B, Hq, Hkv, q_len)
     _check(fn, lib().hpc_decode_step_win(
-        _ptr(q), _ptr(q_scale), _ptr(k_cache), _ptr(v_cache), int(k_cache.shape[0]),
-        float(k_scale), float(v_scale), _ptr(kv_scale), dtype, _ptr(block_table),
-        int(block_table.shape[1]), _ptr(seqlens), B, int(Hq), int(Hkv), HEAD_DIM, int(q_len),
+        _adr(q), _adr(q_scale), _adr(k_cache), _adr(v_cache), int(k_cache.shape[0]),
+        float(k_scale), float(v_scale), _adr(kv_scale), dtype, _adr(block_table),
+        int(block_table.shape[1]), _adr(seqlens), B, int(Hq), int(Hkv), HEAD_DIM, int(q_len),
         int(window), int(sinks), float(sm_scale), int(num_ctas), int(min_tiles_per_cta),
-        ctypes.byref(tmap.c), _ptr(part_o), _ptr(part_lse), _ptr(unit_done), _ptr(out),
-        _stream(stream)))
+        ctypes.byref(tmap.c), _adr(part_o), _adr(part_lse), _adr(unit_done), _adr(out),
+        _raw_stream(dev, stream)))
 
 
 def hpc_prefill_attn_win(q, k_cache, v_cache, block_table, seqlens, Hq, Hkv, q_len, window, sinks,
                          sm_scale, out, flags=None, stream=None):
     """hpc_prefill_attn with a window and sinks (window = 0: plain causal)."""
     fn, B, bf16, i32 = "hpc_prefill_attn_win", int(seqlens.numel()), torch.bfloat16, torch.int32
-    _dense(fn, _current_device(), q=(q, bf16), k_cache=(k_cache, bf16), v_cache=(v_cache, bf16),
-           block_table=(block_table, i32), seqlens=(seqlens, i32), out=(out, bf16),
-           flags=(flags, i32))
+    dev = _current_device()
+    _dense(fn, dev, "q k_cache v_cache out", bf16, q, k_cache, v_cache, out)
+    _dense(fn, dev, "block_table seqlens flags", i32, block_table, seqlens, flags)
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
         _shape(fn, name, t, (int(k_cache.shape[0]), PAGE_SIZE, int(Hkv), HEAD_DIM))
     n = B * int(q_len) * int(Hq) * HEAD_DIM
@@ -594,9 +617,9 @@ def hpc_prefill_attn_win(q, k_cache, v_cache, block_table, seqlens, Hq, Hkv, q_l
     if q.numel() != n or out.numel() < n:
         raise ValueError(f"{fn}: q or out does not hold {B} x {q_len} x {Hq} rows")
     _check(fn, lib().hpc_prefill_attn_win(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), int(k_cache.shape[0]), _ptr(block_table),
-        int(block_table.shape[1]), _ptr(seqlens), B, int(Hq), int(Hkv), HEAD_DIM, int(q_len),
-        int(window), int(sinks), float(sm_scale), _ptr(out), _ptr(flags), _stream(stream)))
+        _adr(q), _adr(k_cache), _adr(v_cache), int(k_cache.shape[0]), _adr(block_table),
+        int(block_table.shape[1]), _adr(seqlens), B, int(Hq), int(Hkv), HEAD_DIM, int(q_len),
+        int(window), int(sinks), float(sm_scale), _adr(out), _adr(flags), _raw_stream(dev, stream)))
 
 
 def hpc_rope_norm_block(qkv, q_norm_w, k_norm_w, positions, token_req, Hq, Hkv, block_table,
@@ -607,12 +630,14 @@ def hpc_rope_norm_block(qkv, q_norm_w, k_norm_w, positions, token_req, Hq, Hkv, 
     kv_scale [num_pages, Hkv, 2, 4]).  q_scale_out given: E4M3 queries, else BF16."""
     fn, f32, i32, e4m3 = "hpc_rope_norm_block", torch.float32, torch.int32, torch.float8_e4m3fn
     N, pages = int(positions.numel()), int(k_cache.shape[0])
-    _dense(fn, _current_device(), q_norm_w=(q_norm_w, torch.bfloat16),
-           k_norm_w=(k_norm_w, torch.bfloat16), positions=(positions, i32),
-           token_req=(token_req, i32), block_table=(block_table, i32), k_cache=(k_cache, e4m3),
-           v_cache=(v_cache, e4m3), kv_scale=(kv_scale, f32),
-           q_out=(q_out, torch.bfloat16 if q_scale_out is None else e4m3),
-           q_scale_out=(q_scale_out, f32), flags=(flags, i32), freq=(freq, torch.float64))
+    dev = _current_device()
+    _dense(fn, dev, "q_norm_w k_norm_w", torch.bfloat16, q_norm_w, k_norm_w)
+    _dense(fn, dev, "positions token_req block_table flags", i32, positions, token_req,
+           block_table, flags)
+    _dense(fn, dev, "k_cache v_cache", e4m3, k_cache, v_cache)
+    _dense(fn, dev, "kv_scale q_scale_out", f32, kv_scale, q_scale_out)
+    _dense(fn, dev, "q_out", torch.bfloat16 if q_scale_out is None else e4m3, q_out)
+    _dense(fn, dev, "freq", torch.float64, freq)
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
         _shape(fn, name, t, (pages, PAGE_SIZE, int(Hkv), HEAD_DIM))
     _shape(fn, "kv_scale", kv_scale, (pages, int(Hkv), 2, PAGE_SIZE // SCALE_BLOCK))
@@ -635,10 +660,10 @@ def hpc_rope_norm_block(qkv, q_norm_w, k_norm_w, positions, token_req, Hq, Hkv, 
                                   1 if norm_first else 0,
                                   None if freq is None else freq.data_ptr())
     _check(fn, lib().hpc_rope_norm_block(
-        _ptr(qkv), stride, _ptr(q_norm_w), _ptr(k_norm_w), _ptr(positions), _ptr(token_req), N,
-        int(Hq), int(Hkv), HEAD_DIM, _ptr(block_table), int(block_table.shape[1]),
-        int(block_table.shape[0]), _ptr(k_cache), _ptr(v_cache), _ptr(kv_scale), pages,
-        _ptr(q_out), _ptr(q_scale_out), _ptr(flags), ctypes.byref(params), _stream(stream)))
+        _adr(qkv), stride, _adr(q_norm_w), _adr(k_norm_w), _adr(positions), _adr(token_req), N,
+        int(Hq), int(Hkv), HEAD_DIM, _adr(block_table), int(block_table.shape[1]),
+        int(block_table.shape[0]), _adr(k_cache), _adr(v_cache), _adr(kv_scale), pages,
+        _adr(q_out), _adr(q_scale_out), _adr(flags), ctypes.byref(params), _raw_stream(dev, stream)))
 
 
 def hpc_kv_read_block(k_cache, v_cache, kv_scale, block_table, starts, seqlens, Hkv, k_out, v_out,
@@ -647,10 +672,12 @@ def hpc_kv_read_block(k_cache, v_cache, kv_scale, block_table, starts, seqlens, 
     cache as BF16 into the pages out_block_table names."""
     fn, f32, i32, e4m3 = "hpc_kv_read_block", torch.float32, torch.int32, torch.float8_e4m3fn
     B, pages, out_pages = int(seqlens.numel()), int(k_cache.shape[0]), int(k_out.shape[0])
-    _dense(fn, _current_device(), k_cache=(k_cache, e4m3), v_cache=(v_cache, e4m3),
-           kv_scale=(kv_scale, f32), block_table=(block_table, i32), starts=(starts, i32),
-           seqlens=(seqlens, i32), k_out=(k_out, torch.bfloat16), v_out=(v_out, torch.bfloat16),
-           out_block_table=(out_block_table, i32), flags=(flags, i32))
+    dev = _current_device()
+    _dense(fn, dev, "k_cache v_cache", e4m3, k_cache, v_cache)
+    _dense(fn, dev, "kv_scale", f32, kv_scale)
+    _dense(fn, dev, "block_table starts seqlens out_block_table flags", i32, block_table, starts,
+           seqlens, out_block_table, flags)
+    _dense(fn, dev, "k_out v_out", torch.bfloat16, k_out, v_out)
     for name, t, n in (("k_cache", k_cache, pages), ("v_cache", v_cache, pages),
                        ("k_out", k_out, out_pages), ("v_out", v_out, out_pages)):
         _shape(fn, name, t, (n, PAGE_SIZE, int(Hkv), HEAD_DIM))
@@ -661,10 +688,10 @@ def hpc_kv_read_block(k_cache, v_cache, kv_scale, block_table, starts, seqlens, 
     if starts is not None and starts.numel() != B:
         raise ValueError(f"{fn}: starts has not {B} entries")
     _check(fn, lib().hpc_kv_read_block(
-        _ptr(k_cache), _ptr(v_cache), _ptr(kv_scale), pages, _ptr(block_table),
-        int(block_table.shape[1]), _ptr(starts), _ptr(seqlens), B, int(Hkv), HEAD_DIM,
-        _ptr(k_out), _ptr(v_out), out_pages, _ptr(out_block_table),
-        int(out_block_table.shape[1]), _ptr(flags), _stream(stream)))
+        _adr(k_cache), _adr(v_cache), _adr(kv_scale), pages, _adr(block_table),
+        int(block_table.shape[1]), _adr(starts), _adr(seqlens), B, int(Hkv), HEAD_DIM,
+        _adr(k_out), _adr(v_out), out_pages, _adr(out_block_table),
+        int(out_block_table.shape[1]), _adr(flags), _raw_stream(dev, stream)))
 
 
 class Workspace:
