@@ -648,8 +648,9 @@ hpc_status hpc_decode_plan_win(const int32_t *d_seqlens, int32_t B, int32_t Hkv,
  *               aligned, for HPC_KV_E4M3_BLOCK; NULL for the others.  Scores
  *               then use q_scale * the block's K scale, values its V scale,
  *               and k_scale and v_scale are ignored.  The scales of blocks
- *               that hold a visible token are finite and not negative; the
- *               others may be anything.
+ *               that hold a visible token are finite, V's not negative and at
+ *               most 2^100 (one below 2^-100 counts as zero); the others may
+ *               be anything.
  * Other arguments as in those calls.
  */
 hpc_status hpc_decode_attn_win(const void *d_q, const float *d_q_scale, const void *d_k_cache,

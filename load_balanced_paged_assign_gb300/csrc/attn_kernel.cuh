@@ -55,10 +55,14 @@
 //    for 16 tokens of K, one of V) as one 32-byte bulk copy beside its tiles.
 //    A consumer warp's 16 tokens are exactly one block, so K's scale is one
 //    more factor of its score scale.  V's scale v_s enters the weights in the
-//    log2 domain: beside the softmax's running maximum m of the scores x, M is
-//    the running maximum of x + log2 v_s, the f16 weights are 2^(x + log2 v_s
-//    - M) <= 1 whatever the scales' range, and O (in units of 2^M) is brought
-//    to the units of 2^m once, when the state is handed over.
+//    reference: with x a score, m is the running maximum of x + log2 v_s, p =
+//    2^(x - m) goes into the softmax's sum (fp32: its range holds any scales
+//    from 2^-100 to 2^100) and w = p v_s, which is <= 1 whatever the scales,
+//    is the f16 weight of V's codes.  A v_s below 2^-100 counts as zero.
+//  * both forms move the reference m only when a score exceeds it by more than
+//    8 (log2 units), which one vote per tile finds out; weights stay <= 2^8
+//    (f16 holds 2^15), the same softmax follows, and the common tile does
+//    without the maximum's shuffles and the rescaling factors.
 //  * the kernel is launched as a programmatic dependent of the assign kernel:
 //    it sets up its barriers, prefetches the block table into L2, derives its
 //    first descriptor from the sequence lengths and starts streaming while
@@ -97,6 +101,8 @@ constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr unsigned kFullMask = 0xffffffffu;
+constexpr float kLazyLog2 = 8.f;           // windowed / block-scaled: how far a score may pass m
+constexpr float kMinVScale = 7.888609052210118e-31f;  // 2^-100
 constexpr int kStateRegs = 36;  // per lane and row block: 32 accumulators, m0, m1, l0, l1
 constexpr int kMaxLast = 16;    // split units whose merge this CTA owes, held at once
 constexpr int kStageStride = kHeadDim + 4;  // floats per head row of the combiner's staging
@@ -952,14 +958,13 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
     // (rows) 8 nb + 2 t4 + c, c = 0, 1 of every block.
     float o[NB][8][4];
     float m[NB][2], l[NB][2], sc[NB][2];
-    float mw[NB][2];  // BLK: running maximum of score + log2 of the V scale (O's reference)
     int lim[NB][2];  // tokens visible to the lane's rows: t < lim (causal for q_len > 1)
     uint32_t qf[NB][8][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            m[nb][c] = mw[nb][c] = kNegInf;
+            m[nb][c] = kNegInf;
             l[nb][c] = sc[nb][c] = 0.f;
             lim[nb][c] = 0;
         }
@@ -1005,7 +1010,7 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
                         sc[nb][c] = p.score_scale * info[stage].qscale[rho];
                         // query token i = rho / G sees tokens below L - q_len + 1 + i
                         lim[nb][c] = rho < p.R ? L - p.q_len + 1 + rho / p.G : L;
-                        m[nb][c] = mw[nb][c] = kNegInf;
+                        m[nb][c] = kNegInf;
                         l[nb][c] = 0.f;
                     }
 #pragma unroll
@@ -1027,12 +1032,15 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
                                   (tok0 < L && (!WIN || tok0 + 15 >= lo0 || tok0 < p.sinks));
             if (slot < ntiles && any_live) {
                 const uint32_t sK = sK0 + stage * Tr::kStageKV, sV = sV0 + stage * Tr::kStageKV;
-                float kf = 1.f, lv = 0.f;  // BLK: the block's K scale, log2 of its V scale
+                // BLK: the block's K scale, its V scale and log2 of it
+                float kf = 1.f, vf = 1.f, lv = 0.f;
                 if (BLK) {
                     const float *bs = reinterpret_cast<const float *>(
                         smem + Tr::kOffScale + stage * Tr::kScaleBytes + slot * kPageScales * 4);
                     kf = bs[sub];
-                    lv = lg2(bs[kPageScales / 2 + sub]);
+                    vf = bs[kPageScales / 2 + sub];
+                    lv = lg2(fmaxf(vf, kMinVScale));
+                    vf = vf < kMinVScale ? 0.f : vf;
                 }
 
                 // ---- S^T = K . Q^T for this warp's 16 tokens x 8 NB rows
@@ -1119,46 +1127,47 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
                     mx[nb][0] = fmaxf(x[nb][0], x[nb][2]);
                     mx[nb][1] = fmaxf(x[nb][1], x[nb][3]);
                 }
+                constexpr bool kLazy = WIN || BLK;
+                bool move = true;  // the reference may have to move
+                if (kLazy) {
+                    bool over = false;
 #pragma unroll
-                for (int o_ = 4; o_ <= 16; o_ <<= 1)
+                    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) {
-                        mx[nb][0] = fmaxf(mx[nb][0], __shfl_xor_sync(kFullMask, mx[nb][0], o_));
-                        mx[nb][1] = fmaxf(mx[nb][1], __shfl_xor_sync(kFullMask, mx[nb][1], o_));
-                    }
+                        for (int c = 0; c < 2; ++c) over |= mx[nb][c] > m[nb][c] + (kLazyLog2 - lv);
+                    move = __any_sync(kFullMask, over);
+                }
+                if (move) {
+#pragma unroll
+                    for (int o_ = 4; o_ <= 16; o_ <<= 1)
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) {
+                            mx[nb][0] = fmaxf(mx[nb][0], __shfl_xor_sync(kFullMask, mx[nb][0], o_));
+                            mx[nb][1] = fmaxf(mx[nb][1], __shfl_xor_sync(kFullMask, mx[nb][1], o_));
+                        }
+                }
                 float al[NB][2];
                 bool rescale = false;
                 uint32_t b0[NB], b1[NB];
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
-                    float ms[2], wf[2];
+                    float ms[2];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const float mn = fmaxf(m[nb][c], mx[nb][c]);
+                        const float mn = !kLazy || move ? fmaxf(m[nb][c], mx[nb][c] + lv) : m[nb][c];
                         ms[c] = mn == kNegInf ? 0.f : mn;
-                        al[nb][c] = ex2(m[nb][c] - ms[c]);
+                        al[nb][c] = !kLazy || move ? ex2(m[nb][c] - ms[c]) : 1.f;
                         m[nb][c] = mn;
-                        if (BLK) {
-                            // l keeps the reference m; O moves to M, and p to the
-                            // weight p 2^(log2 v_s + m - M) <= 1 (the exponent is
-                            // capped so that p = 0 stays 0 for any scales)
-                            l[nb][c] *= al[nb][c];
-                            const float wn = fmaxf(mw[nb][c], mx[nb][c] + lv);
-                            const float wr = wn == kNegInf ? 0.f : wn;
-                            al[nb][c] = ex2(mw[nb][c] - wr);
-                            wf[c] = wn == kNegInf ? 0.f : ex2(fminf(lv + ms[c] - wr, 126.f));
-                            mw[nb][c] = wn;
-                        }
                         rescale |= al[nb][c] != 1.f;
                     }
                     const float p0 = ex2(x[nb][0] - ms[0]), p1 = ex2(x[nb][1] - ms[1]);
                     const float p2 = ex2(x[nb][2] - ms[0]), p3 = ex2(x[nb][3] - ms[1]);
                     uint32_t pk01, pk23;
                     if (BLK) {
-                        pk01 = pack_f16x2(p0 * wf[0], p1 * wf[1]);
-                        pk23 = pack_f16x2(p2 * wf[0], p3 * wf[1]);
-                        l[nb][0] += p0 + p2;
-                        l[nb][1] += p1 + p3;
+                        pk01 = pack_f16x2(p0 * vf, p1 * vf);
+                        pk23 = pack_f16x2(p2 * vf, p3 * vf);
+                        l[nb][0] = l[nb][0] * al[nb][0] + (p0 + p2);
+                        l[nb][1] = l[nb][1] * al[nb][1] + (p1 + p3);
                     } else if (FP8) {
                         pk01 = pack_f16x2(p0, p1);
                         pk23 = pack_f16x2(p2, p3);
@@ -1175,7 +1184,7 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
                     b0[nb] = movmatrix_trans(pk01);
                     b1[nb] = movmatrix_trans(pk23);
                 }
-                if (__any_sync(kFullMask, rescale)) {  // rescale only on a new max
+                if (kLazy ? move : __any_sync(kFullMask, rescale)) {  // rescale only on a new max
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -1222,12 +1231,21 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
             const int k = handed % Tr::kSlots;
             if (!warp_wait(&slot_empty[k], ((handed / Tr::kSlots) & 1u) ^ 1u, abort))
                 return false;
-            if (BLK && (flags & kLast)) {  // O from units of 2^M to units of 2^m, l's
+            if (BLK && (flags & kLast)) {
+                // the references of two warps may lie as far apart as their V
+                // scales, their log-sum-exps only as far as their scores: hand
+                // over the normalised O with the latter (l 1, in one lane of
+                // the eight that share a row)
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const float f = mw[nb][c] == kNegInf ? 0.f : ex2(mw[nb][c] - m[nb][c]);
+                        float z = l[nb][c];
+#pragma unroll
+                        for (int o_ = 4; o_ <= 16; o_ <<= 1) z += __shfl_xor_sync(kFullMask, z, o_);
+                        const float f = z > 0.f ? __fdividef(1.f, z) : 0.f;
+                        m[nb][c] = z > 0.f ? m[nb][c] + lg2(z) : kNegInf;
+                        l[nb][c] = z > 0.f && g == 0 ? 1.f : 0.f;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             o[nb][j][c] *= f;
