@@ -954,6 +954,10 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
     const int tok_k = 16 * sub + (lane & 7) + (mi & 1) * 8;  // K: matrices 1, 3 = rows 8..15
     const int tok_v = 16 * sub + (lane & 7) + (mi >> 1) * 8;  // V^T: matrices 2, 3 = toks 8..15
 
+    constexpr bool kLazy = WIN || BLK;  // see the head of the file
+    // m of a row that has seen no token (finite where d = score - m is formed
+    // before it is looked at: any score then passes it)
+    constexpr float kNoScore = kLazy ? -3e38f : kNegInf;
     // Row block nb holds query rows 8 nb .. 8 nb + 7; this lane owns columns
     // (rows) 8 nb + 2 t4 + c, c = 0, 1 of every block.
     float o[NB][8][4];
@@ -964,7 +968,7 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            m[nb][c] = kNegInf;
+            m[nb][c] = kNoScore;
             l[nb][c] = sc[nb][c] = 0.f;
             lim[nb][c] = 0;
         }
@@ -1010,7 +1014,7 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
                         sc[nb][c] = p.score_scale * info[stage].qscale[rho];
                         // query token i = rho / G sees tokens below L - q_len + 1 + i
                         lim[nb][c] = rho < p.R ? L - p.q_len + 1 + rho / p.G : L;
-                        m[nb][c] = kNegInf;
+                        m[nb][c] = kNoScore;
                         l[nb][c] = 0.f;
                     }
 #pragma unroll
@@ -1028,6 +1032,10 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
             auto live = [&](int t) { return t < L && (!WIN || t >= lo0 || t < p.sinks); };
             // a slice without a live token changes nothing (and its block may
             // hold anything, its scales among it)
+            // every row sees the whole slice (the last query's window begins last,
+            // the first query's ends first): no masks
+            const bool full = kLazy && tok0 + 15 < L - p.q_len + 1 &&
+                              (tok0 + p.window >= L || tok0 + 15 < p.sinks);
             const bool any_live = !(WIN || BLK) ||
                                   (tok0 < L && (!WIN || tok0 + 15 >= lo0 || tok0 < p.sinks));
             if (slot < ntiles && any_live) {
@@ -1095,7 +1103,13 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
                     for (int q = 0; q < 4; ++q) {
                         const int tok = 16 * sub + 2 * t4 + (q & 1) + (q >> 1) * 8;
                         Rv[q] = lds128(sV + tok * 128 + ((g ^ (tok & 7)) << 4));
-                        if (!live(tile * kTile + tok)) Rv[q] = make_uint4(0u, 0u, 0u, 0u);
+                        if (!kLazy && tile * kTile + tok >= L) Rv[q] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    if (kLazy && !full) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (!live(tok0 + 2 * t4 + (q & 1) + (q >> 1) * 8))
+                                Rv[q] = make_uint4(0u, 0u, 0u, 0u);
                     }
                     const uint32_t wA[4] = {Rv[0].x, Rv[0].y, Rv[0].z, Rv[0].w};
                     const uint32_t wB[4] = {Rv[1].x, Rv[1].y, Rv[1].z, Rv[1].w};
@@ -1112,32 +1126,104 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
                 // limit is masked for that row
                 // (WIN: or before its window, unless it is a sink)
                 const int ta = tok0 + g, tb_ = tok0 + g + 8;
-                auto sees = [&](int t, int limit) {
-                    return t < limit && (!WIN || t + p.window >= limit || t < p.sinks);
-                };
-                float x[NB][4], mx[NB][2];
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    const float s0 = BLK ? sc[nb][0] * kf : sc[nb][0];
-                    const float s1 = BLK ? sc[nb][1] * kf : sc[nb][1];
-                    x[nb][0] = sees(ta, lim[nb][0]) ? s4[nb][0] * s0 : kNegInf;
-                    x[nb][1] = sees(ta, lim[nb][1]) ? s4[nb][1] * s1 : kNegInf;
-                    x[nb][2] = sees(tb_, lim[nb][0]) ? s4[nb][2] * s0 : kNegInf;
-                    x[nb][3] = sees(tb_, lim[nb][1]) ? s4[nb][3] * s1 : kNegInf;
-                    mx[nb][0] = fmaxf(x[nb][0], x[nb][2]);
-                    mx[nb][1] = fmaxf(x[nb][1], x[nb][3]);
-                }
-                constexpr bool kLazy = WIN || BLK;
-                bool move = true;  // the reference may have to move
-                if (kLazy) {
-                    bool over = false;
+                uint32_t b0[NB], b1[NB];
+                if constexpr (kLazy) {
+                    // d = score - m, -inf where the row does not see the token
+                    float d[NB][4], top = kNegInf;
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) over |= mx[nb][c] > m[nb][c] + (kLazyLog2 - lv);
-                    move = __any_sync(kFullMask, over);
-                }
-                if (move) {
+                        for (int e = 0; e < 4; ++e)
+                            d[nb][e] = fmaf(s4[nb][e], sc[nb][e & 1] * kf, -m[nb][e & 1]);
+                    if (!full) {
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int t = e < 2 ? ta : tb_, limit = lim[nb][e & 1];
+                                if (!(t < limit && (t + p.window >= limit || t < p.sinks)))
+                                    d[nb][e] = kNegInf;
+                            }
+                    }
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+                        top = fmaxf(fmaxf(top, fmaxf(d[nb][0], d[nb][1])),
+                                    fmaxf(d[nb][2], d[nb][3]));
+                    if (__any_sync(kFullMask, top > kLazyLog2 - lv)) {
+                        float mx[NB][2];
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)  // back to the scores
+                                if (d[nb][e] != kNegInf) d[nb][e] = s4[nb][e] * (sc[nb][e & 1] * kf);
+                            mx[nb][0] = fmaxf(d[nb][0], d[nb][2]);
+                            mx[nb][1] = fmaxf(d[nb][1], d[nb][3]);
+                        }
+#pragma unroll
+                        for (int o_ = 4; o_ <= 16; o_ <<= 1)
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb) {
+                                mx[nb][0] = fmaxf(mx[nb][0], __shfl_xor_sync(kFullMask, mx[nb][0], o_));
+                                mx[nb][1] = fmaxf(mx[nb][1], __shfl_xor_sync(kFullMask, mx[nb][1], o_));
+                            }
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const float mn = fmaxf(m[nb][c], mx[nb][c] + lv);
+                                const float al = ex2(m[nb][c] - mn);
+                                m[nb][c] = mn;
+                                l[nb][c] *= al;
+                                d[nb][c] -= mn;
+                                d[nb][c + 2] -= mn;
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    o[nb][j][c] *= al;
+                                    o[nb][j][c + 2] *= al;
+                                }
+                            }
+                    }
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        float w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[e] = ex2(d[nb][e]);
+                        if (BLK) {
+                            l[nb][0] += w[0] + w[2];
+                            l[nb][1] += w[1] + w[3];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) w[e] *= vf;
+                        }
+                        uint32_t pk01, pk23;
+                        if (FP8) {
+                            pk01 = pack_f16x2(w[0], w[1]);
+                            pk23 = pack_f16x2(w[2], w[3]);
+                            if (!BLK) {
+                                const float2 r01 = f16x2_to_f32x2(pk01), r23 = f16x2_to_f32x2(pk23);
+                                l[nb][0] += r01.x + r23.x;
+                                l[nb][1] += r01.y + r23.y;
+                            }
+                        } else {
+                            pk01 = pack_bf16x2(w[0], w[1]);
+                            pk23 = pack_bf16x2(w[2], w[3]);
+                            l[nb][0] += bf16lo_to_f32(pk01) + bf16lo_to_f32(pk23);
+                            l[nb][1] += bf16hi_to_f32(pk01) + bf16hi_to_f32(pk23);
+                        }
+                        // P^T fragments (k = token, n = row): transpose the 8x8 halves
+                        b0[nb] = movmatrix_trans(pk01);
+                        b1[nb] = movmatrix_trans(pk23);
+                    }
+                } else {
+                    float x[NB][4], mx[NB][2];
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        x[nb][0] = ta < lim[nb][0] ? s4[nb][0] * sc[nb][0] : kNegInf;
+                        x[nb][1] = ta < lim[nb][1] ? s4[nb][1] * sc[nb][1] : kNegInf;
+                        x[nb][2] = tb_ < lim[nb][0] ? s4[nb][2] * sc[nb][0] : kNegInf;
+                        x[nb][3] = tb_ < lim[nb][1] ? s4[nb][3] * sc[nb][1] : kNegInf;
+                        mx[nb][0] = fmaxf(x[nb][0], x[nb][2]);
+                        mx[nb][1] = fmaxf(x[nb][1], x[nb][3]);
+                    }
 #pragma unroll
                     for (int o_ = 4; o_ <= 16; o_ <<= 1)
 #pragma unroll
@@ -1145,55 +1231,49 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
                             mx[nb][0] = fmaxf(mx[nb][0], __shfl_xor_sync(kFullMask, mx[nb][0], o_));
                             mx[nb][1] = fmaxf(mx[nb][1], __shfl_xor_sync(kFullMask, mx[nb][1], o_));
                         }
-                }
-                float al[NB][2];
-                bool rescale = false;
-                uint32_t b0[NB], b1[NB];
+                    float al[NB][2];
+                    bool rescale = false;
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    float ms[2];
+                    for (int nb = 0; nb < NB; ++nb) {
+                        float ms[2];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const float mn = !kLazy || move ? fmaxf(m[nb][c], mx[nb][c] + lv) : m[nb][c];
-                        ms[c] = mn == kNegInf ? 0.f : mn;
-                        al[nb][c] = !kLazy || move ? ex2(m[nb][c] - ms[c]) : 1.f;
-                        m[nb][c] = mn;
-                        rescale |= al[nb][c] != 1.f;
-                    }
-                    const float p0 = ex2(x[nb][0] - ms[0]), p1 = ex2(x[nb][1] - ms[1]);
-                    const float p2 = ex2(x[nb][2] - ms[0]), p3 = ex2(x[nb][3] - ms[1]);
-                    uint32_t pk01, pk23;
-                    if (BLK) {
-                        pk01 = pack_f16x2(p0 * vf, p1 * vf);
-                        pk23 = pack_f16x2(p2 * vf, p3 * vf);
-                        l[nb][0] = l[nb][0] * al[nb][0] + (p0 + p2);
-                        l[nb][1] = l[nb][1] * al[nb][1] + (p1 + p3);
-                    } else if (FP8) {
-                        pk01 = pack_f16x2(p0, p1);
-                        pk23 = pack_f16x2(p2, p3);
-                        const float2 r01 = f16x2_to_f32x2(pk01), r23 = f16x2_to_f32x2(pk23);
-                        l[nb][0] = l[nb][0] * al[nb][0] + r01.x + r23.x;
-                        l[nb][1] = l[nb][1] * al[nb][1] + r01.y + r23.y;
-                    } else {
-                        pk01 = pack_bf16x2(p0, p1);
-                        pk23 = pack_bf16x2(p2, p3);
-                        l[nb][0] = l[nb][0] * al[nb][0] + bf16lo_to_f32(pk01) + bf16lo_to_f32(pk23);
-                        l[nb][1] = l[nb][1] * al[nb][1] + bf16hi_to_f32(pk01) + bf16hi_to_f32(pk23);
-                    }
-                    // P^T fragments (k = token, n = row): transpose the 8x8 halves
-                    b0[nb] = movmatrix_trans(pk01);
-                    b1[nb] = movmatrix_trans(pk23);
-                }
-                if (kLazy ? move : __any_sync(kFullMask, rescale)) {  // rescale only on a new max
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            o[nb][j][0] *= al[nb][0];
-                            o[nb][j][1] *= al[nb][1];
-                            o[nb][j][2] *= al[nb][0];
-                            o[nb][j][3] *= al[nb][1];
+                        for (int c = 0; c < 2; ++c) {
+                            const float mn = fmaxf(m[nb][c], mx[nb][c]);
+                            ms[c] = mn == kNegInf ? 0.f : mn;
+                            al[nb][c] = ex2(m[nb][c] - ms[c]);
+                            m[nb][c] = mn;
+                            rescale |= al[nb][c] != 1.f;
                         }
+                        const float p0 = ex2(x[nb][0] - ms[0]), p1 = ex2(x[nb][1] - ms[1]);
+                        const float p2 = ex2(x[nb][2] - ms[0]), p3 = ex2(x[nb][3] - ms[1]);
+                        uint32_t pk01, pk23;
+                        if (FP8) {
+                            pk01 = pack_f16x2(p0, p1);
+                            pk23 = pack_f16x2(p2, p3);
+                            const float2 r01 = f16x2_to_f32x2(pk01), r23 = f16x2_to_f32x2(pk23);
+                            l[nb][0] = l[nb][0] * al[nb][0] + r01.x + r23.x;
+                            l[nb][1] = l[nb][1] * al[nb][1] + r01.y + r23.y;
+                        } else {
+                            pk01 = pack_bf16x2(p0, p1);
+                            pk23 = pack_bf16x2(p2, p3);
+                            l[nb][0] = l[nb][0] * al[nb][0] + bf16lo_to_f32(pk01) + bf16lo_to_f32(pk23);
+                            l[nb][1] = l[nb][1] * al[nb][1] + bf16hi_to_f32(pk01) + bf16hi_to_f32(pk23);
+                        }
+                        // P^T fragments (k = token, n = row): transpose the 8x8 halves
+                        b0[nb] = movmatrix_trans(pk01);
+                        b1[nb] = movmatrix_trans(pk23);
+                    }
+                    if (__any_sync(kFullMask, rescale)) {  // rescale only on a new max
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                o[nb][j][0] *= al[nb][0];
+                                o[nb][j][1] *= al[nb][1];
+                                o[nb][j][2] *= al[nb][0];
+                                o[nb][j][3] *= al[nb][1];
+                            }
+                    }
                 }
 
                 // ---- O^T += V^T . P^T (one V fragment feeds every row block)
@@ -1205,10 +1285,11 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
                             mma_f16_16816(o[nb][j], va[j][0], va[j][1], va[j][2], va[j][3], b0[nb], b1[nb]);
                 } else {
                     const int tv = tok0 + 2 * t4;  // tokens of a0/a1 halves; +8 for a2/a3
-                    const uint32_t mk01 =
-                        (live(tv) ? 0x0000ffffu : 0u) | (live(tv + 1) ? 0xffff0000u : 0u);
-                    const uint32_t mk23 =
-                        (live(tv + 8) ? 0x0000ffffu : 0u) | (live(tv + 9) ? 0xffff0000u : 0u);
+                    uint32_t mk01 = 0xffffffffu, mk23 = 0xffffffffu;
+                    if (!kLazy || !full) {
+                        mk01 = (live(tv) ? 0x0000ffffu : 0u) | (live(tv + 1) ? 0xffff0000u : 0u);
+                        mk23 = (live(tv + 8) ? 0x0000ffffu : 0u) | (live(tv + 9) ? 0xffff0000u : 0u);
+                    }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const int chunk = (2 * j + (mi & 1)) & 7;
