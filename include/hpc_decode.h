@@ -103,8 +103,8 @@ typedef enum { HPC_KV_BF16 = 0, HPC_KV_FP8_E4M3 = 1, HPC_KV_E4M3_BLOCK = 2 } hpc
  * cap_desc, cap_bins and cap_units give the sizes of desc (entries of four
  * int32), bin_ptr and chunk_count / chunk_off, and are set by the caller.
  * B, Hkv, num_ctas (the number of bins), persistent (0 for a static map, odd
- * for a load-balanced one; a windowed plan keeps a tag of its window above
- * bit 0), min_tiles and max_pages (the planner's arguments) are written by
+ * for a load-balanced one; hpc_decode_plan_win keeps a tag of its window and
+ * whether descriptors are head pairs above bit 0), min_tiles and max_pages (the planner's arguments) are written by
  * the planners (the
  * host-side struct is updated) and read by hpc_decode_attn /
  * hpc_decode_combine, which check B and Hkv against their own arguments.
@@ -630,15 +630,23 @@ hpc_status hpc_prefill_attn(const void *d_q, const void *d_k_cache, const void *
  * hpc_decode_plan for a window: the tiles of a request are its sink tiles
  * and those from its first query's window on, numbered through (descriptor
  * tile t is the request's tile t below ceil(sinks / 64), else t plus the
- * tiles left out).  q_len, window and sinks have to be those of the attention
- * calls that use the map: they are checked against it (HPC_ERR_ARG), and the
- * calls without a window refuse a windowed map.  window = 0 is
- * hpc_decode_plan.  Other arguments as there; 1 <= q_len <= 16.
+ * tiles left out).  kv_dtype, q_len, window and sinks have to be those of the
+ * attention calls that use the map: they are checked against it
+ * (HPC_ERR_ARG), and the calls without a window refuse a windowed map.
+ * Where an 8-bit cache with an even number of KV heads is read with block
+ * scales or a window, a descriptor is a pair of heads: its kv_head h stands
+ * for KV heads 2h and 2h + 1, the units are pairs, and its partials are the
+ * rows of both (2 q_len G, query token by query token), for which cap_desc >=
+ * hpc_decode_desc_capacity(B, Hkv, 2 * num_ctas) is needed (that always
+ * suffices), with part_o and part_lse sized by cap_desc as ever.  In the
+ * other cases window = 0 is hpc_decode_plan.  Other arguments as there;
+ * 1 <= q_len <= 16.
  */
 hpc_status hpc_decode_plan_win(const int32_t *d_seqlens, int32_t B, int32_t Hkv,
                                int32_t max_pages_per_req, int32_t num_ctas,
-                               int32_t min_tiles_per_cta, int32_t q_len, int32_t window,
-                               int32_t sinks, hpc_task_map *map, hpc_stream_t stream);
+                               int32_t min_tiles_per_cta, hpc_kv_dtype kv_dtype, int32_t q_len,
+                               int32_t window, int32_t sinks, hpc_task_map *map,
+                               hpc_stream_t stream);
 
 /*
  * hpc_decode_attn_combine_mq (d_unit_done and d_out given) or

@@ -132,8 +132,8 @@ def lib():
         "hpc_rope_norm": (ctypes.c_int, [vp, i64, vp, vp, vp, vp, i32, i32, i32, i32, vp, i32,
                                          i32, vp, vp, i32, ctypes.c_int, f32, f32, vp, vp, vp,
                                          ctypes.POINTER(hpc_rope_norm_params), vp]),
-        "hpc_decode_plan_win": (ctypes.c_int, [vp, i32, i32, i32, i32, i32, i32, i32, i32, tm,
-                                               vp]),
+        "hpc_decode_plan_win": (ctypes.c_int, [vp, i32, i32, i32, i32, i32, ctypes.c_int, i32,
+                                               i32, i32, tm, vp]),
         "hpc_decode_attn_win": (ctypes.c_int, [vp, vp, vp, vp, i32, f32, f32, vp, ctypes.c_int,
                                                vp, i32, vp, i32, i32, i32, i32, i32, i32, i32,
                                                f32, tm, vp, vp, vp, vp, vp]),
@@ -518,14 +518,16 @@ def hpc_rope_norm(qkv, q_norm_w, k_norm_w, positions, token_req, Hq, Hkv, block_
 
 
 def hpc_decode_plan_win(seqlens, Hkv, max_pages_per_req, num_ctas, min_tiles_per_cta,
-                        tmap: TaskMap, *, q_len=1, window=0, sinks=0, stream=None):
+                        tmap: TaskMap, *, kv_dtype=HPC_KV_BF16, q_len=1, window=0, sinks=0,
+                        stream=None):
     """hpc_decode_plan for queries that see the last `window` tokens and the
-    first `sinks` ones (window = 0: every token)."""
+    first `sinks` ones (window = 0: every token) of a kv_dtype cache."""
     dev = _current_device()
     _dense("hpc_decode_plan_win", dev, "seqlens", torch.int32, seqlens)
     _check("hpc_decode_plan_win", lib().hpc_decode_plan_win(
         _adr(seqlens), int(seqlens.numel()), int(Hkv), int(max_pages_per_req), int(num_ctas),
-        int(min_tiles_per_cta), int(q_len), int(window), int(sinks), ctypes.byref(tmap.c),
+        int(min_tiles_per_cta), int(kv_dtype), int(q_len), int(window), int(sinks),
+        ctypes.byref(tmap.c),
         _raw_stream(dev, stream)))
 
 
@@ -705,7 +707,10 @@ class Workspace:
         else:
             if num_ctas <= 0:
                 num_ctas = hpc_decode_num_ctas(dev.index or 0, kv_dtype)
-            self.tmap = TaskMap.dynamic(B, Hkv, num_ctas, dev)
+            # descriptors of head pairs (8-bit caches, the _win calls) need more room
+            pairs = 2 if kv_dtype != HPC_KV_BF16 else 1
+            cap = hpc_decode_desc_capacity(B, Hkv, pairs * num_ctas)
+            self.tmap = TaskMap(B, Hkv, cap, num_ctas + 1, dev)
         self.num_ctas, self.num_splits = num_ctas, num_splits
         rows = q_len * (Hq // Hkv)  # query rows of one KV head in a descriptor
         cap = max(self.tmap.cap_desc, 1)

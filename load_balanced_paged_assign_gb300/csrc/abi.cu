@@ -104,9 +104,29 @@ hpc_status make_cache_map(CUtensorMap *m, const void *base, int32_t num_pages, i
     return r == CUDA_SUCCESS ? HPC_OK : HPC_ERR_CUDA;
 }
 
-// Kernel variants: {BF16, FP8, windowed BF16, windowed FP8, block-scaled E4M3}
-// x row blocks.
-constexpr int kAttnVariants = 10;
+// Tensor map over one 8-bit cache for the kernels that take `heads`
+// neighbouring heads at once: rank 4 {128 dims, 64 tokens, Hkv, pages}, box
+// {128, 64, heads, 1}: each head's 64 rows of 128 B follow one another.
+hpc_status make_heads_map(CUtensorMap *m, const void *base, int32_t num_pages, int32_t Hkv,
+                          int heads) {
+    auto encode = encoder();
+    if (!encode) return HPC_ERR_CUDA;
+    std::memset(m, 0, sizeof(*m));
+    const cuuint64_t row = (cuuint64_t)Hkv * HPC_HEAD_DIM;  // bytes per token
+    cuuint64_t dims[4] = {HPC_HEAD_DIM, HPC_PAGE_SIZE, (cuuint64_t)Hkv, (cuuint64_t)num_pages};
+    cuuint64_t strides[3] = {row, HPC_HEAD_DIM, row * HPC_PAGE_SIZE};
+    cuuint32_t box[4] = {HPC_HEAD_DIM, HPC_PAGE_SIZE, (cuuint32_t)heads, 1};
+    cuuint32_t elem_strides[4] = {1, 1, 1, 1};
+    const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims,
+                              strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? HPC_OK : HPC_ERR_CUDA;
+}
+
+// Kernel variants: {BF16, FP8, windowed BF16} x row blocks, and {windowed FP8,
+// block-scaled E4M3} x KV heads per descriptor x row blocks.
+constexpr int kAttnVariants = 14;
 
 // Resident CTAs of the attention kernel per device and variant (cached).
 std::atomic<int> g_capacity[kMaxDevices][kAttnVariants];
@@ -129,20 +149,23 @@ int resident_ctas(const AttnConfig &cfg, int which) {
 }
 
 // Kernel variant: KV dtype, windowed or not, row blocks (nb = 1: up to 8
-// query rows per KV head, 2: up to 16).  A block-scaled cache has one form:
-// without a window it runs the windowed one with a window that hides nothing.
-int variant_of(hpc_kv_dtype dt, int nb, bool win = false) {
-    const int kind = dt == HPC_KV_E4M3_BLOCK ? 4 : (dt == HPC_KV_FP8_E4M3 ? 1 : 0) + (win ? 2 : 0);
-    return 2 * kind + (nb - 1);
+// query rows per KV head, 2: up to 16) and KV heads per descriptor.  A
+// block-scaled cache has one form: without a window it runs the windowed one
+// with a window that hides nothing.
+int variant_of(hpc_kv_dtype dt, int nb, bool win = false, int heads = 1) {
+    if (dt == HPC_KV_E4M3_BLOCK) return 10 + 2 * (heads - 1) + (nb - 1);
+    if (dt == HPC_KV_FP8_E4M3 && win) return 6 + 2 * (heads - 1) + (nb - 1);
+    return 2 * ((dt == HPC_KV_FP8_E4M3 ? 1 : 0) + (win ? 2 : 0)) + (nb - 1);
 }
 
-const AttnConfig &config_for(hpc_kv_dtype dt, int nb = 1, bool win = false) {
+const AttnConfig &config_for(hpc_kv_dtype dt, int nb = 1, bool win = false, int heads = 1) {
     static const AttnConfig cfg[kAttnVariants] = {
-        attn_config_bf16(1),     attn_config_bf16(2),     attn_config_fp8(1),
-        attn_config_fp8(2),      attn_config_win_bf16(1), attn_config_win_bf16(2),
-        attn_config_win_fp8(1),  attn_config_win_fp8(2),  attn_config_block(1),
-        attn_config_block(2)};
-    return cfg[variant_of(dt, nb, win)];
+        attn_config_bf16(1),       attn_config_bf16(2),       attn_config_fp8(1),
+        attn_config_fp8(2),        attn_config_win_bf16(1),   attn_config_win_bf16(2),
+        attn_config_win_fp8(1, 1), attn_config_win_fp8(2, 1), attn_config_win_fp8(1, 2),
+        attn_config_win_fp8(2, 2), attn_config_block(1, 1),   attn_config_block(2, 1),
+        attn_config_block(1, 2),   attn_config_block(2, 2)};
+    return cfg[variant_of(dt, nb, win, heads)];
 }
 
 // The window and the block scales of the hpc_decode_*_win calls; the other
@@ -152,17 +175,24 @@ struct AttnForm {
     const float *kv_scale = nullptr;
 };
 
+// KV heads of a descriptor: the kernels over 8-bit caches with a window or
+// block scales take neighbouring heads in pairs (see attn_tc.cuh).
+int heads_per_desc(hpc_kv_dtype dt, int32_t window, int32_t Hkv) {
+    const bool tc = dt == HPC_KV_E4M3_BLOCK || (dt == HPC_KV_FP8_E4M3 && window > 0);
+    return tc && Hkv % 2 == 0 ? 2 : 1;
+}
+
 int32_t sink_tiles_of(int32_t sinks) { return (int32_t)(((int64_t)sinks + kTile - 1) / kTile); }
 
-// What map->persistent holds beside bit 0 for a windowed plan: a value
-// derived from the query count, window and sinks it was planned for (0
-// without a window), so that a call with others is refused.
-int32_t window_tag(int32_t q_len, const AttnForm &f) {
-    if (f.window <= 0) return 0;
+// What map->persistent holds above bit 0: whether its descriptors are head
+// pairs, and above that a value derived from the query count, window and sinks
+// it was planned for (0 without a window).  A call that needs others is refused.
+int32_t window_tag(int32_t q_len, const AttnForm &f, int heads) {
+    if (f.window <= 0) return heads - 1;
     uint64_t x = ((uint64_t)(uint32_t)f.window << 34) ^ ((uint64_t)(uint32_t)f.sinks << 4) ^
                  (uint64_t)(uint32_t)(q_len - 1);
     x *= 0x9E3779B97F4A7C15ull;  // 2^64 / golden ratio: spreads every bit upwards
-    return (int32_t)(x >> 34) | 1;
+    return (int32_t)(((x >> 35) | 1) << 1) | (heads - 1);
 }
 
 // Limits of the hpc_decode_*_win and hpc_prefill_attn_win arguments.
@@ -208,11 +238,18 @@ hpc_status launch_attention(const void *d_q, const float *d_q_scale, const void 
     if (map->B != B || map->Hkv != Hkv || map->num_ctas < 1 || map->num_ctas >= map->cap_bins)
         return HPC_ERR_ARG;
     // planned for this window (the tag is 0 without one)
-    if (map->persistent >> 1 != window_tag(q_len, form)) return HPC_ERR_ARG;
+    const bool win = form.window > 0;
+    const int heads = heads_per_desc(kv_dtype, form.window, Hkv);
+    if (map->persistent >> 1 != window_tag(q_len, form, heads)) return HPC_ERR_ARG;
 
     CUtensorMap tk, tv;
-    st = make_cache_map(&tk, d_k_cache, num_pages, Hkv, fp8);
-    if (st == HPC_OK) st = make_cache_map(&tv, d_v_cache, num_pages, Hkv, fp8);
+    if (fp8 && (block || win)) {
+        st = make_heads_map(&tk, d_k_cache, num_pages, Hkv, heads);
+        if (st == HPC_OK) st = make_heads_map(&tv, d_v_cache, num_pages, Hkv, heads);
+    } else {
+        st = make_cache_map(&tk, d_k_cache, num_pages, Hkv, fp8);
+        if (st == HPC_OK) st = make_cache_map(&tv, d_v_cache, num_pages, Hkv, fp8);
+    }
     if (st != HPC_OK) return st;
 
     AttnParams p;
@@ -231,23 +268,22 @@ hpc_status launch_attention(const void *d_q, const float *d_q_scale, const void 
     p.meta = map->meta;
     p.B = B;
     p.Hq = Hq;
-    p.Hkv = Hkv;
-    p.G = Hq / Hkv;
+    p.Hkv = Hkv / heads;
+    p.G = heads * (Hq / Hkv);
     p.max_pages = max_pages_per_req;
     p.num_pages = num_pages;
     p.q_len = q_len;
     p.R = q_len * p.G;
     p.score_scale = sm_scale * kLog2eF * (fp8 ? k_scale : 1.f);
     p.v_scale = fp8 ? v_scale : 1.f;
-    const bool win = form.window > 0;
     p.window = win ? form.window : kNoWindow;
     p.sinks = win ? form.sinks : 0;
     p.sink_tiles = sink_tiles_of(p.sinks);
     p.kv_scale = form.kv_scale;
 
-    const int nb = p.R > 8 ? 2 : 1;
-    const int variant = variant_of(kv_dtype, nb, win);
-    const AttnConfig &cfg = config_for(kv_dtype, nb, win);
+    const int nb = p.R / heads > 8 ? 2 : 1;
+    const int variant = variant_of(kv_dtype, nb, win, heads);
+    const AttnConfig &cfg = config_for(kv_dtype, nb, win, heads);
     cudaError_t e = prepare_kernel(cfg, variant);
     if (e != cudaSuccess) return HPC_ERR_CUDA;
     int grid = map->num_ctas;  // static map: one CTA per bin
@@ -273,9 +309,9 @@ hpc_status launch_attention(const void *d_q, const float *d_q_scale, const void 
                 ? 1
                 : 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (block) e = launch_attn_block(nb, tk, tv, p, grid, s);
+    if (block) e = launch_attn_block(nb, heads, tk, tv, p, grid, s);
     else if (win)
-        e = fp8 ? launch_attn_win_fp8(nb, tk, tv, p, grid, s)
+        e = fp8 ? launch_attn_win_fp8(nb, heads, tk, tv, p, grid, s)
                 : launch_attn_win_bf16(nb, tk, tv, p, grid, s);
     else
         e = fp8 ? launch_attn_fp8(nb, tk, tv, p, grid, s)
@@ -315,7 +351,9 @@ hpc_status combine_impl(const float *d_part_o, const float *d_part_lse, const hp
     st = check_map(map, true);
     if (st != HPC_OK) return st;
     if (map->B != B || map->Hkv != Hkv || (int64_t)B * Hkv > map->cap_units) return HPC_ERR_ARG;
-    return cuda_status(launch_combine(d_part_o, d_part_lse, *map, B, Hq, Hkv, q_len, d_out,
+    // descriptors of head pairs: half as many units with twice the rows
+    const int heads = 1 + ((map->persistent >> 1) & 1);
+    return cuda_status(launch_combine(d_part_o, d_part_lse, *map, B, Hq, Hkv / heads, q_len, d_out,
                                       static_cast<cudaStream_t>(stream)));
 }
 
@@ -432,7 +470,7 @@ namespace {
 hpc_status plan_impl(const int32_t *d_seqlens, int32_t B, int32_t Hkv, int32_t max_pages_per_req,
                      int32_t num_ctas, int32_t min_tiles_per_cta, hpc_task_map *map,
                      hpc_stream_t stream, const int32_t *bt_prefetch, int32_t q_len = 1,
-                     const AttnForm &form = AttnForm()) {
+                     const AttnForm &form = AttnForm(), int heads = 1) {
     if (B < 0 || Hkv <= 0 || max_pages_per_req <= 0 || num_ctas < 1 || min_tiles_per_cta < 0)
         return HPC_ERR_ARG;
     if (min_tiles_per_cta >= (1 << 29)) return HPC_ERR_ARG;
@@ -441,20 +479,22 @@ hpc_status plan_impl(const int32_t *d_seqlens, int32_t B, int32_t Hkv, int32_t m
     if ((int64_t)B * max_pages_per_req * Hkv >= (int64_t)1 << 30) return HPC_ERR_UNSUPPORTED;
     hpc_status st = check_map(map, true);
     if (st != HPC_OK) return st;
+    // (a head pair's descriptor fills two of the split buffer's, for which
+    // cap_desc stands too: 2 (num_ctas + B Hkv / 2))
     if ((int64_t)num_ctas + 1 > map->cap_bins || (int64_t)B * Hkv > map->cap_units ||
-        (int64_t)map->cap_desc < hpc_decode_desc_capacity(B, Hkv, num_ctas))
+        (int64_t)map->cap_desc < (int64_t)heads * num_ctas + (int64_t)B * Hkv)
         return HPC_ERR_WORKSPACE;
     hpc_task_map m = *map;
     m.B = B;
     m.Hkv = Hkv;
     m.num_ctas = num_ctas;
-    const int32_t tag = window_tag(q_len, form);
+    const int32_t tag = window_tag(q_len, form, heads);
     m.persistent = 1 | (tag << 1);
     m.min_tiles = min_tiles_per_cta;
     m.max_pages = max_pages_per_req;
     PlanWindow win;
     if (form.window > 0) win = {q_len, form.window, sink_tiles_of(form.sinks)};
-    st = cuda_status(launch_assign(d_seqlens, B, Hkv, max_pages_per_req, num_ctas,
+    st = cuda_status(launch_assign(d_seqlens, B, Hkv / heads, max_pages_per_req, num_ctas,
                                    min_tiles_per_cta, m, static_cast<cudaStream_t>(stream),
                                    bt_prefetch, win));
     if (st == HPC_OK) *map = m;
@@ -611,8 +651,11 @@ hpc_status hpc_decode_step(const void *d_q, const float *d_q_scale, const void *
 
 hpc_status hpc_decode_plan_win(const int32_t *d_seqlens, int32_t B, int32_t Hkv,
                                int32_t max_pages_per_req, int32_t num_ctas,
-                               int32_t min_tiles_per_cta, int32_t q_len, int32_t window,
-                               int32_t sinks, hpc_task_map *map, hpc_stream_t stream) {
+                               int32_t min_tiles_per_cta, hpc_kv_dtype kv_dtype, int32_t q_len,
+                               int32_t window, int32_t sinks, hpc_task_map *map,
+                               hpc_stream_t stream) {
+    if (kv_dtype != HPC_KV_BF16 && kv_dtype != HPC_KV_FP8_E4M3 && kv_dtype != HPC_KV_E4M3_BLOCK)
+        return HPC_ERR_ARG;
     if (q_len < 1) return HPC_ERR_ARG;
     if (q_len > HPC_MAX_QUERY_ROWS) return HPC_ERR_UNSUPPORTED;
     hpc_status st = check_window(window, sinks, max_pages_per_req);
@@ -621,7 +664,7 @@ hpc_status hpc_decode_plan_win(const int32_t *d_seqlens, int32_t B, int32_t Hkv,
     form.window = window;
     form.sinks = sinks;
     return plan_impl(d_seqlens, B, Hkv, max_pages_per_req, num_ctas, min_tiles_per_cta, map,
-                     stream, nullptr, q_len, form);
+                     stream, nullptr, q_len, form, heads_per_desc(kv_dtype, window, Hkv));
 }
 
 hpc_status hpc_decode_attn_win(const void *d_q, const float *d_q_scale, const void *d_k_cache,
@@ -673,7 +716,7 @@ hpc_status hpc_decode_step_win(const void *d_q, const float *d_q_scale, const vo
     form.sinks = sinks;
     form.kv_scale = d_kv_scale;
     st = plan_impl(d_seqlens, B, Hkv, max_pages_per_req, num_ctas, min_tiles_per_cta, map, stream,
-                   d_block_table, q_len, form);
+                   d_block_table, q_len, form, heads_per_desc(kv_dtype, window, Hkv));
     if (st != HPC_OK) return st;
     // the attention grid follows the assign kernel directly (after_plan)
     if (d_unit_done)

@@ -1,18 +1,24 @@
-// Windowed form of the persistent attention kernel over an FP8-E4M3 cache.
-#include "attn_kernel.cuh"
+// Windowed decode attention over an E4M3 cache with one scale for the whole
+// cache.
+#include "attn_tc.cuh"
 
 namespace hpc {
 
-// The plain form's pipeline shapes: two tiles per stage (eight consumer
-// warps), four stages.
-using One = AttnVariant<true, 4, 2, 1, true, false>;  // up to 8 query rows per KV head
-using Two = AttnVariant<true, 4, 2, 2, true, false>;  // up to 16
+template <int RB, int HEADS>
+using Tc = TcVariant<RB, HEADS, false>;
 
-AttnConfig attn_config_win_fp8(int nb) { return nb == 2 ? Two::config() : One::config(); }
+// nb = 1: up to 8 query rows per KV head, 2: up to 16; heads: KV heads of a
+// descriptor.
+AttnConfig attn_config_win_fp8(int nb, int heads) {
+    if (heads == 2) return nb == 2 ? Tc<16, 2>::config() : Tc<8, 2>::config();
+    return nb == 2 ? Tc<16, 1>::config() : Tc<8, 1>::config();
+}
 
-cudaError_t launch_attn_win_fp8(int nb, const CUtensorMap &tk, const CUtensorMap &tv,
+cudaError_t launch_attn_win_fp8(int nb, int heads, const CUtensorMap &tk, const CUtensorMap &tv,
                              const AttnParams &p, int grid, cudaStream_t s) {
-    return nb == 2 ? Two::launch(tk, tv, p, grid, s) : One::launch(tk, tv, p, grid, s);
+    if (heads == 2)
+        return nb == 2 ? Tc<16, 2>::launch(tk, tv, p, grid, s) : Tc<8, 2>::launch(tk, tv, p, grid, s);
+    return nb == 2 ? Tc<16, 1>::launch(tk, tv, p, grid, s) : Tc<8, 1>::launch(tk, tv, p, grid, s);
 }
 
 }  // namespace hpc

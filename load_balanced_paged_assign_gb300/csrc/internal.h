@@ -63,6 +63,7 @@ struct AttnParams {
     int num_bins;      // bins in the task map (>= the grid size)
     int min_tiles;     // floor the map was planned with (load-balanced maps)
     int fly;           // 1: derive the first descriptor from the seqlens (load-balanced maps)
+    // (a descriptor of a head pair: Hkv counts pairs, G and R both heads' rows)
     int B, Hq, Hkv, G, max_pages, num_pages;
     int q_len;  // query tokens per request (the last q_len live tokens; causal among them)
     int R;      // query rows per KV head: q_len * G (row rho = i * G + g)
@@ -90,14 +91,14 @@ cudaError_t launch_attn_fp8(int nb, const CUtensorMap &tk, const CUtensorMap &tv
 
 // The windowed forms, and the block-scaled cache's (windowed or not).
 AttnConfig attn_config_win_bf16(int nb);
-AttnConfig attn_config_win_fp8(int nb);
-AttnConfig attn_config_block(int nb);
+AttnConfig attn_config_win_fp8(int nb, int heads);  // heads: KV heads of a descriptor
+AttnConfig attn_config_block(int nb, int heads);
 
 cudaError_t launch_attn_win_bf16(int nb, const CUtensorMap &tk, const CUtensorMap &tv,
                                  const AttnParams &p, int grid, cudaStream_t s);
-cudaError_t launch_attn_win_fp8(int nb, const CUtensorMap &tk, const CUtensorMap &tv,
+cudaError_t launch_attn_win_fp8(int nb, int heads, const CUtensorMap &tk, const CUtensorMap &tv,
                                 const AttnParams &p, int grid, cudaStream_t s);
-cudaError_t launch_attn_block(int nb, const CUtensorMap &tk, const CUtensorMap &tv,
+cudaError_t launch_attn_block(int nb, int heads, const CUtensorMap &tk, const CUtensorMap &tv,
                               const AttnParams &p, int grid, cudaStream_t s);
 
 // bt_prefetch (or null): a block table [B, max_pages] the kernel warms in L2

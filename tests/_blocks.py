@@ -151,14 +151,18 @@ class Case:
 def check_attention(got, ref, mass, kv):
     """|got - ref| within the roundings of the kernels.
 
-    The weights are rounded to the product's type: BF16 2^-8, f16 2^-11 of the
-    value each (and once more in the normaliser, which sums the rounded ones):
-    2 u sum w |v|; the f16 ones below 2^-14 of the largest weight are off by up
-    to 2^-25 of it instead, over at most 4096 tokens here 2^-13 of the largest
-    value.  The output is rounded to BF16: 2^-8 |out|.  Scores are fp32 sums of
+    The weights are rounded to the product's type: BF16 2^-8 of the value (and
+    once more in the normaliser, which sums the rounded ones), 2 u sum w |v|.
+    The 8-bit kernels form a weight in f16 (2^-11) and split it into three E5M2
+    parts, each rounding what the last left by 2^-3 (two bits of fraction): 2^-9
+    in all, and the normaliser is exact: (2^-9 + 2^-11) sum w |v| < 2^-8.6 sum w
+    |v|, below 2 u with u = 2^-9.5.  The f16 weights of a cache without block
+    scales go through the same kernels.  Weights below 2^-14 of the largest are
+    off by up to 2^-25 of it instead, over at most 4096 tokens here 2^-13 of the
+    largest value.  The output is rounded to BF16: 2^-8 |out|.  Scores are fp32 sums of
     128 products, |x| < 32 in these inputs: 128 * 2^-24 * 32 = 2.5e-4 of the
     weight, doubled for the two exponentials (running maximum and merge)."""
-    u = 2.0 ** -8 if kv == "bf16" else 2.0 ** -11
+    u = 2.0 ** -8 if kv == "bf16" else 2.0 ** -9.5
     tol = (2 * u + 5e-4) * mass + 2.0 ** -8 * np.abs(ref) + 1e-30
     if kv != "bf16":
         tol = tol + 2.0 ** -13 * np.abs(mass).max(-1, keepdims=True)

@@ -23,10 +23,10 @@ def fake_map(B=4, Hkv=1, ctas=132, persistent=1):
     return m
 
 
-def plan(q_len=1, window=100, sinks=4, max_pages=32, B=4, seqlens=FAKE, m=None):
+def plan(q_len=1, window=100, sinks=4, max_pages=32, B=4, Hkv=1, dtype=0, seqlens=FAKE, m=None):
     m = m or fake_map()
-    return hd.lib().hpc_decode_plan_win(seqlens, B, 1, max_pages, 132, 2, q_len, window, sinks,
-                                        ctypes.byref(m), None)
+    return hd.lib().hpc_decode_plan_win(seqlens, B, Hkv, max_pages, 132, 2, dtype, q_len, window,
+                                        sinks, ctypes.byref(m), None)
 
 
 def test_plan_refusals():
@@ -40,6 +40,10 @@ def test_plan_refusals():
     assert plan(max_pages=1 << 24) == E.HPC_ERR_UNSUPPORTED  # token indices past 2^30
     assert plan(seqlens=None) == E.HPC_ERR_ARG
     assert plan(B=70) == E.HPC_ERR_WORKSPACE
+    assert plan(dtype=3) == E.HPC_ERR_ARG
+    # descriptors of head pairs: room for 2 num_ctas + B Hkv
+    assert plan(B=4, Hkv=2, dtype=1) == E.HPC_ERR_WORKSPACE
+    assert plan(B=4, Hkv=2, dtype=2, window=0, sinks=0) == E.HPC_ERR_WORKSPACE
 
 
 def attn(step=False, q=FAKE, qs=None, k=FAKE, v=FAKE, num_pages=10, kvs=None, dtype=0, bt=FAKE,

@@ -16,7 +16,8 @@ pytestmark = pytest.mark.gpu
 
 KINDS = ["bf16", "e4m3", "block"]
 # (Hq, Hkv, q_len): query rows per KV head on both sides of 8
-HEADS = [(8, 1, 1), (2, 2, 1), (16, 1, 1), (6, 2, 2), (8, 1, 2), (3, 1, 5)]
+HEADS = [(8, 1, 1), (2, 2, 1), (16, 1, 1), (6, 2, 2), (8, 1, 2), (3, 1, 5), (32, 2, 1), (16, 4, 3),
+         (10, 2, 3), (9, 3, 4), (12, 6, 8)]
 # (window, sinks): inside a tile, tile edges, sinks of several tiles, windows
 # beyond every length, a window of one, sinks beyond the lengths
 WINDOWS = [(1, 0), (5, 3), (64, 0), (65, 64), (100, 65), (130, 200), (700, 1), (10000, 4),
@@ -26,7 +27,7 @@ LENS = [1, 0, 63, 64, 65, 129, 190, 500, 777, 1000, 2, 2300]
 
 @pytest.mark.parametrize("kv", KINDS)
 @pytest.mark.parametrize("win", WINDOWS)
-@pytest.mark.parametrize("heads", [0, 3, 4])
+@pytest.mark.parametrize("heads", [0, 3, 4, 7])
 def test_windowed_decode(kv, win, heads):
     hq, hkv, n = HEADS[heads]
     c = Case(kv, LENS, hq, hkv, n, *win, seed=100 + heads).to_gpu()
@@ -118,7 +119,8 @@ def test_the_plan_leaves_out_exactly_the_hidden_tiles(kv):
     for n, W, S in ((1, 100, 5), (2, 640, 64), (1, 1, 129), (3, 5000, 0)):
         c = Case(kv, LENS, 4, 1, n, W, S, seed=60).to_gpu()
         ws = c.workspace(29)
-        hd.hpc_decode_plan_win(c.sl, 1, c.bt.shape[1], 29, 2, ws.tmap, q_len=n, window=W, sinks=S)
+        hd.hpc_decode_plan_win(c.sl, 1, c.bt.shape[1], 29, 2, ws.tmap, kv_dtype=DTYPE[kv], q_len=n,
+                               window=W, sinks=S)
         torch.cuda.synchronize()
         got = ws.tmap.to_host()
         ref = oracle.assign_closed_form(ow.planned_lengths(LENS, c.bt.shape[1], n, W, S), 1, 29, 2)
@@ -133,7 +135,8 @@ def test_plan_once_then_attention_on_several_layers(kv):
     """A map reused by two layers' attention calls, fused and with the separate combine."""
     c = Case(kv, LENS, 8, 2, 1, 150, 9, seed=61).to_gpu()
     ws = c.workspace()
-    hd.hpc_decode_plan_win(c.sl, 2, c.bt.shape[1], ws.num_ctas, 2, ws.tmap, window=150, sinks=9)
+    hd.hpc_decode_plan_win(c.sl, 2, c.bt.shape[1], ws.num_ctas, 2, ws.tmap, kv_dtype=DTYPE[kv],
+                           window=150, sinks=9)
     args = (c.q, c.qs, c.k, c.v, c.ks, c.vs, c.scale, c.bt, c.sl, 8, 2, 1, 150, 9, c.sm, ws.tmap,
             ws.part_o, ws.part_lse)
     outs = [torch.full((len(LENS), 1, 8, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
