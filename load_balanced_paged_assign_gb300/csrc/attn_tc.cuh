@@ -34,12 +34,14 @@
 // sum takes the fp32 weight.
 //
 // Warps: 0 producer (TMA; K, V, Q and scales of a stage), 1 issues the first
-// products, 10 the second (one warp for both took 1660 cycles a stage, more
-// than HBM does), 2-5 and 6-9 two softmax warpgroups that take the stages in
-// turn.  Each group keeps its own running reference m, sum and accumulator, so
-// neither waits for the other; the group that handles a descriptor's last
-// stage joins the two and writes the result.  The reference moves only when a
-// weight would pass 2^14.5 (one barrier vote per stage); the group then
+// products, 2 the second (one warp for both took 1660 cycles a stage, more than
+// HBM does), 4-7 and 8-11 two softmax warpgroups that take the stages in turn,
+// 12-15 join and write.  Each softmax group keeps its own running reference m,
+// sum and accumulator, so neither waits for the other; at its last stage of a
+// descriptor it publishes the sum and the reference and goes on, and the join
+// group brings the two accumulators together (a softmax group that did so
+// itself stopped for 2 to 3 us at every descriptor).  The reference moves only
+// when a weight would pass 2^14.5 (one barrier vote per stage); the group then
 // rescales its accumulator in TMEM.
 // Every wait is bounded.  Named barriers are reached by all four warps of a
 // group: a wait that failed is voted on there, and the group leaves together.
@@ -61,12 +63,19 @@ struct TcInfo {  // of a stage, written by the producer
 };
 static_assert(sizeof(TcInfo) == 192, "TcInfo layout");
 
+struct TcJoin {  // of a descriptor, for the join group
+    DescInfo di;
+    int only, end, pad;  // only: the group (0, 1) that handled it alone, or -1; end: no more
+};
+static_assert(sizeof(TcJoin) == 32, "TcJoin layout");
+
 constexpr int kTcTokens = 2 * kTile;    // of a stage: the MMA's 128 lanes
-constexpr int kTcThreads = 32 * 11;
-constexpr int kTcGroup = 128;           // threads of a softmax warpgroup
+constexpr int kTcThreads = 32 * 16;
+constexpr int kTcGroup = 128;           // threads of a softmax or join warpgroup
 constexpr float kTcTop = 3.f;           // log2 of the largest weight when the reference moves
 constexpr float kTcMax = 14.5f;         // log2 of the largest weight ever (E5M2 holds 1.75 2^15)
 constexpr int kTcOrds = 4;              // descriptors whose join data may be alive at once
+constexpr int kTcPubs = 8 + 2;          // arrivals that publish one: the groups' warps, two products
 
 // RB: query rows per KV head, padded to 8 or 16.  HEADS: KV heads of a
 // descriptor (AttnParams' Hkv, G and R count descriptors' heads, their query
@@ -92,8 +101,9 @@ struct TcTraits {
     static constexpr int kOffRed = kOffScale + STAGES * kScaleBytes;  // [2][4 warps][16] floats
     static constexpr int kOffSum = kOffRed + 2 * 4 * 16 * 4;     // [ords][2][4][16] row sums
     static constexpr int kOffRef = kOffSum + kTcOrds * 2 * 4 * 16 * 4;  // [ords][2][32]
-    static constexpr int kOffFac = kOffRef + kTcOrds * 2 * 32 * 4;  // [2 groups][3][32]
-    static constexpr int kOffLast = kOffFac + 2 * 3 * 32 * 4;
+    static constexpr int kOffFac = kOffRef + kTcOrds * 2 * 32 * 4;  // [2 groups][32], join [3][32]
+    static constexpr int kOffJoin = kOffFac + 5 * 32 * 4;           // [ords]
+    static constexpr int kOffLast = kOffJoin + kTcOrds * (int)sizeof(TcJoin);
     // full[S], empty[S], s_full[2], p_full[2], o_done[2], o_free[2], pub[ords],
     // end, mma_done
     static constexpr int kOffBar = kOffLast + (kMaxLast + 1) * (int)sizeof(SlotInfo);
@@ -246,6 +256,14 @@ __device__ __forceinline__ void tmem_st_cols(uint32_t t, const float (&v)[N]) {
             "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
             "r"(r[15]), "r"(t)
             : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n) {
+    asm volatile(
+        "{\n\t.reg .b64 st;\n\t"
+        "mbarrier.arrive.release.cta.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+        "r"(n)
+        : "memory");
 }
 
 // True in every thread of the group if it is in one (all four warps reach it).
@@ -508,7 +526,8 @@ __device__ __forceinline__ void tc_producer(const CUtensorMap *tmap_k, const CUt
             break;
         }
         if (lane == 0) {
-            info[stage].flags = kEnd;
+            info[stage].flags = kEnd | (e == 0 ? kFirst : 0);
+            info[stage].ord = ord;
             mbar_arrive(&bar.full[stage]);
         }
         ++ps.it;
@@ -611,8 +630,9 @@ __device__ __forceinline__ bool tc_products(const AttnParams &p, uint8_t *smem, 
         const int flags = uniform(info[s].flags), ord = uniform(info[s].ord);
         const int left = uniform(info[s].left);
         if (flags & kEnd) return true;
-        // its group's last stage of the descriptor: the join waits for it
-        const bool pub = left == 1 || (left == 0 && (flags & kFirst));
+        // its group's last stage of the descriptor: the join waits for it (a
+        // descriptor of one stage stands for both groups)
+        const int pubs = left > 1 ? 0 : left == 0 && (flags & kFirst) ? 2 : 1;
         if (!warp_wait(&bar.p_full[x], (it >> 1) & 1u, abort)) return false;
         if (ord > opened) {  // descriptor ord - 2 has been read out of these columns
             if (ord >= 2 && !warp_wait(&bar.o_free[ord & 1], ((ord >> 1) - 1) & 1, abort))
@@ -634,7 +654,8 @@ __device__ __forceinline__ bool tc_products(const AttnParams &p, uint8_t *smem, 
             }
             umma_commit(&bar.empty[s]);
             umma_commit(&bar.o_done[x]);
-            if (pub) umma_commit(&bar.pub[ord % kTcOrds]);
+            if (pubs > 0) umma_commit(&bar.pub[ord % kTcOrds]);
+            if (pubs > 1) umma_commit(&bar.pub[ord % kTcOrds]);
         }
         ord_of[x] = ord;
         __syncwarp();
@@ -658,8 +679,8 @@ __device__ __forceinline__ bool tc_softmax(const AttnParams &p, uint8_t *smem, u
     float *red = reinterpret_cast<float *>(smem + Tr::kOffRed) + x * 64;
     float *sums = reinterpret_cast<float *>(smem + Tr::kOffSum);
     float *refs = reinterpret_cast<float *>(smem + Tr::kOffRef);
-    float *fac = reinterpret_cast<float *>(smem + Tr::kOffFac) + x * 96;
-    SlotInfo *last = reinterpret_cast<SlotInfo *>(smem + Tr::kOffLast);  // [0].flags: count
+    float *fac = reinterpret_cast<float *>(smem + Tr::kOffFac) + x * 32;
+    TcJoin *joins = reinterpret_cast<TcJoin *>(smem + Tr::kOffJoin);
     const uint32_t lane_base = tmem + ((uint32_t)(32 * q4) << 16);
     const uint32_t p_row = smem_u32(smem + Tr::kOffP) + x * Tr::kPBytes + tid * 16;
 
@@ -681,8 +702,18 @@ __device__ __forceinline__ bool tc_softmax(const AttnParams &p, uint8_t *smem, u
         const bool end = flags & kEnd;
         if (!ok || end) {  // leave together (the others meet both votes below)
             tmem_wait_cols<RB>(dr, d);
+            // (the slot written below was last used by a descriptor that has been
+            // joined once this group's last product is done)
+            if (ok && n > 0) ok = warp_wait(&bar.o_done[x], (n - 1) & 1u, abort);
             group_any(bid, true);
-            return !group_any(bid, !ok);
+            if (group_any(bid, !ok)) return false;
+            if (flags & kFirst) {  // the first terminator: tell the join group
+                const int slot = info[s].ord % kTcOrds;
+                if (tid == 0) joins[slot].end = 1;
+                __syncwarp();
+                if (lane == 0) mbar_arrive_n(&bar.pub[slot], q4 == 0 ? 4 : 2);
+            }
+            return true;
         }
         const int ord = info[s].ord, L = info[s].seqlen, ntiles = info[s].ntiles;
         int tile = info[s].tile0 + pos;
@@ -766,7 +797,7 @@ __device__ __forceinline__ bool tc_softmax(const AttnParams &p, uint8_t *smem, u
             if (tid % 64 == 0)
 #pragma unroll
                 for (int r = 0; r < RB; ++r)
-                    if (HEADS == 2 || tid == 0) fac[64 + 16 * hd + r] = al[r];
+                    if (HEADS == 2 || tid == 0) fac[16 * hd + r] = al[r];
             named_bar_sync(bid, kTcGroup);  // (red may be written again)
             if (!fresh) {
 #pragma unroll
@@ -778,7 +809,7 @@ __device__ __forceinline__ bool tc_softmax(const AttnParams &p, uint8_t *smem, u
                         tmem_ld_cols<RB>(oc + RB * c, o);
 #pragma unroll
                         for (int r = 0; r < RB; ++r)
-                            o[r] *= HEADS == 2 ? fac[64 + 16 * y + r] : al[r];
+                            o[r] *= HEADS == 2 ? fac[16 * y + r] : al[r];
                         tmem_st_cols<RB>(oc + RB * c, o);
                     }
                 }
@@ -828,39 +859,57 @@ __device__ __forceinline__ bool tc_softmax(const AttnParams &p, uint8_t *smem, u
 
         // ---- this group's last stage of the descriptor: publish sum and reference
         const int slot = ord % kTcOrds;
+        const bool alone = (flags & kFirst) && left == 0;  // the descriptor's only stage
         {
-            float v[RB];
-#pragma unroll
-            for (int r = 0; r < RB; ++r) v[r] = l[r];
-            const float t = warp_reduce_rows<RB, false>(v, lane);
+            const float t = warp_reduce_rows<RB, false>(l, lane);
             constexpr int kPer = 32 / RB;  // lanes that hold the same row
             if (lane % kPer == 0) sums[((slot * 2 + x) * 4 + q4) * 16 + lane / kPer] = t;
             if (HEADS == 2 ? tid % 64 == 0 : tid == 0)
 #pragma unroll
                 for (int r = 0; r < RB; ++r) refs[(slot * 2 + x) * 32 + 16 * hd + r] = m[r];
+            if (tid == 0 && left == 0) joins[slot] = TcJoin{di, alone ? x : -1, 0, 0};
         }
-        const bool alone = (flags & kFirst) && left == 0;  // the descriptor's only stage
-        if (left == 1 || alone) {  // once per descriptor
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.pub[slot]);
-        }
-        if (left == 1) continue;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_n(&bar.pub[slot], alone ? 2 : 1);
+    }
+}
 
-        // ---- the descriptor's last stage: join both groups' parts
-        // (pub: the other group's sums and its last product.  Its o_done may
-        // have moved on by a phase, so it says nothing here.)
-        ok = warp_wait(&bar.o_done[x], n & 1u, abort);
-        if (!alone) ok = ok && warp_wait(&bar.pub[slot], (ord / kTcOrds) & 1, abort);
-        if (group_any(bid, !ok)) return false;  // (orders the group's sums as well)
+// ------------------------------------------------------------------ join
+// Of each descriptor in turn: the two groups' accumulators, in the units of
+// their references, under one normalisation, as BF16 output or partial.
+template <int RB, int HEADS, bool BLK>
+__device__ __forceinline__ bool tc_join(const AttnParams &p, uint8_t *smem, uint32_t tmem,
+                                        volatile int *abort) {
+    using Tr = TcTraits<RB, HEADS, BLK>;
+    const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
+    const int tid = 32 * q4 + lane;  // dim of the output
+    const int bid = 3;
+    const TcBars bar = tc_bars<Tr>(smem);
+    const float *sums = reinterpret_cast<const float *>(smem + Tr::kOffSum);
+    const float *refs = reinterpret_cast<const float *>(smem + Tr::kOffRef);
+    float *fac = reinterpret_cast<float *>(smem + Tr::kOffFac) + 64;
+    const TcJoin *joins = reinterpret_cast<const TcJoin *>(smem + Tr::kOffJoin);
+    SlotInfo *last = reinterpret_cast<SlotInfo *>(smem + Tr::kOffLast);  // [0].flags: count
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * q4) << 16);
+    const int Gh = p.G / HEADS, Rh = p.R / HEADS;
+    const bool fused = p.out != nullptr;
+    grid_dependency_wait();  // before this grid's first global writes
+    for (int ord = 0;; ++ord) {
+        const int slot = ord % kTcOrds;
+        const bool ok = warp_wait(&bar.pub[slot], (ord / kTcOrds) & 1, abort);
+        if (group_any(bid, !ok)) return false;
+        const TcJoin j = joins[slot];
+        if (j.end) return true;
+        const DescInfo di = j.di;
         if (tid < 16 * HEADS && tid % 16 < RB) {  // head tid / 16, row tid % 16
             const int y = tid / 16, r = tid % 16;
             float ls[2], z[2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {  // the two groups
+            for (int k = 0; k < 2; ++k) {  // the two softmax groups
                 const float *sk = sums + (slot * 2 + k) * 64 + 32 * y + r;
-                const bool in = k == x || !alone;
-                z[k] = !in ? 0.f
-                           : HEADS == 2 ? sk[0] + sk[16] : (sk[0] + sk[16]) + (sk[32] + sk[48]);
+                z[k] = j.only == (k ^ 1) ? 0.f
+                       : HEADS == 2      ? sk[0] + sk[16]
+                                         : (sk[0] + sk[16]) + (sk[32] + sk[48]);
                 ls[k] = z[k] > 0.f ? refs[(slot * 2 + k) * 32 + tid] + lg2(z[k]) : kNegInf;
             }
             const float M = fmaxf(ls[0], ls[1]);
@@ -881,12 +930,16 @@ __device__ __forceinline__ bool tc_softmax(const AttnParams &p, uint8_t *smem, u
             for (int r = 0; r < RB; ++r) out[y][r] = 0.f;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                if (k != x && alone) continue;
+                if (j.only == (k ^ 1)) continue;
                 const uint32_t oc = lane_base + Tr::o_col(ord & 1, k, y);
+                uint32_t ra[RB], rb[RB], rc[RB];
+                tmem_ld_cols_nowait<RB>(oc, ra);
+                tmem_ld_cols_nowait<RB>(oc + RB, rb);
+                tmem_ld_cols_nowait<RB>(oc + 2 * RB, rc);
                 float a[RB], b[RB], c[RB];
-                tmem_ld_cols<RB>(oc, a);
-                tmem_ld_cols<RB>(oc + RB, b);
-                tmem_ld_cols<RB>(oc + 2 * RB, c);
+                tmem_wait_cols<RB>(ra, a);
+                tmem_wait_cols<RB>(rb, b);
+                tmem_wait_cols<RB>(rc, c);
 #pragma unroll
                 for (int r = 0; r < RB; ++r)  // (a row that saw nothing: factor 0, finite O)
                     out[y][r] = fmaf(fmaf(fmaf(c[r], 0.125f, b[r]), 0.125f, a[r]),
@@ -896,8 +949,6 @@ __device__ __forceinline__ bool tc_softmax(const AttnParams &p, uint8_t *smem, u
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.o_free[ord & 1]);
-        grid_dependency_wait();  // before this grid's first global writes
-        const bool fused = p.out != nullptr;
         if (fused && di.count == 1) {
             __nv_bfloat16 *base = static_cast<__nv_bfloat16 *>(p.out) +
                                   ((size_t)di.req * p.q_len * p.Hq + di.kv_head * p.G) * kHeadDim +
@@ -932,23 +983,21 @@ __device__ __forceinline__ bool tc_softmax(const AttnParams &p, uint8_t *smem, u
             }
             if (fused) {  // count this chunk of a split unit
                 named_bar_sync(bid, kTcGroup);  // the group's stores precede the release below
-                bool merge = false;
                 if (q4 == 0) {
                     int completes = 0;
                     if (lane == 0) {
                         int *ctr = p.unit_done + di.kv_head * p.B + di.req;
                         if (atom_add_acq_rel_gpu(ctr, 1) == di.count - 1) {
                             *ctr = 0;  // every chunk counted: ready for the next launch
-                            const int at = atomicAdd(&last[0].flags, 1);
+                            const int at = last[0].flags++;
                             if (at < kMaxLast) last[1 + at].di = di;
                             completes = at < kMaxLast ? 1 : 2;
                         }
                     }
                     completes = __shfl_sync(kFullMask, completes, 0);
-                    merge = completes == 2;  // list full: merge here, alone
+                    if (completes == 2)  // list full: merge here, alone
+                        for (int rho = 0; rho < p.R; ++rho) merge_unit_head<8>(p, di, rho);
                 }
-                if (merge)
-                    for (int rho = 0; rho < p.R; ++rho) merge_unit_head<8>(p, di, rho);
             }
         }
         named_bar_sync(bid, kTcGroup);  // fac may be written again
@@ -980,8 +1029,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&bar.o_done[y], 1);
             mbar_init(&bar.o_free[y], 4);
         }
-        for (int y = 0; y < kTcOrds; ++y) mbar_init(&bar.pub[y], 4 + 1);  // warps and product
-        mbar_init(bar.end, 8);  // softmax warps
+        for (int y = 0; y < kTcOrds; ++y) mbar_init(&bar.pub[y], kTcPubs);
+        mbar_init(bar.end, 12);  // softmax and join warps
         mbar_init(bar.mma_done, 2);
         *abort = 0;
         last[0].flags = 0;
@@ -1012,7 +1061,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_producer<RB, HEADS, BLK>(&tmap_k, &tmap_v, p, smem, abort);
         return;
     }
-    if (warp == 9 && p.out) {  // fused mode: requests without live tokens get zero rows
+    if (warp == 3) {  // fused mode: requests without live tokens get zero rows
+        if (!p.out) return;
         grid_dependency_wait();
         const int row_vec = p.q_len * p.Hq * kHeadDim * 2 / 16;
         for (int r = blockIdx.x; r < p.B; r += gridDim.x) {
@@ -1021,21 +1071,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                                    (size_t)r * p.q_len * p.Hq * kHeadDim);
             for (int i = lane; i < row_vec; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
         }
+        return;
     }
     const bool ok = warp == 1    ? tc_scores<RB, HEADS, BLK>(p, smem, tmem, abort)
-                    : warp == 10 ? tc_products<RB, HEADS, BLK>(p, smem, tmem, abort)
-                                 : tc_softmax<RB, HEADS, BLK>(p, smem, tmem, (warp - 2) >> 2, abort);
+                    : warp == 2  ? tc_products<RB, HEADS, BLK>(p, smem, tmem, abort)
+                    : warp >= 12 ? tc_join<RB, HEADS, BLK>(p, smem, tmem, abort)
+                                 : tc_softmax<RB, HEADS, BLK>(p, smem, tmem, (warp - 4) >> 2, abort);
     if (!ok) {
         grid_dependency_wait();  // meta[3] is written by the assign kernel
         if (lane == 0) atomicOr(p.meta + 3, (int)HPC_FLAG_TIMEOUT);
         *abort = 1;
     }
-    if (warp == 1 || warp == 10) {
-        // TMEM is freed once every MMA issued has completed and the softmax
-        // groups have read their last result (bounded, like every wait)
+    if (warp == 1 || warp == 2) {
+        // TMEM is freed once every MMA issued has completed and the other
+        // groups have read their last columns (bounded, like every wait)
         if (elect_one()) umma_commit(bar.mma_done);
         __syncwarp();
-        if (warp == 10) return;
+        if (warp == 2) return;
         volatile int no_abort = 0;
         mbar_wait(bar.mma_done, 0, &no_abort);
         mbar_wait(bar.end, 0, &no_abort);
@@ -1044,7 +1096,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tmem_dealloc(tmem, Tr::kTmemCols);
         return;
     }
-    // End of the stream: the softmax warps merge the split units this CTA owes,
+    // End of the stream: all groups' warps merge the split units this CTA owes,
     // four rows of a unit per warp at a time (their loads in flight together).
     tc_fence_before();
     __syncwarp();
@@ -1052,8 +1104,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (!warp_wait(bar.end, 0, abort) || !p.out || *abort) return;
     grid_dependency_wait();
     const int nlast = min(last[0].flags, kMaxLast);
-    const int w = warp - 2, items = nlast * p.R;
-    for (int item = 4 * w; item < items; item += 32) {
+    const int w = warp - 4, items = nlast * p.R;
+    for (int item = 4 * w; item < items; item += 4 * 12) {
         DescInfo dd[4];
         int rr[4];
         bool few = true;
