@@ -307,16 +307,6 @@ __device__ __forceinline__ uint32_t rest8(uint32_t a, uint32_t b) {
     return d;
 }
 
-// One lane of the warp, the same every time, in a form that keeps what the
-// branch computes warp-uniform (the MMA operands are uniform registers).
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r));
-    return r != 0;
-}
-
 // Sums (or maxima) of v[0 .. N-1] over the warp's lanes: on return lane l holds
 // that of row l / (32 / N).
 template <int N, bool MAX>

@@ -29,12 +29,6 @@
 //     only on those rare tiles; the result is the same softmax, since O and
 //     the row sum always share the reference m;
 //   * the epilogue divides O by the row sum and writes BF16.
-// Windowed form (WIN): the KV tiles are the pair's sink tiles and those from
-// its first query's window on, numbered through; a page none of whose tokens
-// the pair sees is not loaded.  A tile with a dead row (past L_r, or before
-// the window and no sink) has those rows of V zeroed by the producer once they
-// have landed, and is handed over on its own barrier, as the last tile is in
-// the causal form.
 // A tcgen05.commit covers every MMA its thread issued before it, so when x's
 // scores for tile j are complete, x's product with tile j - 1 is complete
 // too: the softmax may read and rescale O_x without a further wait.
@@ -48,24 +42,11 @@
 #include <cstring>
 
 #include "internal.h"
+#include "prefill_common.cuh"
 #include "tcgen05.cuh"
 
 namespace hpc {
 namespace {
-
-constexpr int kQB = 128;                 // query rows per Q tile (UMMA M)
-constexpr int kQT = 2;                   // Q tiles per CTA
-constexpr int kKB = 128;                 // KV tokens per tile: two pages
-constexpr int kHalf = 128 * 128;         // 128 rows x 64 BF16: one 128-byte column block
-constexpr int kTileBytes = 2 * kHalf;    // a 128 x 128 BF16 tile (Q, K or V)
-constexpr int kKStages = 2;              // K ring depth
-constexpr int kVStages = 2;              // V ring depth
-constexpr int kSoftmaxWarps = 4 * kQT;
-constexpr int kProducerWarp = kSoftmaxWarps, kMmaWarp = kSoftmaxWarps + 1;
-constexpr int kThreads = (kSoftmaxWarps + 2) * 32;
-constexpr uint32_t kTmemCols = 512;      // S_x / P_x at 128 x; O_x at 256 + 128 x
-constexpr int kOCol = 256;
-constexpr float kRescaleLog2 = 8.f;      // P <= 2^8 between reference moves
 
 // Shared-memory layout (offsets from the 1024-byte aligned base).
 constexpr int kOffQ = 0;
@@ -73,8 +54,8 @@ constexpr int kOffK = kOffQ + kQT * kTileBytes;
 constexpr int kOffV = kOffK + kKStages * kTileBytes;
 constexpr int kOffBar = kOffV + kVStages * kTileBytes;
 // barriers: q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2],
-// p_full[2], o_done[2], mma_done, v_tail[2]
-constexpr int kNumBars = 1 + 2 * kKStages + 3 * kVStages + 3 * kQT + 1;
+// p_full[2], o_done[2], mma_done, v_tail
+constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 3 * kQT + 2;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;  // tmem slot, abort word
 constexpr int kSmemBytes = kOffMisc + 16 + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 227 * 1024, "shared memory over the per-CTA limit");
@@ -86,83 +67,8 @@ struct PrefillArgs {
     int32_t *flags;
     int B, Hq, Hkv, G, q_len, max_pages, num_pages, n_qp;
     float score_scale;  // sm_scale * log2(e)
-    int window, sinks;  // WIN
 };
 
-__device__ __forceinline__ uint64_t policy_evict_normal() {
-    uint64_t p;
-    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
-    return p;
-}
-
-// Lane 0 waits (bounded); the verdict is broadcast and every lane then
-// observes the completed phase itself (acquire).  Warp-uniform result.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    int ok = 1;
-    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort) ? 1 : 0;
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    if (ok) mbar_try_wait(bar, parity);
-    return ok != 0;
-}
-
-// max(a, b, c) in one instruction.
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
-__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
-                                       uint32_t d) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
-                 "r"(d)
-                 : "memory");
-}
-
-// The causal extent of a Q tile: its first query row, the KV tiles its rows
-// read, and the last token its first row sees.
-struct QTile {
-    int first, tiles, lim_first;
-};
-
-__device__ __forceinline__ QTile qtile(int i0, int L, int q_len) {
-    QTile t;
-    t.first = i0;
-    t.lim_first = min(L - q_len + i0, L - 1);
-    t.tiles = 0;
-    if (i0 < q_len) {
-        const int lim_last = min(L - q_len + min(i0 + kQB - 1, q_len - 1), L - 1);
-        t.tiles = lim_last >= 0 ? lim_last / kKB + 1 : 0;
-    }
-    return t;
-}
-
-// The KV tokens a pair of Q tiles reads in the windowed form.
-struct PairWindow {
-    int lo;          // first token of the window of the pair's first query
-    int sinks;       // tokens below it stay visible
-    int sink_tiles;  // 128-token tiles that hold sinks
-    int skip;        // tiles left out behind them
-
-    __device__ __forceinline__ int tile(int j) const { return j < sink_tiles ? j : j + skip; }
-    // no query of the pair sees token t (of a request of L tokens): it lies
-    // past the end, or before the window and is no sink
-    __device__ __forceinline__ bool dead(int t, int L) const {
-        return t >= L || (t < lo && t >= sinks);
-    }
-    // KV tile j holds such a token
-    __device__ __forceinline__ bool dirty(int j, int L) const {
-        const int t = tile(j) * kKB;
-        return t + kKB > L || max(t, sinks) < min(t + kKB, lo);
-    }
-    // page g holds a token that is not
-    __device__ __forceinline__ bool needs_page(int g, int L) const {
-        const int t = g * kTile;
-        return t < L && (t + kTile > lo || t < sinks);
-    }
-};
-
-template <bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_attn_kernel(const __grid_constant__ CUtensorMap tq,
                         const __grid_constant__ CUtensorMap tk,
@@ -178,10 +84,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *p_full = s_full + kQT;       // [x]: P_x written (four warps)
     uint64_t *o_done = p_full + kQT;       // [x]: O_x += P_x V complete
     uint64_t *mma_done = o_done + kQT;
-    // [V stage]: a V tile with its dead rows zeroed (causal form: the last
-    // tile, on the first of them).  One for each stage: a stage's next such
-    // tile is loaded after its last one was consumed, so no phase is passed over
-    uint64_t *v_tail = mma_done + 1;
+    uint64_t *v_tail = mma_done + 1;       // the last V tile with its free slots zeroed
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
     volatile int *abort = reinterpret_cast<volatile int *>(smem + kOffMisc + 4);
 
@@ -225,39 +128,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     QTile qt[kQT];
 #pragma unroll
     for (int x = 0; x < kQT; ++x) qt[x] = qtile(i0 + x * kQB, L, a.q_len);
-    PairWindow pw = {0, 0, 0, 0};
-    if constexpr (WIN) {
-        pw.lo = max(L - a.q_len + i0 + 1 - a.window, 0);
-        pw.sinks = a.sinks;
-        pw.sink_tiles = a.sinks / kKB + (a.sinks % kKB ? 1 : 0);
-        pw.skip = max(pw.lo / kKB - pw.sink_tiles, 0);
-        // a Q tile's causal extent ends behind its first row's window, so it
-        // either has tiles behind the gap or the gap is empty
-#pragma unroll
-        for (int x = 0; x < kQT; ++x)
-            if (qt[x].tiles > 0) qt[x].tiles -= pw.skip;
-    }
     int n = 0;  // KV tiles the CTA reads
 #pragma unroll
     for (int x = 0; x < kQT; ++x) n = max(n, qt[x].tiles);
     const int np = (L + kTile - 1) / kTile;  // pages of the request
-    const bool tail = !WIN && n > 0 && n * kKB > L;   // the last tile holds slots past L_r
-    // zeroes the rows of V tile j (landed in its stage) that no query sees, and
-    // hands the tile over
-    auto clean = [&](int j) {
-        const int s = j % kVStages;
-        if (!warp_wait(&v_full[s], (j / kVStages) & 1u, abort)) return false;
-        uint8_t *vs = smem + kOffV + s * kTileBytes;
-        const int t = pw.tile(j) * kKB;
-        for (int e = lane; e < kKB * 8; e += 32)
-            if (pw.dead(t + (e >> 3), L))
-                for (int h = 0; h < 2; ++h)
-                    sts128(smem_u32(vs + h * kHalf + e * 16), 0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&v_tail[s]);
-        return true;
-    };
+    const bool tail = n > 0 && n * kKB > L;   // the last tile holds slots past L_r
 
     bool ok = true;
     int q_issued = 0, k_issued[kKStages] = {}, v_issued[kVStages] = {};
@@ -281,23 +156,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         int pg = -1;
         for (int j = 0; j < n; ++j) {
             if ((j & 15) == 0) {  // the page numbers of 16 tiles, one per lane
-                if constexpr (WIN) {  // -2: not needed
-                    const int idx = 2 * pw.tile(j + (lane >> 1)) + (lane & 1);
-                    pg = pw.needs_page(idx, L) ? max(__ldg(bt + idx), -1) : -2;
-                } else {
-                    const int idx = 2 * j + lane;
-                    pg = idx < np ? __ldg(bt + idx) : -1;
-                }
+                const int idx = 2 * j + lane;
+                pg = idx < np ? __ldg(bt + idx) : -1;
             }
             const int p0 = __shfl_sync(0xffffffffu, pg, (2 * j) & 31);
             const int p1 = __shfl_sync(0xffffffffu, pg, (2 * j + 1) & 31);
             int good = 1;
             if (lane == 0) {
-                const bool has0 = !WIN || p0 != -2, has1 = WIN ? p1 != -2 : 2 * j + 1 < np;
-                const bool l0 = has0 && p0 >= 0 && p0 < a.num_pages;
+                const bool has1 = 2 * j + 1 < np;
+                const bool l0 = p0 >= 0 && p0 < a.num_pages;
                 const bool l1 = has1 && p1 >= 0 && p1 < a.num_pages;
-                if (((has0 && !l0) || (has1 && !l1)) && a.flags)
-                    atomicOr(a.flags, (int)HPC_FLAG_BAD_PAGE);
+                if ((!l0 || (has1 && !l1)) && a.flags) atomicOr(a.flags, (int)HPC_FLAG_BAD_PAGE);
                 const uint32_t bytes = (uint32_t)((l0 ? 1 : 0) + (l1 ? 1 : 0)) * 2 * kTile * 128;
                 for (int kv = 0; kv < 2 && good; ++kv) {
                     const int st = kv == 0 ? kKStages : kVStages, s = j % st;
@@ -328,15 +197,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = false;
                 break;
             }
-            if constexpr (WIN) {  // tile j - 1 may have landed while j's copies were issued
-                if (j > 0 && pw.dirty(j - 1, L) && !clean(j - 1)) {
-                    ok = false;
-                    break;
-                }
-            }
-        }
-        if constexpr (WIN) {
-            if (ok && n > 0 && pw.dirty(n - 1, L) && !clean(n - 1)) ok = false;
         }
         if (ok && tail) {
             // tokens past L_r (the last page's free slots, or a page the
@@ -395,17 +255,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     umma_commit(&k_empty[0]);
                 }
             }
-            uint32_t cleaned[kVStages] = {};  // WIN: zeroed tiles taken from each stage
             for (int j = 0; ok && j < n; ++j) {
                 const int s = j % kVStages, s1 = (j + 1) % kKStages;
                 const bool next = j + 1 < n;
-                if (WIN && pw.dirty(j, L)) {
-                    ok = mbar_wait(&v_tail[s], cleaned[s] & 1u, abort);
-                    ++cleaned[s];
-                } else {
-                    ok = (j == n - 1 && tail) ? mbar_wait(v_tail, 0, abort)
-                                              : mbar_wait(&v_full[s], (j / kVStages) & 1u, abort);
-                }
+                ok = (j == n - 1 && tail) ? mbar_wait(v_tail, 0, abort)
+                                          : mbar_wait(&v_full[s], (j / kVStages) & 1u, abort);
                 if (ok && next) ok = mbar_wait(&k_full[s1], ((j + 1) / kKStages) & 1u, abort);
                 for (int x = 0; x < kQT && ok; ++x) {
                     if (j >= qt[x].tiles) continue;
@@ -430,9 +284,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const QTile t = qt[x];
         const int rho = 32 * q4 + lane, i = t.first + rho;
         const int lim = min(L - a.q_len + i, L - 1);
-        // WIN: the first token of this row's window, and of the last row's
-        const int lo = WIN ? L - a.q_len + i + 1 - a.window : 0;
-        const int lo_last = WIN ? L - a.q_len + min(t.first + kQB, a.q_len) - a.window : 0;
         const uint32_t row = tmem + ((uint32_t)(32 * q4) << 16);
         const uint32_t scol = row + 128 * x, ocol = row + kOCol + 128 * x;
         const float sc = a.score_scale;
@@ -457,19 +308,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s[c] = __uint_as_float(ra[c]);
                 s[32 + c] = __uint_as_float(rb[c]);
             }
-            const int tok = WIN ? pw.tile(j) * kKB : j * kKB;  // the tile's first token
-            const bool diag = tok + kKB - 1 > t.lim_first;  // the causal diagonal or the end
-            // tokens before some row's window that are no sinks
-            const bool edge = WIN && tok < lo_last && tok + kKB > pw.sinks;
+            const bool diag = j * kKB + kKB - 1 > t.lim_first;  // the causal diagonal or the end
             if (diag) {
 #pragma unroll
                 for (int c = 0; c < 64; ++c)
-                    if (tok + c > lim) s[c] = -INFINITY;
-            }
-            if (edge) {
-#pragma unroll
-                for (int c = 0; c < 64; ++c)
-                    if (tok + c < lo && tok + c >= pw.sinks) s[c] = -INFINITY;
+                    if (j * kKB + c > lim) s[c] = -INFINITY;
             }
             float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -483,12 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (diag) {
 #pragma unroll
                 for (int c = 64; c < 128; ++c)
-                    if (tok + c > lim) s[c] = -INFINITY;
-            }
-            if (edge) {
-#pragma unroll
-                for (int c = 64; c < 128; ++c)
-                    if (tok + c < lo && tok + c >= pw.sinks) s[c] = -INFINITY;
+                    if (j * kKB + c > lim) s[c] = -INFINITY;
             }
 #pragma unroll
             for (int c = 32; c < 64; ++c) mx4[c & 3] = fmax3(mx4[c & 3], s[2 * c], s[2 * c + 1]);
@@ -605,42 +443,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-std::atomic<unsigned> g_prefill_attr_done[2];  // per kernel form, a bit per device
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Tensor map over Q [B * q_len, Hq, 128] BF16 as {64 dims, 2 halves, Hq,
-// tokens}, box {64, 1, 1, 128}: one 64-dim half of 128 consecutive query
-// tokens of one head, rows of 128 bytes (the swizzle span).
-hpc_status make_q_map(CUtensorMap *m, const void *q, int64_t tokens, int32_t Hq) {
-    auto encode = tensor_map_encoder();
-    if (!encode) return HPC_ERR_CUDA;
-    std::memset(m, 0, sizeof(*m));
-    cuuint64_t dims[4] = {64, 2, (cuuint64_t)Hq, (cuuint64_t)tokens};
-    cuuint64_t strides[3] = {128, 256, (cuuint64_t)Hq * 256};
-    cuuint32_t box[4] = {64, 1, 1, kQB};
-    cuuint32_t elem[4] = {1, 1, 1, 1};
-    CUresult res = encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(q), dims,
-                          strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return res == CUDA_SUCCESS ? HPC_OK : HPC_ERR_CUDA;
-}
+std::atomic<unsigned> g_prefill_attr_done{0};
 
 }  // namespace
 }  // namespace hpc
 
 using namespace hpc;
 
-namespace {
-
-// hpc_prefill_attn (window 0) and hpc_prefill_attn_win.
-hpc_status prefill_impl(const void *d_q, const void *d_k_cache, const void *d_v_cache,
-                        int32_t num_pages, const int32_t *d_block_table,
-                        int32_t max_pages_per_req, const int32_t *d_seqlens, int32_t B,
-                        int32_t Hq, int32_t Hkv, int32_t head_dim, int32_t q_len, int32_t window,
-                        int32_t sinks, float sm_scale, void *d_out, int32_t *d_flags,
-                        hpc_stream_t stream) {
+extern "C" hpc_status hpc_prefill_attn(const void *d_q, const void *d_k_cache,
+                                       const void *d_v_cache, int32_t num_pages,
+                                       const int32_t *d_block_table, int32_t max_pages_per_req,
+                                       const int32_t *d_seqlens, int32_t B, int32_t Hq,
+                                       int32_t Hkv, int32_t head_dim, int32_t q_len,
+                                       float sm_scale, void *d_out, int32_t *d_flags,
+                                       hpc_stream_t stream) {
     if (B < 0 || Hq <= 0 || Hkv <= 0 || max_pages_per_req <= 0 || q_len < 1 || num_pages <= 0)
         return HPC_ERR_ARG;
     if (head_dim != HPC_HEAD_DIM || Hq % Hkv != 0) return HPC_ERR_UNSUPPORTED;
@@ -676,19 +492,15 @@ hpc_status prefill_impl(const void *d_q, const void *d_k_cache, const void *d_v_
     a.num_pages = num_pages;
     a.n_qp = (int)n_qp;
     a.score_scale = sm_scale * 1.4426950408889634f;
-    a.window = window;
-    a.sinks = sinks;
-    const bool win = window > 0;
-    const auto fn = win ? prefill_attn_kernel<true> : prefill_attn_kernel<false>;
 
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return HPC_ERR_CUDA;
     const unsigned bit = 1u << (dev & 31);
-    if (!(g_prefill_attr_done[win].load() & bit)) {
-        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) !=
-            cudaSuccess)
+    if (!(g_prefill_attr_done.load() & bit)) {
+        if (cudaFuncSetAttribute(prefill_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kSmemBytes) != cudaSuccess)
             return HPC_ERR_CUDA;
-        g_prefill_attr_done[win].fetch_or(bit);
+        g_prefill_attr_done.fetch_or(bit);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
@@ -700,37 +512,6 @@ hpc_status prefill_impl(const void *d_q, const void *d_k_cache, const void *d_v_
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, fn, tq, tk, tv, a);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_attn_kernel, tq, tk, tv, a);
     return e == cudaSuccess ? HPC_OK : HPC_ERR_CUDA;
-}
-
-}  // namespace
-
-extern "C" hpc_status hpc_prefill_attn(const void *d_q, const void *d_k_cache,
-                                       const void *d_v_cache, int32_t num_pages,
-                                       const int32_t *d_block_table, int32_t max_pages_per_req,
-                                       const int32_t *d_seqlens, int32_t B, int32_t Hq,
-                                       int32_t Hkv, int32_t head_dim, int32_t q_len,
-                                       float sm_scale, void *d_out, int32_t *d_flags,
-                                       hpc_stream_t stream) {
-    return prefill_impl(d_q, d_k_cache, d_v_cache, num_pages, d_block_table, max_pages_per_req,
-                        d_seqlens, B, Hq, Hkv, head_dim, q_len, 0, 0, sm_scale, d_out, d_flags,
-                        stream);
-}
-
-extern "C" hpc_status hpc_prefill_attn_win(const void *d_q, const void *d_k_cache,
-                                           const void *d_v_cache, int32_t num_pages,
-                                           const int32_t *d_block_table,
-                                           int32_t max_pages_per_req, const int32_t *d_seqlens,
-                                           int32_t B, int32_t Hq, int32_t Hkv, int32_t head_dim,
-                                           int32_t q_len, int32_t window, int32_t sinks,
-                                           float sm_scale, void *d_out, int32_t *d_flags,
-                                           hpc_stream_t stream) {
-    if (window < 0 || sinks < 0 || (window == 0 && sinks != 0)) return HPC_ERR_ARG;
-    if (window >= kNoWindow || sinks >= kNoWindow || q_len >= kNoWindow)
-        return HPC_ERR_UNSUPPORTED;
-    if (window > 0 && !(sm_scale > 0.f)) return HPC_ERR_ARG;  // masked before it is scaled
-    return prefill_impl(d_q, d_k_cache, d_v_cache, num_pages, d_block_table, max_pages_per_req,
-                        d_seqlens, B, Hq, Hkv, head_dim, q_len, window, sinks, sm_scale, d_out,
-                        d_flags, stream);
 }

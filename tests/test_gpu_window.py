@@ -288,6 +288,31 @@ def test_windowed_prefill_heads(heads):
     c.check(run_prefill(c))
 
 
+@pytest.mark.parametrize("q_len,heads", [(700, 64), (520, 56), (256, 160)])
+def test_windowed_prefill_of_several_rounds(q_len, heads):
+    """More pairs of Q tiles than SMs (192, 168, 160): CTAs take several, and a
+    short last round is cut into single Q tiles.  Sampled heads and rows."""
+    c = Case("bf16", [q_len, q_len + 500], heads, heads // 8, q_len, 200, 70, seed=507).to_gpu()
+    out = run_prefill(c)
+    rows = sorted({0, 1, 127, 128, 129, 255, q_len - 1, q_len // 2} |
+                  set(range(0, q_len, 37)))
+    rows = [r for r in rows if r < q_len]
+    hs = list(range(0, heads, 7)) + [heads - 1]
+    ref = np.zeros((2, len(rows), len(hs), 128))
+    mass = np.zeros(ref.shape)
+    for r, L in enumerate(c.lens):
+        see = ow.visible(L, q_len, 200, 70)[rows]
+        for k, h in enumerate(hs):
+            # (pages that were given back come as NaN: no row sees their tokens)
+            K, V = (np.nan_to_num(ow.gather(x, c.table[r], L)[:, h // 8]) for x in (c.kf, c.vf))
+            x = np.where(see, c.qf[r, rows, h] @ K.T * c.sm, -np.inf)
+            e = np.exp(x - x.max(-1, keepdims=True))
+            w = e / e.sum(-1, keepdims=True)
+            ref[r, :, k], mass[r, :, k] = w @ V, w @ np.abs(V)
+    check_attention(out[:, rows][:, :, hs], ref, mass, "bf16")
+    assert torch.isfinite(out.float()).all()
+
+
 def test_prefill_without_a_window_is_the_plain_call():
     w = Workload("pw", 2, 4, 2, seqlens=(300, 700), seed=503, q_len=290)
     b = make_batch(w, device="cuda", poison_tail=True)
