@@ -104,8 +104,8 @@ typedef enum { HPC_KV_BF16 = 0, HPC_KV_FP8_E4M3 = 1, HPC_KV_E4M3_BLOCK = 2 } hpc
  * int32), bin_ptr and chunk_count / chunk_off, and are set by the caller.
  * B, Hkv, num_ctas (the number of bins), persistent (0 for a static map, odd
  * for a load-balanced one; hpc_decode_plan_win keeps a tag of its window and
- * whether descriptors are head pairs above bit 0), min_tiles and max_pages (the planner's arguments) are written by
- * the planners (the
+ * whether descriptors are head pairs above bit 0), min_tiles and
+ * max_pages (the planner's arguments) are written by the planners (the
  * host-side struct is updated) and read by hpc_decode_attn /
  * hpc_decode_combine, which check B and Hkv against their own arguments.
  * The attention kernel of a persistent map re-derives each CTA's first
@@ -689,7 +689,8 @@ hpc_status hpc_decode_step_win(const void *d_q, const float *d_q_scale, const vo
 /*
  * hpc_prefill_attn with a window: the request's last q_len live tokens are
  * the queries, over a paged BF16 cache.  window = 0 is hpc_prefill_attn.
- * Other arguments as there.
+ * With a window sm_scale is finite and at least FLT_MIN, and q_len is below
+ * 2^30.  Other arguments as there.
  */
 hpc_status hpc_prefill_attn_win(const void *d_q, const void *d_k_cache, const void *d_v_cache,
                                 int32_t num_pages, const int32_t *d_block_table,

@@ -51,18 +51,10 @@
 //    a descriptor is physical tile t below sink_tiles, else t + skip), so no
 //    page in between is looked up or read.  Tokens no query of the request
 //    sees are treated like those past its length: no score, a zero V row.
-//  * block-scaled form (BLK, FP8): a page brings its 4 + 4 block scales (one
-//    for 16 tokens of K, one of V) as one 32-byte bulk copy beside its tiles.
-//    A consumer warp's 16 tokens are exactly one block, so K's scale is one
-//    more factor of its score scale.  V's scale v_s enters the weights in the
-//    reference: with x a score, m is the running maximum of x + log2 v_s, p =
-//    2^(x - m) goes into the softmax's sum (fp32: its range holds any scales
-//    from 2^-100 to 2^100) and w = p v_s, which is <= 1 whatever the scales,
-//    is the f16 weight of V's codes.  A v_s below 2^-100 counts as zero.
-//  * both forms move the reference m only when a score exceeds it by more than
-//    8 (log2 units), which one vote per tile finds out; weights stay <= 2^8
-//    (f16 holds 2^15), the same softmax follows, and the common tile does
-//    without the maximum's shuffles and the rescaling factors.
+//    The windowed form moves the softmax's reference m only when a score
+//    exceeds it by more than 8 (log2 units), which one vote per tile finds
+//    out; weights stay <= 2^8, the same softmax follows, and the common tile
+//    does without the maximum's shuffles and the rescaling factors.
 //  * the kernel is launched as a programmatic dependent of the assign kernel:
 //    it sets up its barriers, prefetches the block table into L2, derives its
 //    first descriptor from the sequence lengths and starts streaming while
@@ -101,8 +93,7 @@ constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr unsigned kFullMask = 0xffffffffu;
-constexpr float kLazyLog2 = 8.f;           // windowed / block-scaled: how far a score may pass m
-constexpr float kMinVScale = 7.888609052210118e-31f;  // 2^-100
+constexpr float kLazyLog2 = 8.f;  // WIN: how far a score may pass m
 constexpr int kStateRegs = 36;  // per lane and row block: 32 accumulators, m0, m1, l0, l1
 constexpr int kMaxLast = 16;    // split units whose merge this CTA owes, held at once
 constexpr int kStageStride = kHeadDim + 4;  // floats per head row of the combiner's staging
@@ -129,7 +120,7 @@ __device__ __forceinline__ int planned_len(const AttnParams &p, int L) {
     return L;
 }
 
-template <bool FP8, int STAGES, int TPS, int NB, bool WIN = false, bool BLK = false>
+template <bool FP8, int STAGES, int TPS, int NB, bool WIN = false>
 struct AttnTraits {
     static constexpr int kConsumers = kConsumerWarps * TPS;          // consumer warps
     static constexpr int kThreads = 32 * (2 + kConsumers);           // + producer, combiner
@@ -139,13 +130,11 @@ struct AttnTraits {
     static constexpr int kStageKV = TPS * kTileBytes;               // K (or V) bytes per stage
     static constexpr int kRows = 8 * NB;                             // query rows held per stage
     static constexpr int kQBytes = kRows * kHeadDim * kElem;        // Q slot per stage
-    static constexpr int kScaleBytes = BLK ? TPS * kPageScales * 4 : 0;  // block scales per stage
     static constexpr int kState = kStateRegs * NB;                   // state floats per lane
     static constexpr int kSlotFloats = kConsumers * kState * 32;     // one hand-off slot
     // Shared memory of the layout below with `slots` hand-off slots.
     static constexpr int bytes_with(int slots) {
-        return 2 * STAGES * kStageKV + STAGES * kQBytes + STAGES * kScaleBytes +
-               STAGES * (int)sizeof(StageInfo) +
+        return 2 * STAGES * kStageKV + STAGES * kQBytes + STAGES * (int)sizeof(StageInfo) +
                slots * kSlotFloats * 4 + kRows * kStageStride * 4 +
                slots * (int)sizeof(SlotInfo) + (kMaxLast + 1) * (int)sizeof(SlotInfo) +
                (2 * STAGES + 2 * slots + 1) * 8 + 16 + 1024;
@@ -156,8 +145,7 @@ struct AttnTraits {
     static constexpr int kOffK = 0;
     static constexpr int kOffV = kOffK + STAGES * kStageKV;
     static constexpr int kOffQ = kOffV + STAGES * kStageKV;
-    static constexpr int kOffScale = kOffQ + STAGES * kQBytes;
-    static constexpr int kOffInfo = kOffScale + STAGES * kScaleBytes;
+    static constexpr int kOffInfo = kOffQ + STAGES * kQBytes;
     static constexpr int kOffComb = kOffInfo + STAGES * (int)sizeof(StageInfo);
     static constexpr int kOffStage = kOffComb + kSlots * kSlotFloats * 4;
     static constexpr int kOffSlotInfo = kOffStage + kRows * kStageStride * 4;
@@ -384,13 +372,13 @@ __device__ __forceinline__ void walk_chunk(const AttnParams &p, FlyWalk &w, int 
 // which case its last stage's copies are issued before the map is waited for
 // (the stage is released once the layout is written), so the wait overlaps
 // the stage's transfer.  Returns false after a timeout.
-template <bool FP8, int STAGES, int TPS, int NB, bool WIN = false, bool BLK = false>
+template <bool FP8, int STAGES, int TPS, int NB, bool WIN = false>
 __device__ __forceinline__ bool stream_desc(const CUtensorMap *tmap_k, const CUtensorMap *tmap_v,
                                             const AttnParams &p, uint8_t *smem, int h, int r,
                                             int tb, int te, int desc_idx, int bin,
                                             FlyWalk *walk, int bin_pos, ProducerState &ps,
                                             uint64_t policy, volatile int *abort) {
-    using Tr = AttnTraits<FP8, STAGES, TPS, NB, WIN, BLK>;
+    using Tr = AttnTraits<FP8, STAGES, TPS, NB, WIN>;
     const int lane = threadIdx.x & 31;
     StageInfo *info = reinterpret_cast<StageInfo *>(smem + Tr::kOffInfo);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Tr::kOffBar);
@@ -485,8 +473,7 @@ __device__ __forceinline__ bool stream_desc(const CUtensorMap *tmap_k, const CUt
 #pragma unroll
                     for (int g = 0; g < Tr::kRows; ++g) si.qscale[g] = qsg[g];
                 }
-                const uint32_t bytes = 2u * ns * Tr::kTileBytes + (first ? q_bytes : 0u) +
-                                       (BLK ? ns * kPageScales * 4u : 0u);
+                const uint32_t bytes = 2u * ns * Tr::kTileBytes + (first ? q_bytes : 0u);
                 if (defer || late_q) mbar_expect_tx(&full[stage], bytes);  // arrives below
                 else mbar_arrive_expect_tx(&full[stage], bytes);
 #pragma unroll
@@ -497,11 +484,6 @@ __device__ __forceinline__ bool stream_desc(const CUtensorMap *tmap_k, const CUt
                     if (FP8) {
                         tma_load_4d(sk, tmap_k, &full[stage], 0, h, 0, pg[s], policy);
                         tma_load_4d(sv, tmap_v, &full[stage], 0, h, 0, pg[s], policy);
-                        if (BLK)
-                            bulk_load(smem + Tr::kOffScale + stage * Tr::kScaleBytes +
-                                          s * kPageScales * 4,
-                                      p.kv_scale + ((size_t)pg[s] * p.Hkv + h) * kPageScales,
-                                      kPageScales * 4, &full[stage]);
                     } else {
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
@@ -549,11 +531,11 @@ __device__ __forceinline__ bool stream_desc(const CUtensorMap *tmap_k, const CUt
     return true;
 }
 
-template <bool FP8, int STAGES, int TPS, int NB, bool WIN = false, bool BLK = false>
+template <bool FP8, int STAGES, int TPS, int NB, bool WIN = false>
 __device__ __forceinline__ void attn_producer(const CUtensorMap *tmap_k, const CUtensorMap *tmap_v,
                                               const AttnParams &p, uint8_t *smem,
                                               volatile int *abort) {
-    using Tr = AttnTraits<FP8, STAGES, TPS, NB, WIN, BLK>;
+    using Tr = AttnTraits<FP8, STAGES, TPS, NB, WIN>;
     const int lane = threadIdx.x & 31;
     StageInfo *info = reinterpret_cast<StageInfo *>(smem + Tr::kOffInfo);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Tr::kOffBar);
@@ -581,9 +563,10 @@ __device__ __forceinline__ void attn_producer(const CUtensorMap *tmap_k, const C
         int streamed = 0;
         while (ok && w.te > w.tb) {
             const bool derive = streamed + (w.te - w.tb) < kWalkTiles;
-            ok = stream_desc<FP8, STAGES, TPS, NB, WIN, BLK>(tmap_k, tmap_v, p, smem, w.h, w.r, w.tb, w.te,
-                                               -1, blockIdx.x, derive ? &w : nullptr, w.k, ps,
-                                               policy, abort);
+            ok = stream_desc<FP8, STAGES, TPS, NB, WIN>(tmap_k, tmap_v, p, smem, w.h, w.r, w.tb,
+                                                        w.te, -1, blockIdx.x,
+                                                        derive ? &w : nullptr, w.k, ps, policy,
+                                                        abort);
             ++skip;
             streamed += w.te - w.tb;
             if (!derive) break;  // its end read the map
@@ -593,8 +576,9 @@ __device__ __forceinline__ void attn_producer(const CUtensorMap *tmap_k, const C
     } else if (p.fly) {
         int h, r, tb, te;
         if (first_descriptor<WIN>(p, blockIdx.x, h, r, tb, te) && te > tb) {
-            ok = stream_desc<FP8, STAGES, TPS, NB, WIN, BLK>(tmap_k, tmap_v, p, smem, h, r, tb, te, -1,
-                                               blockIdx.x, nullptr, 0, ps, policy, abort);
+            ok = stream_desc<FP8, STAGES, TPS, NB, WIN>(tmap_k, tmap_v, p, smem, h, r, tb, te, -1,
+                                                        blockIdx.x, nullptr, 0, ps, policy,
+                                                        abort);
             skip = 1;
         }
     }
@@ -611,8 +595,9 @@ __device__ __forceinline__ void attn_producer(const CUtensorMap *tmap_k, const C
         const int d_end = p.bin_ptr[bin + 1];
         for (int d = d_begin; d < d_end && ok; ++d) {
             const int4 ds = p.desc[d];
-            ok = stream_desc<FP8, STAGES, TPS, NB, WIN, BLK>(tmap_k, tmap_v, p, smem, ds.x, ds.y, ds.z, ds.w, d,
-                                               bin, nullptr, 0, ps, policy, abort);
+            ok = stream_desc<FP8, STAGES, TPS, NB, WIN>(tmap_k, tmap_v, p, smem, ds.x, ds.y, ds.z,
+                                                        ds.w, d, bin, nullptr, 0, ps, policy,
+                                                        abort);
         }
         if (!dynamic) break;
         grab = __shfl_sync(kFullMask, grab, 0);
@@ -799,10 +784,10 @@ __device__ __forceinline__ int stage_col(int dim) { return dim ^ (((dim >> 4) & 
 
 // Merges the consumers' states of each finished descriptor and writes the
 // result; counts chunks of split units.  Returns false after a timeout.
-template <bool FP8, int STAGES, int TPS, int NB, bool WIN = false, bool BLK = false>
+template <bool FP8, int STAGES, int TPS, int NB, bool WIN = false>
 __device__ __forceinline__ bool attn_combiner(const AttnParams &p, uint8_t *smem,
                                               volatile int *abort) {
-    using Tr = AttnTraits<FP8, STAGES, TPS, NB, WIN, BLK>;
+    using Tr = AttnTraits<FP8, STAGES, TPS, NB, WIN>;
     constexpr int NC = Tr::kConsumers;
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const float *comb = reinterpret_cast<const float *>(smem + Tr::kOffComb);
@@ -931,10 +916,11 @@ __device__ __forceinline__ bool attn_combiner(const AttnParams &p, uint8_t *smem
 }
 
 // ------------------------------------------------------------------ consumer
-template <bool FP8, int STAGES, int TPS, int NB, bool WIN = false, bool BLK = false>
+template <bool FP8, int STAGES, int TPS, int NB, bool WIN = false>
 __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem,
                                               volatile int *abort) {
-    using Tr = AttnTraits<FP8, STAGES, TPS, NB, WIN, BLK>;
+    using Tr = AttnTraits<FP8, STAGES, TPS, NB, WIN>;
+    static_assert(!(FP8 && WIN), "8-bit caches with a window have a kernel of their own");
     const int lane = threadIdx.x & 31, cw = (threadIdx.x >> 5) - 2;
     const int g = lane >> 2, t4 = lane & 3;
     const int slot = cw >> 2;  // which tile of the stage this warp works on
@@ -954,10 +940,9 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
     const int tok_k = 16 * sub + (lane & 7) + (mi & 1) * 8;  // K: matrices 1, 3 = rows 8..15
     const int tok_v = 16 * sub + (lane & 7) + (mi >> 1) * 8;  // V^T: matrices 2, 3 = toks 8..15
 
-    constexpr bool kLazy = WIN || BLK;  // see the head of the file
     // m of a row that has seen no token (finite where d = score - m is formed
     // before it is looked at: any score then passes it)
-    constexpr float kNoScore = kLazy ? -3e38f : kNegInf;
+    constexpr float kNoScore = WIN ? -3e38f : kNegInf;
     // Row block nb holds query rows 8 nb .. 8 nb + 7; this lane owns columns
     // (rows) 8 nb + 2 t4 + c, c = 0, 1 of every block.
     float o[NB][8][4];
@@ -1030,26 +1015,14 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
             // a token below it that is no sink is dead, like one past L
             const int lo0 = WIN ? L - p.q_len + 1 - p.window : 0;
             auto live = [&](int t) { return t < L && (!WIN || t >= lo0 || t < p.sinks); };
-            // a slice without a live token changes nothing (and its block may
-            // hold anything, its scales among it)
             // every row sees the whole slice (the last query's window begins last,
             // the first query's ends first): no masks
-            const bool full = kLazy && tok0 + 15 < L - p.q_len + 1 &&
+            const bool full = WIN && tok0 + 15 < L - p.q_len + 1 &&
                               (tok0 + p.window >= L || tok0 + 15 < p.sinks);
-            const bool any_live = !(WIN || BLK) ||
-                                  (tok0 < L && (!WIN || tok0 + 15 >= lo0 || tok0 < p.sinks));
+            // a slice without a live token changes nothing
+            const bool any_live = !WIN || (tok0 < L && (tok0 + 15 >= lo0 || tok0 < p.sinks));
             if (slot < ntiles && any_live) {
                 const uint32_t sK = sK0 + stage * Tr::kStageKV, sV = sV0 + stage * Tr::kStageKV;
-                // BLK: the block's K scale, its V scale and log2 of it
-                float kf = 1.f, vf = 1.f, lv = 0.f;
-                if (BLK) {
-                    const float *bs = reinterpret_cast<const float *>(
-                        smem + Tr::kOffScale + stage * Tr::kScaleBytes + slot * kPageScales * 4);
-                    kf = bs[sub];
-                    vf = bs[kPageScales / 2 + sub];
-                    lv = lg2(fmaxf(vf, kMinVScale));
-                    vf = vf < kMinVScale ? 0.f : vf;
-                }
 
                 // ---- S^T = K . Q^T for this warp's 16 tokens x 8 NB rows
                 float s4[NB][4];
@@ -1103,13 +1076,7 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
                     for (int q = 0; q < 4; ++q) {
                         const int tok = 16 * sub + 2 * t4 + (q & 1) + (q >> 1) * 8;
                         Rv[q] = lds128(sV + tok * 128 + ((g ^ (tok & 7)) << 4));
-                        if (!kLazy && tile * kTile + tok >= L) Rv[q] = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    if (kLazy && !full) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (!live(tok0 + 2 * t4 + (q & 1) + (q >> 1) * 8))
-                                Rv[q] = make_uint4(0u, 0u, 0u, 0u);
+                        if (tile * kTile + tok >= L) Rv[q] = make_uint4(0u, 0u, 0u, 0u);
                     }
                     const uint32_t wA[4] = {Rv[0].x, Rv[0].y, Rv[0].z, Rv[0].w};
                     const uint32_t wB[4] = {Rv[1].x, Rv[1].y, Rv[1].z, Rv[1].w};
@@ -1127,14 +1094,14 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
                 // (WIN: or before its window, unless it is a sink)
                 const int ta = tok0 + g, tb_ = tok0 + g + 8;
                 uint32_t b0[NB], b1[NB];
-                if constexpr (kLazy) {
+                if constexpr (WIN) {
                     // d = score - m, -inf where the row does not see the token
                     float d[NB][4], top = kNegInf;
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            d[nb][e] = fmaf(s4[nb][e], sc[nb][e & 1] * kf, -m[nb][e & 1]);
+                            d[nb][e] = fmaf(s4[nb][e], sc[nb][e & 1], -m[nb][e & 1]);
                     if (!full) {
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
@@ -1149,13 +1116,13 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
                     for (int nb = 0; nb < NB; ++nb)
                         top = fmaxf(fmaxf(top, fmaxf(d[nb][0], d[nb][1])),
                                     fmaxf(d[nb][2], d[nb][3]));
-                    if (__any_sync(kFullMask, top > kLazyLog2 - lv)) {
+                    if (__any_sync(kFullMask, top > kLazyLog2)) {
                         float mx[NB][2];
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e)  // back to the scores
-                                if (d[nb][e] != kNegInf) d[nb][e] = s4[nb][e] * (sc[nb][e & 1] * kf);
+                                if (d[nb][e] != kNegInf) d[nb][e] = s4[nb][e] * sc[nb][e & 1];
                             mx[nb][0] = fmaxf(d[nb][0], d[nb][2]);
                             mx[nb][1] = fmaxf(d[nb][1], d[nb][3]);
                         }
@@ -1170,7 +1137,7 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
                         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                             for (int c = 0; c < 2; ++c) {
-                                const float mn = fmaxf(m[nb][c], mx[nb][c] + lv);
+                                const float mn = fmaxf(m[nb][c], mx[nb][c]);
                                 const float al = ex2(m[nb][c] - mn);
                                 m[nb][c] = mn;
                                 l[nb][c] *= al;
@@ -1188,27 +1155,10 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
                         float w[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) w[e] = ex2(d[nb][e]);
-                        if (BLK) {
-                            l[nb][0] += w[0] + w[2];
-                            l[nb][1] += w[1] + w[3];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) w[e] *= vf;
-                        }
-                        uint32_t pk01, pk23;
-                        if (FP8) {
-                            pk01 = pack_f16x2(w[0], w[1]);
-                            pk23 = pack_f16x2(w[2], w[3]);
-                            if (!BLK) {
-                                const float2 r01 = f16x2_to_f32x2(pk01), r23 = f16x2_to_f32x2(pk23);
-                                l[nb][0] += r01.x + r23.x;
-                                l[nb][1] += r01.y + r23.y;
-                            }
-                        } else {
-                            pk01 = pack_bf16x2(w[0], w[1]);
-                            pk23 = pack_bf16x2(w[2], w[3]);
-                            l[nb][0] += bf16lo_to_f32(pk01) + bf16lo_to_f32(pk23);
-                            l[nb][1] += bf16hi_to_f32(pk01) + bf16hi_to_f32(pk23);
-                        }
+                        const uint32_t pk01 = pack_bf16x2(w[0], w[1]);
+                        const uint32_t pk23 = pack_bf16x2(w[2], w[3]);
+                        l[nb][0] += bf16lo_to_f32(pk01) + bf16lo_to_f32(pk23);
+                        l[nb][1] += bf16hi_to_f32(pk01) + bf16hi_to_f32(pk23);
                         // P^T fragments (k = token, n = row): transpose the 8x8 halves
                         b0[nb] = movmatrix_trans(pk01);
                         b1[nb] = movmatrix_trans(pk23);
@@ -1286,7 +1236,7 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
                 } else {
                     const int tv = tok0 + 2 * t4;  // tokens of a0/a1 halves; +8 for a2/a3
                     uint32_t mk01 = 0xffffffffu, mk23 = 0xffffffffu;
-                    if (!kLazy || !full) {
+                    if (!WIN || !full) {
                         mk01 = (live(tv) ? 0x0000ffffu : 0u) | (live(tv + 1) ? 0xffff0000u : 0u);
                         mk23 = (live(tv + 8) ? 0x0000ffffu : 0u) | (live(tv + 9) ? 0xffff0000u : 0u);
                     }
@@ -1312,28 +1262,6 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
             const int k = handed % Tr::kSlots;
             if (!warp_wait(&slot_empty[k], ((handed / Tr::kSlots) & 1u) ^ 1u, abort))
                 return false;
-            if (BLK && (flags & kLast)) {
-                // the references of two warps may lie as far apart as their V
-                // scales, their log-sum-exps only as far as their scores: hand
-                // over the normalised O with the latter (l 1, in one lane of
-                // the eight that share a row)
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        float z = l[nb][c];
-#pragma unroll
-                        for (int o_ = 4; o_ <= 16; o_ <<= 1) z += __shfl_xor_sync(kFullMask, z, o_);
-                        const float f = z > 0.f ? __fdividef(1.f, z) : 0.f;
-                        m[nb][c] = z > 0.f ? m[nb][c] + lg2(z) : kNegInf;
-                        l[nb][c] = z > 0.f && g == 0 ? 1.f : 0.f;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            o[nb][j][c] *= f;
-                            o[nb][j][c + 2] *= f;
-                        }
-                    }
-            }
             if (flags & kLast) {  // lane-major: 9 NB float4 per lane, conflict-free
                 float4 *dst = reinterpret_cast<float4 *>(
                     comb + ((k * Tr::kConsumers + cw) * 32 + lane) * Tr::kState);
@@ -1357,11 +1285,11 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
 }
 
 // ------------------------------------------------------------------ kernel
-template <bool FP8, int STAGES, int TPS, int NB, bool WIN = false, bool BLK = false>
-__global__ void __launch_bounds__(AttnTraits<FP8, STAGES, TPS, NB, WIN, BLK>::kThreads, 1)
+template <bool FP8, int STAGES, int TPS, int NB, bool WIN = false>
+__global__ void __launch_bounds__(AttnTraits<FP8, STAGES, TPS, NB, WIN>::kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const __grid_constant__ CUtensorMap tmap_v, const AttnParams p) {
-    using Tr = AttnTraits<FP8, STAGES, TPS, NB, WIN, BLK>;
+    using Tr = AttnTraits<FP8, STAGES, TPS, NB, WIN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Tr::kOffBar);
@@ -1404,7 +1332,7 @@ __global__ void __launch_bounds__(AttnTraits<FP8, STAGES, TPS, NB, WIN, BLK>::kT
     __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) {
-        attn_producer<FP8, STAGES, TPS, NB, WIN, BLK>(&tmap_k, &tmap_v, p, smem, abort);
+        attn_producer<FP8, STAGES, TPS, NB, WIN>(&tmap_k, &tmap_v, p, smem, abort);
         return;
     }
     // Every global write of this grid (outputs, partials, counters) comes
@@ -1420,8 +1348,8 @@ __global__ void __launch_bounds__(AttnTraits<FP8, STAGES, TPS, NB, WIN, BLK>::kT
             for (int i = lane; i < row_vec; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
         }
     }
-    bool ok = warp == 1 ? attn_combiner<FP8, STAGES, TPS, NB, WIN, BLK>(p, smem, abort)
-                        : attn_consumer<FP8, STAGES, TPS, NB, WIN, BLK>(p, smem, abort);
+    bool ok = warp == 1 ? attn_combiner<FP8, STAGES, TPS, NB, WIN>(p, smem, abort)
+                        : attn_consumer<FP8, STAGES, TPS, NB, WIN>(p, smem, abort);
     if (!ok) {
         grid_dependency_wait();  // meta[3] is written by the assign kernel
         if (lane == 0) atomicOr(p.meta + 3, (int)HPC_FLAG_TIMEOUT);
@@ -1472,11 +1400,11 @@ __global__ void __launch_bounds__(AttnTraits<FP8, STAGES, TPS, NB, WIN, BLK>::kT
 // Launches one instantiation as a programmatic dependent of the previous
 // kernel in the stream (the assign kernel): its prologue overlaps that
 // kernel's tail.
-template <bool FP8, int STAGES, int TPS, int NB, bool WIN, bool BLK>
+template <bool FP8, int STAGES, int TPS, int NB, bool WIN>
 struct AttnVariant {
-    using Tr = AttnTraits<FP8, STAGES, TPS, NB, WIN, BLK>;
+    using Tr = AttnTraits<FP8, STAGES, TPS, NB, WIN>;
     static AttnConfig config() {
-        return {reinterpret_cast<const void *>(&attn_kernel<FP8, STAGES, TPS, NB, WIN, BLK>),
+        return {reinterpret_cast<const void *>(&attn_kernel<FP8, STAGES, TPS, NB, WIN>),
                 Tr::kSmemBytes, Tr::kThreads};
     }
     static cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const AttnParams &p,
@@ -1491,7 +1419,7 @@ struct AttnVariant {
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, attn_kernel<FP8, STAGES, TPS, NB, WIN, BLK>, tk, tv, p);
+        return cudaLaunchKernelEx(&cfg, attn_kernel<FP8, STAGES, TPS, NB, WIN>, tk, tv, p);
     }
 };
 

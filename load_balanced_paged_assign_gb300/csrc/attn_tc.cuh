@@ -74,6 +74,12 @@ constexpr int kTcThreads = 32 * 16;
 constexpr int kTcGroup = 128;           // threads of a softmax or join warpgroup
 constexpr float kTcTop = 3.f;           // log2 of the largest weight when the reference moves
 constexpr float kTcMax = 14.5f;         // log2 of the largest weight ever (E5M2 holds 1.75 2^15)
+// A V scale below 2^-100 counts as zero.  In the reference none counts as less
+// than 2^-88: the softmax's sum, in units of up to 2^(14.5 + 88), must hold all
+// tokens of a request (2^25), and a weight at the reference's top (2^3) then
+// still stands 2^10 above the three parts' last step at a scale of 2^-100.
+constexpr float kMinVScale = 7.888609052210118e-31f;  // 2^-100
+constexpr float kMinVRef = 3.2311742677852644e-27f;   // 2^-88
 constexpr int kTcOrds = 4;              // descriptors whose join data may be alive at once
 constexpr int kTcPubs = 8 + 2;          // arrivals that publish one: the groups' warps, two products
 
@@ -729,7 +735,7 @@ __device__ __forceinline__ bool tc_softmax(const AttnParams &p, uint8_t *smem, u
                               (tid >> 6) * kPageScales + ((tid & 63) / kScaleBlock);
             kf = live ? bs[0] : 0.f;
             vf = live ? bs[kPageScales / 2] : 0.f;
-            lv = lg2(fmaxf(vf, kMinVScale));
+            lv = lg2(fmaxf(vf, kMinVRef));
             vf = vf < kMinVScale ? 0.f : vf;
         }
         // every row sees the warp's 32 tokens: no masks

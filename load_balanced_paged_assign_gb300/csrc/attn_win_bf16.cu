@@ -4,8 +4,8 @@
 namespace hpc {
 
 // The plain form's pipeline shapes: one tile per stage, four stages.
-using One = AttnVariant<false, 4, 1, 1, true, false>;  // up to 8 query rows per KV head
-using Two = AttnVariant<false, 4, 1, 2, true, false>;  // up to 16
+using One = AttnVariant<false, 4, 1, 1, true>;  // up to 8 query rows per KV head
+using Two = AttnVariant<false, 4, 1, 2, true>;  // up to 16
 
 AttnConfig attn_config_win_bf16(int nb) { return nb == 2 ? Two::config() : One::config(); }
 

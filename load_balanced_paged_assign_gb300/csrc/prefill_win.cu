@@ -32,6 +32,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 
 #include "internal.h"
@@ -663,8 +664,9 @@ extern "C" hpc_status hpc_prefill_attn_win(const void *d_q, const void *d_k_cach
     if (B < 0 || Hq <= 0 || Hkv <= 0 || max_pages_per_req <= 0 || q_len < 1 || num_pages <= 0)
         return HPC_ERR_ARG;
     if (head_dim != HPC_HEAD_DIM || Hq % Hkv != 0) return HPC_ERR_UNSUPPORTED;
-    // scores are masked before they are scaled: the scale may not turn -inf round
-    if (!std::isfinite(sm_scale) || !(sm_scale > 0.f)) return HPC_ERR_ARG;
+    // scores are masked before they are scaled: the scale may not turn -inf
+    // round, nor be flushed to zero
+    if (!std::isfinite(sm_scale) || !(sm_scale >= FLT_MIN)) return HPC_ERR_ARG;
     if (B == 0) return HPC_OK;
     if (!d_q || !d_k_cache || !d_v_cache || !d_block_table || !d_seqlens || !d_out)
         return HPC_ERR_ARG;

@@ -119,6 +119,14 @@ def test_prefill_refusals():
     assert call(max_pages=1 << 24) == UNS
 
 
+def test_prefill_refuses_a_scale_that_is_flushed_to_zero():
+    def call(sm):
+        return hd.lib().hpc_prefill_attn_win(FAKE, FAKE, FAKE, 100, FAKE, 8, FAKE, 0, 8, 2, 128,
+                                             300, 128, 4, sm, FAKE, None, None)
+
+    assert call(2.0 ** -127) == E.HPC_ERR_ARG and call(2.0 ** -126) == E.HPC_OK
+
+
 def test_write_refusals():
     P = E.hpc_rope_norm_params
 

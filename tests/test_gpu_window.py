@@ -75,6 +75,51 @@ def test_block_scales_of_any_size():
     assert not got.float().abs().sum()
 
 
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -126, 2.0 ** -100])
+def test_tiny_v_scales_over_many_tokens(scale):
+    """In units of a V scale of 2^-100 the softmax's sum over 24,000 tokens whose
+    weights stand 2^11.2 above the first ones' (the reference stays where those
+    put it) would pass 2^128: 2^(100 + 3 + 11.2) * 12,000 for each half."""
+    c = Case("block", [24000], 8, 1, 1, 0, 0, seed=42, poison=False)
+    rows = c.table[0]
+    c.k.view(torch.uint8).zero_()
+    c.k.view(torch.uint8)[torch.from_numpy(rows[4:]), :, :, 0] = 0x38  # 1.0 from token 256 on
+    c.q.view(torch.uint8).zero_()
+    c.q.view(torch.uint8)[..., 0] = 0x38
+    c.qs.fill_(11.2 * np.log(2.0) / c.sm)
+    s = c.scale.numpy()
+    s[:, :, 0] = 1.0
+    s[:, :, 1] = scale
+    c.qf = c.q.float().double().numpy() * c.qs.double().numpy()[..., None]
+    from oracle import block_cache as bc
+    c.kf, c.vf = (bc.values(x.view(torch.uint8).numpy(), s, i) for i, x in enumerate((c.k, c.v)))
+    got, _ = c.to_gpu().step(ctas=1)
+    if scale < 2.0 ** -100:  # counts as zero
+        assert not got.float().abs().sum()
+        return
+    ref, mass = c.reference()
+    # scaled up by 2^90 (exactly), where the bound's absolute parts mean nothing
+    up = 2.0 ** 90
+    check_attention(got.double() * up, ref * up, mass * up, "block")
+
+
+def test_static_map_of_an_odd_number_of_heads():
+    """Without a window and without head pairs a map of equal splits serves too."""
+    c = Case("block", [300, 1, 0, 700], 6, 3, 1, 0, 0, seed=43).to_gpu()
+    ws = hd.Workspace(4, 6, 3, num_splits=5, kv_dtype=DTYPE["block"])
+    hd.hpc_decode_plan_static(c.sl, 3, c.bt.shape[1], 5, ws.tmap)
+    out = torch.full((4, 1, 6, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    args = (c.q, c.qs, c.k, c.v, c.ks, c.vs, c.scale, c.bt, c.sl, 6, 3, 1, 0, 0, c.sm, ws.tmap,
+            ws.part_o, ws.part_lse)
+    hd.hpc_decode_attn_win(*args, out, ws.unit_done)
+    c.check(out)
+    two = torch.full_like(out, float("nan"))
+    hd.hpc_decode_attn_win(*args)
+    hd.hpc_decode_combine_mq(ws.part_o, ws.part_lse, ws.tmap, 4, 6, 3, 1, two)
+    c.check(two)
+    assert not int(torch.count_nonzero(ws.unit_done))
+
+
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("n", [1, 2])
 def test_without_a_window_it_is_the_plain_step(kv, n):
