@@ -193,16 +193,19 @@ def _bad(fn: str, name: str, t, dtype, dev: int):
 
 
 def _dense(fn: str, dev: int, names: str, dtype, *tensors):
-    """Checks that each tensor (or None) is a row-major array of `dtype` on the device
-    `dev`, as the pointers handed to the library are taken to be."""
+    """Raises for the first tensor (or None) that is no row-major array of `dtype` on the
+    device `dev`, as the pointers handed to the library are taken to be."""
     for i, t in enumerate(tensors):
-        if t is not None and (t.dtype is not dtype or not t.is_contiguous() or
-                              t.get_device() != dev):
+        if t is not None and not _is_dense(t, dtype, dev):
             _bad(fn, names.split()[i], t, dtype, dev)
 
 
+def _is_dense(t, dtype, dev: int) -> bool:
+    return t.dtype is dtype and t.is_contiguous() and t.get_device() == dev
+
+
 def _shape(fn: str, name: str, t, want: tuple):
-    if tuple(t.shape) != want:
+    if t.shape != want:
         raise ValueError(f"{fn}: {name} is {tuple(t.shape)}, not {want}")
 
 
@@ -214,7 +217,7 @@ def _current_device() -> int:
     global _HAS_CUDA
     if _HAS_CUDA is None:
         _HAS_CUDA = torch.cuda.is_available()
-    return torch.cuda.current_device() if _HAS_CUDA else -1
+    return torch._C._cuda_getDevice() if _HAS_CUDA else -1
 
 
 def _raw_stream(dev: int, stream):
@@ -531,39 +534,52 @@ def hpc_decode_plan_win(seqlens, Hkv, max_pages_per_req, num_ctas, min_tiles_per
         _raw_stream(dev, stream)))
 
 
-def _win_args(fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, Hq, Hkv, q_len,
-              part_o, part_lse, out, unit_done):
+def _win_args(fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, B, Hq, Hkv, q_len,
+              part_o, part_lse, out, unit_done, cap_desc):
     """The checks of the windowed decode calls; returns (KV dtype, device)."""
-    block = kv_scale is not None
+    block, dev, i32, f32 = kv_scale is not None, _current_device(), torch.int32, torch.float32
     kv = torch.float8_e4m3fn if block else k_cache.dtype
-    B, dev = seqlens.numel(), _current_device()
-    _dense(fn, dev, "q k_cache v_cache", kv, q, k_cache, v_cache)
-    _dense(fn, dev, "q_scale kv_scale part_o part_lse", torch.float32, q_scale, kv_scale, part_o,
-           part_lse)
-    _dense(fn, dev, "block_table seqlens unit_done", torch.int32, block_table, seqlens, unit_done)
-    _dense(fn, dev, "out", torch.bfloat16, out)
-    pages, rows = int(k_cache.shape[0]), B * int(q_len) * int(Hq)
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _shape(fn, name, t, (pages, PAGE_SIZE, int(Hkv), HEAD_DIM))
+    # (the calls are short enough for the host to bound them: one expression,
+    # and the reason is looked for only where it does not hold)
+    if not (q.dtype is kv and k_cache.dtype is kv and v_cache.dtype is kv
+            and block_table.dtype is i32 and seqlens.dtype is i32
+            and part_o.dtype is f32 and part_lse.dtype is f32
+            and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and block_table.is_contiguous() and seqlens.is_contiguous()
+            and part_o.is_contiguous() and part_lse.is_contiguous()
+            and dev == q.get_device() == k_cache.get_device() == v_cache.get_device()
+            == block_table.get_device() == seqlens.get_device() == part_o.get_device()
+            == part_lse.get_device()
+            and (q_scale is None or _is_dense(q_scale, f32, dev))
+            and (kv_scale is None or _is_dense(kv_scale, f32, dev))
+            and (unit_done is None or _is_dense(unit_done, i32, dev))
+            and (out is None or _is_dense(out, torch.bfloat16, dev))):
+        _dense(fn, dev, "q k_cache v_cache", kv, q, k_cache, v_cache)
+        _dense(fn, dev, "q_scale kv_scale part_o part_lse", f32, q_scale, kv_scale, part_o,
+               part_lse)
+        _dense(fn, dev, "block_table seqlens unit_done", i32, block_table, seqlens, unit_done)
+        _dense(fn, dev, "out", torch.bfloat16, out)
+    pages, rows = k_cache.shape[0], B * q_len * Hq
+    want = (pages, PAGE_SIZE, Hkv, HEAD_DIM)
+    if k_cache.shape != want or v_cache.shape != want:
+        _shape(fn, "k_cache", k_cache, want)
+        _shape(fn, "v_cache", v_cache, want)
     if block:
-        _shape(fn, "kv_scale", kv_scale, (pages, int(Hkv), 2, PAGE_SIZE // SCALE_BLOCK))
+        _shape(fn, "kv_scale", kv_scale, (pages, Hkv, 2, PAGE_SIZE // SCALE_BLOCK))
     if block_table.dim() != 2 or block_table.shape[0] < B:
         raise ValueError(f"{fn}: block_table has not a row for each of the {B} requests")
     if q.numel() != rows * HEAD_DIM or (out is not None and out.numel() < rows * HEAD_DIM):
         raise ValueError(f"{fn}: q or out does not hold {B} x {q_len} x {Hq} rows")
     if q_scale is not None and q_scale.numel() != rows:
         raise ValueError(f"{fn}: q_scale does not hold {B} x {q_len} x {Hq} scales")
-    return HPC_KV_E4M3_BLOCK if block else kv_dtype_of(k_cache), dev
-
-
-def _split_args(fn, tmap, part_o, part_lse, unit_done, B, Hq, Hkv, q_len):
-    """Room in the split buffer and the counters for what the map may hold."""
-    rows = tmap.cap_desc * int(q_len) * (int(Hq) // max(int(Hkv), 1))
+    # room in the split buffer and the counters for what the map may hold
+    rows = cap_desc * q_len * (Hq // max(Hkv, 1))
     if part_o.numel() < rows * HEAD_DIM or part_lse.numel() < rows:
-        raise ValueError(f"{fn}: part_o or part_lse is smaller than the map's {tmap.cap_desc} "
+        raise ValueError(f"{fn}: part_o or part_lse is smaller than the map's {cap_desc} "
                          f"descriptors need")
-    if unit_done is not None and unit_done.numel() < B * int(Hkv):
+    if unit_done is not None and unit_done.numel() < B * Hkv:
         raise ValueError(f"{fn}: unit_done holds fewer than {B} x {Hkv} counters")
+    return HPC_KV_E4M3_BLOCK if block else kv_dtype_of(k_cache), dev
 
 
 def hpc_decode_attn_win(q, q_scale, k_cache, v_cache, k_scale, v_scale, kv_scale, block_table,
@@ -573,16 +589,18 @@ def hpc_decode_attn_win(q, q_scale, k_cache, v_cache, k_scale, v_scale, kv_scale
     hpc_decode_plan_win.  kv_scale: the block scales [num_pages, Hkv, 2, 4] of a
     block-scaled cache, else None.  out and unit_done given: combine fused in;
     both None: partials only."""
-    fn, B = "hpc_decode_attn_win", int(seqlens.numel())
-    dtype, dev = _win_args(fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, Hq,
-                           Hkv, q_len, part_o, part_lse, out, unit_done)
-    _split_args(fn, tmap, part_o, part_lse, unit_done, B, Hq, Hkv, q_len)
-    _check(fn, lib().hpc_decode_attn_win(
-        _adr(q), _adr(q_scale), _adr(k_cache), _adr(v_cache), int(k_cache.shape[0]),
-        float(k_scale), float(v_scale), _adr(kv_scale), dtype, _adr(block_table),
-        int(block_table.shape[1]), _adr(seqlens), B, int(Hq), int(Hkv), HEAD_DIM, int(q_len),
-        int(window), int(sinks), float(sm_scale), ctypes.byref(tmap.c), _adr(part_o),
-        _adr(part_lse), _adr(unit_done), _adr(out), _raw_stream(dev, stream)))
+    fn = "hpc_decode_attn_win"
+    B, Hq, Hkv, q_len = seqlens.numel(), int(Hq), int(Hkv), int(q_len)
+    dtype, dev = _win_args(fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, B, Hq,
+                           Hkv, q_len, part_o, part_lse, out, unit_done, tmap.cap_desc)
+    status = lib().hpc_decode_attn_win(
+        q.data_ptr(), _adr(q_scale), k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0],
+        float(k_scale), float(v_scale), _adr(kv_scale), dtype, block_table.data_ptr(),
+        block_table.shape[1], seqlens.data_ptr(), B, Hq, Hkv, HEAD_DIM, q_len, int(window),
+        int(sinks), float(sm_scale), ctypes.byref(tmap.c), part_o.data_ptr(), part_lse.data_ptr(),
+        _adr(unit_done), _adr(out), _raw_stream(dev, stream))
+    if status != HPC_OK:
+        _check(fn, status)
 
 
 def hpc_decode_step_win(q, q_scale, k_cache, v_cache, k_scale, v_scale, kv_scale, block_table,
@@ -591,37 +609,50 @@ def hpc_decode_step_win(q, q_scale, k_cache, v_cache, k_scale, v_scale, kv_scale
                         stream=None):
     """hpc_decode_plan_win and hpc_decode_attn_win in one call (unit_done None:
     with the separate combine kernel)."""
-    fn, B = "hpc_decode_step_win", int(seqlens.numel())
-    dtype, dev = _win_args(fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, Hq,
-                           Hkv, q_len, part_o, part_lse, out, unit_done)
-    _split_args(fn, tmap, part_o, part_lse, unit_done, B, Hq, Hkv, q_len)
-    _check(fn, lib().hpc_decode_step_win(
-        _adr(q), _adr(q_scale), _adr(k_cache), _adr(v_cache), int(k_cache.shape[0]),
-        float(k_scale), float(v_scale), _adr(kv_scale), dtype, _adr(block_table),
-        int(block_table.shape[1]), _adr(seqlens), B, int(Hq), int(Hkv), HEAD_DIM, int(q_len),
-        int(window), int(sinks), float(sm_scale), int(num_ctas), int(min_tiles_per_cta),
-        ctypes.byref(tmap.c), _adr(part_o), _adr(part_lse), _adr(unit_done), _adr(out),
-        _raw_stream(dev, stream)))
+    fn = "hpc_decode_step_win"
+    B, Hq, Hkv, q_len = seqlens.numel(), int(Hq), int(Hkv), int(q_len)
+    dtype, dev = _win_args(fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, B, Hq,
+                           Hkv, q_len, part_o, part_lse, out, unit_done, tmap.cap_desc)
+    status = lib().hpc_decode_step_win(
+        q.data_ptr(), _adr(q_scale), k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0],
+        float(k_scale), float(v_scale), _adr(kv_scale), dtype, block_table.data_ptr(),
+        block_table.shape[1], seqlens.data_ptr(), B, Hq, Hkv, HEAD_DIM, q_len, int(window),
+        int(sinks), float(sm_scale), int(num_ctas), int(min_tiles_per_cta), ctypes.byref(tmap.c),
+        part_o.data_ptr(), part_lse.data_ptr(), _adr(unit_done), _adr(out),
+        _raw_stream(dev, stream))
+    if status != HPC_OK:
+        _check(fn, status)
 
 
 def hpc_prefill_attn_win(q, k_cache, v_cache, block_table, seqlens, Hq, Hkv, q_len, window, sinks,
                          sm_scale, out, flags=None, stream=None):
     """hpc_prefill_attn with a window and sinks (window = 0: plain causal)."""
-    fn, B, bf16, i32 = "hpc_prefill_attn_win", int(seqlens.numel()), torch.bfloat16, torch.int32
-    dev = _current_device()
-    _dense(fn, dev, "q k_cache v_cache out", bf16, q, k_cache, v_cache, out)
-    _dense(fn, dev, "block_table seqlens flags", i32, block_table, seqlens, flags)
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _shape(fn, name, t, (int(k_cache.shape[0]), PAGE_SIZE, int(Hkv), HEAD_DIM))
-    n = B * int(q_len) * int(Hq) * HEAD_DIM
+    fn, bf16, i32, dev = "hpc_prefill_attn_win", torch.bfloat16, torch.int32, _current_device()
+    B, Hq, Hkv, q_len = seqlens.numel(), int(Hq), int(Hkv), int(q_len)
+    if not (q.dtype is bf16 and k_cache.dtype is bf16 and v_cache.dtype is bf16
+            and out.dtype is bf16 and block_table.dtype is i32 and seqlens.dtype is i32
+            and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and out.is_contiguous() and block_table.is_contiguous() and seqlens.is_contiguous()
+            and dev == q.get_device() == k_cache.get_device() == v_cache.get_device()
+            == out.get_device() == block_table.get_device() == seqlens.get_device()
+            and (flags is None or _is_dense(flags, i32, dev))):
+        _dense(fn, dev, "q k_cache v_cache out", bf16, q, k_cache, v_cache, out)
+        _dense(fn, dev, "block_table seqlens flags", i32, block_table, seqlens, flags)
+    want = (k_cache.shape[0], PAGE_SIZE, Hkv, HEAD_DIM)
+    if k_cache.shape != want or v_cache.shape != want:
+        _shape(fn, "k_cache", k_cache, want)
+        _shape(fn, "v_cache", v_cache, want)
+    n = B * q_len * Hq * HEAD_DIM
     if block_table.dim() != 2 or block_table.shape[0] < B:
         raise ValueError(f"{fn}: block_table has not a row for each of the {B} requests")
     if q.numel() != n or out.numel() < n:
         raise ValueError(f"{fn}: q or out does not hold {B} x {q_len} x {Hq} rows")
-    _check(fn, lib().hpc_prefill_attn_win(
-        _adr(q), _adr(k_cache), _adr(v_cache), int(k_cache.shape[0]), _adr(block_table),
-        int(block_table.shape[1]), _adr(seqlens), B, int(Hq), int(Hkv), HEAD_DIM, int(q_len),
-        int(window), int(sinks), float(sm_scale), _adr(out), _adr(flags), _raw_stream(dev, stream)))
+    status = lib().hpc_prefill_attn_win(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), want[0], block_table.data_ptr(),
+        block_table.shape[1], seqlens.data_ptr(), B, Hq, Hkv, HEAD_DIM, q_len, int(window),
+        int(sinks), float(sm_scale), out.data_ptr(), _adr(flags), _raw_stream(dev, stream))
+    if status != HPC_OK:
+        _check(fn, status)
 
 
 def hpc_rope_norm_block(qkv, q_norm_w, k_norm_w, positions, token_req, Hq, Hkv, block_table,
@@ -631,22 +662,38 @@ def hpc_rope_norm_block(qkv, q_norm_w, k_norm_w, positions, token_req, Hq, Hkv, 
     """hpc_rope_norm writing into a block-scaled cache (E4M3 k_cache, v_cache and
     kv_scale [num_pages, Hkv, 2, 4]).  q_scale_out given: E4M3 queries, else BF16."""
     fn, f32, i32, e4m3 = "hpc_rope_norm_block", torch.float32, torch.int32, torch.float8_e4m3fn
-    N, pages = int(positions.numel()), int(k_cache.shape[0])
-    dev = _current_device()
-    _dense(fn, dev, "q_norm_w k_norm_w", torch.bfloat16, q_norm_w, k_norm_w)
-    _dense(fn, dev, "positions token_req block_table flags", i32, positions, token_req,
-           block_table, flags)
-    _dense(fn, dev, "k_cache v_cache", e4m3, k_cache, v_cache)
-    _dense(fn, dev, "kv_scale q_scale_out", f32, kv_scale, q_scale_out)
-    _dense(fn, dev, "q_out", torch.bfloat16 if q_scale_out is None else e4m3, q_out)
-    _dense(fn, dev, "freq", torch.float64, freq)
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _shape(fn, name, t, (pages, PAGE_SIZE, int(Hkv), HEAD_DIM))
-    _shape(fn, "kv_scale", kv_scale, (pages, int(Hkv), 2, PAGE_SIZE // SCALE_BLOCK))
+    bf16, N, pages, Hq, Hkv = torch.bfloat16, positions.numel(), k_cache.shape[0], int(Hq), int(Hkv)
+    dev, q_type = _current_device(), torch.bfloat16 if q_scale_out is None else e4m3
+    if not (q_norm_w.dtype is bf16 and k_norm_w.dtype is bf16 and positions.dtype is i32
+            and block_table.dtype is i32 and k_cache.dtype is e4m3 and v_cache.dtype is e4m3
+            and kv_scale.dtype is f32 and q_out.dtype is q_type
+            and q_norm_w.is_contiguous() and k_norm_w.is_contiguous()
+            and positions.is_contiguous() and block_table.is_contiguous()
+            and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and kv_scale.is_contiguous() and q_out.is_contiguous()
+            and dev == q_norm_w.get_device() == k_norm_w.get_device() == positions.get_device()
+            == block_table.get_device() == k_cache.get_device() == v_cache.get_device()
+            == kv_scale.get_device() == q_out.get_device()
+            and (token_req is None or _is_dense(token_req, i32, dev))
+            and (flags is None or _is_dense(flags, i32, dev))
+            and (q_scale_out is None or _is_dense(q_scale_out, f32, dev))
+            and (freq is None or _is_dense(freq, torch.float64, dev))):
+        _dense(fn, dev, "q_norm_w k_norm_w", bf16, q_norm_w, k_norm_w)
+        _dense(fn, dev, "positions token_req block_table flags", i32, positions, token_req,
+               block_table, flags)
+        _dense(fn, dev, "k_cache v_cache", e4m3, k_cache, v_cache)
+        _dense(fn, dev, "kv_scale q_scale_out", f32, kv_scale, q_scale_out)
+        _dense(fn, dev, "q_out", q_type, q_out)
+        _dense(fn, dev, "freq", torch.float64, freq)
+    want = (pages, PAGE_SIZE, Hkv, HEAD_DIM)
+    if k_cache.shape != want or v_cache.shape != want:
+        _shape(fn, "k_cache", k_cache, want)
+        _shape(fn, "v_cache", v_cache, want)
+    _shape(fn, "kv_scale", kv_scale, (pages, Hkv, 2, PAGE_SIZE // SCALE_BLOCK))
     if qkv.dtype is not torch.bfloat16 or qkv.dim() != 2 or (N and qkv.stride(1) != 1) or \
             qkv.shape[0] < N or qkv.shape[1] < (Hq + 2 * Hkv) * HEAD_DIM:
         raise ValueError(f"{fn}: qkv is not a BF16 matrix of {N} rows of {Hq} + 2 x {Hkv} heads")
-    if qkv.get_device() != k_cache.get_device():
+    if qkv.get_device() != dev:
         raise ValueError(f"{fn}: qkv is on {qkv.device}, not on the current device")
     if q_norm_w.numel() != HEAD_DIM or k_norm_w.numel() != HEAD_DIM or \
             (freq is not None and freq.numel() != HEAD_DIM // 2):
@@ -657,15 +704,17 @@ def hpc_rope_norm_block(qkv, q_norm_w, k_norm_w, positions, token_req, Hq, Hkv, 
     if block_table.dim() != 2 or (token_req is not None and token_req.numel() != N):
         raise ValueError(f"{fn}: block_table is no matrix or token_req has not {N} entries")
     # a stride says nothing where there are not two rows
-    stride = int(qkv.stride(0)) if qkv.shape[0] > 1 else int(qkv.shape[1])
+    stride = qkv.stride(0) if qkv.shape[0] > 1 else qkv.shape[1]
     params = hpc_rope_norm_params(float(eps), float(rope_base), int(rope_layout),
-                                  1 if norm_first else 0,
-                                  None if freq is None else freq.data_ptr())
-    _check(fn, lib().hpc_rope_norm_block(
-        _adr(qkv), stride, _adr(q_norm_w), _adr(k_norm_w), _adr(positions), _adr(token_req), N,
-        int(Hq), int(Hkv), HEAD_DIM, _adr(block_table), int(block_table.shape[1]),
-        int(block_table.shape[0]), _adr(k_cache), _adr(v_cache), _adr(kv_scale), pages,
-        _adr(q_out), _adr(q_scale_out), _adr(flags), ctypes.byref(params), _raw_stream(dev, stream)))
+                                  1 if norm_first else 0, _adr(freq))
+    status = lib().hpc_rope_norm_block(
+        qkv.data_ptr(), stride, q_norm_w.data_ptr(), k_norm_w.data_ptr(), positions.data_ptr(),
+        _adr(token_req), N, Hq, Hkv, HEAD_DIM, block_table.data_ptr(), block_table.shape[1],
+        block_table.shape[0], k_cache.data_ptr(), v_cache.data_ptr(), kv_scale.data_ptr(), pages,
+        q_out.data_ptr(), _adr(q_scale_out), _adr(flags), ctypes.byref(params),
+        _raw_stream(dev, stream))
+    if status != HPC_OK:
+        _check(fn, status)
 
 
 def hpc_kv_read_block(k_cache, v_cache, kv_scale, block_table, starts, seqlens, Hkv, k_out, v_out,
@@ -673,27 +722,45 @@ def hpc_kv_read_block(k_cache, v_cache, kv_scale, block_table, starts, seqlens, 
     """Tokens starts[r] .. seqlens[r] - 1 (starts None: from 0) of a block-scaled
     cache as BF16 into the pages out_block_table names."""
     fn, f32, i32, e4m3 = "hpc_kv_read_block", torch.float32, torch.int32, torch.float8_e4m3fn
-    B, pages, out_pages = int(seqlens.numel()), int(k_cache.shape[0]), int(k_out.shape[0])
-    dev = _current_device()
-    _dense(fn, dev, "k_cache v_cache", e4m3, k_cache, v_cache)
-    _dense(fn, dev, "kv_scale", f32, kv_scale)
-    _dense(fn, dev, "block_table starts seqlens out_block_table flags", i32, block_table, starts,
-           seqlens, out_block_table, flags)
-    _dense(fn, dev, "k_out v_out", torch.bfloat16, k_out, v_out)
-    for name, t, n in (("k_cache", k_cache, pages), ("v_cache", v_cache, pages),
-                       ("k_out", k_out, out_pages), ("v_out", v_out, out_pages)):
-        _shape(fn, name, t, (n, PAGE_SIZE, int(Hkv), HEAD_DIM))
-    _shape(fn, "kv_scale", kv_scale, (pages, int(Hkv), 2, PAGE_SIZE // SCALE_BLOCK))
+    bf16, dev, Hkv, B = torch.bfloat16, _current_device(), int(Hkv), seqlens.numel()
+    pages, out_pages = k_cache.shape[0], k_out.shape[0]
+    if not (k_cache.dtype is e4m3 and v_cache.dtype is e4m3 and kv_scale.dtype is f32
+            and block_table.dtype is i32 and seqlens.dtype is i32 and out_block_table.dtype is i32
+            and k_out.dtype is bf16 and v_out.dtype is bf16
+            and k_cache.is_contiguous() and v_cache.is_contiguous() and kv_scale.is_contiguous()
+            and block_table.is_contiguous() and seqlens.is_contiguous()
+            and out_block_table.is_contiguous() and k_out.is_contiguous()
+            and v_out.is_contiguous()
+            and dev == k_cache.get_device() == v_cache.get_device() == kv_scale.get_device()
+            == block_table.get_device() == seqlens.get_device() == out_block_table.get_device()
+            == k_out.get_device() == v_out.get_device()
+            and (starts is None or _is_dense(starts, i32, dev))
+            and (flags is None or _is_dense(flags, i32, dev))):
+        _dense(fn, dev, "k_cache v_cache", e4m3, k_cache, v_cache)
+        _dense(fn, dev, "kv_scale", f32, kv_scale)
+        _dense(fn, dev, "block_table starts seqlens out_block_table flags", i32, block_table,
+               starts, seqlens, out_block_table, flags)
+        _dense(fn, dev, "k_out v_out", bf16, k_out, v_out)
+    want, out_want = (pages, PAGE_SIZE, Hkv, HEAD_DIM), (out_pages, PAGE_SIZE, Hkv, HEAD_DIM)
+    if k_cache.shape != want or v_cache.shape != want or k_out.shape != out_want or \
+            v_out.shape != out_want:
+        _shape(fn, "k_cache", k_cache, want)
+        _shape(fn, "v_cache", v_cache, want)
+        _shape(fn, "k_out", k_out, out_want)
+        _shape(fn, "v_out", v_out, out_want)
+    _shape(fn, "kv_scale", kv_scale, (pages, Hkv, 2, PAGE_SIZE // SCALE_BLOCK))
     for name, t in (("block_table", block_table), ("out_block_table", out_block_table)):
         if t.dim() != 2 or t.shape[0] < B:
             raise ValueError(f"{fn}: {name} has not a row for each of the {B} requests")
     if starts is not None and starts.numel() != B:
         raise ValueError(f"{fn}: starts has not {B} entries")
-    _check(fn, lib().hpc_kv_read_block(
-        _adr(k_cache), _adr(v_cache), _adr(kv_scale), pages, _adr(block_table),
-        int(block_table.shape[1]), _adr(starts), _adr(seqlens), B, int(Hkv), HEAD_DIM,
-        _adr(k_out), _adr(v_out), out_pages, _adr(out_block_table),
-        int(out_block_table.shape[1]), _adr(flags), _raw_stream(dev, stream)))
+    status = lib().hpc_kv_read_block(
+        k_cache.data_ptr(), v_cache.data_ptr(), kv_scale.data_ptr(), pages, block_table.data_ptr(),
+        block_table.shape[1], _adr(starts), seqlens.data_ptr(), B, Hkv, HEAD_DIM, k_out.data_ptr(),
+        v_out.data_ptr(), out_pages, out_block_table.data_ptr(), out_block_table.shape[1],
+        _adr(flags), _raw_stream(dev, stream))
+    if status != HPC_OK:
+        _check(fn, status)
 
 
 class Workspace:
