@@ -42,14 +42,21 @@
 namespace hpc {
 namespace {
 
+constexpr int kStages = 4;                    // depth of the K and V rings, in pages
+constexpr int kPageHalf = kTile * 128;        // 64 tokens x 64 dims
+constexpr int kPageBytes = 2 * kPageHalf;     // a page of K or V of one head
+constexpr int kCleanWarp = kMmaWarp + kQT;    // (an MMA warp for each Q tile)
+constexpr int kWinThreads = (kCleanWarp + 1) * 32;
+// TMEM: the scores of Q tile x's even and odd pages at 128 x and 128 x + 64
+// (P over their first 32 columns), O_x at kOCol + 128 x
 constexpr int kOffQ = 0;
 constexpr int kOffK = kOffQ + kQT * kTileBytes;
-constexpr int kOffV = kOffK + kKStages * kTileBytes;
-constexpr int kOffO = kOffV + kVStages * kTileBytes;  // [x]: half of an output tile, BF16
+constexpr int kOffV = kOffK + kStages * kPageBytes;
+constexpr int kOffO = kOffV + kStages * kPageBytes;  // [x]: half of an output tile, BF16
 constexpr int kOffBar = kOffO + kQT * kHalf;
-// barriers: q_full, q_free, k_full[2], k_empty[2], v_full[2], v_empty[2],
-// v_clean[2], s_full[2], p_full[2], o_done[2], o_free[2], mma_done, end
-constexpr int kNumBars = 2 + 2 * kKStages + 3 * kVStages + 4 * kQT + 2;
+// barriers: q_full, q_free, k_full[S], k_empty[S], v_full[S], v_empty[S],
+// v_clean[S], s_full[x][2], p_full[x][2], o_done[x][2], o_free[x], mma_done, end
+constexpr int kNumBars = 2 + 5 * kStages + 7 * kQT + 2;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;  // tmem slot, abort word
 constexpr int kSmemBytes = kOffMisc + 16 + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 227 * 1024, "shared memory over the per-CTA limit");
@@ -70,36 +77,27 @@ struct WinArgs {
 struct Item {
     bool single;
     int r, hq, i0, L;
-    int tiles[kQT];      // causal extent of each Q tile, in the item's tiles
-    int n;               // KV tiles of the item: two of its pages each
-    int lo;              // first token of the window of the pair's first query
+    int n;                 // its KV pages
     int sink_pages, skip;  // pages that hold sinks; pages left out behind them
-    int alone;           // tile that only the first Q tile sees, or -1
+    int lo[kQT];           // first token of the window of each Q tile's first query
+    int lim[kQT];          // last token its last query sees (-1: none)
 
-    // the item's page c among the request's, and tile j's token of column c
+    // the item's page c among the request's
     __device__ __forceinline__ int page(int c) const { return c < sink_pages ? c : c + skip; }
-    __device__ __forceinline__ int token(int j, int c) const {
-        return page(2 * j + (c >> 6)) * kTile + (c & 63);
-    }
-    __device__ __forceinline__ bool active(int x, int j) const {
-        return j < tiles[x] && (x == 0 || j != alone);
+    // some query of Q tile x sees a token of page g
+    __device__ __forceinline__ bool active(int x, int g, int sinks) const {
+        const int t = g * kTile;
+        return t <= lim[x] && (t + kTile > lo[x] || t < sinks);
     }
     // no query of the pair sees token t: past the end, or before the window
     // and no sink
     __device__ __forceinline__ bool dead(int t, int sinks) const {
-        return t >= L || (t < lo && t >= sinks);
+        return t >= L || (t < lo[0] && t >= sinks);
     }
-    // page g holds such a token, or one that is not
-    __device__ __forceinline__ bool dirty_page(int g, int sinks) const {
+    // page g holds such a token
+    __device__ __forceinline__ bool dirty(int g, int sinks) const {
         const int t = g * kTile;
-        return t + kTile > L || max(t, sinks) < min(t + kTile, lo);
-    }
-    __device__ __forceinline__ bool needs_page(int g, int sinks) const {
-        const int t = g * kTile;
-        return t < L && (t + kTile > lo || t < sinks);
-    }
-    __device__ __forceinline__ bool dirty(int j, int sinks) const {
-        return dirty_page(page(2 * j), sinks) || dirty_page(page(2 * j + 1), sinks);
+        return t + kTile > L || max(t, sinks) < min(t + kTile, lo[0]);
     }
 };
 
@@ -121,68 +119,32 @@ __device__ __forceinline__ Item item_of(const WinArgs &a, int item, int L) {
     it.hq = rem % a.Hq;
     it.i0 = qp * kQT * kQB + (it.single ? ((item - a.pairs) & 1) * kQB : 0);
     it.L = L;
-    it.lo = max(L - a.q_len + it.i0 + 1 - a.window, 0);
     it.sink_pages = a.sinks / kTile + (a.sinks % kTile ? 1 : 0);
-    it.skip = max(it.lo / kTile - it.sink_pages, 0);
-    it.n = 0;
+    int last = -1;  // last token that a query of the item sees
 #pragma unroll
     for (int x = 0; x < kQT; ++x) {
         const int first = it.i0 + x * kQB;
-        // last token that the tile's rows see
-        const int lim_last = min(L - a.q_len + min(first + kQB - 1, a.q_len - 1), L - 1);
-        it.tiles[x] = 0;
-        // (the extent ends behind the first row's window: it has pages behind
-        // the gap, or the gap is empty)
-        if (first < a.q_len && lim_last >= 0 && (x == 0 || !it.single))
-            it.tiles[x] = (lim_last / kTile + 1 - it.skip + 1) / 2;
-        it.n = max(it.n, it.tiles[x]);
+        it.lo[x] = max(L - a.q_len + first + 1 - a.window, 0);
+        it.lim[x] = -1;
+        if (first < a.q_len && (x == 0 || !it.single))
+            it.lim[x] = min(L - a.q_len + min(first + kQB - 1, a.q_len - 1), L - 1);
+        last = max(last, it.lim[x]);
     }
-    // the second Q tile's windows begin two pages later
-    it.alone = it.lo > 0 && it.lo / kTile >= it.sink_pages && it.sink_pages % 2 == 0
-                   ? it.sink_pages / 2
-                   : -1;
+    it.skip = max(it.lo[0] / kTile - it.sink_pages, 0);
+    // (a window's first page is not behind the last token its query sees, so
+    // with a gap the count does not fall below the sinks')
+    it.n = last < 0 ? 0 : last / kTile + 1 - it.skip;
     return it;
 }
 
-// Sets the scores of a tile (128 TMEM columns from `col`, the pages of tokens
-// tok0 .. and tok1 ..) that the row does not see to -inf: query i of a request
-// of L tokens sees tokens <= lim that are >= lo or < sinks.  Done in TMEM, 32
-// columns at a time, before the softmax reads them: the warp's rows i0 .. i0 +
-// 31 are consecutive, so whole groups are seen or hidden by all of them and only
-// the groups that a border crosses are read and compared.  Out of line: it is
-// rare, and the softmax needs its registers.
-__device__ __noinline__ void mask_tile(uint32_t col, int tok0, int tok1, int i0, int L, int q_len,
-                                       int window, int sinks) {
-    const int p0 = L - q_len + i0, i = i0 + (int)(threadIdx.x & 31);
-    const int lim0 = min(p0, L - 1), lim31 = min(p0 + 31, L - 1);
-    const int lo0 = p0 + 1 - window, lo31 = lo0 + 31;
-    const int lim = min(L - q_len + i, L - 1), lo = L - q_len + i + 1 - window;
-#pragma unroll 1
-    for (int w = 0; w < 4; ++w) {
-        const int t = (w < 2 ? tok0 : tok1) + 32 * (w & 1);
-        if (t + 31 <= lim0 && (t >= lo31 || t + 31 < sinks)) continue;  // all see all of it
-        uint32_t r[32];
-        if (t > lim31 || (t + 31 < lo0 && t >= sinks)) {  // none sees any
-#pragma unroll
-            for (int c = 0; c < 32; ++c) r[c] = 0xff800000u;
-        } else {
-            tmem_ld32_nowait(col + 32 * w, r);
-            tmem_wait_ld32(r);
-            if (t >= sinks) {  // one interval [lo, lim]
-                const unsigned span = (unsigned)(lim - lo);
-                const int from = lo - t;
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    if ((unsigned)(c - from) > span) r[c] = 0xff800000u;
-            } else {
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    if (c > lim - t || (c < lo - t && c >= sinks - t)) r[c] = 0xff800000u;
-            }
-        }
-        tmem_st32_nowait(col + 32 * w, r);
-        tmem_wait_st32(r);
-    }
+// A value that is the same in every lane, as one that the compiler knows to be:
+// the MMAs take their operands from uniform registers, and moving each there
+// costs more than the MMA.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_or_sync(0xffffffffu, v); }
+
+// The low bits up to and with bit k.
+__device__ __forceinline__ uint64_t bits_to(int k) {
+    return k < 0 ? 0ull : k >= 63 ? ~0ull : (2ull << k) - 1;
 }
 
 __device__ __forceinline__ int clamped_len(const WinArgs &a, int item) {
@@ -190,7 +152,7 @@ __device__ __forceinline__ int clamped_len(const WinArgs &a, int item) {
     return min(max(L, 0), a.max_pages * kTile);
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kWinThreads, 1)
     prefill_win_kernel(const __grid_constant__ CUtensorMap tq,
                        const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv,
@@ -200,25 +162,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kOffBar);
     uint64_t *q_full = bars, *q_free = bars + 1;
-    uint64_t *k_full = bars + 2, *k_empty = k_full + kKStages;
-    uint64_t *v_full = k_empty + kKStages, *v_empty = v_full + kVStages;
-    uint64_t *v_clean = v_empty + kVStages;  // [stage]: a V tile with its dead rows zeroed
-    uint64_t *s_full = v_clean + kVStages;   // [x]: S_x complete (and every MMA before it)
-    uint64_t *p_full = s_full + kQT;         // [x]: P_x written (four warps)
-    uint64_t *o_done = p_full + kQT;         // [x]: O_x += P_x V complete
-    uint64_t *o_free = o_done + kQT;         // [x]: O_x read out (four warps)
+    uint64_t *k_full = bars + 2, *k_empty = k_full + kStages;
+    uint64_t *v_full = k_empty + kStages, *v_empty = v_full + kStages;
+    uint64_t *v_clean = v_empty + kStages;  // [stage]: a V page with its dead rows zeroed
+    uint64_t *s_full = v_clean + kStages;   // [x][b]: the scores of an even or odd page
+    uint64_t *p_full = s_full + 2 * kQT;    // [x][b]: its P written (four warps)
+    uint64_t *o_done = p_full + 2 * kQT;    // [x][b]: O_x += P V of that page complete
+    uint64_t *o_free = o_done + 2 * kQT;    // [x]: O_x read out (four warps)
     uint64_t *mma_done = o_free + kQT, *end = mma_done + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
     volatile int *abort = reinterpret_cast<volatile int *>(smem + kOffMisc + 4);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        // one arrival (an expect-tx arrival or a tcgen05.commit) per phase,
-        // except where a Q tile's four warps arrive, and all eight at the end
+        // arrivals: one (an expect-tx arrival or a tcgen05.commit), but from a Q
+        // tile's four warps on p_full and o_free, all eight at the end, both MMA
+        // warps on q_free, k_empty, v_empty and mma_done, and the warp that
+        // zeroes rows on v_empty
         for (int b = 0; b < kNumBars; ++b) {
-            const bool per_warp = (&bars[b] >= p_full && &bars[b] < o_done) ||
-                                  (&bars[b] >= o_free && &bars[b] < mma_done);
-            mbar_init(&bars[b], per_warp ? 4 : &bars[b] == end ? kSoftmaxWarps : 1);
+            uint64_t *bar = &bars[b];
+            int n = 1;
+            if (bar == q_free || (bar >= k_empty && bar < v_full) || bar == mma_done) n = kQT;
+            if (bar >= v_empty && bar < v_clean) n = kQT + 1;
+            if ((bar >= p_full && bar < o_done) || (bar >= o_free && bar < mma_done)) n = 4;
+            if (bar == end) n = kSoftmaxWarps;
+            mbar_init(bar, n);
         }
         *abort = 0;
         fence_barrier_init();
@@ -234,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = uniform(*tmem_slot);
     grid_dependency_wait();  // Q, the caches and the lengths may come from the previous kernel
 
     const int step = gridDim.x;
@@ -243,24 +211,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == kProducerWarp) {
         const uint64_t pol = policy_evict_normal();
-        uint32_t kt = 0;           // tiles issued
-        uint32_t q_items = 0;      // items whose Q has been issued
-        bool pending = false;      // tile kt - 1 has dead rows to zero
-        Item was;                  // ... of this item
-        int was_j = 0;
-        auto clean = [&]() {
-            const int s = (int)((kt - 1) % kVStages);
-            if (!warp_wait(&v_full[s], ((kt - 1) / kVStages) & 1u, abort)) return false;
-            uint8_t *vs = smem + kOffV + s * kTileBytes;
-            for (int e = lane; e < kKB * 8; e += 32)
-                if (was.dead(was.token(was_j, e >> 3), a.sinks))
-                    for (int h = 0; h < 2; ++h)
-                        sts128(smem_u32(vs + h * kHalf + e * 16), 0u, 0u, 0u, 0u);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&v_clean[s]);
-            return true;
-        };
+        uint32_t kt = 0;       // pages issued
+        uint32_t q_items = 0;  // items whose Q has been issued
+        bool k_only = false;   // page kt: K issued, V not
         for (int idx = blockIdx.x; ok && idx < a.items; idx += step) {
             const Item it = item_of(a, idx, next_L);
             if (lane == 0 && a.flags && it.hq == 0 && it.i0 == 0) {
@@ -270,18 +223,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (idx + step < a.items) next_L = clamped_len(a, idx + step);
             if (it.n == 0) continue;
-            if (q_items > 0 && !warp_wait(q_free, (q_items - 1) & 1u, abort)) {
+            if (q_items > 0 && !mbar_wait_warp(q_free, (q_items - 1) & 1u, abort)) {
                 ok = false;
                 break;
             }
             if (lane == 0) {
                 uint32_t bytes = 0;
 #pragma unroll
-                for (int x = 0; x < kQT; ++x) bytes += it.tiles[x] > 0 ? kTileBytes : 0;
+                for (int x = 0; x < kQT; ++x) bytes += it.lim[x] >= 0 ? kTileBytes : 0;
                 mbar_arrive_expect_tx(q_full, bytes);
 #pragma unroll
                 for (int x = 0; x < kQT; ++x)
-                    if (it.tiles[x] > 0)
+                    if (it.lim[x] >= 0)
                         for (int h = 0; h < 2; ++h)
                             tma_load_4d(smem + kOffQ + x * kTileBytes + h * kHalf, &tq, q_full, 0,
                                         h, it.hq, it.r * a.q_len + it.i0 + x * kQB, pol);
@@ -290,158 +243,166 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t *bt = a.block_table + (size_t)it.r * a.max_pages;
             const int hkv = it.hq / a.G;
             int pg = -1;
-            for (int j = 0; j < it.n; ++j) {
-                if ((j & 15) == 0) {  // the pages of 16 tiles, one per lane; -2: not needed
-                    const int g = it.page(2 * j + lane);
-                    pg = it.needs_page(g, a.sinks) ? max(__ldg(bt + g), -1) : -2;
-                }
-                const int p0 = __shfl_sync(0xffffffffu, pg, (2 * j) & 31);
-                const int p1 = __shfl_sync(0xffffffffu, pg, (2 * j + 1) & 31);
-                const bool l0 = p0 >= 0 && p0 < a.num_pages, l1 = p1 >= 0 && p1 < a.num_pages;
-                if (((p0 != -2 && !l0) || (p1 != -2 && !l1)) && lane == 0 && a.flags)
-                    atomicOr(a.flags, (int)HPC_FLAG_BAD_PAGE);
-                const uint32_t bytes = (uint32_t)((l0 ? 1 : 0) + (l1 ? 1 : 0)) * 2 * kTile * 128;
+            for (int j = 0; j < it.n; ++j, ++kt) {
+                if ((j & 31) == 0)  // the entries of 32 pages, one per lane
+                    pg = j + lane < it.n ? __ldg(bt + it.page(j + lane)) : 0;
+                const int page = __shfl_sync(0xffffffffu, pg, j & 31);
+                const bool good = page >= 0 && page < a.num_pages;
+                if (!good && lane == 0 && a.flags) atomicOr(a.flags, (int)HPC_FLAG_BAD_PAGE);
+                const int s = (int)(kt % kStages);
 #pragma unroll
-                for (int kv = 0; kv < 2 && ok; ++kv) {
-                    // V of the tile before has landed by now, or nearly: its dead
-                    // rows go before this tile's V has room
-                    if (kv == 1 && pending) {
-                        pending = false;
-                        ok = clean();
-                        if (!ok) break;
-                    }
-                    const int st = kv == 0 ? kKStages : kVStages, s = (int)(kt % st);
+                for (int kv = 0; kv < 2; ++kv) {
                     uint64_t *full = kv == 0 ? &k_full[s] : &v_full[s];
-                    ok = warp_wait(kv == 0 ? &k_empty[s] : &v_empty[s], ((kt / st) & 1u) ^ 1u,
-                                   abort);
-                    if (ok && lane == 0) {
-                        if (bytes == 0) {
-                            mbar_arrive(full);
-                        } else {
-                            mbar_arrive_expect_tx(full, bytes);
-                            const CUtensorMap *map = kv == 0 ? &tk : &tv;
-                            uint8_t *dst = smem + (kv == 0 ? kOffK : kOffV) + s * kTileBytes;
-                            for (int h = 0; h < 2; ++h) {
-                                if (l0)
-                                    tma_load_5d(dst + h * kHalf, map, full, 0, h, hkv, 0, p0, pol);
-                                if (l1)
-                                    tma_load_5d(dst + h * kHalf + kTile * 128, map, full, 0, h,
-                                                hkv, 0, p1, pol);
-                            }
-                        }
+                    ok = ok && mbar_wait_warp(kv == 0 ? &k_empty[s] : &v_empty[s],
+                                         ((kt / kStages) & 1u) ^ 1u, abort);
+                    if (!ok || lane != 0) continue;
+                    if (!good) {
+                        mbar_arrive(full);
+                        continue;
                     }
+                    mbar_arrive_expect_tx(full, kPageBytes);
+                    uint8_t *dst = smem + (kv == 0 ? kOffK : kOffV) + s * kPageBytes;
+                    for (int h = 0; h < 2; ++h)
+                        tma_load_5d(dst + h * kPageHalf, kv == 0 ? &tk : &tv, full, 0, h, hkv, 0,
+                                    page, pol);
+                    k_only = kv == 0;
                 }
                 if (!ok) break;
-                ++kt;
-                pending = it.dirty(j, a.sinks);
-                was = it;
-                was_j = j;
             }
         }
-        if (ok && pending && !clean()) ok = false;
         // no copy may land after the CTA has left: the last one issued into
         // each buffer (bounded)
         __syncwarp();
         if (!ok || *abort) {
             volatile int no_abort = 0;
             if (q_items > 0) mbar_wait(q_full, (q_items - 1) & 1u, &no_abort);
-            for (uint32_t t = kt > 2 ? kt - 2 : 0; t < kt; ++t) {
-                mbar_wait(&k_full[t % kKStages], (t / kKStages) & 1u, &no_abort);
-                mbar_wait(&v_full[t % kVStages], (t / kVStages) & 1u, &no_abort);
+            for (uint32_t t = kt > kStages ? kt - kStages : 0; t < kt; ++t) {
+                mbar_wait(&k_full[t % kStages], (t / kStages) & 1u, &no_abort);
+                mbar_wait(&v_full[t % kStages], (t / kStages) & 1u, &no_abort);
             }
+            if (k_only && lane == 0)
+                mbar_wait(&k_full[kt % kStages], (kt / kStages) & 1u, &no_abort);
             __syncwarp();
         }
-    } else if (warp == kMmaWarp) {
-        const uint32_t idesc_s = idesc_bf16_f32(kQB, kKB);
+    } else if (warp < kCleanWarp && warp >= kMmaWarp) {
+        const int x = (int)uniform(warp - kMmaWarp);  // the Q tile
+        const uint32_t idesc_s = idesc_bf16_f32(kQB, kTile);
         const uint32_t idesc_o = idesc_bf16_f32_bmn(kQB, kHeadDim);
         const uint64_t dq0 = smem_desc_k128(smem_u32(smem + kOffQ));
         const uint64_t dk0 = smem_desc_k128(smem_u32(smem + kOffK));
-        const uint64_t dv0 = smem_desc_mn128(smem_u32(smem + kOffV), kHalf);
-        // S_x = Q_x K^T into x's score columns (K tile in stage s)
-        auto issue_s = [&](int x, uint32_t s) {
-            const uint64_t dq = dq0 + (uint64_t)((x * kTileBytes) >> 4);
-            const uint64_t dk = dk0 + (uint64_t)((s * kTileBytes) >> 4);
+        const uint64_t dv0 = smem_desc_mn128(smem_u32(smem + kOffV), kPageHalf);
+        const uint64_t dq = dq0 + (uint64_t)((x * kTileBytes) >> 4);
+        // S = Q_x K^T of a page into score buffer b (K page in stage s)
+        auto issue_s = [&](uint32_t b, uint32_t s) {
+            const uint64_t dk = dk0 + (uint64_t)((s * kPageBytes) >> 4);
 #pragma unroll
             for (int k = 0; k < kHeadDim / 16; ++k) {
-                const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-                umma_bf16(tmem + 128 * x, dq + off, dk + off, idesc_s, k > 0);
+                const uint32_t in = (k & 3) * 32;  // bytes within a half's rows
+                umma_bf16(tmem + 128 * x + 64 * b, dq + (((k >> 2) * kHalf + in) >> 4),
+                          dk + (((k >> 2) * kPageHalf + in) >> 4), idesc_s, k > 0);
             }
-            umma_commit(&s_full[x]);
+            umma_commit(&s_full[2 * x + b]);
+            umma_commit(&k_empty[s]);
         };
-        // O_x += P_x V (V tile in stage s), P_x from TMEM
-        auto issue_pv = [&](int x, uint32_t s, bool acc) {
-            const uint64_t dv = dv0 + (uint64_t)((s * kTileBytes) >> 4);
+        // O_x += P V of a page (V page in stage s), P from TMEM
+        auto issue_pv = [&](uint32_t b, uint32_t s, bool acc) {
+            const uint64_t dv = dv0 + (uint64_t)((s * kPageBytes) >> 4);
 #pragma unroll
-            for (int k = 0; k < kKB / 16; ++k)
-                umma_bf16_ts(tmem + kOCol + 128 * x, tmem + 128 * x + 8 * k,
+            for (int k = 0; k < kTile / 16; ++k)
+                umma_bf16_ts(tmem + kOCol + 128 * x, tmem + 128 * x + 64 * b + 8 * k,
                              dv + (uint64_t)((k * 16 * 128) >> 4), idesc_o, acc || k > 0);
-            umma_commit(&o_done[x]);
+            umma_commit(&o_done[2 * x + b]);
+            umma_commit(&v_empty[s]);
         };
         uint32_t kt = 0, q_items = 0;
-        uint32_t cleaned[kVStages] = {};  // zeroed tiles taken from each stage
-        uint32_t np[kQT] = {};            // P tiles taken
-        uint32_t outs[kQT] = {};          // items whose O_x has been claimed
+        uint32_t cleaned = 0;     // bit s: parity of the zeroed pages taken from stage s
+        uint32_t sp = 0, pp = 0;  // score pages issued, P pages taken
+        uint32_t outs = 0;        // items whose O_x has been claimed
         for (int idx = blockIdx.x; ok && idx < a.items; idx += step) {
             const Item it = item_of(a, idx, next_L);
             if (idx + step < a.items) next_L = clamped_len(a, idx + step);
             if (it.n == 0) continue;
-            bool started[kQT] = {};
-            ok = warp_wait(q_full, q_items & 1u, abort) &&
-                 warp_wait(&k_full[kt % kKStages], (kt / kKStages) & 1u, abort);
+            bool started = false;
+            ok = mbar_wait_warp(q_full, q_items & 1u, abort);
             ++q_items;
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-                for (int x = 0; x < kQT; ++x)
-                    if (it.active(x, 0)) issue_s(x, kt % kKStages);
-                umma_commit(&k_empty[kt % kKStages]);
-                if (it.n == 1) umma_commit(q_free);
-            }
-            __syncwarp();
-            for (int j = 0; ok && j < it.n; ++j, ++kt) {
-                const uint32_t s = kt % kVStages, s1 = (kt + 1) % kKStages;
-                const bool next = j + 1 < it.n;
-                if (it.dirty(j, a.sinks)) {
-                    ok = warp_wait(&v_clean[s], cleaned[s] & 1u, abort);
-                    ++cleaned[s];
-                } else {
-                    ok = warp_wait(&v_full[s], (kt / kVStages) & 1u, abort);
-                }
-                if (ok && next)
-                    ok = warp_wait(&k_full[s1], ((kt + 1) / kKStages) & 1u, abort);
-#pragma unroll
-                for (int x = 0; x < kQT; ++x) {
-                    if (!ok) break;
-                    const bool now = it.active(x, j), then = next && it.active(x, j + 1);
-                    if (now) {
-                        ok = warp_wait(&p_full[x], np[x] & 1u, abort);
-                        ++np[x];
-                        if (ok && !started[x]) {  // the item before has been read out of O_x
-                            if (outs[x] > 0) ok = warp_wait(&o_free[x], (outs[x] - 1) & 1u, abort);
-                            ++outs[x];
-                        }
-                        if (!ok) break;
+            // The scores run two pages ahead of the products: both buffers are then
+            // in use, one at the softmax and one being filled.  Pages that the Q tile
+            // does not see are waited for and passed on all the same (a phase of a
+            // barrier may not be left out).
+            for (int j = -2; ok && j < it.n; ++j) {
+                const int js = j + 2;
+                if (j >= 0) {
+                    const int g = it.page(j);
+                    const uint32_t vs = kt % kStages;
+                    if (it.dirty(g, a.sinks)) {
+                        ok = mbar_wait_warp(&v_clean[vs], cleaned >> vs & 1u, abort);
+                        cleaned ^= 1u << vs;
+                    } else {
+                        ok = mbar_wait_warp(&v_full[vs], (kt / kStages) & 1u, abort);
                     }
+                    const bool now = it.active(x, g, a.sinks);
+                    if (ok && now)
+                        ok = mbar_wait_warp(&p_full[2 * x + (pp & 1u)], (pp >> 1) & 1u, abort);
+                    if (ok && now && !started && outs++ > 0)  // O_x of the item before is out
+                        ok = mbar_wait_warp(&o_free[x], (outs - 2) & 1u, abort);
+                    if (!ok) break;
                     tc_fence_after();
+                    const uint32_t u = uniform((now ? 1u : 0u) | (pp & 1u) << 1 |
+                                               (started ? 4u : 0u) | vs << 3);
                     if (elect_one()) {
-                        if (now) issue_pv(x, s, started[x]);
-                        if (then) issue_s(x, s1);
+                        if (u & 1u) issue_pv(u >> 1 & 1u, u >> 3, u & 4u);
+                        else mbar_arrive(&v_empty[u >> 3]);
                     }
                     __syncwarp();
-                    started[x] |= now;
+                    started |= now;
+                    pp += now;
+                    ++kt;
                 }
-                if (!ok) break;
-                if (elect_one()) {
-                    umma_commit(&v_empty[s]);  // after both Q tiles' products with V_j
-                    if (next) umma_commit(&k_empty[s1]);  // after both Q tiles' scores with K_j+1
-                    if (j + 2 == it.n) umma_commit(q_free);  // the item's last scores
+                if (js < it.n) {
+                    const uint32_t kts = j >= 0 ? kt + 1 : kt + js, ks = kts % kStages;
+                    ok = mbar_wait_warp(&k_full[ks], (kts / kStages) & 1u, abort);
+                    if (!ok) break;
+                    const bool next = it.active(x, it.page(js), a.sinks);
+                    const uint32_t u = uniform((next ? 1u : 0u) | (sp & 1u) << 1 |
+                                               (js == it.n - 1 ? 4u : 0u) | ks << 3);
+                    if (elect_one()) {
+                        if (u & 1u) issue_s(u >> 1 & 1u, u >> 3);
+                        else mbar_arrive(&k_empty[u >> 3]);
+                        if (u & 4u) umma_commit(q_free);  // the item's last scores
+                    }
+                    __syncwarp();
+                    sp += next;
                 }
-                __syncwarp();
             }
         }
         // arrives once every MMA issued has completed (TMEM is freed after it)
         if (elect_one()) umma_commit(mma_done);
         __syncwarp();
+    } else if (warp == kCleanWarp) {
+        // zeroes the V rows that no query of the pair sees (it passes every page,
+        // so that its stage's phases cannot run away from it)
+        uint32_t kt = 0;
+        for (int idx = blockIdx.x; ok && idx < a.items; idx += step) {
+            const Item it = item_of(a, idx, next_L);
+            if (idx + step < a.items) next_L = clamped_len(a, idx + step);
+            for (int j = 0; j < it.n; ++j, ++kt) {
+                const uint32_t s = kt % kStages;
+                ok = mbar_wait_warp(&v_full[s], (kt / kStages) & 1u, abort);
+                if (!ok) break;
+                const int g = it.page(j);
+                if (it.dirty(g, a.sinks)) {
+                    const uint32_t vs = smem_u32(smem + kOffV + s * kPageBytes);
+                    for (int e = lane; e < kTile * 8; e += 32)
+                        if (it.dead(g * kTile + (e >> 3), a.sinks))
+                            for (int h = 0; h < 2; ++h)
+                                sts128(vs + h * kPageHalf + e * 16, 0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&v_clean[s]);
+                }
+                if (lane == 0) mbar_arrive(&v_empty[s]);
+            }
+        }
     } else {
         // softmax of Q tile x: thread = one query row, warp w reads TMEM
         // lanes 32 (w mod 4) ..
@@ -450,56 +411,52 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t row = tmem + ((uint32_t)(32 * q4) << 16);
         const uint32_t scol = row + 128 * x, ocol = row + kOCol + 128 * x;
         const float sc = a.score_scale;
-        uint32_t ns = 0;  // score tiles taken
+        uint32_t ns = 0;  // score pages taken
         for (int idx = blockIdx.x; ok && idx < a.items; idx += step) {
             const Item it = item_of(a, idx, next_L);
             if (idx + step < a.items) next_L = clamped_len(a, idx + step);
             if (x > 0 && it.single) continue;
-            const int tiles = it.tiles[x], L = it.L, first = it.i0 + x * kQB;
-            // the last token its first row sees, the first of its last row's window
-            const int lim_first = min(L - a.q_len + first, L - 1);
-            const int lo_last = L - a.q_len + min(first + kQB, a.q_len) - a.window;
+            const int first = it.i0 + x * kQB;
+            // the tokens the row sees, and those that all of the warp's rows see
+            const int p0 = it.L - a.q_len + first + 32 * q4;
+            const int lim = min(p0 + lane, it.L - 1), lo = p0 + lane + 1 - a.window;
+            const int lim_all = min(p0, it.L - 1), lo_all = p0 + 32 - a.window;
             float m_ref = -INFINITY, l = 0.f;
             bool started = false;
-            for (int j = 0; j < tiles; ++j) {
-                if (!it.active(x, j)) continue;
-                if (!warp_wait(&s_full[x], ns & 1u, abort)) {
+            for (int j = 0; j < it.n; ++j) {
+                const int g = it.page(j), t = g * kTile;
+                if (!it.active(x, g, a.sinks)) continue;
+                const uint32_t b = ns & 1u;
+                if (!mbar_wait_warp(&s_full[2 * x + b], (ns >> 1) & 1u, abort)) {
                     ok = false;
                     break;
                 }
-                ++ns;
                 tc_fence_after();
-                const int tok0 = it.token(j, 0), tok1 = it.token(j, kTile);
-                // some row does not see all of it: the diagonal or the end, or
-                // tokens before a window that are no sinks
-                if (tok1 + kTile - 1 > lim_first || (tok0 < lo_last && tok0 + kTile > a.sinks) ||
-                    (tok1 < lo_last && tok1 + kTile > a.sinks))
-                    mask_tile(scol, tok0, tok1, first + 32 * q4, L, a.q_len, a.window, a.sinks);
-                // the row's 128 scores in two halves: the second half loads while
-                // the first is reduced
-                uint32_t ra[32], rb[32], rc[32], rd[32];
-                tmem_ld32_nowait(scol, ra);
-                tmem_ld32_nowait(scol + 32, rb);
+                uint32_t ra[32], rb[32];
+                tmem_ld32_nowait(scol + 64 * b, ra);
+                tmem_ld32_nowait(scol + 64 * b + 32, rb);
                 tmem_wait_ld32x2(ra, rb);
-                tmem_ld32_nowait(scol + 64, rc);
-                tmem_ld32_nowait(scol + 96, rd);
-                float s[128];
+                float s[kTile];
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
                     s[c] = __uint_as_float(ra[c]);
                     s[32 + c] = __uint_as_float(rb[c]);
                 }
+                // some row of the warp does not see all of it: the diagonal or the
+                // end, or tokens before a window that are no sinks
+                if (t + kTile - 1 > lim_all || (t < lo_all && t + kTile > a.sinks)) {
+                    const uint64_t sees = bits_to(lim - t) &
+                                          (~bits_to(lo - 1 - t) | bits_to(a.sinks - 1 - t));
+                    const uint32_t w0 = (uint32_t)sees, w1 = (uint32_t)(sees >> 32);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        if (!(w0 >> c & 1u)) s[c] = -INFINITY;
+                        if (!(w1 >> c & 1u)) s[32 + c] = -INFINITY;
+                    }
+                }
                 float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 32; ++c) mx4[c & 3] = fmax3(mx4[c & 3], s[2 * c], s[2 * c + 1]);
-                tmem_wait_ld32x2(rc, rd);
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    s[64 + c] = __uint_as_float(rc[c]);
-                    s[96 + c] = __uint_as_float(rd[c]);
-                }
-#pragma unroll
-                for (int c = 32; c < 64; ++c)
+                for (int c = 0; c < kTile / 2; ++c)
                     mx4[c & 3] = fmax3(mx4[c & 3], s[2 * c], s[2 * c + 1]);
                 const float mx = fmax3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]);
                 const float m_tile = mx * sc;
@@ -507,32 +464,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float new_ref = need ? m_tile : m_ref;
                 const float factor = need ? ex2(m_ref - new_ref) : 1.f;
                 const float base = new_ref == -INFINITY ? 0.f : new_ref;
-                // P as packed BF16 pairs, written over the first 64 score columns
-                // in two stores: the first is in flight while the second half is
-                // computed
-                uint32_t pa[32], pb[32];
+                // P as packed BF16 pairs, over the first half of the scores
+                uint32_t pk[32];
                 float2 ps[4] = {};
                 const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(-base, -base);
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {  // two columns per instruction
                     const float2 e = __ffma2_rn(make_float2(s[2 * c], s[2 * c + 1]), sc2, nb2);
-                    const float p0 = ex2(e.x), p1 = ex2(e.y);
-                    ps[c & 3] = __fadd2_rn(ps[c & 3], make_float2(p0, p1));
-                    pa[c] = pack_bf16x2(p0, p1);
+                    const float e0 = ex2(e.x), e1 = ex2(e.y);
+                    ps[c & 3] = __fadd2_rn(ps[c & 3], make_float2(e0, e1));
+                    pk[c] = pack_bf16x2(e0, e1);
                 }
-                tmem_st32_nowait(scol, pa);
-#pragma unroll
-                for (int c = 32; c < 64; ++c) {
-                    const float2 e = __ffma2_rn(make_float2(s[2 * c], s[2 * c + 1]), sc2, nb2);
-                    const float p0 = ex2(e.x), p1 = ex2(e.y);
-                    ps[c & 3] = __fadd2_rn(ps[c & 3], make_float2(p0, p1));
-                    pb[c - 32] = pack_bf16x2(p0, p1);
-                }
+                tmem_st32_nowait(scol + 64 * b, pk);
                 const float2 pq = __fadd2_rn(__fadd2_rn(ps[0], ps[1]), __fadd2_rn(ps[2], ps[3]));
                 l = l * factor + (pq.x + pq.y);
-                // O_x is settled: its product with the previous tile completed
-                // before these scores did
                 if (started && __any_sync(0xffffffffu, need)) {
+                    // O_x is settled once its last product is done (the product two
+                    // before that, the same barrier's last, was issued before these
+                    // scores' own: the phase cannot be mistaken)
+                    if (!mbar_wait_warp(&o_done[2 * x + (b ^ 1u)], ((ns - 1) >> 1) & 1u, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
                         float o[64];
@@ -543,17 +497,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 started = true;
-                tmem_st32_nowait(scol + 32, pb);
-                tmem_wait_st32x2(pa, pb);
+                tmem_wait_st32(pk);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[x]);
+                if (lane == 0) mbar_arrive(&p_full[2 * x + b]);
                 m_ref = new_ref;
+                ++ns;
             }
             // epilogue: O / l as BF16 (zeros for rows that see nothing)
             bool have = ok && started;
             if (have) {
-                if (!warp_wait(&o_done[x], (ns - 1) & 1u, abort))
+                if (!mbar_wait_warp(&o_done[2 * x + ((ns - 1) & 1u)], ((ns - 1) >> 1) & 1u, abort))
                     ok = have = false;
                 else
                     tc_fence_after();
@@ -721,7 +675,7 @@ extern "C" hpc_status hpc_prefill_attn_win(const void *d_q, const void *d_k_cach
     a.items = (int)(a.pairs + 2 * (pairs - a.pairs));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)std::min<int64_t>(a.items, sms));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kWinThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
