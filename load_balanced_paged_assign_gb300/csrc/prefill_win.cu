@@ -42,7 +42,7 @@
 namespace hpc {
 namespace {
 
-constexpr int kStages = 4;                    // depth of the K and V rings, in pages
+constexpr int kStages = 4;                    // depth of the ring, in pages of K and V
 constexpr int kPageHalf = kTile * 128;        // 64 tokens x 64 dims
 constexpr int kPageBytes = 2 * kPageHalf;     // a page of K or V of one head
 constexpr int kCleanWarp = kMmaWarp + kQT;    // (an MMA warp for each Q tile)
@@ -54,9 +54,9 @@ constexpr int kOffK = kOffQ + kQT * kTileBytes;
 constexpr int kOffV = kOffK + kStages * kPageBytes;
 constexpr int kOffO = kOffV + kStages * kPageBytes;  // [x]: half of an output tile, BF16
 constexpr int kOffBar = kOffO + kQT * kHalf;
-// barriers: q_full, q_free, k_full[S], k_empty[S], v_full[S], v_empty[S],
-// v_clean[S], s_full[x][2], p_full[x][2], o_done[x][2], o_free[x], mma_done, end
-constexpr int kNumBars = 2 + 5 * kStages + 7 * kQT + 2;
+// barriers: q_full, q_free, full[S], clean[S], empty[S], s_full[x][2],
+// p_full[x][2], o_done[x][2], o_free[x], mma_done, end
+constexpr int kNumBars = 2 + 3 * kStages + 7 * kQT + 2;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;  // tmem slot, abort word
 constexpr int kSmemBytes = kOffMisc + 16 + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 227 * 1024, "shared memory over the per-CTA limit");
@@ -162,10 +162,10 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kOffBar);
     uint64_t *q_full = bars, *q_free = bars + 1;
-    uint64_t *k_full = bars + 2, *k_empty = k_full + kStages;
-    uint64_t *v_full = k_empty + kStages, *v_empty = v_full + kStages;
-    uint64_t *v_clean = v_empty + kStages;  // [stage]: a V page with its dead rows zeroed
-    uint64_t *s_full = v_clean + kStages;   // [x][b]: the scores of an even or odd page
+    uint64_t *full = bars + 2;             // [stage]: K and V of a page have landed
+    uint64_t *clean = full + kStages;      // [stage]: the dead rows of its V are zeroed
+    uint64_t *empty = clean + kStages;     // [stage]: its products are done
+    uint64_t *s_full = empty + kStages;    // [x][b]: the scores of an even or odd page
     uint64_t *p_full = s_full + 2 * kQT;    // [x][b]: its P written (four warps)
     uint64_t *o_done = p_full + 2 * kQT;    // [x][b]: O_x += P V of that page complete
     uint64_t *o_free = o_done + 2 * kQT;    // [x]: O_x read out (four warps)
@@ -177,13 +177,13 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     if (threadIdx.x == 0) {
         // arrivals: one (an expect-tx arrival or a tcgen05.commit), but from a Q
         // tile's four warps on p_full and o_free, all eight at the end, both MMA
-        // warps on q_free, k_empty, v_empty and mma_done, and the warp that
-        // zeroes rows on v_empty
+        // warps on q_free, empty and mma_done, and the warp that zeroes rows on
+        // empty
         for (int b = 0; b < kNumBars; ++b) {
             uint64_t *bar = &bars[b];
             int n = 1;
-            if (bar == q_free || (bar >= k_empty && bar < v_full) || bar == mma_done) n = kQT;
-            if (bar >= v_empty && bar < v_clean) n = kQT + 1;
+            if (bar == q_free || bar == mma_done) n = kQT;
+            if (bar >= empty && bar < s_full) n = kQT + 1;
             if ((bar >= p_full && bar < o_done) || (bar >= o_free && bar < mma_done)) n = 4;
             if (bar == end) n = kSoftmaxWarps;
             mbar_init(bar, n);
@@ -213,7 +213,6 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         const uint64_t pol = policy_evict_normal();
         uint32_t kt = 0;       // pages issued
         uint32_t q_items = 0;  // items whose Q has been issued
-        bool k_only = false;   // page kt: K issued, V not
         for (int idx = blockIdx.x; ok && idx < a.items; idx += step) {
             const Item it = item_of(a, idx, next_L);
             if (lane == 0 && a.flags && it.hq == 0 && it.i0 == 0) {
@@ -250,24 +249,18 @@ __global__ void __launch_bounds__(kWinThreads, 1)
                 const bool good = page >= 0 && page < a.num_pages;
                 if (!good && lane == 0 && a.flags) atomicOr(a.flags, (int)HPC_FLAG_BAD_PAGE);
                 const int s = (int)(kt % kStages);
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    uint64_t *full = kv == 0 ? &k_full[s] : &v_full[s];
-                    ok = ok && mbar_wait_warp(kv == 0 ? &k_empty[s] : &v_empty[s],
-                                         ((kt / kStages) & 1u) ^ 1u, abort);
-                    if (!ok || lane != 0) continue;
-                    if (!good) {
-                        mbar_arrive(full);
-                        continue;
-                    }
-                    mbar_arrive_expect_tx(full, kPageBytes);
-                    uint8_t *dst = smem + (kv == 0 ? kOffK : kOffV) + s * kPageBytes;
-                    for (int h = 0; h < 2; ++h)
-                        tma_load_5d(dst + h * kPageHalf, kv == 0 ? &tk : &tv, full, 0, h, hkv, 0,
-                                    page, pol);
-                    k_only = kv == 0;
-                }
+                ok = mbar_wait_warp(&empty[s], ((kt / kStages) & 1u) ^ 1u, abort);
                 if (!ok) break;
+                if (lane == 0 && !good) {
+                    mbar_arrive(&full[s]);
+                } else if (lane == 0) {
+                    mbar_arrive_expect_tx(&full[s], 2 * kPageBytes);
+                    uint8_t *k = smem + kOffK + s * kPageBytes, *v = smem + kOffV + s * kPageBytes;
+                    for (int h = 0; h < 2; ++h)
+                        tma_load_5d(k + h * kPageHalf, &tk, &full[s], 0, h, hkv, 0, page, pol);
+                    for (int h = 0; h < 2; ++h)
+                        tma_load_5d(v + h * kPageHalf, &tv, &full[s], 0, h, hkv, 0, page, pol);
+                }
             }
         }
         // no copy may land after the CTA has left: the last one issued into
@@ -276,12 +269,8 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         if (!ok || *abort) {
             volatile int no_abort = 0;
             if (q_items > 0) mbar_wait(q_full, (q_items - 1) & 1u, &no_abort);
-            for (uint32_t t = kt > kStages ? kt - kStages : 0; t < kt; ++t) {
-                mbar_wait(&k_full[t % kStages], (t / kStages) & 1u, &no_abort);
-                mbar_wait(&v_full[t % kStages], (t / kStages) & 1u, &no_abort);
-            }
-            if (k_only && lane == 0)
-                mbar_wait(&k_full[kt % kStages], (kt / kStages) & 1u, &no_abort);
+            for (uint32_t t = kt > kStages ? kt - kStages : 0; t < kt; ++t)
+                mbar_wait(&full[t % kStages], (t / kStages) & 1u, &no_abort);
             __syncwarp();
         }
     } else if (warp < kCleanWarp && warp >= kMmaWarp) {
@@ -302,7 +291,6 @@ __global__ void __launch_bounds__(kWinThreads, 1)
                           dk + (((k >> 2) * kPageHalf + in) >> 4), idesc_s, k > 0);
             }
             umma_commit(&s_full[2 * x + b]);
-            umma_commit(&k_empty[s]);
         };
         // O_x += P V of a page (V page in stage s), P from TMEM
         auto issue_pv = [&](uint32_t b, uint32_t s, bool acc) {
@@ -312,7 +300,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
                 umma_bf16_ts(tmem + kOCol + 128 * x, tmem + 128 * x + 64 * b + 8 * k,
                              dv + (uint64_t)((k * 16 * 128) >> 4), idesc_o, acc || k > 0);
             umma_commit(&o_done[2 * x + b]);
-            umma_commit(&v_empty[s]);
+            umma_commit(&empty[s]);  // (this page's scores are done too)
         };
         uint32_t kt = 0, q_items = 0;
         uint32_t cleaned = 0;     // bit s: parity of the zeroed pages taken from stage s
@@ -330,50 +318,37 @@ __global__ void __launch_bounds__(kWinThreads, 1)
             // does not see are waited for and passed on all the same (a phase of a
             // barrier may not be left out).
             for (int j = -2; ok && j < it.n; ++j) {
-                const int js = j + 2;
-                if (j >= 0) {
-                    const int g = it.page(j);
-                    const uint32_t vs = kt % kStages;
-                    if (it.dirty(g, a.sinks)) {
-                        ok = mbar_wait_warp(&v_clean[vs], cleaned >> vs & 1u, abort);
-                        cleaned ^= 1u << vs;
-                    } else {
-                        ok = mbar_wait_warp(&v_full[vs], (kt / kStages) & 1u, abort);
-                    }
-                    const bool now = it.active(x, g, a.sinks);
-                    if (ok && now)
-                        ok = mbar_wait_warp(&p_full[2 * x + (pp & 1u)], (pp >> 1) & 1u, abort);
-                    if (ok && now && !started && outs++ > 0)  // O_x of the item before is out
-                        ok = mbar_wait_warp(&o_free[x], (outs - 2) & 1u, abort);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t u = uniform((now ? 1u : 0u) | (pp & 1u) << 1 |
-                                               (started ? 4u : 0u) | vs << 3);
-                    if (elect_one()) {
-                        if (u & 1u) issue_pv(u >> 1 & 1u, u >> 3, u & 4u);
-                        else mbar_arrive(&v_empty[u >> 3]);
-                    }
-                    __syncwarp();
-                    started |= now;
-                    pp += now;
-                    ++kt;
+                const int js = j + 2, g = it.page(j), gs = it.page(js);
+                const uint32_t ks = (kt + js) % kStages, vs = (kt + j) % kStages;
+                const bool now = j >= 0 && it.active(x, g, a.sinks);
+                const bool next = js < it.n && it.active(x, gs, a.sinks);
+                const uint32_t u = uniform(
+                    (now ? 1u : 0u) | (next ? 2u : 0u) | (started ? 4u : 0u) | (pp & 1u) << 3 |
+                    (sp & 1u) << 4 | (js == it.n - 1 ? 32u : 0u) | (j >= 0 ? 64u : 0u) | vs << 8 |
+                    ks << 16);
+                if (js < it.n) ok = mbar_wait_warp(&full[ks], ((kt + js) / kStages) & 1u, abort);
+                if (ok && j >= 0 && it.dirty(g, a.sinks)) {
+                    ok = mbar_wait_warp(&clean[vs], cleaned >> vs & 1u, abort);
+                    cleaned ^= 1u << vs;
                 }
-                if (js < it.n) {
-                    const uint32_t kts = j >= 0 ? kt + 1 : kt + js, ks = kts % kStages;
-                    ok = mbar_wait_warp(&k_full[ks], (kts / kStages) & 1u, abort);
-                    if (!ok) break;
-                    const bool next = it.active(x, it.page(js), a.sinks);
-                    const uint32_t u = uniform((next ? 1u : 0u) | (sp & 1u) << 1 |
-                                               (js == it.n - 1 ? 4u : 0u) | ks << 3);
-                    if (elect_one()) {
-                        if (u & 1u) issue_s(u >> 1 & 1u, u >> 3);
-                        else mbar_arrive(&k_empty[u >> 3]);
-                        if (u & 4u) umma_commit(q_free);  // the item's last scores
-                    }
-                    __syncwarp();
-                    sp += next;
+                if (ok && now)
+                    ok = mbar_wait_warp(&p_full[2 * x + (pp & 1u)], (pp >> 1) & 1u, abort);
+                if (ok && now && !started && outs++ > 0)  // O_x of the item before is out
+                    ok = mbar_wait_warp(&o_free[x], (outs - 2) & 1u, abort);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    if (u & 1u) issue_pv(u >> 3 & 1u, u >> 8 & 0xffu, u & 4u);
+                    else if (u & 64u) mbar_arrive(&empty[u >> 8 & 0xffu]);
+                    if (u & 2u) issue_s(u >> 4 & 1u, u >> 16);
+                    if (u & 32u) umma_commit(q_free);  // the item's last scores
                 }
+                __syncwarp();
+                started |= now;
+                pp += now;
+                sp += next;
             }
+            kt += it.n;
         }
         // arrives once every MMA issued has completed (TMEM is freed after it)
         if (elect_one()) umma_commit(mma_done);
@@ -387,7 +362,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
             if (idx + step < a.items) next_L = clamped_len(a, idx + step);
             for (int j = 0; j < it.n; ++j, ++kt) {
                 const uint32_t s = kt % kStages;
-                ok = mbar_wait_warp(&v_full[s], (kt / kStages) & 1u, abort);
+                ok = mbar_wait_warp(&full[s], (kt / kStages) & 1u, abort);
                 if (!ok) break;
                 const int g = it.page(j);
                 if (it.dirty(g, a.sinks)) {
@@ -398,9 +373,9 @@ __global__ void __launch_bounds__(kWinThreads, 1)
                                 sts128(vs + h * kPageHalf + e * 16, 0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&v_clean[s]);
+                    if (lane == 0) mbar_arrive(&clean[s]);
                 }
-                if (lane == 0) mbar_arrive(&v_empty[s]);
+                if (lane == 0) mbar_arrive(&empty[s]);
             }
         }
     } else {
