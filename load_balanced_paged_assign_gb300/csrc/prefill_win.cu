@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         uint32_t sp = 0, pp = 0;  // score pages issued, P pages taken
         uint32_t outs = 0;        // items whose O_x has been claimed
         for (int idx = blockIdx.x; ok && idx < a.items; idx += step) {
-            const Item it = item_of(a, idx, next_L);
+            const Item it = item_of(a, idx, (int)uniform(next_L));
             if (idx + step < a.items) next_L = clamped_len(a, idx + step);
             if (it.n == 0) continue;
             bool started = false;
@@ -322,10 +322,6 @@ __global__ void __launch_bounds__(kWinThreads, 1)
                 const uint32_t ks = (kt + js) % kStages, vs = (kt + j) % kStages;
                 const bool now = j >= 0 && it.active(x, g, a.sinks);
                 const bool next = js < it.n && it.active(x, gs, a.sinks);
-                const uint32_t u = uniform(
-                    (now ? 1u : 0u) | (next ? 2u : 0u) | (started ? 4u : 0u) | (pp & 1u) << 3 |
-                    (sp & 1u) << 4 | (js == it.n - 1 ? 32u : 0u) | (j >= 0 ? 64u : 0u) | vs << 8 |
-                    ks << 16);
                 if (js < it.n) ok = mbar_wait_warp(&full[ks], ((kt + js) / kStages) & 1u, abort);
                 if (ok && j >= 0 && it.dirty(g, a.sinks)) {
                     ok = mbar_wait_warp(&clean[vs], cleaned >> vs & 1u, abort);
@@ -338,10 +334,10 @@ __global__ void __launch_bounds__(kWinThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    if (u & 1u) issue_pv(u >> 3 & 1u, u >> 8 & 0xffu, u & 4u);
-                    else if (u & 64u) mbar_arrive(&empty[u >> 8 & 0xffu]);
-                    if (u & 2u) issue_s(u >> 4 & 1u, u >> 16);
-                    if (u & 32u) umma_commit(q_free);  // the item's last scores
+                    if (now) issue_pv(pp & 1u, vs, started);
+                    else if (j >= 0) mbar_arrive(&empty[vs]);
+                    if (next) issue_s(sp & 1u, ks);
+                    if (js == it.n - 1) umma_commit(q_free);  // the item's last scores
                 }
                 __syncwarp();
                 started |= now;
