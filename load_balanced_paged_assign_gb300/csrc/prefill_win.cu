@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
     volatile int *abort = reinterpret_cast<volatile int *>(smem + kOffMisc + 4);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         // arrivals: one (an expect-tx arrival or a tcgen05.commit), but from a Q
         // tile's four warps on p_full and o_free, all eight at the end, both MMA
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         uint32_t kt = 0;       // pages issued
         uint32_t q_items = 0;  // items whose Q has been issued
         for (int idx = blockIdx.x; ok && idx < a.items; idx += step) {
-            const Item it = item_of(a, idx, next_L);
+            const Item it = item_of(a, idx, (int)uniform(next_L));
             if (lane == 0 && a.flags && it.hq == 0 && it.i0 == 0) {
                 const int raw = __ldg(a.seqlens + it.r);
                 if (raw < 0 || raw > a.max_pages * kTile)
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
             __syncwarp();
         }
     } else if (warp < kCleanWarp && warp >= kMmaWarp) {
-        const int x = (int)uniform(warp - kMmaWarp);  // the Q tile
+        const int x = warp - kMmaWarp;  // the Q tile
         const uint32_t idesc_s = idesc_bf16_f32(kQB, kTile);
         const uint32_t idesc_o = idesc_bf16_f32_bmn(kQB, kHeadDim);
         const uint64_t dq0 = smem_desc_k128(smem_u32(smem + kOffQ));
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         // so that its stage's phases cannot run away from it)
         uint32_t kt = 0;
         for (int idx = blockIdx.x; ok && idx < a.items; idx += step) {
-            const Item it = item_of(a, idx, next_L);
+            const Item it = item_of(a, idx, (int)uniform(next_L));
             if (idx + step < a.items) next_L = clamped_len(a, idx + step);
             for (int j = 0; j < it.n; ++j, ++kt) {
                 const uint32_t s = kt % kStages;
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         const float sc = a.score_scale;
         uint32_t ns = 0;  // score pages taken
         for (int idx = blockIdx.x; ok && idx < a.items; idx += step) {
-            const Item it = item_of(a, idx, next_L);
+            const Item it = item_of(a, idx, (int)uniform(next_L));
             if (idx + step < a.items) next_L = clamped_len(a, idx + step);
             if (x > 0 && it.single) continue;
             const int first = it.i0 + x * kQB;
