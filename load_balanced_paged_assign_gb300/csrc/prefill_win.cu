@@ -54,7 +54,7 @@ constexpr int kOffK = kOffQ + kQT * kTileBytes;
 constexpr int kOffV = kOffK + kStages * kPageBytes;
 constexpr int kOffO = kOffV + kStages * kPageBytes;  // [x]: half of an output tile, BF16
 constexpr int kOffBar = kOffO + kQT * kHalf;
-// barriers: q_full, q_free, full[S], clean[S], empty[S], s_full[x][2],
+// barriers: q_full, q_free, full[S], ready[S], empty[S], s_full[x][2],
 // p_full[x][2], o_done[x][2], o_free[x], mma_done, end
 constexpr int kNumBars = 2 + 3 * kStages + 7 * kQT + 2;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;  // tmem slot, abort word
@@ -72,6 +72,15 @@ struct WinArgs {
     float score_scale;  // sm_scale * log2(e)
 };
 
+// What a Q tile sees of an item's KV pages: the first n1, and those from n1 +
+// gap on, cnt in all.
+struct Seen {
+    int n1, gap, cnt;
+    __device__ __forceinline__ bool sees(int c) const {
+        return c < n1 || (c >= n1 + gap && c < gap + cnt);
+    }
+};
+
 // One item: a request, a query head and a pair of Q tiles (or one of them, the
 // first of the two then), with the KV pages it reads.
 struct Item {
@@ -79,25 +88,22 @@ struct Item {
     int r, hq, i0, L;
     int n;                 // its KV pages
     int sink_pages, skip;  // pages that hold sinks; pages left out behind them
-    int lo[kQT];           // first token of the window of each Q tile's first query
-    int lim[kQT];          // last token its last query sees (-1: none)
+    int lo;                // first token of the window of its first query
+    Seen a, b;             // what the first and the second Q tile see of its pages
 
     // the item's page c among the request's
     __device__ __forceinline__ int page(int c) const { return c < sink_pages ? c : c + skip; }
-    // some query of Q tile x sees a token of page g
-    __device__ __forceinline__ bool active(int x, int g, int sinks) const {
-        const int t = g * kTile;
-        return t <= lim[x] && (t + kTile > lo[x] || t < sinks);
-    }
+    // (selected, not indexed: an item stays in registers)
+    __device__ __forceinline__ Seen seen(int x) const { return x ? b : a; }
     // no query of the pair sees token t: past the end, or before the window
     // and no sink
     __device__ __forceinline__ bool dead(int t, int sinks) const {
-        return t >= L || (t < lo[0] && t >= sinks);
+        return t >= L || (t < lo && t >= sinks);
     }
     // page g holds such a token
     __device__ __forceinline__ bool dirty(int g, int sinks) const {
         const int t = g * kTile;
-        return t + kTile > L || max(t, sinks) < min(t + kTile, lo[0]);
+        return t + kTile > L || max(t, sinks) < min(t + kTile, lo);
     }
 };
 
@@ -119,21 +125,29 @@ __device__ __forceinline__ Item item_of(const WinArgs &a, int item, int L) {
     it.hq = rem % a.Hq;
     it.i0 = qp * kQT * kQB + (it.single ? ((item - a.pairs) & 1) * kQB : 0);
     it.L = L;
+    it.lo = max(L - a.q_len + it.i0 + 1 - a.window, 0);
     it.sink_pages = a.sinks / kTile + (a.sinks % kTile ? 1 : 0);
-    int last = -1;  // last token that a query of the item sees
-#pragma unroll
-    for (int x = 0; x < kQT; ++x) {
+    it.skip = max(it.lo / kTile - it.sink_pages, 0);
+    it.n = 0;
+    auto seen = [&](int x) {
+        Seen v = {0, 0, 0};
         const int first = it.i0 + x * kQB;
-        it.lo[x] = max(L - a.q_len + first + 1 - a.window, 0);
-        it.lim[x] = -1;
-        if (first < a.q_len && (x == 0 || !it.single))
-            it.lim[x] = min(L - a.q_len + min(first + kQB - 1, a.q_len - 1), L - 1);
-        last = max(last, it.lim[x]);
-    }
-    it.skip = max(it.lo[0] / kTile - it.sink_pages, 0);
-    // (a window's first page is not behind the last token its query sees, so
-    // with a gap the count does not fall below the sinks')
-    it.n = last < 0 ? 0 : last / kTile + 1 - it.skip;
+        // the last token its last query sees, the first of its first query's window
+        const int lim = min(L - a.q_len + min(first + kQB - 1, a.q_len - 1), L - 1);
+        const int lo = max(L - a.q_len + first + 1 - a.window, 0);
+        if (first < a.q_len && lim >= 0 && (x == 0 || !it.single)) {
+            const int last = lim / kTile;
+            v.n1 = min(it.sink_pages, last + 1);
+            v.gap = max(lo / kTile - it.skip, it.sink_pages) - v.n1;
+            v.cnt = max(last + 1 - it.skip - v.gap, v.n1);
+            // (a window's first page is not behind the last token its query sees, so
+            // with pages left out there are some behind them)
+            it.n = max(it.n, last + 1 - it.skip);
+        }
+        return v;
+    };
+    it.a = seen(0);
+    it.b = seen(1);
     return it;
 }
 
@@ -163,8 +177,8 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kOffBar);
     uint64_t *q_full = bars, *q_free = bars + 1;
     uint64_t *full = bars + 2;             // [stage]: K and V of a page have landed
-    uint64_t *clean = full + kStages;      // [stage]: the dead rows of its V are zeroed
-    uint64_t *empty = clean + kStages;     // [stage]: its products are done
+    uint64_t *ready = full + kStages;      // [stage]: and the dead rows of V are zeroed
+    uint64_t *empty = ready + kStages;     // [stage]: its products are done
     uint64_t *s_full = empty + kStages;    // [x][b]: the scores of an even or odd page
     uint64_t *p_full = s_full + 2 * kQT;    // [x][b]: its P written (four warps)
     uint64_t *o_done = p_full + 2 * kQT;    // [x][b]: O_x += P V of that page complete
@@ -176,14 +190,12 @@ __global__ void __launch_bounds__(kWinThreads, 1)
     const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         // arrivals: one (an expect-tx arrival or a tcgen05.commit), but from a Q
-        // tile's four warps on p_full and o_free, all eight at the end, both MMA
-        // warps on q_free, empty and mma_done, and the warp that zeroes rows on
-        // empty
+        // tile's four warps on p_full and o_free, all eight at the end, and for
+        // both Q tiles on q_free, empty and mma_done
         for (int b = 0; b < kNumBars; ++b) {
             uint64_t *bar = &bars[b];
             int n = 1;
-            if (bar == q_free || bar == mma_done) n = kQT;
-            if (bar >= empty && bar < s_full) n = kQT + 1;
+            if (bar == q_free || bar == mma_done || (bar >= empty && bar < s_full)) n = kQT;
             if ((bar >= p_full && bar < o_done) || (bar >= o_free && bar < mma_done)) n = 4;
             if (bar == end) n = kSoftmaxWarps;
             mbar_init(bar, n);
@@ -229,11 +241,11 @@ __global__ void __launch_bounds__(kWinThreads, 1)
             if (lane == 0) {
                 uint32_t bytes = 0;
 #pragma unroll
-                for (int x = 0; x < kQT; ++x) bytes += it.lim[x] >= 0 ? kTileBytes : 0;
+                for (int x = 0; x < kQT; ++x) bytes += it.seen(x).cnt > 0 ? kTileBytes : 0;
                 mbar_arrive_expect_tx(q_full, bytes);
 #pragma unroll
                 for (int x = 0; x < kQT; ++x)
-                    if (it.lim[x] >= 0)
+                    if (it.seen(x).cnt > 0)
                         for (int h = 0; h < 2; ++h)
                             tma_load_4d(smem + kOffQ + x * kTileBytes + h * kHalf, &tq, q_full, 0,
                                         h, it.hq, it.r * a.q_len + it.i0 + x * kQB, pol);
@@ -303,46 +315,59 @@ __global__ void __launch_bounds__(kWinThreads, 1)
             umma_commit(&empty[s]);  // (this page's scores are done too)
         };
         uint32_t kt = 0, q_items = 0;
-        uint32_t cleaned = 0;     // bit s: parity of the zeroed pages taken from stage s
         uint32_t sp = 0, pp = 0;  // score pages issued, P pages taken
         uint32_t outs = 0;        // items whose O_x has been claimed
         for (int idx = blockIdx.x; ok && idx < a.items; idx += step) {
             const Item it = item_of(a, idx, (int)uniform(next_L));
             if (idx + step < a.items) next_L = clamped_len(a, idx + step);
             if (it.n == 0) continue;
-            bool started = false;
+            const Seen sn = it.seen(x);
+            const int n1 = sn.n1, gap = sn.gap, cnt = sn.cnt;
             ok = mbar_wait_warp(q_full, q_items & 1u, abort);
             ++q_items;
             // The scores run two pages ahead of the products: both buffers are then
-            // in use, one at the softmax and one being filled.  Pages that the Q tile
-            // does not see are waited for and passed on all the same (a phase of a
-            // barrier may not be left out).
-            for (int j = -2; ok && j < it.n; ++j) {
-                const int js = j + 2, g = it.page(j), gs = it.page(js);
-                const uint32_t ks = (kt + js) % kStages, vs = (kt + j) % kStages;
-                const bool now = j >= 0 && it.active(x, g, a.sinks);
-                const bool next = js < it.n && it.active(x, gs, a.sinks);
-                if (js < it.n) ok = mbar_wait_warp(&full[ks], ((kt + js) / kStages) & 1u, abort);
-                if (ok && j >= 0 && it.dirty(g, a.sinks)) {
-                    ok = mbar_wait_warp(&clean[vs], cleaned >> vs & 1u, abort);
-                    cleaned ^= 1u << vs;
-                }
-                if (ok && now)
+            // in use, one at the softmax and one being filled.  (Pages that the Q
+            // tile does not see are passed by: at most two together, and all of an
+            // item have landed when the next one's Q has, so a stage's phases are
+            // met in order.)
+            uint32_t ks = kt + (n1 == 0 ? gap : 0), vs = ks;  // pages of the next scores, products
+            for (int c = -2; c < cnt; ++c) {
+                const bool next = c + 2 < cnt;
+                // behind a gap the next page waits for the stage that this product frees
+                const bool late = next && ks - vs >= kStages;
+                if (next && !late)
+                    ok = mbar_wait_warp(&ready[ks % kStages], (ks / kStages) & 1u, abort);
+                if (ok && c >= 0) {
                     ok = mbar_wait_warp(&p_full[2 * x + (pp & 1u)], (pp >> 1) & 1u, abort);
-                if (ok && now && !started && outs++ > 0)  // O_x of the item before is out
-                    ok = mbar_wait_warp(&o_free[x], (outs - 2) & 1u, abort);
+                    if (ok && c == 0 && outs++ > 0)  // O_x of the item before is out
+                        ok = mbar_wait_warp(&o_free[x], (outs - 2) & 1u, abort);
+                }
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    if (now) issue_pv(pp & 1u, vs, started);
-                    else if (j >= 0) mbar_arrive(&empty[vs]);
-                    if (next) issue_s(sp & 1u, ks);
-                    if (js == it.n - 1) umma_commit(q_free);  // the item's last scores
+                    if (c >= 0) issue_pv(pp & 1u, vs % kStages, c > 0);
+                    if (next && !late) issue_s(sp & 1u, ks % kStages);
                 }
                 __syncwarp();
-                started |= now;
-                pp += now;
-                sp += next;
+                if (late) {
+                    ok = mbar_wait_warp(&ready[ks % kStages], (ks / kStages) & 1u, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) issue_s(sp & 1u, ks % kStages);
+                    __syncwarp();
+                }
+                if (c + 3 == cnt || (c == -2 && cnt < 2)) {  // the item's last scores
+                    if (elect_one()) umma_commit(q_free);
+                    __syncwarp();
+                }
+                if (c >= 0) {
+                    ++pp;
+                    vs += c + 1 == n1 ? gap + 1 : 1;
+                }
+                if (next) {
+                    ++sp;
+                    ks += c + 3 == n1 ? gap + 1 : 1;
+                }
             }
             kt += it.n;
         }
@@ -350,8 +375,8 @@ __global__ void __launch_bounds__(kWinThreads, 1)
         if (elect_one()) umma_commit(mma_done);
         __syncwarp();
     } else if (warp == kCleanWarp) {
-        // zeroes the V rows that no query of the pair sees (it passes every page,
-        // so that its stage's phases cannot run away from it)
+        // zeroes the V rows that no query of the pair sees, and lets go of a page
+        // for a Q tile that does not see it
         uint32_t kt = 0;
         for (int idx = blockIdx.x; ok && idx < a.items; idx += step) {
             const Item it = item_of(a, idx, (int)uniform(next_L));
@@ -369,9 +394,13 @@ __global__ void __launch_bounds__(kWinThreads, 1)
                                 sts128(vs + h * kPageHalf + e * 16, 0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&clean[s]);
                 }
-                if (lane == 0) mbar_arrive(&empty[s]);
+                if (lane == 0) {
+                    mbar_arrive(&ready[s]);
+#pragma unroll
+                    for (int x = 0; x < kQT; ++x)
+                        if (!it.seen(x).sees(j)) mbar_arrive(&empty[s]);
+                }
             }
         }
     } else {
@@ -392,11 +421,11 @@ __global__ void __launch_bounds__(kWinThreads, 1)
             const int p0 = it.L - a.q_len + first + 32 * q4;
             const int lim = min(p0 + lane, it.L - 1), lo = p0 + lane + 1 - a.window;
             const int lim_all = min(p0, it.L - 1), lo_all = p0 + 32 - a.window;
+            const Seen sn = it.seen(x);
             float m_ref = -INFINITY, l = 0.f;
             bool started = false;
-            for (int j = 0; j < it.n; ++j) {
-                const int g = it.page(j), t = g * kTile;
-                if (!it.active(x, g, a.sinks)) continue;
+            for (int c = 0; c < sn.cnt; ++c) {
+                const int t = it.page(c < sn.n1 ? c : c + sn.gap) * kTile;
                 const uint32_t b = ns & 1u;
                 if (!mbar_wait_warp(&s_full[2 * x + b], (ns >> 1) & 1u, abort)) {
                     ok = false;
