@@ -67,6 +67,7 @@ struct WinArgs {
     __nv_bfloat16 *out;
     int32_t *flags;
     int B, Hq, G, q_len, max_pages, num_pages, n_qp;
+    int heads;         // query heads of a pair: 2 (of one Q tile each), or 1 (of two)
     int pairs, items;  // items: `pairs` pairs of Q tiles, then single Q tiles
     int window, sinks;
     float score_scale;  // sm_scale * log2(e)
@@ -81,11 +82,14 @@ struct Seen {
     }
 };
 
-// One item: a request, a query head and a pair of Q tiles (or one of them, the
-// first of the two then), with the KV pages it reads.
+// One item: a request and a pair of Q tiles (or one of them, the first of the
+// two then), with the KV pages it reads.  A pair is the same rows of two query
+// heads of a KV head, which see the same pages, where the group is even, and
+// else two tiles of one head.
 struct Item {
     bool single;
     int r, hq, i0, L;
+    int dh, di;            // the second tile's head and first row, less the first's
     int n;                 // its KV pages
     int sink_pages, skip;  // pages that hold sinks; pages left out behind them
     int lo;                // first token of the window of its first query
@@ -119,11 +123,14 @@ __device__ __forceinline__ Item item_of(const WinArgs &a, int item, int L) {
     Item it;
     const int idx = pair_of(a, item);
     it.single = item >= a.pairs;
-    const int per_qp = a.B * a.Hq;
+    const int per_req = a.Hq / a.heads, per_qp = a.B * per_req;
     const int qp = a.n_qp - 1 - idx / per_qp, rem = idx % per_qp;
-    it.r = rem / a.Hq;
-    it.hq = rem % a.Hq;
-    it.i0 = qp * kQT * kQB + (it.single ? ((item - a.pairs) & 1) * kQB : 0);
+    const int second = it.single ? (item - a.pairs) & 1 : 0;
+    it.dh = a.heads - 1;
+    it.di = a.heads == 2 ? 0 : kQB;
+    it.r = rem / per_req;
+    it.hq = rem % per_req * a.heads + second * it.dh;
+    it.i0 = qp * (kQB + it.di) + second * it.di;
     it.L = L;
     it.lo = max(L - a.q_len + it.i0 + 1 - a.window, 0);
     it.sink_pages = a.sinks / kTile + (a.sinks % kTile ? 1 : 0);
@@ -131,7 +138,7 @@ __device__ __forceinline__ Item item_of(const WinArgs &a, int item, int L) {
     it.n = 0;
     auto seen = [&](int x) {
         Seen v = {0, 0, 0};
-        const int first = it.i0 + x * kQB;
+        const int first = it.i0 + x * it.di;
         // the last token its last query sees, the first of its first query's window
         const int lim = min(L - a.q_len + min(first + kQB - 1, a.q_len - 1), L - 1);
         const int lo = max(L - a.q_len + first + 1 - a.window, 0);
@@ -162,7 +169,8 @@ __device__ __forceinline__ uint64_t bits_to(int k) {
 }
 
 __device__ __forceinline__ int clamped_len(const WinArgs &a, int item) {
-    const int L = __ldg(a.seqlens + pair_of(a, item) % (a.B * a.Hq) / a.Hq);
+    const int per_req = a.Hq / a.heads;
+    const int L = __ldg(a.seqlens + pair_of(a, item) % (a.B * per_req) / per_req);
     return min(max(L, 0), a.max_pages * kTile);
 }
 
@@ -248,7 +256,8 @@ __global__ void __launch_bounds__(kWinThreads, 1)
                     if (it.seen(x).cnt > 0)
                         for (int h = 0; h < 2; ++h)
                             tma_load_4d(smem + kOffQ + x * kTileBytes + h * kHalf, &tq, q_full, 0,
-                                        h, it.hq, it.r * a.q_len + it.i0 + x * kQB, pol);
+                                        h, it.hq + x * it.dh,
+                                        it.r * a.q_len + it.i0 + x * it.di, pol);
             }
             ++q_items;
             const int32_t *bt = a.block_table + (size_t)it.r * a.max_pages;
@@ -416,7 +425,7 @@ __global__ void __launch_bounds__(kWinThreads, 1)
             const Item it = item_of(a, idx, (int)uniform(next_L));
             if (idx + step < a.items) next_L = clamped_len(a, idx + step);
             if (x > 0 && it.single) continue;
-            const int first = it.i0 + x * kQB;
+            const int first = it.i0 + x * it.di;
             // the tokens the row sees, and those that all of the warp's rows see
             const int p0 = it.L - a.q_len + first + 32 * q4;
             const int lim = min(p0 + lane, it.L - 1), lo = p0 + lane + 1 - a.window;
@@ -547,8 +556,8 @@ __global__ void __launch_bounds__(kWinThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0 && store && first + 32 * q4 < a.q_len) {
-                    tma_store_5d(&to, smem + kOffO + x * kHalf + 32 * q4 * 128, 0, hf, it.hq,
-                                 first + 32 * q4, it.r);
+                    tma_store_5d(&to, smem + kOffO + x * kHalf + 32 * q4 * 128, 0, hf,
+                                 it.hq + x * it.dh, first + 32 * q4, it.r);
                     bulk_commit_group();
                 }
             }
@@ -626,8 +635,10 @@ extern "C" hpc_status hpc_prefill_attn_win(const void *d_q, const void *d_k_cach
         return HPC_ERR_ARG;
     if (!aligned16(d_q) || !aligned16(d_k_cache) || !aligned16(d_v_cache) || !aligned16(d_out))
         return HPC_ERR_ARG;
-    const int64_t n_qp = ((int64_t)q_len + kQT * kQB - 1) / (kQT * kQB);
-    const int64_t pairs = n_qp * B * Hq;
+    const int G = Hq / Hkv, heads = G % 2 == 0 ? 2 : 1;
+    const int rows = heads == 2 ? kQB : kQT * kQB;  // query rows that a pair spans
+    const int64_t n_qp = ((int64_t)q_len + rows - 1) / rows;
+    const int64_t pairs = n_qp * B * (Hq / heads);
     // (items + a grid's stride, query rows and token indices stay in int32)
     if (pairs >= ((int64_t)1 << 29) || (int64_t)B * q_len >= ((int64_t)1 << 31) ||
         q_len >= kNoWindow || (int64_t)max_pages_per_req * HPC_PAGE_SIZE >= ((int64_t)1 << 30))
@@ -647,7 +658,8 @@ extern "C" hpc_status hpc_prefill_attn_win(const void *d_q, const void *d_k_cach
     a.flags = d_flags;
     a.B = B;
     a.Hq = Hq;
-    a.G = Hq / Hkv;
+    a.G = G;
+    a.heads = heads;
     a.q_len = q_len;
     a.max_pages = max_pages_per_req;
     a.num_pages = num_pages;
