@@ -48,6 +48,11 @@
 namespace hpc {
 namespace {
 
+constexpr int kKB = 128;                 // KV tokens per tile: two pages
+constexpr int kKStages = 2;              // K ring depth
+constexpr int kVStages = 2;              // V ring depth
+constexpr int kThreads = (kSoftmaxWarps + 2) * 32;
+
 // Shared-memory layout (offsets from the 1024-byte aligned base).
 constexpr int kOffQ = 0;
 constexpr int kOffK = kOffQ + kQT * kTileBytes;
@@ -68,6 +73,34 @@ struct PrefillArgs {
     int B, Hq, Hkv, G, q_len, max_pages, num_pages, n_qp;
     float score_scale;  // sm_scale * log2(e)
 };
+
+// Lane 0 waits (bounded); the verdict is broadcast and every lane then
+// observes the completed phase itself (acquire).  Warp-uniform result.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    int ok = 1;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort) ? 1 : 0;
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (ok) mbar_try_wait(bar, parity);
+    return ok != 0;
+}
+
+// The causal extent of a Q tile: its first query row, the KV tiles its rows
+// read, and the last token its first row sees.
+struct QTile {
+    int first, tiles, lim_first;
+};
+
+__device__ __forceinline__ QTile qtile(int i0, int L, int q_len) {
+    QTile t;
+    t.first = i0;
+    t.lim_first = min(L - q_len + i0, L - 1);
+    t.tiles = 0;
+    if (i0 < q_len) {
+        const int lim_last = min(L - q_len + min(i0 + kQB - 1, q_len - 1), L - 1);
+        t.tiles = lim_last >= 0 ? lim_last / kKB + 1 : 0;
+    }
+    return t;
+}
 
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_attn_kernel(const __grid_constant__ CUtensorMap tq,

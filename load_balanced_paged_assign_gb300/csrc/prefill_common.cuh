@@ -1,6 +1,6 @@
 // What the causal (prefill.cu) and the windowed (prefill_win.cu) prompt
-// attention share: tile shapes, small wrappers, the causal extent of a Q tile,
-// the tensor map over the queries.
+// attention share: the Q tiles' shape, small wrappers, the tensor map over the
+// queries.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -15,15 +15,11 @@ namespace {
 
 constexpr int kQB = 128;                 // query rows per Q tile (UMMA M)
 constexpr int kQT = 2;                   // Q tiles per CTA
-constexpr int kKB = 128;                 // KV tokens per tile: two pages
 constexpr int kHalf = 128 * 128;         // 128 rows x 64 BF16: one 128-byte column block
 constexpr int kTileBytes = 2 * kHalf;    // a 128 x 128 BF16 tile (Q, K or V)
-constexpr int kKStages = 2;              // K ring depth
-constexpr int kVStages = 2;              // V ring depth
 constexpr int kSoftmaxWarps = 4 * kQT;
 constexpr int kProducerWarp = kSoftmaxWarps, kMmaWarp = kSoftmaxWarps + 1;
-constexpr int kThreads = (kSoftmaxWarps + 2) * 32;
-constexpr uint32_t kTmemCols = 512;      // S_x / P_x at 128 x; O_x at 256 + 128 x
+constexpr uint32_t kTmemCols = 512;      // S_x / P_x from 128 x on; O_x at 256 + 128 x
 constexpr int kOCol = 256;
 constexpr float kRescaleLog2 = 8.f;      // P <= 2^8 between reference moves
 
@@ -31,16 +27,6 @@ __device__ __forceinline__ uint64_t policy_evict_normal() {
     uint64_t p;
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
     return p;
-}
-
-// Lane 0 waits (bounded); the verdict is broadcast and every lane then
-// observes the completed phase itself (acquire).  Warp-uniform result.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    int ok = 1;
-    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort) ? 1 : 0;
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    if (ok) mbar_try_wait(bar, parity);
-    return ok != 0;
 }
 
 // max(a, b, c) in one instruction.
@@ -55,24 +41,6 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
                  "r"(d)
                  : "memory");
-}
-
-// The causal extent of a Q tile: its first query row, the KV tiles its rows
-// read, and the last token its first row sees.
-struct QTile {
-    int first, tiles, lim_first;
-};
-
-__device__ __forceinline__ QTile qtile(int i0, int L, int q_len) {
-    QTile t;
-    t.first = i0;
-    t.lim_first = min(L - q_len + i0, L - 1);
-    t.tiles = 0;
-    if (i0 < q_len) {
-        const int lim_last = min(L - q_len + min(i0 + kQB - 1, q_len - 1), L - 1);
-        t.tiles = lim_last >= 0 ? lim_last / kKB + 1 : 0;
-    }
-    return t;
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

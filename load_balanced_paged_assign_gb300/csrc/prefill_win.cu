@@ -2,29 +2,36 @@
 // the fifth-generation tensor cores: query position p sees token j <= p when
 // j > p - window or j < sinks.
 //
-// The tile work is the causal kernel's (prefill.cu): two 128-row Q tiles share
-// every 128-token K/V tile, S_x = Q_x K^T into TMEM, one softmax thread per row
-// writing P over the scores, O_x += P_x V with P read from TMEM.  What differs
-// follows from a window's items being short (a window of 1024 tokens is 10
-// tiles where a causal 8K prompt averages 33):
-//   * the CTAs are persistent, one per SM, and an item's start and end overlap
-//     its neighbours': the producer brings the next item's Q as soon as the last
-//     scores are computed and keeps the K/V ring filled across items, the next
-//     item's first scores are issued while this one's output is read out, and
-//     TMEM and barriers are set up once.  (One CTA per item, as the causal
-//     kernel has them, took 390 us instead of 375 on 8192 queries of 64 heads
-//     with a window of 1024, and 202 instead of 186 on 2 x 1000 with 2000.)
-//   * an item's KV pages are its sink pages and those from its first query's
-//     window on, numbered through and taken two to a tile (so a tile may join
-//     the last sink page and the first window page); no other page is looked up
-//     or loaded, and the second Q tile skips a tile that only the first one sees;
-//   * a tile's masked scores are overwritten in TMEM before the softmax reads
-//     them, and the output goes out by TMA through shared memory: both kept the
-//     softmax warps from their next tile, a masked tile for as long again as its
-//     softmax, the output rows for 4700 cycles an item;
-//   * a tile with a dead row (past L_r, or before the window and no sink) has
-//     those rows of V zeroed by the producer once they have landed, and is
-//     handed over on its own barrier (0 * NaN would reach O).
+// Two 128-row Q tiles share every KV page: S = Q_x K^T into TMEM, one softmax
+// thread per row (online, in fp32: a reference that moves when a score passes it
+// by 2^8, P written over the scores as BF16, half a step of 2^-8, the row sum from
+// the unrounded weights), O_x += P V with P read from TMEM.  What bounds it is the
+// tensor pipe: at N = 64 the scores' MMAs are limited by their operands' reads
+// from shared memory (A 32 KB + B 16 KB at 128 bytes a cycle, 384 cycles; O's take
+// 256), 1280 cycles a page for both Q tiles where a page takes 1400.
+//   * The unit is a page, not two.  A Q tile has two 64-column score buffers in
+//     TMEM, and its scores run two pages ahead of its products, so that the
+//     softmax of a page meets the next one's scores ready (with one buffer of 128
+//     it waited for 2100 to 2600 of a tile's 5300 cycles).  Only pages that some
+//     row sees are computed, and 64 scores leave registers for the masks.
+//   * Each Q tile has its own MMA warp: an issuing warp stands still while its
+//     MMAs wait for the pipe, and one for both tiles left the pipe idle for half
+//     of a page.  What these warps compute per page is held to a few uniform
+//     instructions, and one barrier stands for a page of K and V.
+//   * Where the GQA group is even a pair is the same rows of two heads: both Q
+//     tiles see the same pages (18 instead of 20 with a window of 1024) and end
+//     together.  Else it is two Q tiles of one head.
+//   * The CTAs are persistent, one per SM: the next item's Q and pages come in
+//     while this one's last scores are taken, and its first scores are computed
+//     while the output goes out, by TMA through shared memory.  (Reading O out by
+//     warps of their own costs the softmax its registers: 231 and 246 us against
+//     231; stores of 32 bytes a lane instead of TMA: 238.)
+//   * Tokens that no query of the pair sees (past L_r, or before the window and no
+//     sink) may hold anything: a warp of its own zeroes their V rows once the page
+//     has landed (0 * NaN would reach O) and passes every page on.
+// 8192 queries of 64 heads with a window of 1024 and 64 sinks (273 GFLOP): 231 us,
+// 1180 TFLOP/s; 2 x 1000 behind 3111 tokens with a window of 2000: 122 us.
+//
 // All barrier phases are counted across items.  Every wait is bounded; on a
 // timeout the CTA raises the error flag, waits (bounded) for its copies and
 // MMAs in flight, frees TMEM and leaves.
@@ -64,7 +71,6 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory over the per-CTA limit");
 struct WinArgs {
     const int32_t *seqlens;
     const int32_t *block_table;
-    __nv_bfloat16 *out;
     int32_t *flags;
     int B, Hq, G, q_len, max_pages, num_pages, n_qp;
     int heads;         // query heads of a pair: 2 (of one Q tile each), or 1 (of two)
@@ -654,7 +660,6 @@ extern "C" hpc_status hpc_prefill_attn_win(const void *d_q, const void *d_k_cach
     WinArgs a;
     a.seqlens = d_seqlens;
     a.block_table = d_block_table;
-    a.out = static_cast<__nv_bfloat16 *>(d_out);
     a.flags = d_flags;
     a.B = B;
     a.Hq = Hq;
