@@ -9,12 +9,13 @@
 // below 2^-6 are subnormal), and a block that grows over several calls is
 // re-scaled exactly.
 //
-// Both are streaming kernels bound by HBM (a token's fused QKV row in, queries
-// and codes out; codes in, BF16 rows out); the comments at the kernels say how
-// the work is cut.
+// Both stream a token's data through once (its fused QKV row in, queries and
+// codes out; codes in, BF16 rows out); the comments at the kernels say how the
+// work is cut and what they reach.
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "internal.h"
@@ -228,16 +229,22 @@ __device__ __forceinline__ void write_run(const BlockWriteArgs &a, const BlockWr
     }
 }
 
-// Query rows 8 b .. 8 b + 7 of a token (half-warp `half` holds 8 b + 2 i + half).
-template <int LAYOUT, bool NF, bool Q8>
-__device__ __forceinline__ void write_queries(const BlockWriteArgs &a, const float *tab, int t,
-                                              int b, int lane) {
+// Query rows 8 b .. 8 b + 7 of a token (half-warp `half` holds 8 b + 2 i + half):
+// their words, and from them the outputs.
+template <int LAYOUT>
+__device__ __forceinline__ void load_queries(const BlockWriteArgs &a, int t, int b, int lane,
+                                             uint4 (&v)[4]) {
     const int half = lane >> 4, s = lane & 15;
     const char *src = reinterpret_cast<const char *>(a.qkv + (size_t)t * a.stride);
-    uint4 v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         v[i] = load_words<LAYOUT>(src + (size_t)min(8 * b + 2 * i + half, a.Hq - 1) * kRowBytes, s);
+}
+
+template <int LAYOUT, bool NF, bool Q8>
+__device__ __forceinline__ void write_queries(const BlockWriteArgs &a, const float *tab, int t,
+                                              int b, int lane, const uint4 (&v)[4]) {
+    const int half = lane >> 4, s = lane & 15;
     float c[4], sn[4], nsn[4], w[8];
     load_angles(tab, s, c, sn, nsn);
     unpack8(load_words<LAYOUT>(reinterpret_cast<const char *>(a.q_w), s), w);
@@ -272,12 +279,17 @@ __device__ __forceinline__ void write_queries(const BlockWriteArgs &a, const flo
 // one if its (request, position / 16) is not its predecessor's.  Work items
 // (a run's rows of one head, K or V; 8 query rows of a token) go round the
 // eight warps.  Each row is read once, straight into registers (16 bytes a
-// lane, 4 to 8 rows in flight per half-warp).
-#ifndef HPC_BW_CTAS
-#define HPC_BW_CTAS 3  // resident CTAs per SM the register budget must allow
-#endif
+// lane, 4 to 8 rows in flight per half-warp), the next query item's while this
+// one's are worked on.  8192 tokens of 64 + 2 x 8 heads, BF16 queries (319 MB):
+// 65 us, 72% of the measured copy rate (71 us without the look-ahead); chunks of
+// 6 to 15 tokens are within 1%, four resident CTAs (64 registers) spill and two
+// take 81 us, and prefetching the rows to L2 at the start costs 9 us more.  What
+// bounds it is the latency of each item's chain of shuffles and conversions at 24
+// warps per SM, the warps the registers allow.
+constexpr int kBwCtas = 3;  // resident CTAs per SM the register budget must allow
 template <int LAYOUT, bool NF, bool Q8>
-__global__ void __launch_bounds__(kBwThreads, HPC_BW_CTAS) rope_norm_block_kernel(const BlockWriteArgs a) {
+__global__ void __launch_bounds__(kBwThreads, kBwCtas)
+    rope_norm_block_kernel(const BlockWriteArgs a) {
     __shared__ __align__(16) BlockWriteShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dependency_wait();  // everything read may come from the kernel before
@@ -342,15 +354,25 @@ __global__ void __launch_bounds__(kBwThreads, HPC_BW_CTAS) rope_norm_block_kerne
     __syncthreads();
     const int per_run = 2 * a.Hkv, kv_items = sh.runs * per_run;
     const int per_token = (a.Hq + 7) / 8, items = kv_items + own * per_token;
-    for (int it = warp; it < items; it += kBwWarps) {
-        if (it < kv_items) {
-            const int r = it / per_run, h = it - r * per_run;
-            if (h < a.Hkv) write_run<LAYOUT, NF, true>(a, sh, t0, sh.run[r], h, lane);
-            else write_run<LAYOUT, NF, false>(a, sh, t0, sh.run[r], h - a.Hkv, lane);
-        } else {
-            const int q = it - kv_items, k = q / per_token;
-            write_queries<LAYOUT, NF, Q8>(a, sh.ang + k * 128, t0 + k, q - k * per_token, lane);
-        }
+    int it = warp;
+    for (; it < kv_items; it += kBwWarps) {
+        const int r = it / per_run, h = it - r * per_run;
+        if (h < a.Hkv) write_run<LAYOUT, NF, true>(a, sh, t0, sh.run[r], h, lane);
+        else write_run<LAYOUT, NF, false>(a, sh, t0, sh.run[r], h - a.Hkv, lane);
+    }
+    // (an item's rows are loaded while the last one's are worked on)
+    uint4 v[4], next[4];
+    int k = (it - kv_items) / per_token, b = it - kv_items - k * per_token;
+    if (it < items) load_queries<LAYOUT>(a, t0 + k, b, lane, v);
+    while (it < items) {
+        it += kBwWarps;
+        const int k1 = (it - kv_items) / per_token, b1 = it - kv_items - k1 * per_token;
+        if (it < items) load_queries<LAYOUT>(a, t0 + k1, b1, lane, next);
+        write_queries<LAYOUT, NF, Q8>(a, sh.ang + k * 128, t0 + k, b, lane, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = next[i];
+        k = k1;
+        b = b1;
     }
 }
 
@@ -413,7 +435,8 @@ __device__ __forceinline__ void widen16(uint4 q, float f, uint4 *dst) {
 // once per CTA), so a batch of very different lengths, or one request alone,
 // loads the SMs evenly.  A block's tokens are contiguous for all heads: a
 // thread takes 16 codes (16 bytes in, 32 out) of K and the same of V at a
-// time, two of each in flight.
+// time, two of each in flight.  8192 tokens of 8 heads (50 MB): 9 to 10 us, a
+// launch and 74 to 83% of the measured copy rate; HBM bounds it.
 __global__ void __launch_bounds__(kRdThreads) kv_read_block_kernel(const BlockReadArgs a) {
     extern __shared__ int s_end[];  // [B] blocks of the requests up to and with r
     __shared__ int s_scan[kRdThreads / 32];
@@ -497,11 +520,18 @@ __global__ void __launch_bounds__(kRdThreads) kv_read_block_kernel(const BlockRe
 bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+std::atomic<int> g_sms[64];  // per device, once asked for
+
+// SMs of the current device, or -1.
 int sm_count() {
     int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
+    sms = g_sms[dev].load();
+    if (sms == 0) {
+        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return -1;
+        g_sms[dev].store(sms);
+    }
     return sms;
 }
 
