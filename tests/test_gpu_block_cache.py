@@ -208,6 +208,42 @@ def test_no_tokens_and_token_t_is_request_t():
     assert torch.equal(s, s2.view(torch.uint8))
 
 
+def test_write_and_read_of_pages_beyond_32_bit_offsets():
+    """The same tokens into the end of a cache of more than 2^32 bytes."""
+    pro = Prologue([(r, p) for r in range(2) for p in range(30, 70)], 16, 8, 2, 2, seed=18).run()
+    P = pro.P
+    N = P + (5 << 30) // (64 * 8 * 128)
+    at = (N - 1 - torch.arange(P)).cuda()
+    far = []
+    for host in (*pro.codes0, pro.scale0):
+        t = torch.from_numpy(host.copy()).cuda()
+        big = torch.empty((N,) + t.shape[1:], dtype=t.dtype, device="cuda")
+        big[at] = t
+        far.append(big)
+    k, v, s = far[0].view(E4M3), far[1].view(E4M3), far[2]
+    table = torch.from_numpy(N - 1 - pro.table).cuda()
+    q, qs = torch.zeros_like(pro.q), torch.zeros_like(pro.qs)
+    hd.hpc_rope_norm_block(pro.full.cuda(), pro.wq.cuda(), pro.wk.cuda(),
+                           torch.from_numpy(pro.pos).cuda(), torch.from_numpy(pro.req).cuda(), 16,
+                           8, table, k, v, s, q, qs)
+    for big, small in ((k, pro.k), (v, pro.v)):
+        assert torch.equal(big.view(torch.uint8)[at], small.view(torch.uint8))
+    assert torch.equal(s[at], pro.scale)
+    assert torch.equal(q.view(torch.uint8), pro.q.view(torch.uint8)) and torch.equal(qs, pro.qs)
+    lens = torch.tensor([70, 70], dtype=torch.int32, device="cuda")
+    outs = []
+    for kc, vc, sc, bt in ((k, v, s, table),
+                           (pro.k, pro.v, pro.scale, torch.from_numpy(pro.table).cuda())):
+        out = [torch.zeros((4, 64, 8, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        hd.hpc_kv_read_block(kc, vc, sc, bt, None, lens, 8, *out,
+                             torch.arange(4, dtype=torch.int32, device="cuda").view(2, 2))
+        outs.append(out)
+    for i in range(2):
+        assert torch.equal(outs[0][i].view(torch.int16), outs[1][i].view(torch.int16))
+    del far, k, v, s
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------------ read back
 def run_read(codes, scale, table, starts, lens, Hkv, out_pages, out_table, fill=-77.0):
     k, v = (torch.from_numpy(c).cuda().view(E4M3) for c in codes)

@@ -358,6 +358,75 @@ def test_windowed_prefill_of_several_rounds(q_len, heads):
     assert torch.isfinite(out.float()).all()
 
 
+@pytest.mark.parametrize("q_len", [300, 520, 700])
+def test_windowed_prefill_of_several_rounds_of_an_odd_group(q_len):
+    """Three query heads to a KV head: pairs are two Q tiles of a head (300 leaves
+    the second of the last pair without rows), their last round cut into single
+    tiles; requests shorter than q_len leave the first tile without tokens."""
+    c = Case("bf16", [q_len, q_len + 200, q_len - 290], 63, 21, q_len, 90, 70, seed=508).to_gpu()
+    c.check(run_prefill(c))
+
+
+@pytest.mark.parametrize("heads", [(4, 2), (3, 1)])
+@pytest.mark.parametrize("win", [(5000, 0), (4096, 130), (64, 2500), (6000, 1)])
+def test_windowed_prefill_of_many_pages(heads, win):
+    """More pages than a warp fetches entries of at once, sinks among them."""
+    c = Case("bf16", [6000, 4200, 130], *heads, 200, *win, seed=509).to_gpu()
+    c.check(run_prefill(c))
+
+
+@pytest.mark.parametrize("kv", KINDS)
+def test_requests_that_share_pages(kv):
+    """A common prefix: the same pages in several rows of the block table, and one
+    page twice in a row."""
+    c = Case(kv, [700, 640, 300], 8, 2, 2, 260, 20, seed=510, poison=False)
+    c.table[1, :6] = c.table[0, :6]
+    c.table[2, :3] = c.table[0, :3]
+    c.table[0, 9] = c.table[0, 8]
+    c.to_gpu()
+    got, _ = c.step()
+    c.check(got)
+    if kv == "bf16":
+        c.check(run_prefill(c))
+
+
+@pytest.mark.parametrize("kv", KINDS)
+def test_pages_beyond_32_bit_offsets(kv):
+    """The same pages at the end of a cache of more than 2^32 bytes."""
+    c = Case(kv, [300, 700], 16, 8, 1, 200, 70, seed=512, poison=False).to_gpu()
+    near, _ = c.step()
+    if kv == "bf16":
+        near_prefill = run_prefill(c)
+    P = c.k.shape[0]
+    N = P + (5 << 30) // (c.k[0].numel() * c.k.element_size())
+    at = (N - 1 - torch.arange(P)).cuda()
+    for name in ("k", "v", "scale"):
+        t = getattr(c, name)
+        if t is not None:
+            far = torch.empty((N,) + t.shape[1:], dtype=t.dtype, device="cuda")
+            far.view(torch.uint8)[at] = t.view(torch.uint8)
+            setattr(c, name, far)
+    c.bt = torch.where(c.bt >= 0, N - 1 - c.bt, c.bt)
+    got, _ = c.step()
+    assert torch.equal(got.view(torch.int16), near.view(torch.int16))
+    if kv == "bf16":
+        assert torch.equal(run_prefill(c).view(torch.int16), near_prefill.view(torch.int16))
+    del c
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("kv", KINDS)
+def test_more_split_units_than_a_cta_keeps_for_the_end(kv):
+    """Thousands of bins of one tile: a CTA completes more split units than it
+    lists (16), and merges the others on the spot."""
+    rng = np.random.default_rng(9)
+    lens = [int(x) for x in rng.integers(65, 300, 1300)]
+    c = Case(kv, lens, 8, 4, 1, 150, 3, seed=511).to_gpu()
+    for fused in (True, False):
+        got, ws = c.step(ctas=16000, floor=1, fused=fused)
+        c.check(got)
+
+
 def test_prefill_without_a_window_is_the_plain_call():
     w = Workload("pw", 2, 4, 2, seqlens=(300, 700), seed=503, q_len=290)
     b = make_batch(w, device="cuda", poison_tail=True)
