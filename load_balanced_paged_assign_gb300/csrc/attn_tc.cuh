@@ -1023,7 +1023,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     volatile int *abort = reinterpret_cast<volatile int *>(smem + Tr::kOffMisc);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Tr::kOffMisc + 4);
     SlotInfo *last = reinterpret_cast<SlotInfo *>(smem + Tr::kOffLast);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&bar.full[s], 1);   // producer arrive + bytes
@@ -1044,6 +1044,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         prefetch_tensormap(&tmap_k);
         prefetch_tensormap(&tmap_v);
     }
+    if (warp == 0) {  // needs the barriers only, which it has set up itself
+        __syncwarp();
+        asm volatile("barrier.cta.arrive 4, %0;" ::"n"(kTcThreads) : "memory");
+        grid_launch_dependents();
+        tc_producer<RB, HEADS, BLK>(&tmap_k, &tmap_v, p, smem, abort);
+        return;
+    }
     if (warp == 1) {
         tmem_alloc(tmem_slot, Tr::kTmemCols);
         tmem_relinquish();
@@ -1060,13 +1067,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     grid_launch_dependents();
     tc_fence_before();
-    __syncthreads();
+    asm volatile("barrier.cta.sync 4, %0;" ::"n"(kTcThreads) : "memory");
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    if (warp == 0) {
-        tc_producer<RB, HEADS, BLK>(&tmap_k, &tmap_v, p, smem, abort);
-        return;
-    }
+    const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
     if (warp == 3) {  // fused mode: requests without live tokens get zero rows
         if (!p.out) return;
         grid_dependency_wait();
