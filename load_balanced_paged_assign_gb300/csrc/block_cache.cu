@@ -73,12 +73,42 @@ struct RunInfo {
 
 struct BlockWriteShared {
     float ang[kBwTokens * 128];  // per token and group of 4 frequencies: 4 cosines, 4 sines
-    float fhi[64], flo[64];
+    float fhi[64], flo[64];  // the frequencies over pi, in two floats
     long long slot[32];  // page * 64 + offset, or -1
     int pos[32];
     RunInfo run[kBwMaxChunk];
     int runs, tokens;  // runs that start here; tokens whose angles are needed
 };
+
+// x^(-1/2) and 448 / m to about a rounding: a step of Newton's method from the
+// approximations (2 ulp), for a value that a whole row of codes follows.  (Zero
+// and infinity, of rows with infinities or next to nothing, stay as they are.)
+__device__ __forceinline__ float root_inverse(float x) {
+    const float y = rsqrtf(x);
+    const float r = fmaf(0.5f * y, fmaf(-x * y, y, 1.f), y);
+    return y > 0.f && y <= 3.402823466e38f ? r : y;
+}
+__device__ __forceinline__ float quotient448(float m) {
+    const float y = __fdividef(kMaxE4m3, m);
+    const float r = fmaf(fmaf(-y, m, kMaxE4m3), y * (1.f / kMaxE4m3), y);
+    return y > 0.f && y <= 3.402823466e38f ? r : y;
+}
+
+// cos and sin of pi pos (hi + lo), to about their own rounding (a code near a
+// tie between two E4M3 values follows the angle's error).  The product's integer
+// part goes exactly, its rounding error and the low part are added with what
+// that addition loses, d, which the functions' first derivatives bring in.
+__device__ __forceinline__ float2 half_turns(int pos, float hi, float lo) {
+    const float p = (float)pos;  // exact: 0 <= pos < 2^24 for valid tokens
+    const float prod = p * hi;
+    const float e = fmaf(p, lo, fmaf(p, hi, -prod));
+    const float r = prod - 2.f * rintf(0.5f * prod);  // exact, in [-1, 1]
+    const float t = r + e, b = t - r;
+    const float d = 3.14159265f * ((r - (t - b)) + (e - b));
+    float s, c;
+    sincospif(t, &s, &c);
+    return make_float2(fmaf(-d, s, c), fmaf(d, c, s));
+}
 
 __device__ __forceinline__ void load_angles(const float *tab, int s, float (&c)[4], float (&sn)[4],
                                             float (&nsn)[4]) {
@@ -97,7 +127,7 @@ __device__ __forceinline__ void norm_rope(float (&x)[8], const float (&w)[8], co
     float ss = sumsq8(x);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(kAll, ss, o);
-    const float inv = rsqrtf(fmaf(ss, 1.0f / kHeadDim, eps));
+    const float inv = root_inverse(fmaf(ss, 1.0f / kHeadDim, eps));
     if constexpr (NF) {
         mul8(x, w);
         rotate<LAYOUT>(x, c, sn, nsn);
@@ -262,7 +292,7 @@ __device__ __forceinline__ void write_queries(const BlockWriteArgs &a, const flo
             for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
             // codes = y * 448 / max|y|, the scale max|y| / 448 (1 for a zero row)
             const bool live = m > 0.f;
-            scale8(x, live ? __fdividef(kMaxE4m3, m) : 0.f);
+            scale8(x, live ? quotient448(m) : 0.f);
             if (row < a.Hq) {
                 store_e4m3<LAYOUT>(static_cast<char *>(a.q_out) + out * kHeadDim, s, x);
                 if (s == 0) a.q_scale_out[out] = live ? m * (1.0f / kMaxE4m3) : 1.f;
@@ -297,9 +327,10 @@ __global__ void __launch_bounds__(kBwThreads, kBwCtas)
     if (tid >= 64 && tid < 128) {
         const int i = tid - 64;
         const double f = a.freq ? a.freq[i] : pow(a.base, -(double)i / 64.0);
-        const float hi = (float)f;
+        const double g = f * 0.318309886183790671538;  // 1 / pi
+        const float hi = (float)g;
         sh.fhi[i] = hi;
-        sh.flo[i] = (float)(f - (double)hi);
+        sh.flo[i] = (float)(g - (double)hi);
     }
     if (warp == 0) {  // lane l: token t0 - 1 + l
         const int t = t0 - 1 + lane;
@@ -349,7 +380,7 @@ __global__ void __launch_bounds__(kBwThreads, kBwCtas)
     __syncthreads();
     for (int i = tid; i < sh.tokens * 64; i += kBwThreads) {
         const int f = i & 63, k = i >> 6;
-        store_angle(sh.ang + k * 128, f, rope_angle(sh.pos[k], sh.fhi[f], sh.flo[f]));
+        store_angle(sh.ang + k * 128, f, half_turns(sh.pos[k], sh.fhi[f], sh.flo[f]));
     }
     __syncthreads();
     const int per_run = 2 * a.Hkv, kv_items = sh.runs * per_run;

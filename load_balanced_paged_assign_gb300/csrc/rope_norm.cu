@@ -51,6 +51,11 @@ constexpr int kRnThreads = 32 * kRnWarps;
 constexpr int kMaxStages = 8;
 constexpr int kStageBudget = 40 * 1024;  // QKV bytes a CTA keeps in flight (at least 2 stages)
 
+constexpr float kTwoPiHi = 6.2831854820251465f;     // fp32(2 pi)
+constexpr float kTwoPiLo = -1.7484555314695172e-7f;  // 2 pi - fp32(2 pi)
+constexpr float kInvTwoPi = 0.159154937f;
+constexpr float kInvPi = 0.318309873f;
+
 enum RowKind { kQ = 0, kK = 1, kV = 2 };
 
 struct RopeNormArgs {
@@ -76,6 +81,38 @@ struct RopeNormArgs {
     int stages;
     int norm_first;
 };
+
+// x[k] / s correctly rounded to FP32 for the 8 values, from y = RN(1/s):
+// q = RN(x y) is within an ulp of x / s, r = x - s q is exact (one FMA), and
+// RN(q + r y) is the correctly rounded quotient (Markstein's theorem on
+// division with a fused multiply-add); two values per instruction.
+__device__ __forceinline__ void div8(float (&x)[8], float s, float y) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        const float2 v = make_float2(x[2 * h], x[2 * h + 1]);
+        const float2 q = __fmul2_rn(v, make_float2(y, y));
+        const float2 r = __ffma2_rn(make_float2(-s, -s), q, v);
+        const float2 o = __ffma2_rn(r, make_float2(y, y), q);
+        x[2 * h] = o.x, x[2 * h + 1] = o.y;
+    }
+}
+
+// cos/sin of pos * freq_i, freq_i = hi + lo (two floats), reduced modulo 2 pi.
+__device__ __forceinline__ float2 rope_angle(int pos, float hi, float lo) {
+    const float p = (float)pos;                 // exact: |pos| < 2^24 for valid tokens
+    const float prod = p * hi;
+    const float err = fmaf(p, hi, -prod);       // exact rounding error of the product
+    const float k = rintf(prod * kInvTwoPi);
+    float r = fmaf(-k, kTwoPiHi, prod);
+    r = fmaf(-k, kTwoPiLo, r);
+    r += fmaf(p, lo, err);                      // the small terms, |.| < 1.5
+    const float k2 = rintf(r * kInvTwoPi);      // back into [-pi, pi]
+    r = fmaf(-k2, kTwoPiHi, r);
+    r = fmaf(-k2, kTwoPiLo, r);
+    float s, c;
+    sincospif(r * kInvPi, &s, &c);
+    return make_float2(c, s);
+}
 
 // ------------------------------------------------------------ one batch of rows
 // NP row pairs of one kind.  Pair i of the batch is rows row0 + 16 i and

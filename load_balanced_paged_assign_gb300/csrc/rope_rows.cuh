@@ -1,6 +1,5 @@
 // Head-row arithmetic shared by the prologues (rope_norm.cu, block_cache.cu):
-// how a half-warp holds a row, the rotation, the RMS and the E4M3 conversion,
-// and the RoPE angle of a position.
+// how a half-warp holds a row, the rotation, the RMS and the E4M3 conversion.
 #pragma once
 
 #include "internal.h"
@@ -11,10 +10,6 @@ namespace {
 
 constexpr int kRowBytes = kHeadDim * 2;  // one BF16 head row
 constexpr int kMaxPosition = 1 << 24;    // positions are exact in fp32 below this
-constexpr float kTwoPiHi = 6.2831854820251465f;     // fp32(2 pi)
-constexpr float kTwoPiLo = -1.7484555314695172e-7f;  // 2 pi - fp32(2 pi)
-constexpr float kInvTwoPi = 0.159154937f;
-constexpr float kInvPi = 0.318309873f;
 
 // ------------------------------------------------------------ lane layout
 // A head row is handled by one half-warp (16 lanes, 8 dims each), so a warp
@@ -150,38 +145,6 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 __device__ __forceinline__ float absmax8(const float (&x)[8]) {
     return fmax3(fmax3(fabsf(x[0]), fabsf(x[1]), fabsf(x[2])),
                  fmax3(fabsf(x[3]), fabsf(x[4]), fabsf(x[5])), fmaxf(fabsf(x[6]), fabsf(x[7])));
-}
-
-// x[k] / s correctly rounded to FP32 for the 8 values, from y = RN(1/s):
-// q = RN(x y) is within an ulp of x / s, r = x - s q is exact (one FMA), and
-// RN(q + r y) is the correctly rounded quotient (Markstein's theorem on
-// division with a fused multiply-add); two values per instruction.
-__device__ __forceinline__ void div8(float (&x)[8], float s, float y) {
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-        const float2 v = make_float2(x[2 * h], x[2 * h + 1]);
-        const float2 q = __fmul2_rn(v, make_float2(y, y));
-        const float2 r = __ffma2_rn(make_float2(-s, -s), q, v);
-        const float2 o = __ffma2_rn(r, make_float2(y, y), q);
-        x[2 * h] = o.x, x[2 * h + 1] = o.y;
-    }
-}
-
-// cos/sin of pos * freq_i, freq_i = hi + lo (two floats), reduced modulo 2 pi.
-__device__ __forceinline__ float2 rope_angle(int pos, float hi, float lo) {
-    const float p = (float)pos;                 // exact: |pos| < 2^24 for valid tokens
-    const float prod = p * hi;
-    const float err = fmaf(p, hi, -prod);       // exact rounding error of the product
-    const float k = rintf(prod * kInvTwoPi);
-    float r = fmaf(-k, kTwoPiHi, prod);
-    r = fmaf(-k, kTwoPiLo, r);
-    r += fmaf(p, lo, err);                      // the small terms, |.| < 1.5
-    const float k2 = rintf(r * kInvTwoPi);      // back into [-pi, pi]
-    r = fmaf(-k2, kTwoPiHi, r);
-    r = fmaf(-k2, kTwoPiLo, r);
-    float s, c;
-    sincospif(r * kInvPi, &s, &c);
-    return make_float2(c, s);
 }
 
 // (cos, sin) of frequency i into a buffer of the angle table.
