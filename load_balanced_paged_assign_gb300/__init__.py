@@ -6,7 +6,9 @@ attention inputs; the assign kernel builds a per-step task map of balanced
 tile bins, the persistent attention kernel drains the bins into split
 partials, and the combine kernel merges them into BF16 output.  Beside the
 decode path: extend / prefill attention on tcgen05 tensor cores and the
-router GEMM with a BF16 hi/lo split of FP32 weights.  This package
+router GEMM with a BF16 hi/lo split of FP32 weights; an 8-bit cache with a
+scale for each 16 tokens and head (written, read back, attended over) and
+attention with a sliding window and sinks.  This package
 holds the build step, the ctypes binding and the seeded workload generators.
 """
 

@@ -45,10 +45,10 @@
 // rescales its accumulator in TMEM.
 // Measured (queries, plan and merges included; the part of the measured copy
 // rate that the cache's bytes alone make):
-//   64 requests of 1K to 128K, 8 heads on 1, block scales, 560 MB: 93 us, 89%
-//   64 of 512 to 16K, 64 heads on 8, two tokens, block scales, 731 MB: 126 us, 86%
-//   128 of 1K to 32K, 16 on 2, window 1024, 69 MB: 25 us, 41%
-//   48 of 500 to 16K, 48 on 8, two tokens, window 2048, 155 MB: 46 us, 50%
+//   64 requests of 1K to 128K, 8 heads on 1, block scales, 560 MB: 92 us, 90%
+//   64 of 512 to 16K, 64 heads on 8, two tokens, block scales, 731 MB: 125 us, 86%
+//   128 of 1K to 32K, 16 on 2, window 1024, 69 MB: 24 us, 42%
+//   48 of 500 to 16K, 48 on 8, two tokens, window 2048, 155 MB: 42 us, 54%
 // The long streams run at the rate of HBM; what the short ones add is fixed: 5 us
 // from the launch to the first stage's landing (lengths, block table, tiles, one
 // after the other) and 6 to 8 us from the last landing to the end (softmax and

@@ -1,6 +1,6 @@
 // Windowed form of the persistent attention kernel over a BF16 cache: its
 // 2 bytes a value leave the warp-level MMAs time enough.  64 requests of 1K to 16K
-// tokens, 64 heads on 8, window 4096 and 64 sinks (819 MB): 128 us, 94% of the
+// tokens, 64 heads on 8, window 4096 and 64 sinks (819 MB): 129 us, 93% of the
 // measured copy rate; HBM bounds it.
 #include "attn_kernel.cuh"
 

@@ -311,7 +311,7 @@ __device__ __forceinline__ void write_queries(const BlockWriteArgs &a, const flo
 // eight warps.  Each row is read once, straight into registers (16 bytes a
 // lane, 4 to 8 rows in flight per half-warp), the next query item's while this
 // one's are worked on.  8192 tokens of 64 + 2 x 8 heads, BF16 queries (319 MB):
-// 65 us, 72% of the measured copy rate (71 us without the look-ahead); chunks of
+// 66 us, 71% of the measured copy rate (71 us without the look-ahead); chunks of
 // 6 to 15 tokens are within 1%, four resident CTAs (64 registers) spill and two
 // take 81 us, and prefetching the rows to L2 at the start costs 9 us more.  What
 // bounds it is the latency of each item's chain of shuffles and conversions at 24

@@ -28,8 +28,9 @@
 //   * Tokens that no query of the pair sees (past L_r, or before the window and no
 //     sink) may hold anything: a warp of its own zeroes their V rows once the page
 //     has landed (0 * NaN would reach O) and passes every page on.
-// 8192 queries of 64 heads with a window of 1024 and 64 sinks (273 GFLOP): 231 us,
-// 1180 TFLOP/s; 2 x 1000 behind 3111 tokens with a window of 2000: 122 us.
+// 8192 queries of 64 heads with a window of 1024 and 64 sinks (273 GFLOP): 232 us,
+// 1175 TFLOP/s (245 us in long runs, under the power limit); 2 x 1000 behind 3111
+// tokens with a window of 2000 (132 GFLOP): 124 us; 512 with 128: 12.6 us.
 //
 // All barrier phases are counted across items.  Every wait is bounded; on a
 // timeout the CTA raises the error flag, waits (bounded) for its copies and
