@@ -1,9 +1,9 @@
-"""Builds libhpcdecode.so in the package directory (nvcc, sm_103a only).
+"""Builds libhpcdecode.so (nvcc, sm_103a only) and the binding's extension module
+_tensors.so (g++, against the installed PyTorch) in the package directory.
 
-The translation units are compiled in parallel and linked with the CUDA
-runtime statically, so the library needs nothing at run time beyond the
-NVIDIA driver.  Rebuilds only when a source or header is newer than the
-library.
+The library's translation units are compiled in parallel and linked with the
+CUDA runtime statically, so it needs nothing at run time beyond the NVIDIA
+driver.  Each is rebuilt only when a source or header is newer.
 """
 
 from __future__ import annotations
@@ -12,6 +12,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -19,6 +20,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB_PATH = os.path.join(HERE, "libhpcdecode.so")
+EXT_PATH = os.path.join(HERE, "_tensors.so")
+EXT_SOURCE = os.path.join(CSRC, "tensors.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -45,14 +48,44 @@ def is_stale() -> bool:
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
+def build_extension(force: bool = False) -> str:
+    """Compile _tensors.so, the check of a call's tensors."""
+    if not force and os.path.exists(EXT_PATH) and \
+            os.path.getmtime(EXT_PATH) > max(os.path.getmtime(f) for f in (EXT_SOURCE, __file__)):
+        return EXT_PATH
+    import torch
+    base = os.path.dirname(torch.__file__)
+    staged = EXT_PATH + f".{os.getpid()}.tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(base, "include"),
+           "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"), EXT_SOURCE,
+           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-o", staged]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {EXT_SOURCE}:\n{res.stderr}")
+    os.replace(staged, EXT_PATH)
+    return EXT_PATH
+
+
 def build(force: bool = False, verbose: bool = False, defines=(), out: str | None = None) -> str:
     """Compile the library (to `out`, default the package's libhpcdecode.so).
 
     `defines` are extra -D settings, e.g. the pipeline shape of the attention
     kernels (HPC_BF16_STAGES, HPC_BF16_TPS, HPC_FP8_STAGES, HPC_FP8_TPS)."""
     target = out or LIB_PATH
-    if not force and not defines and out is None and not is_stale():
-        return LIB_PATH
+    own = out is None and not defines
+    with ThreadPoolExecutor(1) as pool:  # beside the library's compilation
+        extension = pool.submit(build_extension, force) if own else None
+        if force or not own or is_stale():
+            _build_library(target, verbose, defines)
+        if extension:
+            extension.result()
+    return target
+
+
+def _build_library(target: str, verbose: bool, defines) -> None:
     nvcc = _nvcc()
     flags = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE,
                     "--expt-relaxed-constexpr"] + [f"-D{d}" for d in defines]
@@ -77,7 +110,6 @@ def build(force: bool = False, verbose: bool = False, defines=(), out: str | Non
         staged = target + f".{os.getpid()}.tmp"
         shutil.copyfile(out_tmp, staged)
         os.replace(staged, target)
-    return target
 
 
 if __name__ == "__main__":

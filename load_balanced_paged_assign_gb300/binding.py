@@ -185,28 +185,46 @@ def kv_dtype_of(t: torch.Tensor) -> int:
     raise TypeError(f"unsupported KV cache dtype {t.dtype}")
 
 
-def _bad(fn: str, name: str, t, dtype, dev: int):
-    """ValueError saying why `t` is no dense array of `dtype` on the device `dev`."""
-    why = f"{t.dtype}, not {dtype}" if t.dtype is not dtype else \
-        "not contiguous" if not t.is_contiguous() else f"on {t.device}, not on the current device"
-    raise ValueError(f"{fn}: {name} is {why}")
+_DENSE = None  # _tensors.dense, once a call has needed it
+_BF16, _E4M3, _F32, _F64, _I32 = (torch.bfloat16, torch.float8_e4m3fn, torch.float32,
+                                  torch.float64, torch.int32)
 
 
-def _dense(fn: str, dev: int, names: str, dtype, *tensors):
-    """Raises for the first tensor (or None) that is no row-major array of `dtype` on the
-    device `dev`, as the pointers handed to the library are taken to be."""
-    for i, t in enumerate(tensors):
-        if t is not None and not _is_dense(t, dtype, dev):
-            _bad(fn, names.split()[i], t, dtype, dev)
+def _load_dense():
+    global _DENSE
+    try:
+        from . import _tensors
+    except ImportError as e:
+        raise RuntimeError("the extension module _tensors is missing: build it first "
+                           "(python -c 'import __graft_entry__ as g; g.build()')") from e
+    _DENSE = _tensors.dense
+    return _DENSE
 
 
-def _is_dense(t, dtype, dev: int) -> bool:
-    return t.dtype is dtype and t.is_contiguous() and t.get_device() == dev
+def _arrays(fn: str, dev: int, names: str, types: tuple, *tensors) -> tuple:
+    """The tensors' (addresses, shapes, element counts), None for None; raises for the first
+    that is no row-major array of its type on the device `dev`, as the library takes its
+    pointers to be."""
+    got = (_DENSE or _load_dense())(dev, types, *tensors)
+    if type(got) is int:
+        t, name, dtype = tensors[got], names.split()[got], types[got]
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{fn}: {name} is a {type(t).__name__}, not a tensor")
+        why = f"{t.dtype}, not {dtype}" if t.dtype is not dtype else \
+            "not contiguous" if not t.is_contiguous() else \
+            f"on {t.device}, not on the current device"
+        raise ValueError(f"{fn}: {name} is {why}")
+    return got
 
 
-def _shape(fn: str, name: str, t, want: tuple):
-    if t.shape != want:
-        raise ValueError(f"{fn}: {name} is {tuple(t.shape)}, not {want}")
+def _shape(fn: str, name: str, shape: tuple, want: tuple):
+    if shape != want:
+        raise ValueError(f"{fn}: {name} is {shape}, not {want}")
+
+
+def _table(fn: str, name: str, shape: tuple, B: int):
+    if len(shape) != 2 or shape[0] < B:
+        raise ValueError(f"{fn}: {name} has not a row for each of the {B} requests")
 
 
 _HAS_CUDA = None
@@ -225,11 +243,6 @@ def _raw_stream(dev: int, stream):
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else None
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _adr(t):
-    """A tensor's address as ctypes takes it (None for no tensor)."""
-    return None if t is None else t.data_ptr()
 
 
 class TaskMap:
@@ -526,60 +539,47 @@ def hpc_decode_plan_win(seqlens, Hkv, max_pages_per_req, num_ctas, min_tiles_per
     """hpc_decode_plan for queries that see the last `window` tokens and the
     first `sinks` ones (window = 0: every token) of a kv_dtype cache."""
     dev = _current_device()
-    _dense("hpc_decode_plan_win", dev, "seqlens", torch.int32, seqlens)
+    (adr,), _, (B,) = _arrays("hpc_decode_plan_win", dev, "seqlens", (_I32,), seqlens)
     _check("hpc_decode_plan_win", lib().hpc_decode_plan_win(
-        _adr(seqlens), int(seqlens.numel()), int(Hkv), int(max_pages_per_req), int(num_ctas),
+        adr, B, int(Hkv), int(max_pages_per_req), int(num_ctas),
         int(min_tiles_per_cta), int(kv_dtype), int(q_len), int(window), int(sinks),
         ctypes.byref(tmap.c),
         _raw_stream(dev, stream)))
 
 
-def _win_args(fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, B, Hq, Hkv, q_len,
+_WIN_NAMES = ("q k_cache v_cache q_scale kv_scale block_table seqlens part_o part_lse unit_done "
+              "out")
+_WIN_TYPES = [(t, t, t, _F32, _F32, _I32, _I32, _F32, _F32, _I32, _BF16) for t in (_BF16, _E4M3)]
+
+
+def _win_args(fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, Hq, Hkv, q_len,
               part_o, part_lse, out, unit_done, cap_desc):
-    """The checks of the windowed decode calls; returns (KV dtype, device)."""
-    block, dev, i32, f32 = kv_scale is not None, _current_device(), torch.int32, torch.float32
-    kv = torch.float8_e4m3fn if block else k_cache.dtype
-    # (the calls are short enough for the host to bound them: one expression,
-    # and the reason is looked for only where it does not hold)
-    if not (q.dtype is kv and k_cache.dtype is kv and v_cache.dtype is kv
-            and block_table.dtype is i32 and seqlens.dtype is i32
-            and part_o.dtype is f32 and part_lse.dtype is f32
-            and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
-            and block_table.is_contiguous() and seqlens.is_contiguous()
-            and part_o.is_contiguous() and part_lse.is_contiguous()
-            and dev == q.get_device() == k_cache.get_device() == v_cache.get_device()
-            == block_table.get_device() == seqlens.get_device() == part_o.get_device()
-            == part_lse.get_device()
-            and (q_scale is None or _is_dense(q_scale, f32, dev))
-            and (kv_scale is None or _is_dense(kv_scale, f32, dev))
-            and (unit_done is None or _is_dense(unit_done, i32, dev))
-            and (out is None or _is_dense(out, torch.bfloat16, dev))):
-        _dense(fn, dev, "q k_cache v_cache", kv, q, k_cache, v_cache)
-        _dense(fn, dev, "q_scale kv_scale part_o part_lse", f32, q_scale, kv_scale, part_o,
-               part_lse)
-        _dense(fn, dev, "block_table seqlens unit_done", i32, block_table, seqlens, unit_done)
-        _dense(fn, dev, "out", torch.bfloat16, out)
-    pages, rows = k_cache.shape[0], B * q_len * Hq
-    want = (pages, PAGE_SIZE, Hkv, HEAD_DIM)
-    if k_cache.shape != want or v_cache.shape != want:
-        _shape(fn, "k_cache", k_cache, want)
-        _shape(fn, "v_cache", v_cache, want)
+    """The checks of the windowed decode calls; returns (KV dtype, device, requests, pages,
+    pages per request, addresses in the order of _WIN_NAMES)."""
+    block, dev = kv_scale is not None, _current_device()
+    e4m3 = block or k_cache.dtype is _E4M3
+    adr, shape, count = _arrays(fn, dev, _WIN_NAMES, _WIN_TYPES[e4m3], q, k_cache, v_cache, q_scale,
+                                kv_scale, block_table, seqlens, part_o, part_lse, unit_done, out)
+    pages, table, B = shape[1][0] if shape[1] else 0, shape[5], count[6]
+    rows, want = B * q_len * Hq, (pages, PAGE_SIZE, Hkv, HEAD_DIM)
+    _shape(fn, "k_cache", shape[1], want)
+    _shape(fn, "v_cache", shape[2], want)
     if block:
-        _shape(fn, "kv_scale", kv_scale, (pages, Hkv, 2, PAGE_SIZE // SCALE_BLOCK))
-    if block_table.dim() != 2 or block_table.shape[0] < B:
-        raise ValueError(f"{fn}: block_table has not a row for each of the {B} requests")
-    if q.numel() != rows * HEAD_DIM or (out is not None and out.numel() < rows * HEAD_DIM):
+        _shape(fn, "kv_scale", shape[4], (pages, Hkv, 2, PAGE_SIZE // SCALE_BLOCK))
+    _table(fn, "block_table", table, B)
+    if count[0] != rows * HEAD_DIM or (out is not None and count[10] < rows * HEAD_DIM):
         raise ValueError(f"{fn}: q or out does not hold {B} x {q_len} x {Hq} rows")
-    if q_scale is not None and q_scale.numel() != rows:
+    if q_scale is not None and count[3] != rows:
         raise ValueError(f"{fn}: q_scale does not hold {B} x {q_len} x {Hq} scales")
     # room in the split buffer and the counters for what the map may hold
     rows = cap_desc * q_len * (Hq // max(Hkv, 1))
-    if part_o.numel() < rows * HEAD_DIM or part_lse.numel() < rows:
+    if count[7] < rows * HEAD_DIM or count[8] < rows:
         raise ValueError(f"{fn}: part_o or part_lse is smaller than the map's {cap_desc} "
                          f"descriptors need")
-    if unit_done is not None and unit_done.numel() < B * Hkv:
+    if unit_done is not None and count[9] < B * Hkv:
         raise ValueError(f"{fn}: unit_done holds fewer than {B} x {Hkv} counters")
-    return HPC_KV_E4M3_BLOCK if block else kv_dtype_of(k_cache), dev
+    kv = HPC_KV_E4M3_BLOCK if block else HPC_KV_FP8_E4M3 if e4m3 else HPC_KV_BF16
+    return kv, dev, B, pages, table[1], adr
 
 
 def hpc_decode_attn_win(q, q_scale, k_cache, v_cache, k_scale, v_scale, kv_scale, block_table,
@@ -590,15 +590,15 @@ def hpc_decode_attn_win(q, q_scale, k_cache, v_cache, k_scale, v_scale, kv_scale
     block-scaled cache, else None.  out and unit_done given: combine fused in;
     both None: partials only."""
     fn = "hpc_decode_attn_win"
-    B, Hq, Hkv, q_len = seqlens.numel(), int(Hq), int(Hkv), int(q_len)
-    dtype, dev = _win_args(fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, B, Hq,
-                           Hkv, q_len, part_o, part_lse, out, unit_done, tmap.cap_desc)
+    Hq, Hkv, q_len = int(Hq), int(Hkv), int(q_len)
+    kv, dev, B, pages, cols, (q_, k_, v_, qs_, sc_, bt_, sl_, po_, pl_, ud_, out_) = _win_args(
+        fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, Hq, Hkv, q_len, part_o,
+        part_lse, out, unit_done, tmap.cap_desc)
     status = lib().hpc_decode_attn_win(
-        q.data_ptr(), _adr(q_scale), k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0],
-        float(k_scale), float(v_scale), _adr(kv_scale), dtype, block_table.data_ptr(),
-        block_table.shape[1], seqlens.data_ptr(), B, Hq, Hkv, HEAD_DIM, q_len, int(window),
-        int(sinks), float(sm_scale), ctypes.byref(tmap.c), part_o.data_ptr(), part_lse.data_ptr(),
-        _adr(unit_done), _adr(out), _raw_stream(dev, stream))
+        q_, qs_, k_, v_, pages, float(k_scale), float(v_scale), sc_, kv, bt_, cols, sl_, B, Hq,
+        Hkv, HEAD_DIM, q_len, int(window), int(sinks),
+        float(sm_scale), ctypes.byref(tmap.c), po_, pl_, ud_, out_,
+        _raw_stream(dev, stream))
     if status != HPC_OK:
         _check(fn, status)
 
@@ -610,16 +610,15 @@ def hpc_decode_step_win(q, q_scale, k_cache, v_cache, k_scale, v_scale, kv_scale
     """hpc_decode_plan_win and hpc_decode_attn_win in one call (unit_done None:
     with the separate combine kernel)."""
     fn = "hpc_decode_step_win"
-    B, Hq, Hkv, q_len = seqlens.numel(), int(Hq), int(Hkv), int(q_len)
-    dtype, dev = _win_args(fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, B, Hq,
-                           Hkv, q_len, part_o, part_lse, out, unit_done, tmap.cap_desc)
+    Hq, Hkv, q_len = int(Hq), int(Hkv), int(q_len)
+    kv, dev, B, pages, cols, (q_, k_, v_, qs_, sc_, bt_, sl_, po_, pl_, ud_, out_) = _win_args(
+        fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, Hq, Hkv, q_len, part_o,
+        part_lse, out, unit_done, tmap.cap_desc)
     status = lib().hpc_decode_step_win(
-        q.data_ptr(), _adr(q_scale), k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0],
-        float(k_scale), float(v_scale), _adr(kv_scale), dtype, block_table.data_ptr(),
-        block_table.shape[1], seqlens.data_ptr(), B, Hq, Hkv, HEAD_DIM, q_len, int(window),
-        int(sinks), float(sm_scale), int(num_ctas), int(min_tiles_per_cta), ctypes.byref(tmap.c),
-        part_o.data_ptr(), part_lse.data_ptr(), _adr(unit_done), _adr(out),
-        _raw_stream(dev, stream))
+        q_, qs_, k_, v_, pages, float(k_scale), float(v_scale), sc_, kv, bt_, cols, sl_, B, Hq,
+        Hkv, HEAD_DIM, q_len, int(window), int(sinks),
+        float(sm_scale), int(num_ctas), int(min_tiles_per_cta), ctypes.byref(tmap.c), po_, pl_, ud_,
+        out_, _raw_stream(dev, stream))
     if status != HPC_OK:
         _check(fn, status)
 
@@ -627,32 +626,28 @@ def hpc_decode_step_win(q, q_scale, k_cache, v_cache, k_scale, v_scale, kv_scale
 def hpc_prefill_attn_win(q, k_cache, v_cache, block_table, seqlens, Hq, Hkv, q_len, window, sinks,
                          sm_scale, out, flags=None, stream=None):
     """hpc_prefill_attn with a window and sinks (window = 0: plain causal)."""
-    fn, bf16, i32, dev = "hpc_prefill_attn_win", torch.bfloat16, torch.int32, _current_device()
-    B, Hq, Hkv, q_len = seqlens.numel(), int(Hq), int(Hkv), int(q_len)
-    if not (q.dtype is bf16 and k_cache.dtype is bf16 and v_cache.dtype is bf16
-            and out.dtype is bf16 and block_table.dtype is i32 and seqlens.dtype is i32
-            and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
-            and out.is_contiguous() and block_table.is_contiguous() and seqlens.is_contiguous()
-            and dev == q.get_device() == k_cache.get_device() == v_cache.get_device()
-            == out.get_device() == block_table.get_device() == seqlens.get_device()
-            and (flags is None or _is_dense(flags, i32, dev))):
-        _dense(fn, dev, "q k_cache v_cache out", bf16, q, k_cache, v_cache, out)
-        _dense(fn, dev, "block_table seqlens flags", i32, block_table, seqlens, flags)
-    want = (k_cache.shape[0], PAGE_SIZE, Hkv, HEAD_DIM)
-    if k_cache.shape != want or v_cache.shape != want:
-        _shape(fn, "k_cache", k_cache, want)
-        _shape(fn, "v_cache", v_cache, want)
-    n = B * q_len * Hq * HEAD_DIM
-    if block_table.dim() != 2 or block_table.shape[0] < B:
-        raise ValueError(f"{fn}: block_table has not a row for each of the {B} requests")
-    if q.numel() != n or out.numel() < n:
+    fn, dev = "hpc_prefill_attn_win", _current_device()
+    Hq, Hkv, q_len = int(Hq), int(Hkv), int(q_len)
+    (q_, k_, v_, out_, bt_, sl_, fl_), shape, count = _arrays(
+        fn, dev, "q k_cache v_cache out block_table seqlens flags",
+        (_BF16, _BF16, _BF16, _BF16, _I32, _I32, _I32), q, k_cache, v_cache, out, block_table,
+        seqlens, flags)
+    B, pages, table = count[5], shape[1][0] if shape[1] else 0, shape[4]
+    want, n = (pages, PAGE_SIZE, Hkv, HEAD_DIM), B * q_len * Hq * HEAD_DIM
+    _shape(fn, "k_cache", shape[1], want)
+    _shape(fn, "v_cache", shape[2], want)
+    _table(fn, "block_table", table, B)
+    if count[0] != n or count[3] < n:
         raise ValueError(f"{fn}: q or out does not hold {B} x {q_len} x {Hq} rows")
     status = lib().hpc_prefill_attn_win(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), want[0], block_table.data_ptr(),
-        block_table.shape[1], seqlens.data_ptr(), B, Hq, Hkv, HEAD_DIM, q_len, int(window),
-        int(sinks), float(sm_scale), out.data_ptr(), _adr(flags), _raw_stream(dev, stream))
+        q_, k_, v_, pages, bt_, table[1], sl_, B, Hq, Hkv, HEAD_DIM, q_len,
+        int(window), int(sinks), float(sm_scale), out_, fl_, _raw_stream(dev, stream))
     if status != HPC_OK:
         _check(fn, status)
+
+
+_WRITE_TYPES = [(_BF16, _BF16, _I32, _I32, _I32, _E4M3, _E4M3, _F32, q, _F32, _I32, _F64)
+                for q in (_BF16, _E4M3)]  # BF16 queries, E4M3 queries
 
 
 def hpc_rope_norm_block(qkv, q_norm_w, k_norm_w, positions, token_req, Hq, Hkv, block_table,
@@ -661,58 +656,38 @@ def hpc_rope_norm_block(qkv, q_norm_w, k_norm_w, positions, token_req, Hq, Hkv, 
                         freq=None, stream=None):
     """hpc_rope_norm writing into a block-scaled cache (E4M3 k_cache, v_cache and
     kv_scale [num_pages, Hkv, 2, 4]).  q_scale_out given: E4M3 queries, else BF16."""
-    fn, f32, i32, e4m3 = "hpc_rope_norm_block", torch.float32, torch.int32, torch.float8_e4m3fn
-    bf16, N, pages, Hq, Hkv = torch.bfloat16, positions.numel(), k_cache.shape[0], int(Hq), int(Hkv)
-    dev, q_type = _current_device(), torch.bfloat16 if q_scale_out is None else e4m3
-    if not (q_norm_w.dtype is bf16 and k_norm_w.dtype is bf16 and positions.dtype is i32
-            and block_table.dtype is i32 and k_cache.dtype is e4m3 and v_cache.dtype is e4m3
-            and kv_scale.dtype is f32 and q_out.dtype is q_type
-            and q_norm_w.is_contiguous() and k_norm_w.is_contiguous()
-            and positions.is_contiguous() and block_table.is_contiguous()
-            and k_cache.is_contiguous() and v_cache.is_contiguous()
-            and kv_scale.is_contiguous() and q_out.is_contiguous()
-            and dev == q_norm_w.get_device() == k_norm_w.get_device() == positions.get_device()
-            == block_table.get_device() == k_cache.get_device() == v_cache.get_device()
-            == kv_scale.get_device() == q_out.get_device()
-            and (token_req is None or _is_dense(token_req, i32, dev))
-            and (flags is None or _is_dense(flags, i32, dev))
-            and (q_scale_out is None or _is_dense(q_scale_out, f32, dev))
-            and (freq is None or _is_dense(freq, torch.float64, dev))):
-        _dense(fn, dev, "q_norm_w k_norm_w", bf16, q_norm_w, k_norm_w)
-        _dense(fn, dev, "positions token_req block_table flags", i32, positions, token_req,
-               block_table, flags)
-        _dense(fn, dev, "k_cache v_cache", e4m3, k_cache, v_cache)
-        _dense(fn, dev, "kv_scale q_scale_out", f32, kv_scale, q_scale_out)
-        _dense(fn, dev, "q_out", q_type, q_out)
-        _dense(fn, dev, "freq", torch.float64, freq)
+    fn, dev = "hpc_rope_norm_block", _current_device()
+    Hq, Hkv = int(Hq), int(Hkv)
+    (wq_, wk_, pos_, req_, bt_, k_, v_, sc_, q_, qs_, fl_, fr_), shape, count = _arrays(
+        fn, dev, "q_norm_w k_norm_w positions token_req block_table k_cache v_cache kv_scale q_out "
+        "q_scale_out flags freq", _WRITE_TYPES[q_scale_out is not None], q_norm_w, k_norm_w,
+        positions, token_req, block_table, k_cache, v_cache, kv_scale, q_out, q_scale_out, flags,
+        freq)
+    N, table, pages, rows = count[2], shape[4], shape[5][0] if shape[5] else 0, qkv.shape
     want = (pages, PAGE_SIZE, Hkv, HEAD_DIM)
-    if k_cache.shape != want or v_cache.shape != want:
-        _shape(fn, "k_cache", k_cache, want)
-        _shape(fn, "v_cache", v_cache, want)
-    _shape(fn, "kv_scale", kv_scale, (pages, Hkv, 2, PAGE_SIZE // SCALE_BLOCK))
-    if qkv.dtype is not torch.bfloat16 or qkv.dim() != 2 or (N and qkv.stride(1) != 1) or \
-            qkv.shape[0] < N or qkv.shape[1] < (Hq + 2 * Hkv) * HEAD_DIM:
+    _shape(fn, "k_cache", shape[5], want)
+    _shape(fn, "v_cache", shape[6], want)
+    _shape(fn, "kv_scale", shape[7], (pages, Hkv, 2, PAGE_SIZE // SCALE_BLOCK))
+    if qkv.dtype is not _BF16 or len(rows) != 2 or (N and qkv.stride(1) != 1) or rows[0] < N or \
+            rows[1] < (Hq + 2 * Hkv) * HEAD_DIM:
         raise ValueError(f"{fn}: qkv is not a BF16 matrix of {N} rows of {Hq} + 2 x {Hkv} heads")
     if qkv.get_device() != dev:
         raise ValueError(f"{fn}: qkv is on {qkv.device}, not on the current device")
-    if q_norm_w.numel() != HEAD_DIM or k_norm_w.numel() != HEAD_DIM or \
-            (freq is not None and freq.numel() != HEAD_DIM // 2):
+    if count[0] != HEAD_DIM or count[1] != HEAD_DIM or \
+            (freq is not None and count[11] != HEAD_DIM // 2):
         raise ValueError(f"{fn}: norm weights hold {HEAD_DIM} values, freq {HEAD_DIM // 2}")
-    if q_out.numel() < N * Hq * HEAD_DIM or (q_scale_out is not None and
-                                             q_scale_out.numel() < N * Hq):
+    if count[8] < N * Hq * HEAD_DIM or (q_scale_out is not None and count[9] < N * Hq):
         raise ValueError(f"{fn}: q_out or q_scale_out does not hold {N} x {Hq} rows")
-    if block_table.dim() != 2 or (token_req is not None and token_req.numel() != N):
+    if len(table) != 2 or (token_req is not None and count[3] != N):
         raise ValueError(f"{fn}: block_table is no matrix or token_req has not {N} entries")
     # a stride says nothing where there are not two rows
-    stride = qkv.stride(0) if qkv.shape[0] > 1 else qkv.shape[1]
+    stride = qkv.stride(0) if rows[0] > 1 else rows[1]
     params = hpc_rope_norm_params(float(eps), float(rope_base), int(rope_layout),
-                                  1 if norm_first else 0, _adr(freq))
+                                  1 if norm_first else 0, fr_)
     status = lib().hpc_rope_norm_block(
-        qkv.data_ptr(), stride, q_norm_w.data_ptr(), k_norm_w.data_ptr(), positions.data_ptr(),
-        _adr(token_req), N, Hq, Hkv, HEAD_DIM, block_table.data_ptr(), block_table.shape[1],
-        block_table.shape[0], k_cache.data_ptr(), v_cache.data_ptr(), kv_scale.data_ptr(), pages,
-        q_out.data_ptr(), _adr(q_scale_out), _adr(flags), ctypes.byref(params),
-        _raw_stream(dev, stream))
+        qkv.data_ptr(), stride, wq_, wk_, pos_, req_, N, Hq, Hkv, HEAD_DIM, bt_,
+        table[1], table[0], k_, v_, sc_, pages, q_, qs_, fl_,
+        ctypes.byref(params), _raw_stream(dev, stream))
     if status != HPC_OK:
         _check(fn, status)
 
@@ -721,44 +696,25 @@ def hpc_kv_read_block(k_cache, v_cache, kv_scale, block_table, starts, seqlens, 
                       out_block_table, flags=None, stream=None):
     """Tokens starts[r] .. seqlens[r] - 1 (starts None: from 0) of a block-scaled
     cache as BF16 into the pages out_block_table names."""
-    fn, f32, i32, e4m3 = "hpc_kv_read_block", torch.float32, torch.int32, torch.float8_e4m3fn
-    bf16, dev, Hkv, B = torch.bfloat16, _current_device(), int(Hkv), seqlens.numel()
-    pages, out_pages = k_cache.shape[0], k_out.shape[0]
-    if not (k_cache.dtype is e4m3 and v_cache.dtype is e4m3 and kv_scale.dtype is f32
-            and block_table.dtype is i32 and seqlens.dtype is i32 and out_block_table.dtype is i32
-            and k_out.dtype is bf16 and v_out.dtype is bf16
-            and k_cache.is_contiguous() and v_cache.is_contiguous() and kv_scale.is_contiguous()
-            and block_table.is_contiguous() and seqlens.is_contiguous()
-            and out_block_table.is_contiguous() and k_out.is_contiguous()
-            and v_out.is_contiguous()
-            and dev == k_cache.get_device() == v_cache.get_device() == kv_scale.get_device()
-            == block_table.get_device() == seqlens.get_device() == out_block_table.get_device()
-            == k_out.get_device() == v_out.get_device()
-            and (starts is None or _is_dense(starts, i32, dev))
-            and (flags is None or _is_dense(flags, i32, dev))):
-        _dense(fn, dev, "k_cache v_cache", e4m3, k_cache, v_cache)
-        _dense(fn, dev, "kv_scale", f32, kv_scale)
-        _dense(fn, dev, "block_table starts seqlens out_block_table flags", i32, block_table,
-               starts, seqlens, out_block_table, flags)
-        _dense(fn, dev, "k_out v_out", bf16, k_out, v_out)
+    fn, dev, Hkv = "hpc_kv_read_block", _current_device(), int(Hkv)
+    (k_, v_, sc_, bt_, st_, sl_, ko_, vo_, ot_, fl_), shape, count = _arrays(
+        fn, dev, "k_cache v_cache kv_scale block_table starts seqlens k_out v_out out_block_table "
+        "flags", (_E4M3, _E4M3, _F32, _I32, _I32, _I32, _BF16, _BF16, _I32, _I32), k_cache, v_cache,
+        kv_scale, block_table, starts, seqlens, k_out, v_out, out_block_table, flags)
+    B, pages, out_pages = count[5], *(shape[i][0] if shape[i] else 0 for i in (0, 6))
     want, out_want = (pages, PAGE_SIZE, Hkv, HEAD_DIM), (out_pages, PAGE_SIZE, Hkv, HEAD_DIM)
-    if k_cache.shape != want or v_cache.shape != want or k_out.shape != out_want or \
-            v_out.shape != out_want:
-        _shape(fn, "k_cache", k_cache, want)
-        _shape(fn, "v_cache", v_cache, want)
-        _shape(fn, "k_out", k_out, out_want)
-        _shape(fn, "v_out", v_out, out_want)
-    _shape(fn, "kv_scale", kv_scale, (pages, Hkv, 2, PAGE_SIZE // SCALE_BLOCK))
-    for name, t in (("block_table", block_table), ("out_block_table", out_block_table)):
-        if t.dim() != 2 or t.shape[0] < B:
-            raise ValueError(f"{fn}: {name} has not a row for each of the {B} requests")
-    if starts is not None and starts.numel() != B:
+    _shape(fn, "k_cache", shape[0], want)
+    _shape(fn, "v_cache", shape[1], want)
+    _shape(fn, "k_out", shape[6], out_want)
+    _shape(fn, "v_out", shape[7], out_want)
+    _shape(fn, "kv_scale", shape[2], (pages, Hkv, 2, PAGE_SIZE // SCALE_BLOCK))
+    _table(fn, "block_table", shape[3], B)
+    _table(fn, "out_block_table", shape[8], B)
+    if starts is not None and count[4] != B:
         raise ValueError(f"{fn}: starts has not {B} entries")
     status = lib().hpc_kv_read_block(
-        k_cache.data_ptr(), v_cache.data_ptr(), kv_scale.data_ptr(), pages, block_table.data_ptr(),
-        block_table.shape[1], _adr(starts), seqlens.data_ptr(), B, Hkv, HEAD_DIM, k_out.data_ptr(),
-        v_out.data_ptr(), out_pages, out_block_table.data_ptr(), out_block_table.shape[1],
-        _adr(flags), _raw_stream(dev, stream))
+        k_, v_, sc_, pages, bt_, shape[3][1], st_, sl_, B, Hkv, HEAD_DIM, ko_, vo_, out_pages, ot_,
+        shape[8][1], fl_, _raw_stream(dev, stream))
     if status != HPC_OK:
         _check(fn, status)
 

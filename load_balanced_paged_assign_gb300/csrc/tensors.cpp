@@ -1,0 +1,92 @@
+// The binding's look at its tensors, in one call: a decode step names eleven, and
+// asking each for its type, layout, device, address and sizes from Python takes
+// 4.5 us of the 13 that enqueueing a step took (1 of 10.8 here).
+#include <torch/csrc/Dtype.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <exception>
+
+namespace {
+
+// (owned references; null after an error)
+PyObject *shape_of(const at::Tensor &t) {
+    const auto sizes = t.sizes();
+    PyObject *out = PyTuple_New((Py_ssize_t)sizes.size());
+    for (size_t d = 0; out && d < sizes.size(); ++d) {
+        PyObject *n = PyLong_FromLongLong(sizes[d]);
+        if (n) PyTuple_SET_ITEM(out, d, n);
+        else Py_CLEAR(out);
+    }
+    return out;
+}
+
+// dense(device, dtypes, *tensors): (addresses, shapes, element counts) of the
+// tensors, None for None, if each is a row-major array of its type on the CUDA
+// device of that number (-1: in host memory); otherwise the index of the first that
+// is not.
+PyObject *dense(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n < 2 || !PyTuple_Check(args[1]) || PyTuple_GET_SIZE(args[1]) != n - 2) {
+        PyErr_SetString(PyExc_TypeError, "dense(device, dtypes, *tensors): a type for each");
+        return nullptr;
+    }
+    const long device = PyLong_AsLong(args[0]);
+    if (device == -1 && PyErr_Occurred()) return nullptr;
+    PyObject *lists[3] = {PyTuple_New(n - 2), PyTuple_New(n - 2), PyTuple_New(n - 2)};
+    PyObject *out = lists[0] && lists[1] && lists[2] ? PyTuple_New(3) : nullptr;
+    if (!out) {
+        for (PyObject *l : lists) Py_XDECREF(l);
+        return nullptr;
+    }
+    for (int k = 0; k < 3; ++k) PyTuple_SET_ITEM(out, k, lists[k]);
+    try {
+        for (Py_ssize_t i = 0; i < n - 2; ++i) {
+            PyObject *o = args[i + 2], *type = PyTuple_GET_ITEM(args[1], i);
+            PyObject *found[3] = {Py_None, Py_None, Py_None};
+            if (o == Py_None) {
+                for (PyObject *f : found) Py_INCREF(f);
+            } else {
+                if (!THPVariable_Check(o) || !THPDtype_Check(type)) {
+                    Py_DECREF(out);
+                    return PyLong_FromSsize_t(i);
+                }
+                const at::Tensor &t = THPVariable_Unpack(o);
+                if (t.scalar_type() != reinterpret_cast<THPDtype *>(type)->scalar_type ||
+                    !t.is_contiguous() ||
+                    !(device < 0 ? t.is_cpu() : t.is_cuda() && t.get_device() == device)) {
+                    Py_DECREF(out);
+                    return PyLong_FromSsize_t(i);
+                }
+                found[0] = PyLong_FromVoidPtr(const_cast<void *>(t.const_data_ptr()));
+                found[1] = shape_of(t);
+                found[2] = PyLong_FromLongLong(t.numel());
+            }
+            bool whole = true;
+            for (int k = 0; k < 3; ++k) {
+                whole &= found[k] != nullptr;
+                if (found[k]) PyTuple_SET_ITEM(lists[k], i, found[k]);
+            }
+            if (!whole) {
+                Py_DECREF(out);
+                return nullptr;
+            }
+        }
+    } catch (const std::exception &e) {  // a tensor without storage
+        Py_DECREF(out);
+        PyErr_SetString(PyExc_ValueError, e.what());
+        return nullptr;
+    }
+    return out;
+}
+
+PyMethodDef methods[] = {
+    {"dense", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(dense)), METH_FASTCALL,
+     "dense(device, dtypes, *tensors): (addresses, shapes, element counts), or the index of the "
+     "first tensor that is no row-major array of its type on the device"},
+    {nullptr, nullptr, 0, nullptr}};
+
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods,
+                      nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__tensors() { return PyModule_Create(&module); }

@@ -170,6 +170,27 @@ def test_read_refusals():
 
 # ---------------------------------------------------------------- binding
 @pytest.mark.skipif(torch.cuda.is_available(), reason="CPU tensors stand in for device ones")
+def test_the_extension_looks_at_tensors():
+    from load_balanced_paged_assign_gb300._tensors import dense
+    f32, i32, bf16 = torch.float32, torch.int32, torch.bfloat16
+    x, n = torch.zeros((3, 4)), torch.zeros(0, dtype=i32)
+    s = torch.zeros((), dtype=bf16)
+    assert dense(-1, (f32, i32, f32, bf16), x, n, None, s) == (
+        (x.data_ptr(), n.data_ptr(), None, s.data_ptr()), ((3, 4), (0,), None, ()), (12, 0, None, 1))
+    assert dense(-1, (f32, f32), x[1:], x[:, 1:]) == 1  # rows are dense, columns are not
+    assert dense(-1, (f32, f32), x.T, x) == 0
+    assert dense(-1, (i32,), x) == 0 and dense(0, (f32,), x) == 0
+    assert dense(-1, (f32, f32), x, x.to("meta")) == 1
+    assert dense(-1, (f32,), [1.0]) == 0 and dense(-1, ("f32",), x) == 0
+    assert dense(-1, ()) == ((), (), ())
+    for bad in ((-1, (f32,)), (-1, [f32], x), ("a", (f32,), x), (-1,)):
+        with pytest.raises(TypeError):
+            dense(*bad)
+    for _ in range(1000):  # nothing it returns is kept or dropped once too often
+        dense(-1, (f32, i32, f32), x, n, None)
+        dense(-1, (f32, i32), x, x)
+
+
 def test_binding_refuses_what_is_no_dense_array_of_its_type():
     bf16, e4m3 = torch.bfloat16, torch.float8_e4m3fn
     cache = torch.zeros((3, 64, 2, 128), dtype=bf16)
