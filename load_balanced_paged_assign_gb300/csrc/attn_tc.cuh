@@ -45,8 +45,8 @@
 // rescales its accumulator in TMEM.
 // Measured (queries, plan and merges included; the part of the measured copy
 // rate that the cache's bytes alone make):
-//   64 requests of 1K to 128K, 8 heads on 1, block scales, 560 MB: 92 us, 90%
-//   64 of 512 to 16K, 64 heads on 8, two tokens, block scales, 731 MB: 125 us, 86%
+//   64 requests of 1K to 128K, 8 heads on 1, block scales, 560 MB: 91 us, 91%
+//   64 of 512 to 16K, 64 heads on 8, two tokens, block scales, 731 MB: 124 us, 87%
 //   128 of 1K to 32K, 16 on 2, window 1024, 69 MB: 24 us, 42%
 //   48 of 500 to 16K, 48 on 8, two tokens, window 2048, 155 MB: 42 us, 54%
 // The long streams run at the rate of HBM; what the short ones add is fixed: 5 us
