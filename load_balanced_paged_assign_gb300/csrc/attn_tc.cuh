@@ -1105,8 +1105,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tmem_dealloc(tmem, Tr::kTmemCols);
         return;
     }
-    // End of the stream: all groups' warps merge the split units this CTA owes,
-    // four rows of a unit per warp at a time (their loads in flight together).
+    // End of the stream: all groups' warps merge the split units this CTA owes, two
+    // rows of a unit per warp at a time, their loads in flight together (four took
+    // 1 us longer in short launches: more of them sit in one warp, and their code is
+    // fetched for a single run).
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar.end);
@@ -1114,21 +1116,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     grid_dependency_wait();
     const int nlast = min(last[0].flags, kMaxLast);
     const int w = warp - 4, items = nlast * p.R;
-    for (int item = 4 * w; item < items; item += 4 * 12) {
-        DescInfo dd[4];
-        int rr[4];
+    for (int item = 2 * w; item < items; item += 2 * 12) {
+        DescInfo dd[2];
+        int rr[2];
         bool few = true;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {  // (past the end: the last row again)
+        for (int k = 0; k < 2; ++k) {  // (past the end: the last row again)
             const int e = min(item + k, items - 1);
             dd[k] = last[1 + e / p.R].di;
             rr[k] = e % p.R;
             few &= dd[k].count <= 32;
         }
         if (few) {
-            merge_unit_rows<4, 4>(p, dd, rr);
+            merge_unit_rows<4, 2>(p, dd, rr);
         } else {
-            for (int k = 0; k < 4 && item + k < items; ++k) merge_unit_head<8>(p, dd[k], rr[k]);
+            for (int k = 0; k < 2 && item + k < items; ++k) merge_unit_head<8>(p, dd[k], rr[k]);
         }
     }
 }
