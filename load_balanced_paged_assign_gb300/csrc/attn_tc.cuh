@@ -346,6 +346,11 @@ __device__ __forceinline__ float warp_reduce_rows(float (&v)[N], int lane) {
     return s;
 }
 
+// A value that is the same in every lane, as one that the compiler knows to be.
+__device__ __forceinline__ int uniform(int v) {
+    return (int)__reduce_or_sync(kFullMask, (unsigned)v);
+}
+
 // ------------------------------------------------------------------ producer
 // One descriptor through the ring; see stream_desc in attn_kernel.cuh for the
 // derived-descriptor cases (desc_idx < 0) and the deferred map look-up.
@@ -361,6 +366,7 @@ __device__ __forceinline__ bool tc_stream(const CUtensorMap *tmap_k, const CUten
     TcInfo *info = reinterpret_cast<TcInfo *>(smem + Tr::kOffInfo);
     const TcBars bar = tc_bars<Tr>(smem);
     if (tb >= te) return true;
+    h = uniform(h), r = uniform(r), tb = uniform(tb), te = uniform(te);
     const int L = clamp_len(p, p.seqlens[r]);
     const int skip = window_skip(L, p.q_len, p.window, p.sink_tiles);
     const int u = h * p.B + r;
@@ -396,8 +402,8 @@ __device__ __forceinline__ bool tc_stream(const CUtensorMap *tmap_k, const CUten
         }
         for (int k = 0; k < nt; k += Tr::kPages) {
             const int ns = min(Tr::kPages, nt - k), t = t0 + k;
-            const int pg0 = __shfl_sync(kFullMask, page, k);
-            const int pg1 = __shfl_sync(kFullMask, page, min(k + 1, 31));
+            const int pg0 = uniform(__shfl_sync(kFullMask, page, k));
+            const int pg1 = uniform(__shfl_sync(kFullMask, page, min(k + 1, 31)));
             const bool first = t == tb, last = t + ns == te;
             const bool defer = last && desc_idx < 0 && !walk && !ps.waited;
             int idx = desc_idx, count = 0, chunk_off = 0;
@@ -415,13 +421,15 @@ __device__ __forceinline__ bool tc_stream(const CUtensorMap *tmap_k, const CUten
             if (!warp_wait(&bar.empty[stage], ((ps.it / STAGES) & 1u) ^ 1u, abort)) return false;
             uint64_t *full = &bar.full[stage];
             TcInfo &si = info[stage];
-            if (lane == 0) {
+            if (elect_one()) {
                 mbar_expect_tx(full, (uint32_t)(ns * HEADS) *
                                              (2u * Tr::kTileBytes + (BLK ? kPageScales * 4u : 0u)) +
                                          (first ? q_bytes : 0u));
                 uint8_t *sk = smem + Tr::kOffK + stage * Tr::kStageKV;
                 uint8_t *sv = smem + Tr::kOffV + stage * Tr::kStageKV;
-                for (int s = 0; s < ns; ++s) {
+#pragma unroll
+                for (int s = 0; s < Tr::kPages; ++s) {
+                    if (s >= ns) break;
                     const int pg = s ? pg1 : pg0;
                     tma_load_4d(sk + s * Tr::kTileBytes, tmap_k, full, 0, 0, HEADS * h, pg, policy);
                     tma_load_4d(sv + s * Tr::kTileBytes, tmap_v, full, 0, 0, HEADS * h, pg, policy);
@@ -553,10 +561,6 @@ __device__ __forceinline__ void tc_producer(const CUtensorMap *tmap_k, const CUt
 }
 
 // ------------------------------------------------------------------ MMA issue
-// A value that is the same in every lane, as one that the compiler knows to be.
-__device__ __forceinline__ int uniform(int v) {
-    return (int)__reduce_or_sync(kFullMask, (unsigned)v);
-}
 
 // First products: S of each stage, once it has landed and its group has taken
 // the scores of the stage before the last.
