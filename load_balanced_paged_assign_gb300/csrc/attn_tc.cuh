@@ -45,14 +45,14 @@
 // rescales its accumulator in TMEM.
 // Measured (queries, plan and merges included; the part of the measured copy
 // rate that the cache's bytes alone make):
-//   64 requests of 1K to 128K, 8 heads on 1, block scales, 560 MB: 91 us, 91%
-//   64 of 512 to 16K, 64 heads on 8, two tokens, block scales, 731 MB: 124 us, 87%
-//   128 of 1K to 32K, 16 on 2, window 1024, 69 MB: 24 us, 42%
-//   48 of 500 to 16K, 48 on 8, two tokens, window 2048, 155 MB: 42 us, 54%
+//   64 requests of 1K to 128K, 8 heads on 1, block scales, 560 MB: 89 us, 93%
+//   64 of 512 to 16K, 64 heads on 8, two tokens, block scales, 731 MB: 122 us, 88%
+//   128 of 1K to 32K, 16 on 2, window 1024, 69 MB: 23 us, 44%
+//   48 of 500 to 16K, 48 on 8, two tokens, window 2048, 155 MB: 41 us, 56%
 // The long streams run at the rate of HBM; what the short ones add is fixed: 5 us
 // from the launch to the first stage's landing (lengths, block table, tiles, one
 // after the other) and 6 to 8 us from the last landing to the end (softmax and
-// product 2, join 2, the merges of units split between CTAs 2.5).
+// product 2, join 2, the merges of units split between CTAs 1.5 to 2.5).
 // Every wait is bounded.  Named barriers are reached by all four warps of a
 // group: a wait that failed is voted on there, and the group leaves together.
 #pragma once

@@ -1,6 +1,6 @@
 // The binding's look at its tensors, in one call: a decode step names eleven, and
 // asking each for its type, layout, device, address and sizes from Python takes
-// 4.5 us of the 13 that enqueueing a step took (1 of 10.8 here).
+// 4.5 us of the 13 that enqueueing a step took (1 of 10 here).
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
