@@ -5,9 +5,10 @@
 // Two 128-row Q tiles share every KV page: S = Q_x K^T into TMEM, one softmax
 // thread per row (online, in fp32: a reference that moves when a score passes it
 // by 2^8, P written over the scores as BF16, half a step of 2^-8), O_x += P V with
-// P read from TMEM.  What bounds it is the tensor pipe: at N = 64 the scores' MMAs are limited by their operands' reads
-// from shared memory (A 32 KB + B 16 KB at 128 bytes a cycle, 384 cycles; O's take
-// 256), 1280 cycles a page for both Q tiles where a page takes 1400.
+// P read from TMEM.  What bounds it is the tensor pipe: at N = 64 the scores' MMAs
+// are limited by their operands' reads from shared memory (A 32 KB + B 16 KB at 128
+// bytes a cycle, 384 cycles; O's take 256), 1280 cycles a page for both Q tiles
+// where a page takes 1400.
 //   * The unit is a page, not two.  A Q tile has two 64-column score buffers in
 //     TMEM, and its scores run two pages ahead of its products, so that the
 //     softmax of a page meets the next one's scores ready (with one buffer of 128

@@ -278,6 +278,34 @@ def test_repeated_and_captured_launches_are_identical():
     c2.check(out)
 
 
+@pytest.mark.parametrize("kv", KINDS)
+def test_two_captured_graphs_share_a_workspace(kv):
+    """Steps over a window and over the whole context, captured with one workspace
+    and replayed in turn on one stream: each leaves it as the other needs it."""
+    c = Case(kv, [3000, 64, 777, 1], 16, 2, 1, 512, 8, seed=68, poison=False).to_gpu()
+    ws = c.workspace()
+    graphs, outs, eager = [], [], []
+    for window, sinks in ((512, 8), (0, 0)):
+        c.window, c.sinks = window, sinks
+        eager.append(c.step(ws=ws)[0])
+        out = torch.zeros_like(eager[-1])
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            hd.hpc_decode_step_win(c.q, c.qs, c.k, c.v, c.ks, c.vs, c.scale, c.bt, c.sl, 16, 2, 1,
+                                   window, sinks, c.sm, ws.num_ctas, 2, ws.tmap, ws.part_o,
+                                   ws.part_lse, out, unit_done=ws.unit_done)
+        graphs.append(g)
+        outs.append(out)
+    for k in (0, 1, 1, 0, 1, 0):
+        outs[k].zero_()
+        graphs[k].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[k].view(torch.int16), eager[k].view(torch.int16))
+    assert int(torch.count_nonzero(ws.unit_done)) == 0
+
+
 def test_two_streams_with_their_own_workspaces():
     cases = [Case(kv, LENS, 8, 1, 1, 200, 4, seed=66 + i).to_gpu()
              for i, kv in enumerate(("block", "bf16"))]
