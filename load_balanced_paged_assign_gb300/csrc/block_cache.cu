@@ -82,12 +82,15 @@ struct BlockWriteShared {
 
 // x^(-1/2) and 448 / m to about a rounding: a step of Newton's method from the
 // approximations (2 ulp), for a value that a whole row of codes follows.  (Zero
-// and infinity, of rows with infinities or next to nothing, stay as they are.)
+// and infinity, of rows with infinities, stay as they are.)  The quotient is taken
+// of maxima between kQueryLow and kQueryHigh.
 __device__ __forceinline__ float root_inverse(float x) {
     const float y = rsqrtf(x);
     const float r = fmaf(0.5f * y, fmaf(-x * y, y, 1.f), y);
     return y > 0.f && y <= 3.402823466e38f ? r : y;
 }
+constexpr float kQueryLow = 7.888609052210118e-31f;  // 2^-100
+constexpr float kQueryHigh = 1.2676506002282294e30f;  // 2^100
 __device__ __forceinline__ float quotient448(float m) {
     const float y = __fdividef(kMaxE4m3, m);
     const float r = fmaf(fmaf(-y, m, kMaxE4m3), y * (1.f / kMaxE4m3), y);
@@ -292,7 +295,13 @@ __device__ __forceinline__ void write_queries(const BlockWriteArgs &a, const flo
             for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
             // codes = y * 448 / max|y|, the scale max|y| / 448 (1 for a zero row)
             const bool live = m > 0.f;
-            scale8(x, live ? quotient448(m) : 0.f);
+            float mid = m;
+            if (live && !(m >= kQueryLow && m <= kQueryHigh)) {  // 448 / m may leave fp32's range
+                const float lift = m < kQueryLow ? kQueryHigh : kQueryLow;  // exact, for the maximum too
+                scale8(x, lift);
+                mid = m * lift;
+            }
+            scale8(x, live ? quotient448(mid) : 0.f);
             if (row < a.Hq) {
                 store_e4m3<LAYOUT>(static_cast<char *>(a.q_out) + out * kHeadDim, s, x);
                 if (s == 0) a.q_scale_out[out] = live ? m * (1.0f / kMaxE4m3) : 1.f;
