@@ -29,9 +29,9 @@
 //   * Tokens that no query of the pair sees (past L_r, or before the window and no
 //     sink) may hold anything: a warp of its own zeroes their V rows once the page
 //     has landed (0 * NaN would reach O) and passes every page on.
-// 8192 queries of 64 heads with a window of 1024 and 64 sinks (273 GFLOP): 232 us,
-// 1175 TFLOP/s (245 us in long runs, under the power limit); 2 x 1000 behind 3111
-// tokens with a window of 2000 (132 GFLOP): 124 us; 512 with 128: 12.6 us.
+// 8192 queries of 64 heads with a window of 1024 and 64 sinks (273 GFLOP): 237 us,
+// 1150 TFLOP/s (250 us in long runs, under the power limit); 2 x 1000 behind 3111
+// tokens with a window of 2000 (132 GFLOP): 127 us; 512 with 128: 12.7 us.
 //
 // All barrier phases are counted across items.  Every wait is bounded; on a
 // timeout the CTA raises the error flag, waits (bounded) for its copies and
@@ -169,6 +169,12 @@ __device__ __forceinline__ Item item_of(const WinArgs &a, int item, int L) {
 // the MMAs take their operands from uniform registers, and moving each there
 // costs more than the MMA.
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_or_sync(0xffffffffu, v); }
+
+// acc += a BF16 value, without widening it first (the widened pairs in paired adds:
+// 241 us for 8192 queries instead of 237).
+__device__ __forceinline__ void add_bf16(float &acc, uint16_t x) {
+    asm("add.f32.bf16 %0, %1, %0;" : "+f"(acc) : "h"(x));
+}
 
 // The low bits up to and with bit k.
 __device__ __forceinline__ uint64_t bits_to(int k) {
@@ -438,12 +444,6 @@ __global__ void __launch_bounds__(kWinThreads, 1)
             const int lim = min(p0 + lane, it.L - 1), lo = p0 + lane + 1 - a.window;
             const int lim_all = min(p0, it.L - 1), lo_all = p0 + 32 - a.window;
             const Seen sn = it.seen(x);
-            // Over few pages the sum takes the weights as they were rounded: where a
-            // row has a handful of tokens the heaviest one's rounding is not averaged
-            // out, and cancels against its own in the sum (13 tokens: off by 0.0018 of
-            // the output's norm instead of 0.0029).  Longer rows are off by 0.0021
-            // instead of 0.0019 (BF16 outputs alone: 0.0017), and 4% faster.
-            const bool few = sn.cnt <= 4;
             float m_ref = -INFINITY, l = 0.f;
             bool started = false;
             for (int c = 0; c < sn.cnt; ++c) {
@@ -488,25 +488,26 @@ __global__ void __launch_bounds__(kWinThreads, 1)
                 const float base = new_ref == -INFINITY ? 0.f : new_ref;
                 // P as packed BF16 pairs, over the first half of the scores
                 uint32_t pk[32];
-                float2 ps[4] = {};
                 const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(-base, -base);
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {  // two columns per instruction
                     const float2 e = __ffma2_rn(make_float2(s[2 * c], s[2 * c + 1]), sc2, nb2);
-                    const float e0 = ex2(e.x), e1 = ex2(e.y);
-                    ps[c & 3] = __fadd2_rn(ps[c & 3], make_float2(e0, e1));
-                    pk[c] = pack_bf16x2(e0, e1);
+                    pk[c] = pack_bf16x2(ex2(e.x), ex2(e.y));
                 }
                 tmem_st32_nowait(scol + 64 * b, pk);
-                if (few) {
-                    ps[0] = ps[1] = ps[2] = ps[3] = make_float2(0.f, 0.f);
+                // The sum takes the weights as they were rounded: the heaviest one's
+                // rounding then cancels against its own in the product, which a row with
+                // one heavy token needs, however many it sees (a token that holds nearly
+                // all of the weight comes out to its BF16 rounding; with the unrounded
+                // sum, 2% faster, twice as far off).
+                float ps[8] = {};
 #pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        ps[c & 3] = __fadd2_rn(ps[c & 3], make_float2(bf16lo_to_f32(pk[c]),
-                                                                      bf16hi_to_f32(pk[c])));
+                for (int c = 0; c < 32; ++c) {
+                    add_bf16(ps[2 * (c & 3)], (uint16_t)pk[c]);
+                    add_bf16(ps[2 * (c & 3) + 1], (uint16_t)(pk[c] >> 16));
                 }
-                const float2 pq = __fadd2_rn(__fadd2_rn(ps[0], ps[1]), __fadd2_rn(ps[2], ps[3]));
-                l = l * factor + (pq.x + pq.y);
+                l = l * factor + (((ps[0] + ps[1]) + (ps[2] + ps[3])) +
+                                  ((ps[4] + ps[5]) + (ps[6] + ps[7])));
                 if (started && __any_sync(0xffffffffu, need)) {
                     // O_x is settled once its last product is done (the product two
                     // before that, the same barrier's last, was issued before these
