@@ -69,13 +69,15 @@ struct TcInfo {  // of a stage, written by the producer
     int flags, seqlen, desc_idx, count;
     int chunk_off, skip, left, ord;  // left: stages of the descriptor after this one
     float qscale[2 * kMaxRows];  // of head y's row r at 16 y + r
-    int pad[4];
+    int group;  // softmax group (0, 1) of the descriptor's first stage
+    int pad[3];
 };
 static_assert(sizeof(TcInfo) == 192, "TcInfo layout");
 
 struct TcJoin {  // of a descriptor, for the join group
     DescInfo di;
-    int only, end, pad;  // only: the group (0, 1) that handled it alone, or -1; end: no more
+    int only, end;  // only: the group (0, 1) that handled it alone, or -1; end: no more
+    int group;      // the group that handled its first stage
 };
 static_assert(sizeof(TcJoin) == 32, "TcJoin layout");
 
@@ -369,7 +371,7 @@ __device__ __forceinline__ bool tc_stream(const CUtensorMap *tmap_k, const CUten
     h = uniform(h), r = uniform(r), tb = uniform(tb), te = uniform(te);
     const int L = clamp_len(p, p.seqlens[r]);
     const int skip = window_skip(L, p.q_len, p.window, p.sink_tiles);
-    const int u = h * p.B + r;
+    const int u = h * p.B + r, group = (int)(ps.it & 1u);
     // lane: row i G + g' of the descriptor, g' = y Gh + g of its head y
     float qs = 1.f;
     int qs_at = -1;
@@ -452,6 +454,7 @@ __device__ __forceinline__ bool tc_stream(const CUtensorMap *tmap_k, const CUten
                 si.skip = skip;
                 si.left = (te - t - ns + Tr::kPages - 1) / Tr::kPages;
                 si.ord = ord;
+                si.group = group;
             }
             if (defer) {  // the stage's copies are on their way
                 wait_for_map(ps);
@@ -858,7 +861,7 @@ __device__ __forceinline__ bool tc_softmax(const AttnParams &p, uint8_t *smem, u
 #pragma unroll
             for (int c = 0; c < 8; ++c) sts128(v + 16 * c, 0u, 0u, 0u, 0u);
         }
-        const int left = info[s].left;
+        const int left = info[s].left, group = info[s].group;
         const DescInfo di = {info[s].req, info[s].kv_head, info[s].desc_idx, info[s].count,
                              info[s].chunk_off};
         fence_proxy_async_smem();
@@ -877,7 +880,7 @@ __device__ __forceinline__ bool tc_softmax(const AttnParams &p, uint8_t *smem, u
             if (HEADS == 2 ? tid % 64 == 0 : tid == 0)
 #pragma unroll
                 for (int r = 0; r < RB; ++r) refs[(slot * 2 + x) * 32 + 16 * hd + r] = m[r];
-            if (tid == 0 && left == 0) joins[slot] = TcJoin{di, alone ? x : -1, 0, 0};
+            if (tid == 0 && left == 0) joins[slot] = TcJoin{di, alone ? x : -1, 0, group};
         }
         __syncwarp();
         if (lane == 0) mbar_arrive_n(&bar.pub[slot], alone ? 2 : 1);
@@ -932,6 +935,10 @@ __device__ __forceinline__ bool tc_join(const AttnParams &p, uint8_t *smem, uint
             fac[64 + tid] = Z > 0.f ? (M + lg2(Z)) * kLn2 : kNegInf;  // natural-log LSE
         }
         named_bar_sync(bid, kTcGroup);
+        // the group of the descriptor's first stage first: where a stage stands in
+        // the CTA's stream (a race, with more bins than CTAs) decides which one that
+        // is, and may not decide how the sum below rounds
+        const int group = uniform(j.group);
         float out[HEADS][RB];
         tc_fence_after();
 #pragma unroll
@@ -939,7 +946,8 @@ __device__ __forceinline__ bool tc_join(const AttnParams &p, uint8_t *smem, uint
 #pragma unroll
             for (int r = 0; r < RB; ++r) out[y][r] = 0.f;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int n = 0; n < 2; ++n) {
+                const int k = n ^ group;
                 if (j.only == (k ^ 1)) continue;
                 const uint32_t oc = lane_base + Tr::o_col(ord & 1, k, y);
                 uint32_t ra[RB], rb[RB], rc[RB];
