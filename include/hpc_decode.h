@@ -102,12 +102,13 @@ typedef enum { HPC_KV_BF16 = 0, HPC_KV_FP8_E4M3 = 1, HPC_KV_E4M3_BLOCK = 2 } hpc
  *               left zero by every attention launch.
  * cap_desc, cap_bins and cap_units give the sizes of desc (entries of four
  * int32), bin_ptr and chunk_count / chunk_off, and are set by the caller.
- * B, Hkv, num_ctas (the number of bins), persistent (0 for a static map, odd
- * for a load-balanced one; hpc_decode_plan_win keeps a tag of its window and
- * whether descriptors are head pairs above bit 0), min_tiles and
- * max_pages (the planner's arguments) are written by the planners (the
- * host-side struct is updated) and read by hpc_decode_attn /
- * hpc_decode_combine, which check B and Hkv against their own arguments.
+ * B, Hkv, num_ctas (the number of bins), persistent (0 for a static map, 1
+ * for a load-balanced one, 3 for one whose descriptors are head pairs),
+ * min_tiles and max_pages (the planner's arguments), and q_len, window and
+ * sinks (hpc_decode_plan_win's where it was given a window, else 0) are
+ * written by the planners (the host-side struct is updated) and read by
+ * hpc_decode_attn / hpc_decode_combine and the calls with a window, which
+ * check B, Hkv and the window against their own arguments.
  * The attention kernel of a persistent map re-derives each CTA's first
  * descriptor from the sequence lengths so it can start before the map is
  * complete; the map and the sequence lengths must describe the same batch.
@@ -125,6 +126,7 @@ typedef struct {
     int32_t *meta;
     int32_t cap_desc, cap_bins, cap_units;
     int32_t B, Hkv, num_ctas, persistent, min_tiles, max_pages;
+    int32_t q_len, window, sinks;
 } hpc_task_map;
 
 /* Library version string (static storage). */

@@ -51,7 +51,8 @@ class hpc_task_map(ctypes.Structure):
         ("cap_desc", ctypes.c_int32), ("cap_bins", ctypes.c_int32), ("cap_units", ctypes.c_int32),
         ("B", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("num_ctas", ctypes.c_int32),
         ("persistent", ctypes.c_int32), ("min_tiles", ctypes.c_int32),
-        ("max_pages", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32), ("q_len", ctypes.c_int32), ("window", ctypes.c_int32),
+        ("sinks", ctypes.c_int32),
     ]
 
 
@@ -257,8 +258,7 @@ class TaskMap:
         self.chunk_off = torch.zeros(units, dtype=torch.int32, device=dev)
         self.meta = torch.zeros(8, dtype=torch.int32, device=dev)
         self.c = hpc_task_map(_ptr(self.desc), _ptr(self.bin_ptr), _ptr(self.chunk_count),
-                              _ptr(self.chunk_off), _ptr(self.meta), cap_desc, cap_bins, units, 0,
-                              0, 0, 0, 0, 0)
+                              _ptr(self.chunk_off), _ptr(self.meta), cap_desc, cap_bins, units)
 
     @classmethod
     def dynamic(cls, B: int, Hkv: int, num_ctas: int, device="cuda"):

@@ -184,15 +184,11 @@ int heads_per_desc(hpc_kv_dtype dt, int32_t window, int32_t Hkv) {
 
 int32_t sink_tiles_of(int32_t sinks) { return (int32_t)(((int64_t)sinks + kTile - 1) / kTile); }
 
-// What map->persistent holds above bit 0: whether its descriptors are head
-// pairs, and above that a value derived from the query count, window and sinks
-// it was planned for (0 without a window).  A call that needs others is refused.
-int32_t window_tag(int32_t q_len, const AttnForm &f, int heads) {
-    if (f.window <= 0) return heads - 1;
-    uint64_t x = ((uint64_t)(uint32_t)f.window << 34) ^ ((uint64_t)(uint32_t)f.sinks << 4) ^
-                 (uint64_t)(uint32_t)(q_len - 1);
-    x *= 0x9E3779B97F4A7C15ull;  // 2^64 / golden ratio: spreads every bit upwards
-    return (int32_t)(((x >> 35) | 1) << 1) | (heads - 1);
+// A call needs the map of its own window, sinks and (with a window) query count,
+// and of its own kind of descriptors: bit 1 of map->persistent says head pairs.
+bool planned_for(const hpc_task_map &map, int32_t q_len, const AttnForm &f, int heads) {
+    return map.persistent >> 1 == heads - 1 && map.window == f.window && map.sinks == f.sinks &&
+           (f.window == 0 || map.q_len == q_len);
 }
 
 // Limits of the hpc_decode_*_win and hpc_prefill_attn_win arguments.
@@ -237,10 +233,9 @@ hpc_status launch_attention(const void *d_q, const float *d_q_scale, const void 
     if (st != HPC_OK) return st;
     if (map->B != B || map->Hkv != Hkv || map->num_ctas < 1 || map->num_ctas >= map->cap_bins)
         return HPC_ERR_ARG;
-    // planned for this window (the tag is 0 without one)
     const bool win = form.window > 0;
     const int heads = heads_per_desc(kv_dtype, form.window, Hkv);
-    if (map->persistent >> 1 != window_tag(q_len, form, heads)) return HPC_ERR_ARG;
+    if (!planned_for(*map, q_len, form, heads)) return HPC_ERR_ARG;
 
     CUtensorMap tk, tv;
     if (fp8 && (block || win)) {
@@ -351,6 +346,7 @@ hpc_status combine_impl(const float *d_part_o, const float *d_part_lse, const hp
     st = check_map(map, true);
     if (st != HPC_OK) return st;
     if (map->B != B || map->Hkv != Hkv || (int64_t)B * Hkv > map->cap_units) return HPC_ERR_ARG;
+    if (map->window > 0 && map->q_len != q_len) return HPC_ERR_ARG;
     // descriptors of head pairs: half as many units with twice the rows
     const int heads = 1 + ((map->persistent >> 1) & 1);
     return cuda_status(launch_combine(d_part_o, d_part_lse, *map, B, Hq, Hkv / heads, q_len, d_out,
@@ -488,10 +484,12 @@ hpc_status plan_impl(const int32_t *d_seqlens, int32_t B, int32_t Hkv, int32_t m
     m.B = B;
     m.Hkv = Hkv;
     m.num_ctas = num_ctas;
-    const int32_t tag = window_tag(q_len, form, heads);
-    m.persistent = 1 | (tag << 1);
+    m.persistent = 1 | (heads - 1) << 1;
     m.min_tiles = min_tiles_per_cta;
     m.max_pages = max_pages_per_req;
+    m.q_len = form.window > 0 ? q_len : 0;
+    m.window = form.window;
+    m.sinks = form.sinks;
     PlanWindow win;
     if (form.window > 0) win = {q_len, form.window, sink_tiles_of(form.sinks)};
     st = cuda_status(launch_assign(d_seqlens, B, Hkv / heads, max_pages_per_req, num_ctas,
@@ -530,6 +528,7 @@ hpc_status hpc_decode_plan_static(const int32_t *d_seqlens, int32_t B, int32_t H
     m.persistent = 0;
     m.min_tiles = num_splits;
     m.max_pages = max_pages_per_req;
+    m.q_len = m.window = m.sinks = 0;
     st = cuda_status(launch_static_plan(d_seqlens, B, Hkv, max_pages_per_req, num_splits, m,
                                         static_cast<cudaStream_t>(stream)));
     if (st == HPC_OK) *map = m;

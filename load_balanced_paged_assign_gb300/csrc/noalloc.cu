@@ -139,6 +139,7 @@ extern "C" hpc_status hpc_decode_step_noalloc(
     map.cap_bins = num_ctas + 1;
     map.cap_units = (int32_t)units;
     map.B = map.Hkv = map.num_ctas = map.persistent = map.min_tiles = map.max_pages = 0;
+    map.q_len = map.window = map.sinks = 0;
     hpc_status st = hpc_decode_step(
         d_q, d_q_scale, d_k_cache, d_v_cache, num_pages, k_scale, v_scale, kv_dtype,
         d_block_table, max_pages_per_req, d_seqlens, B, Hq, Hkv, head_dim, sm_scale, num_ctas,

@@ -1,0 +1,40 @@
+"""Maps that a call refuses (no GPU: fake, never-dereferenced device pointers)."""
+
+import ctypes
+
+import pytest
+
+import load_balanced_paged_assign_gb300 as hd
+from load_balanced_paged_assign_gb300 import binding as E
+from test_abi_window_cpu import FAKE, attn, fake_map
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from load_balanced_paged_assign_gb300 import _build
+    _build.build()
+
+
+def window_map(q_len=1, window=200, sinks=4, **kw):
+    m = fake_map(**kw)
+    m.q_len, m.window, m.sinks = q_len, window, sinks
+    return m
+
+
+def test_a_window_is_checked_exactly():
+    for q_len, window, sinks in ((1, 15885, 2599), (1, 20874, 17266), (1, 201, 4), (1, 200, 5),
+                                 (1, 4, 200), (2, 200, 4), (1, 0, 0)):
+        assert attn(q_len=q_len, window=window, sinks=sinks, m=window_map()) == E.HPC_ERR_ARG
+    # head pairs or not goes by the cache's type and heads: two KV heads of E4M3 are one
+    kw = dict(Hq=8, Hkv=2, dtype=1, qs=FAKE, window=200, sinks=4)
+    assert attn(m=window_map(Hkv=2, persistent=1), **kw) == E.HPC_ERR_ARG
+    assert attn(m=window_map(Hkv=2, persistent=3), **dict(kw, dtype=0, qs=None)) == E.HPC_ERR_ARG
+
+
+def test_the_combine_takes_the_maps_query_count():
+    m = window_map(q_len=2)
+    assert hd.lib().hpc_decode_combine_mq(FAKE, FAKE, ctypes.byref(m), 4, 8, 1, 128, 1, FAKE,
+                                          None) == E.HPC_ERR_ARG
+    m = window_map(q_len=1)
+    assert hd.lib().hpc_decode_combine_mq(FAKE, FAKE, ctypes.byref(m), 4, 8, 1, 128, 2, FAKE,
+                                          None) == E.HPC_ERR_ARG

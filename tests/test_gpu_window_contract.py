@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import load_balanced_paged_assign_gb300 as hd
-from _blocks import Case
+from _blocks import DTYPE, Case
 from oracle import window as ow
 
 pytestmark = pytest.mark.gpu
@@ -35,3 +35,36 @@ def test_more_bins_than_ctas_repeat_bit_for_bit(kv, heads):
             assert torch.equal(a, b)
     assert int(hd.hpc_decode_read_meta(ws.tmap)[1]) == 9
     c.check(out)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3", "block"])
+def test_a_map_of_another_window_is_refused(kv):
+    """Every window, sinks and q_len but the map's own, also where they are far
+    apart (200 and 4 against 15885 and 2599)."""
+    c = Case(kv, [900, 64, 300], 8, 2, 1, 200, 4, seed=92, poison=False).to_gpu()
+    ws = c.workspace()
+    hd.hpc_decode_plan_win(c.sl, 2, c.bt.shape[1], ws.num_ctas, 2, ws.tmap, kv_dtype=DTYPE[kv],
+                           window=200, sinks=4)
+    out = torch.zeros((3, 1, 8, 128), dtype=torch.bfloat16, device="cuda")
+
+    def attn(window, sinks):
+        hd.hpc_decode_attn_win(c.q, c.qs, c.k, c.v, c.ks, c.vs, c.scale, c.bt, c.sl, 8, 2, 1,
+                               window, sinks, c.sm, ws.tmap, ws.part_o, ws.part_lse, out,
+                               ws.unit_done)
+
+    attn(200, 4)
+    c.check(out)
+    for window, sinks in ((15885, 2599), (20874, 17266), (201, 4), (200, 5), (4, 200), (0, 0)):
+        with pytest.raises(hd.HpcError):
+            attn(window, sinks)
+    torch.cuda.synchronize()
+    # and a map of one query per request for two
+    c2 = Case(kv, [900, 64, 300], 8, 2, 2, 200, 4, seed=92, poison=False).to_gpu()
+    ws2 = c2.workspace()
+    hd.hpc_decode_plan_win(c.sl, 2, c.bt.shape[1], ws.num_ctas, 2, ws2.tmap, kv_dtype=DTYPE[kv],
+                           q_len=1, window=200, sinks=4)
+    out2 = torch.zeros((3, 2, 8, 128), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(hd.HpcError):
+        hd.hpc_decode_attn_win(c2.q, c2.qs, c2.k, c2.v, c2.ks, c2.vs, c2.scale, c2.bt, c2.sl, 8, 2,
+                               2, 200, 4, c2.sm, ws2.tmap, ws2.part_o, ws2.part_lse, out2,
+                               ws2.unit_done)
