@@ -282,12 +282,12 @@ class TaskMap:
         """The map as host lists (synchronises the current stream)."""
         meta = self.meta.tolist()
         n = int(meta[2])
-        B, Hkv = int(self.c.B), int(self.c.Hkv)
+        units = int(self.c.B) * int(self.c.Hkv) // (2 if self.c.persistent & 2 else 1)  # pairs
         return dict(total_tiles=meta[0], budget=meta[1], num_desc=n, flags=meta[3],
                     desc=[tuple(d) for d in self.desc[:n].tolist()],
                     bin_ptr=self.bin_ptr[:self.num_ctas + 1].tolist(),
-                    chunk_count=self.chunk_count[:B * Hkv].tolist(),
-                    chunk_off=self.chunk_off[:B * Hkv].tolist())
+                    chunk_count=self.chunk_count[:units].tolist(),
+                    chunk_off=self.chunk_off[:units].tolist())
 
 
 def hpc_decode_version() -> str:

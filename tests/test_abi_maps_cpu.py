@@ -38,3 +38,13 @@ def test_the_combine_takes_the_maps_query_count():
     m = window_map(q_len=1)
     assert hd.lib().hpc_decode_combine_mq(FAKE, FAKE, ctypes.byref(m), 4, 8, 1, 128, 2, FAKE,
                                           None) == E.HPC_ERR_ARG
+
+
+def test_to_host_of_a_map_of_head_pairs():
+    """Units are pairs of heads: half as many counts, none left from an earlier plan."""
+    m = E.TaskMap(3, 4, 20, 9, device="cpu")
+    m.chunk_count[:] = 7
+    m.c.B, m.c.Hkv, m.c.num_ctas, m.c.persistent = 3, 4, 8, 1
+    assert len(m.to_host()["chunk_count"]) == len(m.to_host()["chunk_off"]) == 12
+    m.c.persistent = 3
+    assert len(m.to_host()["chunk_count"]) == len(m.to_host()["chunk_off"]) == 6

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import load_balanced_paged_assign_gb300 as hd
+import oracle
 from _blocks import DTYPE, Case
 from oracle import window as ow
 
@@ -68,3 +69,21 @@ def test_a_map_of_another_window_is_refused(kv):
         hd.hpc_decode_attn_win(c2.q, c2.qs, c2.k, c2.v, c2.ks, c2.vs, c2.scale, c2.bt, c2.sl, 8, 2,
                                2, 200, 4, c2.sm, ws2.tmap, ws2.part_o, ws2.part_lse, out2,
                                ws2.unit_done)
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "block"])
+def test_a_map_of_head_pairs_on_the_host(kv):
+    """to_host of a map whose units are pairs of heads: the pairs' counts, and nothing
+    that an earlier plan left behind them."""
+    lens = [700, 64, 0, 1200, 300]
+    c = Case(kv, lens, 8, 4, 1, 500, 4, seed=93, poison=False).to_gpu()
+    ws = c.workspace(40)
+    hd.hpc_decode_plan(c.sl, 4, c.bt.shape[1], 40, 1, ws.tmap)  # single heads
+    hd.hpc_decode_plan_win(c.sl, 4, c.bt.shape[1], 40, 1, ws.tmap, kv_dtype=DTYPE[kv],
+                           window=500, sinks=4)
+    torch.cuda.synchronize()
+    got = ws.tmap.to_host()
+    ref = oracle.assign_closed_form(ow.planned_lengths(lens, c.bt.shape[1], 1, 500, 4), 2, 40, 1)
+    for name in ("total_tiles", "budget", "num_desc", "desc", "bin_ptr", "chunk_count",
+                 "chunk_off"):
+        assert got[name] == getattr(ref, name), name
