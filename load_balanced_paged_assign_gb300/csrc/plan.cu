@@ -63,12 +63,12 @@ __device__ __forceinline__ int live_len(const int32_t *seqlens, int r, int max_p
 
 constexpr size_t kPrefetchMaxBytes = 4u << 20;  // block-table bytes warmed in L2 at most
 
-__global__ void __launch_bounds__(kPlanThreads)
-    assign_kernel(const int32_t *__restrict__ seqlens, int B, int Hkv, int max_pages,
-                  int num_ctas, int floor, int4 *__restrict__ desc, int32_t *__restrict__ bin_ptr,
-                  int32_t *__restrict__ chunk_count, int32_t *__restrict__ chunk_off,
-                  int32_t *__restrict__ meta, int cap_desc, const int32_t *bt_prefetch,
-                  const PlanWindow win) {
+template <bool WIN>
+__device__ __forceinline__ void
+assign(const int32_t *__restrict__ seqlens, int B, int Hkv, int max_pages, int num_ctas, int floor,
+       int4 *__restrict__ desc, int32_t *__restrict__ bin_ptr, int32_t *__restrict__ chunk_count,
+       int32_t *__restrict__ chunk_off, int32_t *__restrict__ meta, int cap_desc,
+       const int32_t *bt_prefetch, const PlanWindow &win) {
     extern __shared__ int s_end[];  // [B] inclusive prefix of tiles per request
     __shared__ int s_scan[32];
     __shared__ unsigned s_flags;
@@ -87,15 +87,16 @@ __global__ void __launch_bounds__(kPlanThreads)
     if (tid == 0) s_flags = 0;
     unsigned flags = 0;
 
-    // a1: tiles per request, n_r = ceil(L_r / 64) less the tiles that no query's
-    // window reaches, and their running sum.
+    // a1: tiles per request, n_r = ceil(L_r / 64) (WIN: less the tiles that no
+    // query's window reaches), and their running sum.
     int carry = 0;
     for (int base = 0; base < B; base += blockDim.x) {
         const int r = base + tid;
         int n = 0;
         if (r < B) {
             const int L = live_len(seqlens, r, max_pages, flags);
-            n = tiles_of(L) - window_skip(L, win.q_len, win.window, win.sink_tiles);
+            n = tiles_of(L);
+            if (WIN) n -= window_skip(L, win.q_len, win.window, win.sink_tiles);
         }
         int chunk_total;
         const int incl = block_inclusive_scan(n, s_scan, chunk_total);
@@ -164,6 +165,27 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
 }
 
+// Two kernels, as the window's 12 bytes of arguments make every step behind a plan
+// 0.2 to 0.5 us longer (the argument bank is read cold, line by line).
+__global__ void __launch_bounds__(kPlanThreads)
+    assign_kernel(const int32_t *__restrict__ seqlens, int B, int Hkv, int max_pages,
+                  int num_ctas, int floor, int4 *__restrict__ desc, int32_t *__restrict__ bin_ptr,
+                  int32_t *__restrict__ chunk_count, int32_t *__restrict__ chunk_off,
+                  int32_t *__restrict__ meta, int cap_desc, const int32_t *bt_prefetch) {
+    assign<false>(seqlens, B, Hkv, max_pages, num_ctas, floor, desc, bin_ptr, chunk_count,
+                  chunk_off, meta, cap_desc, bt_prefetch, PlanWindow());
+}
+
+__global__ void __launch_bounds__(kPlanThreads)
+    assign_window_kernel(const int32_t *__restrict__ seqlens, int B, int Hkv, int max_pages,
+                         int num_ctas, int floor, int4 *__restrict__ desc,
+                         int32_t *__restrict__ bin_ptr, int32_t *__restrict__ chunk_count,
+                         int32_t *__restrict__ chunk_off, int32_t *__restrict__ meta,
+                         int cap_desc, const int32_t *bt_prefetch, const PlanWindow win) {
+    assign<true>(seqlens, B, Hkv, max_pages, num_ctas, floor, desc, bin_ptr, chunk_count,
+                 chunk_off, meta, cap_desc, bt_prefetch, win);
+}
+
 // Static split-KV plan: bin u * S + s is split s of unit u.
 __global__ void __launch_bounds__(kPlanThreads)
     static_plan_kernel(const int32_t *__restrict__ seqlens, int B, int Hkv, int max_pages,
@@ -228,9 +250,12 @@ cudaError_t launch_assign(const int32_t *seqlens, int B, int Hkv, int max_pages,
                           int floor, const hpc_task_map &map, cudaStream_t s,
                           const int32_t *bt_prefetch, const PlanWindow &win) {
     const int smem = assign_smem_bytes(B);
+    const bool plain = win.window == kNoWindow;
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(assign_kernel,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const void *kernel = plain ? reinterpret_cast<const void *>(&assign_kernel)
+                                   : reinterpret_cast<const void *>(&assign_window_kernel);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             smem);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
@@ -243,9 +268,14 @@ cudaError_t launch_assign(const int32_t *seqlens, int B, int Hkv, int max_pages,
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, assign_kernel, seqlens, B, Hkv, max_pages, num_ctas, floor,
-                              reinterpret_cast<int4 *>(map.desc), map.bin_ptr, map.chunk_count,
-                              map.chunk_off, map.meta, map.cap_desc, bt_prefetch, win);
+    int4 *desc = reinterpret_cast<int4 *>(map.desc);
+    if (plain)
+        return cudaLaunchKernelEx(&cfg, assign_kernel, seqlens, B, Hkv, max_pages, num_ctas, floor,
+                                  desc, map.bin_ptr, map.chunk_count, map.chunk_off, map.meta,
+                                  map.cap_desc, bt_prefetch);
+    return cudaLaunchKernelEx(&cfg, assign_window_kernel, seqlens, B, Hkv, max_pages, num_ctas,
+                              floor, desc, map.bin_ptr, map.chunk_count, map.chunk_off, map.meta,
+                              map.cap_desc, bt_prefetch, win);
 }
 
 cudaError_t launch_static_plan(const int32_t *seqlens, int B, int Hkv, int max_pages,
