@@ -743,6 +743,8 @@ hpc_status hpc_decode_step_host(const void *h_q, const float *h_q_scale, const i
                                 int32_t *d_unit_done, hpc_stream_t stream) {
     hpc_status st = check_shapes(B, Hq, Hkv, head_dim, max_pages_per_req);
     if (st != HPC_OK) return st;
+    // (before the copies, whose sizes go by the type)
+    if (kv_dtype != HPC_KV_BF16 && kv_dtype != HPC_KV_FP8_E4M3) return HPC_ERR_ARG;
     const bool fp8 = kv_dtype == HPC_KV_FP8_E4M3;
     if (B > 0 && (!h_q || !h_seqlens || !h_block_table || !h_out || !d_q || !d_seqlens ||
                   !d_block_table || !d_out))
