@@ -22,6 +22,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB_PATH = os.path.join(HERE, "libhpcdecode.so")
 EXT_PATH = os.path.join(HERE, "_tensors.so")
 EXT_SOURCE = os.path.join(CSRC, "tensors.cpp")
+EXT_STAMP = EXT_PATH + ".stamp"  # what the module was built for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -48,9 +49,29 @@ def is_stale() -> bool:
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
+def extension_target() -> str:
+    """What _tensors.so depends on beside its source: it looks into PyTorch's own
+    structures, so a module of another PyTorch or Python is not one to load."""
+    import torch
+    return f"{torch.__version__} {torch.__file__} {sysconfig.get_config_var('SOABI')} " \
+           f"abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+
+
+def extension_built_for() -> str | None:
+    """extension_target() of the module in the tree ("" if it does not say), None without one."""
+    if not os.path.exists(EXT_PATH):
+        return None
+    try:
+        with open(EXT_STAMP) as f:
+            return f.read()
+    except FileNotFoundError:
+        return ""
+
+
 def build_extension(force: bool = False) -> str:
     """Compile _tensors.so, the check of a call's tensors."""
-    if not force and os.path.exists(EXT_PATH) and \
+    target = extension_target()
+    if not force and extension_built_for() == target and \
             os.path.getmtime(EXT_PATH) > max(os.path.getmtime(f) for f in (EXT_SOURCE, __file__)):
         return EXT_PATH
     import torch
@@ -66,6 +87,9 @@ def build_extension(force: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed on {EXT_SOURCE}:\n{res.stderr}")
     os.replace(staged, EXT_PATH)
+    with open(staged, "w") as f:
+        f.write(target)
+    os.replace(staged, EXT_STAMP)
     return EXT_PATH
 
 

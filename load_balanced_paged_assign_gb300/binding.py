@@ -193,6 +193,11 @@ _BF16, _E4M3, _F32, _F64, _I32 = (torch.bfloat16, torch.float8_e4m3fn, torch.flo
 
 def _load_dense():
     global _DENSE
+    built = _build.extension_built_for()
+    if built is not None and built != _build.extension_target():
+        raise RuntimeError(f"the extension module _tensors was built for another PyTorch or Python "
+                           f"({built or 'unknown'}): build it again (python -c 'import __graft_entry__ as g; "
+                           f"g.build()')")
     try:
         from . import _tensors
     except ImportError as e:

@@ -1,0 +1,57 @@
+"""The build of the binding's extension module: when it is made again, and what a
+call says where it cannot be used (a stand-in for the compiler; nothing is built)."""
+
+import os
+import stat
+
+import pytest
+
+import load_balanced_paged_assign_gb300 as hd
+from load_balanced_paged_assign_gb300 import _build
+from load_balanced_paged_assign_gb300 import binding as E
+
+
+@pytest.fixture
+def compiler(tmp_path, monkeypatch):
+    """A module path of its own, and a compiler that writes a file and counts its runs."""
+    log = tmp_path / "runs"
+    cxx = tmp_path / "cxx"
+    cxx.write_text(f'#!/bin/sh\necho run >> {log}\nwhile [ "$1" != -o ]; do shift; done\n'
+                   'echo module > "$2"\n')
+    cxx.chmod(cxx.stat().st_mode | stat.S_IXUSR)
+    monkeypatch.setenv("CXX", str(cxx))
+    monkeypatch.setattr(_build, "EXT_PATH", str(tmp_path / "_tensors.so"))
+    monkeypatch.setattr(_build, "EXT_STAMP", str(tmp_path / "_tensors.so.stamp"), raising=False)
+    return lambda: log.read_text().count("run") if log.exists() else 0
+
+
+def test_the_module_is_built_again_for_another_pytorch(compiler, monkeypatch):
+    import torch
+    _build.build_extension()
+    _build.build_extension()
+    assert compiler() == 1
+    monkeypatch.setattr(torch, "__version__", "9.9.9")
+    _build.build_extension()
+    assert compiler() == 2
+    _build.build_extension()
+    assert compiler() == 2
+    os.remove(_build.EXT_STAMP)  # one that does not say what it was built for
+    _build.build_extension()
+    assert compiler() == 3
+
+
+def test_a_module_of_another_pytorch_is_not_loaded(compiler, monkeypatch):
+    import torch
+    _build.build_extension()
+    monkeypatch.setattr(E, "_DENSE", None)
+
+    def refused():
+        with pytest.raises(RuntimeError, match="another PyTorch"):
+            hd.hpc_decode_plan_win(torch.zeros(1, dtype=torch.int32), 1, 1, 1, 1, None)
+        return E._DENSE is None
+
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "9.9.9")
+        assert refused()
+    os.remove(_build.EXT_STAMP)
+    assert refused()
