@@ -193,16 +193,17 @@ _BF16, _E4M3, _F32, _F64, _I32 = (torch.bfloat16, torch.float8_e4m3fn, torch.flo
 
 def _load_dense():
     global _DENSE
+    how = "(python -c 'import __graft_entry__ as g; g.build()')"
     built = _build.extension_built_for()
     if built is not None and built != _build.extension_target():
-        raise RuntimeError(f"the extension module _tensors was built for another PyTorch or Python "
-                           f"({built or 'unknown'}): build it again (python -c 'import __graft_entry__ as g; "
-                           f"g.build()')")
+        raise RuntimeError("the extension module _tensors was built for another PyTorch or Python "
+                           f"({built or 'unknown'}): build it again {how}")
     try:
         from . import _tensors
     except ImportError as e:
-        raise RuntimeError("the extension module _tensors is missing: build it first "
-                           "(python -c 'import __graft_entry__ as g; g.build()')") from e
+        why = "is missing: build it first" if built is None else \
+            f"cannot be loaded ({e}): build it again"
+        raise RuntimeError(f"the extension module _tensors {why} {how}") from e
     _DENSE = _tensors.dense
     return _DENSE
 

@@ -55,3 +55,26 @@ def test_a_module_of_another_pytorch_is_not_loaded(compiler, monkeypatch):
         assert refused()
     os.remove(_build.EXT_STAMP)
     assert refused()
+
+
+def test_a_module_that_does_not_load_says_why(compiler, monkeypatch):
+    import sys
+    import torch
+    package = hd.__name__
+    monkeypatch.setattr(E, "_DENSE", None)
+    monkeypatch.delattr(sys.modules[package], "_tensors", raising=False)
+
+    class Broken:  # finds the module, and cannot load it
+        @staticmethod
+        def find_spec(name, path=None, target=None):
+            if name == package + "._tensors":
+                raise ImportError("undefined symbol: some_symbol")
+
+    monkeypatch.delitem(sys.modules, package + "._tensors", raising=False)
+    monkeypatch.setattr(sys, "meta_path", [Broken] + sys.meta_path)
+    call = (torch.zeros(1, dtype=torch.int32), 1, 1, 1, 1, None)
+    with pytest.raises(RuntimeError, match="is missing"):
+        hd.hpc_decode_plan_win(*call)
+    _build.build_extension()
+    with pytest.raises(RuntimeError, match="undefined symbol: some_symbol"):
+        hd.hpc_decode_plan_win(*call)
