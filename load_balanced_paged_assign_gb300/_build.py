@@ -3,7 +3,8 @@ _tensors.so (g++, against the installed PyTorch) in the package directory.
 
 The library's translation units are compiled in parallel and linked with the
 CUDA runtime statically, so it needs nothing at run time beyond the NVIDIA
-driver.  Each is rebuilt only when a source or header is newer.
+driver.  Each is rebuilt only when a source or header is newer, the module also
+for another PyTorch or Python.
 """
 
 from __future__ import annotations
@@ -14,6 +15,7 @@ import shutil
 import subprocess
 import sysconfig
 import tempfile
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -94,7 +96,10 @@ def build_extension(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, defines=(), out: str | None = None) -> str:
-    """Compile the library (to `out`, default the package's libhpcdecode.so).
+    """Compile the library (to `out`, default the package's libhpcdecode.so) and, beside the
+    package's own, the binding's extension module.  That needs g++ and PyTorch's headers, which
+    a caller of the C ABI need not have: where it cannot be made the library is, with a
+    warning (build_extension() raises, and so do the calls that need the module).
 
     `defines` are extra -D settings, e.g. the pipeline shape of the attention
     kernels (HPC_BF16_STAGES, HPC_BF16_TPS, HPC_FP8_STAGES, HPC_FP8_TPS)."""
@@ -105,7 +110,10 @@ def build(force: bool = False, verbose: bool = False, defines=(), out: str | Non
         if force or not own or is_stale():
             _build_library(target, verbose, defines)
         if extension:
-            extension.result()
+            try:
+                extension.result()
+            except (RuntimeError, OSError, ImportError) as e:
+                warnings.warn(f"the binding's extension module _tensors was not built: {e}")
     return target
 
 

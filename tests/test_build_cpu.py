@@ -78,3 +78,21 @@ def test_a_module_that_does_not_load_says_why(compiler, monkeypatch):
     _build.build_extension()
     with pytest.raises(RuntimeError, match="undefined symbol: some_symbol"):
         hd.hpc_decode_plan_win(*call)
+
+
+@pytest.mark.parametrize("without", ["compiler", "headers"])
+def test_the_library_is_built_without_the_module(compiler, monkeypatch, without):
+    """A caller of the C ABI needs nvcc only: no g++, or no PyTorch, is a warning."""
+    made = []
+    monkeypatch.setattr(_build, "is_stale", lambda: True)
+    monkeypatch.setattr(_build, "_build_library", lambda *a: made.append(a[0]))
+    if without == "compiler":
+        monkeypatch.setenv("CXX", "/nonexistent/g++")
+    else:
+        import sys
+        monkeypatch.setitem(sys.modules, "torch", None)  # import torch fails
+    with pytest.warns(UserWarning, match="_tensors was not built"):
+        assert _build.build() == _build.LIB_PATH
+    assert made == [_build.LIB_PATH] and not os.path.exists(_build.EXT_PATH)
+    with pytest.raises((RuntimeError, OSError, ImportError)):
+        _build.build_extension()
