@@ -726,7 +726,8 @@ def hpc_kv_read_block(k_cache, v_cache, kv_scale, block_table, starts, seqlens, 
 
 
 class Workspace:
-    """Split buffer, output and task map sized for one batch shape."""
+    """Split buffer, output and task map sized for one batch shape, for the plain and the
+    windowed calls over kv_dtype caches."""
 
     def __init__(self, B: int, Hq: int, Hkv: int, *, num_ctas: int = 0, num_splits: int = 0,
                  device="cuda", kv_dtype: int = HPC_KV_BF16, q_len: int = 1):
@@ -736,8 +737,9 @@ class Workspace:
         else:
             if num_ctas <= 0:
                 num_ctas = hpc_decode_num_ctas(dev.index or 0, kv_dtype)
-            # descriptors of head pairs (8-bit caches, the _win calls) need more room
-            pairs = 2 if kv_dtype != HPC_KV_BF16 else 1
+            # descriptors of head pairs (the _win calls, over 8-bit caches of an even
+            # number of heads) need more room
+            pairs = 2 if kv_dtype != HPC_KV_BF16 and Hkv % 2 == 0 else 1
             cap = hpc_decode_desc_capacity(B, Hkv, pairs * num_ctas)
             self.tmap = TaskMap(B, Hkv, cap, num_ctas + 1, dev)
         self.num_ctas, self.num_splits = num_ctas, num_splits

@@ -48,3 +48,14 @@ def test_to_host_of_a_map_of_head_pairs():
     assert len(m.to_host()["chunk_count"]) == len(m.to_host()["chunk_off"]) == 12
     m.c.persistent = 3
     assert len(m.to_host()["chunk_count"]) == len(m.to_host()["chunk_off"]) == 6
+
+
+@pytest.mark.parametrize("kv", [E.HPC_KV_BF16, E.HPC_KV_FP8_E4M3, E.HPC_KV_E4M3_BLOCK])
+@pytest.mark.parametrize("heads", [1, 2, 3, 4])
+def test_a_workspace_has_room_for_the_descriptors_its_calls_make(kv, heads):
+    """num_ctas + B Hkv of them; head pairs (8-bit caches, an even number of heads)
+    take the room of two: 2 num_ctas + B Hkv, and nothing else does."""
+    ws = hd.Workspace(5, 8 * heads, heads, num_ctas=30, kv_dtype=kv, device="cpu")
+    pairs = kv != E.HPC_KV_BF16 and heads % 2 == 0
+    assert ws.tmap.cap_desc == 30 * (2 if pairs else 1) + 5 * heads
+    assert ws.part_o.shape == (ws.tmap.cap_desc, 8, 128)
