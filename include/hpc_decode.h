@@ -457,6 +457,8 @@ hpc_status hpc_decode_step_noalloc(const void *d_q, const float *d_q_scale, cons
  *   V is not normalised or rotated;
  *   FP8 query: scale = amax / 448 over the head row (1 for an all-zero
  *     row), codes = E4M3 round-to-nearest-even of y / scale (saturating);
+ *     a row whose amax before the norm's factor is below 1.3166e-36 takes
+ *     that as its amax;
  *   FP8 K and V: E4M3 of y / k_scale and v / v_scale (saturating).
  * The arithmetic is fp32.  The rotation angle pos * freq is formed as an
  * exact fp32 product plus its rounding error against an fp64 frequency and

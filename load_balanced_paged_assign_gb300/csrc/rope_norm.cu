@@ -55,6 +55,10 @@ constexpr float kTwoPiHi = 6.2831854820251465f;     // fp32(2 pi)
 constexpr float kTwoPiLo = -1.7484555314695172e-7f;  // 2 pi - fp32(2 pi)
 constexpr float kInvTwoPi = 0.159154937f;
 constexpr float kInvPi = 0.318309873f;
+// The least maximum of an FP8 query row before the norm's factor: 448 over a smaller
+// one is infinite (and a zero beside it NaN).  A test for such rows that scales them
+// up first took 3 to 5% of a prompt's time; this costs 0.4 of 61.6 us.
+constexpr float kLeastMax = 1.3166e-36f;
 
 enum RowKind { kQ = 0, kK = 1, kV = 2 };
 
@@ -198,9 +202,10 @@ __device__ __forceinline__ void rows_batch(const RopeNormArgs &a, const char *st
                             amax[i] = fmaxf(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], o));
 #pragma unroll
                     for (int i = 0; i < NP; ++i) {
-                        const float ymax = amax[i] * inv[i];
-                        const bool live = ymax > 0.f;
-                        const float mul = live ? __fdividef(448.0f, amax[i]) : 0.f;
+                        const bool live = amax[i] * inv[i] > 0.f;
+                        const float top = fmaxf(amax[i], kLeastMax);
+                        const float ymax = top * inv[i];
+                        const float mul = live ? __fdividef(448.0f, top) : 0.f;
                         scale8(x[i], mul);
                         if (valid[i]) {
                             const size_t qrow = (size_t)t * a.Hq + row[i];
