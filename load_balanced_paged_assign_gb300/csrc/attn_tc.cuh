@@ -87,11 +87,13 @@ constexpr int kTcGroup = 128;           // threads of a softmax or join warpgrou
 constexpr float kTcTop = 3.f;           // log2 of the largest weight when the reference moves
 constexpr float kTcMax = 14.5f;         // log2 of the largest weight ever (E5M2 holds 1.75 2^15)
 // A V scale below 2^-100 counts as zero.  In the reference none counts as less
-// than 2^-88: the softmax's sum, in units of up to 2^(14.5 + 88), must hold all
-// tokens of a request (2^25), and a weight at the reference's top (2^3) then
-// still stands 2^10 above the three parts' last step at a scale of 2^-100.
+// than 2^-88: the softmax's sum, of terms of up to 2^(14.5 + 88), must hold all
+// tokens of a request (below 2^30; it is kept times 2^-8, and so stays below 2^125),
+// and a weight at the reference's top (2^3) then still stands 2^10 above the three
+// parts' last step at a scale of 2^-100.
 constexpr float kMinVScale = 7.888609052210118e-31f;  // 2^-100
 constexpr float kMinVRef = 3.2311742677852644e-27f;   // 2^-88
+constexpr float kSumLog2 = -8.f, kSumUnit = 1.f / 256;  // of the sum: what its terms are times
 constexpr int kTcOrds = 4;              // descriptors whose join data may be alive at once
 constexpr int kTcPubs = 8 + 2;          // arrivals that publish one: the groups' warps, two products
 
@@ -833,8 +835,8 @@ __device__ __forceinline__ bool tc_softmax(const AttnParams &p, uint8_t *smem, u
 #pragma unroll
         for (int i = 0; i < RB / 2; ++i) {
             const float a = ex2(d[2 * i] - m[2 * i]), b = ex2(d[2 * i + 1] - m[2 * i + 1]);
-            l[2 * i] += a;
-            l[2 * i + 1] += b;
+            l[2 * i] = fmaf(a, kSumUnit, l[2 * i]);
+            l[2 * i + 1] = fmaf(b, kSumUnit, l[2 * i + 1]);
             const uint32_t w = BLK ? pack_f16x2(a * vf, b * vf) : pack_f16x2(a, b);
             h0[i] = e5m2x2_of_f16x2(w);
             const uint32_t r1 = rest8(w, f16x2_of_e5m2x2(h0[i]));
@@ -923,15 +925,16 @@ __device__ __forceinline__ bool tc_join(const AttnParams &p, uint8_t *smem, uint
                 z[k] = j.only == (k ^ 1) ? 0.f
                        : HEADS == 2      ? sk[0] + sk[16]
                                          : (sk[0] + sk[16]) + (sk[32] + sk[48]);
-                ls[k] = z[k] > 0.f ? refs[(slot * 2 + k) * 32 + tid] + lg2(z[k]) : kNegInf;
+                ls[k] = z[k] > 0.f ? refs[(slot * 2 + k) * 32 + tid] + (lg2(z[k]) - kSumLog2)
+                                   : kNegInf;
             }
             const float M = fmaxf(ls[0], ls[1]);
             const float e0 = z[0] > 0.f ? ex2(ls[0] - M) : 0.f;
             const float e1 = z[1] > 0.f ? ex2(ls[1] - M) : 0.f;
             const float Z = e0 + e1;
-            // out = sum_k O_k / z_k * e_k / Z
-            fac[tid] = z[0] > 0.f ? p.v_scale * e0 / (z[0] * Z) : 0.f;
-            fac[32 + tid] = z[1] > 0.f ? p.v_scale * e1 / (z[1] * Z) : 0.f;
+            // out = sum_k O_k / z_k * e_k / Z (z in units of 1 / kSumUnit)
+            fac[tid] = z[0] > 0.f ? p.v_scale * e0 / (z[0] * Z) * kSumUnit : 0.f;
+            fac[32 + tid] = z[1] > 0.f ? p.v_scale * e1 / (z[1] * Z) * kSumUnit : 0.f;
             fac[64 + tid] = Z > 0.f ? (M + lg2(Z)) * kLn2 : kNegInf;  // natural-log LSE
         }
         named_bar_sync(bid, kTcGroup);
