@@ -87,3 +87,84 @@ def test_a_map_of_head_pairs_on_the_host(kv):
     for name in ("total_tiles", "budget", "num_desc", "desc", "bin_ptr", "chunk_count",
                  "chunk_off"):
         assert got[name] == getattr(ref, name), name
+
+
+def test_write_read_and_decode_captured_on_another_stream():
+    """The cache written, read back and attended over, captured together on a stream of
+    its own and replayed with other rows: what the calls one by one leave."""
+    from _blocks import E4M3, Prologue
+    tokens = [(r, p) for r, n in enumerate((70, 16, 33)) for p in range(n)]
+    pro = Prologue(tokens, 8, 2, B=3, max_pages=2, seed=94)
+    other = Prologue(tokens, 8, 2, B=3, max_pages=2, seed=95)
+    lens = torch.tensor([70, 16, 33], dtype=torch.int32, device="cuda")
+    table = torch.from_numpy(pro.table).cuda()
+    ws = hd.Workspace(3, 8, 2, kv_dtype=hd.HPC_KV_E4M3_BLOCK)
+    last = torch.tensor([69, 85, 118], device="cuda")  # the requests' last tokens
+    pos, req = torch.from_numpy(pro.pos).cuda(), torch.from_numpy(pro.req).cuda()
+    wq, wk = pro.wq.cuda(), pro.wk.cuda()
+
+    def buffers():
+        k, v = (torch.from_numpy(c.copy()).cuda().view(E4M3) for c in pro.codes0)
+        b = dict(qkv=pro.full.cuda(), k=k, v=v, s=torch.from_numpy(pro.scale0.copy()).cuda(),
+                 q=torch.zeros((pro.N, 8, 128), device="cuda").to(E4M3),
+                 qs=torch.zeros((pro.N, 8), device="cuda"),
+                 out=torch.zeros((3, 1, 8, 128), dtype=torch.bfloat16, device="cuda"))
+        b["ko"] = torch.zeros((pro.P, 64, 2, 128), dtype=torch.bfloat16, device="cuda")
+        b["vo"] = torch.zeros_like(b["ko"])
+        b["q1"], b["qs1"] = b["q"][:3].clone(), b["qs"][:3].clone()
+        return b
+
+    def run(b, stream=None):
+        hd.hpc_rope_norm_block(b["qkv"], wq, wk, pos, req, 8, 2, table, b["k"], b["v"], b["s"],
+                               b["q"], b["qs"], stream=stream)
+        hd.hpc_kv_read_block(b["k"], b["v"], b["s"], table, None, lens, 2, b["ko"], b["vo"], table,
+                             stream=stream)
+        b["q1"].view(torch.uint8).copy_(b["q"].view(torch.uint8)[last])
+        b["qs1"].copy_(b["qs"][last])
+        hd.hpc_decode_step_win(b["q1"], b["qs1"], b["k"], b["v"], 1.0, 1.0, b["s"], table, lens, 8,
+                               2, 1, 40, 4, 128 ** -0.5, ws.num_ctas, 2, ws.tmap, ws.part_o,
+                               ws.part_lse, b["out"], unit_done=ws.unit_done, stream=stream)
+
+    def same(a, b):
+        torch.cuda.synchronize()
+        for name in a:
+            assert torch.equal(a[name].view(torch.uint8), b[name].view(torch.uint8)), name
+
+    eager, replayed, named = buffers(), buffers(), buffers()
+    run(eager)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(named, stream=side)
+    same(eager, named)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        run(replayed)
+    graph.replay()
+    same(eager, replayed)
+    for b in (eager, replayed):
+        b["qkv"].copy_(other.full)
+    run(eager)
+    graph.replay()
+    same(eager, replayed)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3", "block"])
+def test_no_requests(kv):
+    """An empty batch: nothing is written, and the workspace serves the next step."""
+    c = Case(kv, [200, 64], 8, 2, 1, 100, 4, seed=96, poison=False).to_gpu()
+    ws = c.workspace()
+    out = torch.full((2, 1, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    none = [None if t is None else t[:0] for t in (c.q, c.qs, c.bt, c.sl)]
+    for done in (ws.unit_done, None):
+        hd.hpc_decode_step_win(none[0], none[1], c.k, c.v, c.ks, c.vs, c.scale, none[2], none[3],
+                               8, 2, 1, 100, 4, c.sm, ws.num_ctas, 2, ws.tmap, ws.part_o,
+                               ws.part_lse, out, unit_done=done)
+    torch.cuda.synchronize()
+    assert (out == 7.0).all() and ws.tmap.to_host()["num_desc"] == 0
+    got, _ = c.step(ws=ws)
+    c.check(got)
+    if kv == "bf16":
+        hd.hpc_prefill_attn_win(none[0], c.k, c.v, none[2], none[3], 8, 2, 1, 100, 4, c.sm, out)
+        torch.cuda.synchronize()
+        assert (out == 7.0).all()
