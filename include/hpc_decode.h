@@ -663,7 +663,8 @@ hpc_status hpc_decode_plan_win(const int32_t *d_seqlens, int32_t B, int32_t Hkv,
  *               that hold a visible token are finite, V's not negative and at
  *               most 2^100 (one below 2^-100 counts as zero); the others may
  *               be anything.
- * Other arguments as in those calls.
+ * With a window or block scales sm_scale * log2(e) * k_scale (k_scale where it
+ * counts) is finite (HPC_ERR_ARG).  Other arguments as in those calls.
  */
 hpc_status hpc_decode_attn_win(const void *d_q, const float *d_q_scale, const void *d_k_cache,
                                const void *d_v_cache, int32_t num_pages, float k_scale,
@@ -693,8 +694,8 @@ hpc_status hpc_decode_step_win(const void *d_q, const float *d_q_scale, const vo
 /*
  * hpc_prefill_attn with a window: the request's last q_len live tokens are
  * the queries, over a paged BF16 cache.  window = 0 is hpc_prefill_attn.
- * With a window sm_scale is finite and at least FLT_MIN, and q_len is below
- * 2^30.  Other arguments as there.
+ * With a window sm_scale is at least FLT_MIN and finite times log2(e), and
+ * q_len is below 2^30.  Other arguments as there.
  */
 hpc_status hpc_prefill_attn_win(const void *d_q, const void *d_k_cache, const void *d_v_cache,
                                 int32_t num_pages, const int32_t *d_block_table,

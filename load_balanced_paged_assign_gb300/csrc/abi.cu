@@ -235,6 +235,9 @@ hpc_status launch_attention(const void *d_q, const float *d_q_scale, const void 
         return HPC_ERR_ARG;
     const bool win = form.window > 0;
     const int heads = heads_per_desc(kv_dtype, form.window, Hkv);
+    // what the scores are multiplied by (an infinite one would make a zero score NaN)
+    const float score_scale = sm_scale * kLog2eF * (fp8 ? k_scale : 1.f);
+    if ((win || block) && !std::isfinite(score_scale)) return HPC_ERR_ARG;
     if (!planned_for(*map, q_len, form, heads)) return HPC_ERR_ARG;
 
     CUtensorMap tk, tv;
@@ -269,7 +272,7 @@ hpc_status launch_attention(const void *d_q, const float *d_q_scale, const void 
     p.num_pages = num_pages;
     p.q_len = q_len;
     p.R = q_len * p.G;
-    p.score_scale = sm_scale * kLog2eF * (fp8 ? k_scale : 1.f);
+    p.score_scale = score_scale;
     p.v_scale = fp8 ? v_scale : 1.f;
     p.window = win ? form.window : kNoWindow;
     p.sinks = win ? form.sinks : 0;

@@ -649,8 +649,9 @@ extern "C" hpc_status hpc_prefill_attn_win(const void *d_q, const void *d_k_cach
         return HPC_ERR_ARG;
     if (head_dim != HPC_HEAD_DIM || Hq % Hkv != 0) return HPC_ERR_UNSUPPORTED;
     // scores are masked before they are scaled: the scale may not turn -inf
-    // round, nor be flushed to zero
-    if (!std::isfinite(sm_scale) || !(sm_scale >= FLT_MIN)) return HPC_ERR_ARG;
+    // round, nor be flushed to zero, nor make a zero score NaN
+    const float score_scale = sm_scale * 1.4426950408889634f;  // times log2(e)
+    if (!std::isfinite(score_scale) || !(sm_scale >= FLT_MIN)) return HPC_ERR_ARG;
     if (B == 0) return HPC_OK;
     if (!d_q || !d_k_cache || !d_v_cache || !d_block_table || !d_seqlens || !d_out)
         return HPC_ERR_ARG;
@@ -686,7 +687,7 @@ extern "C" hpc_status hpc_prefill_attn_win(const void *d_q, const void *d_k_cach
     a.n_qp = (int)n_qp;
     a.window = window;
     a.sinks = sinks;
-    a.score_scale = sm_scale * 1.4426950408889634f;
+    a.score_scale = score_scale;
 
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return HPC_ERR_CUDA;

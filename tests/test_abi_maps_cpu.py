@@ -59,3 +59,16 @@ def test_a_workspace_has_room_for_the_descriptors_its_calls_make(kv, heads):
     pairs = kv != E.HPC_KV_BF16 and heads % 2 == 0
     assert ws.tmap.cap_desc == 30 * (2 if pairs else 1) + 5 * heads
     assert ws.part_o.shape == (ws.tmap.cap_desc, 8, 128)
+
+
+def test_scales_that_are_infinite_once_multiplied():
+    """sm_scale * log2(e) (* k_scale) past fp32's range: scores of zero would be NaN."""
+    m = dict(m=window_map())
+    assert attn(window=200, sinks=4, sm=3e38, **m) == E.HPC_ERR_ARG
+    assert attn(dtype=2, kvs=FAKE, qs=FAKE, sm=3e38) == E.HPC_ERR_ARG
+
+    def prompt(sm):
+        return hd.lib().hpc_prefill_attn_win(FAKE, FAKE, FAKE, 100, FAKE, 8, FAKE, 0, 8, 2, 128,
+                                             300, 128, 4, sm, FAKE, None, None)
+
+    assert prompt(3e38) == E.HPC_ERR_ARG and prompt(2e38) == E.HPC_OK
