@@ -717,7 +717,9 @@ hpc_status hpc_prefill_attn_win(const void *d_q, const void *d_k_cache, const vo
  * whose positions share position / 16.  They have to be neighbours in the
  * call's token list (as a request's consecutive tokens are); tokens of one
  * block in several places of the list leave that block's contents
- * unspecified.  Where a run holds a position twice, the later token stays.
+ * unspecified.  Where a run holds a position twice, the later token stays.  Of
+ * a run of more than 16 tokens the first 16 are written, and
+ * HPC_FLAG_BAD_SEQLEN is raised.
  * For each head, and for K and V apart:
  *   a  = the largest finite |y| over the run's rows,
  *   s* = the smallest power of two >= 2^-126 with a <= 448 s*,
@@ -729,7 +731,11 @@ hpc_status hpc_prefill_attn_win(const void *d_q, const void *d_k_cache, const vo
  *   codes = E4M3(y / s), round to nearest even, saturating (an infinite y
  *   becomes +-448, NaN stays NaN).
  * With powers of two the quotients are exact and a growing scale re-rounds
- * only codes that leave E4M3's normal range.
+ * only codes that leave E4M3's normal range.  The scales so left reach from
+ * 2^-126 to 2^120, further than those hpc_decode_attn_win takes of V: a V
+ * block whose largest value is at most 448 * 2^-101 counts as zero there (and
+ * is read back as it is by hpc_kv_read_block), and V values above 448 * 2^100
+ * (5.7e32) are not for it.
  *   d_kv_scale     device fp32 [num_pages, Hkv, 2, 4], read and written
  *   d_q_out        BF16 [num_tokens, Hq, 128] (d_q_scale_out NULL: what
  *                  hpc_prefill_attn_win takes) or E4M3 with d_q_scale_out

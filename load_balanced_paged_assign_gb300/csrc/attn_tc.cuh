@@ -53,6 +53,9 @@
 // from the launch to the first stage's landing (lengths, block table, tiles, one
 // after the other) and 6 to 8 us from the last landing to the end (softmax and
 // product 2, join 2, the merges of units split between CTAs 1.5 to 2.5).
+// With 16 rows per KV head (draft tokens, or a group above 8) the 128 registers that
+// 512 threads leave are not enough for the softmax warps: 60 bytes are spilled with
+// head pairs and 112 with single heads.  With 8 rows nothing is.
 // Every wait is bounded.  Named barriers are reached by all four warps of a
 // group: a wait that failed is voted on there, and the group leaves together.
 #pragma once

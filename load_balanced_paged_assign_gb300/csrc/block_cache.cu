@@ -475,8 +475,9 @@ __device__ __forceinline__ void widen16(uint4 q, float f, uint4 *dst) {
 // once per CTA), so a batch of very different lengths, or one request alone,
 // loads the SMs evenly.  A block's tokens are contiguous for all heads: a
 // thread takes 16 codes (16 bytes in, 32 out) of K and the same of V at a
-// time, two of each in flight.  8192 tokens of 8 heads (50 MB): 9 to 10 us, a
-// launch and 74 to 83% of the measured copy rate; HBM bounds it.
+// time, two of each in flight.  8192 tokens of 8 heads (17 MB in, 34 MB out): 9 to
+// 10 us, a launch and the loads' latency (long scoreboard 10 a warp instruction; DRAM
+// at 19% of its peak, as the output still sits in L2 when it ends).
 __global__ void __launch_bounds__(kRdThreads) kv_read_block_kernel(const BlockReadArgs a) {
     extern __shared__ int s_end[];  // [B] blocks of the requests up to and with r
     __shared__ int s_scan[kRdThreads / 32];

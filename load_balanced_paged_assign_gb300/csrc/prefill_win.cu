@@ -5,15 +5,21 @@
 // Two 128-row Q tiles share every KV page: S = Q_x K^T into TMEM, one softmax
 // thread per row (online, in fp32: a reference that moves when a score passes it
 // by 2^8, P written over the scores as BF16, half a step of 2^-8), O_x += P V with
-// P read from TMEM.  What bounds it is the tensor pipe: at N = 64 the scores' MMAs
-// are limited by their operands' reads from shared memory (A 32 KB + B 16 KB at 128
-// bytes a cycle, 384 cycles; O's take 256), 1280 cycles a page for both Q tiles
-// where a page takes 1400.
+// P read from TMEM.  Within an item the tensor pipe bounds it: at N = 64 the scores'
+// MMAs are limited by their operands' reads from shared memory (A 32 KB + B 16 KB at
+// 128 bytes a cycle, 384 cycles; O's take 256), 1250 cycles a page for both Q tiles,
+// timed alone in alternation, where a page takes 1430 (softmax 1075, its wait for the
+// scores 355).  Of the launch that is 78%: an item of 8192 queries with a window of
+// 1024 takes 31.9k cycles, 24.7k of them for its 17.3 pages, 0.7k until its first
+// scores, 3.0k from its last to its output (0.9k of it the last product) and 3.5k for
+// its bookkeeping and its share of the launch's start.  So the pipe multiplies in 57%
+// of the launch's cycles (1024 of 1430 would be 72%).
 //   * The unit is a page, not two.  A Q tile has two 64-column score buffers in
 //     TMEM, and its scores run two pages ahead of its products, so that the
-//     softmax of a page meets the next one's scores ready (with one buffer of 128
-//     it waited for 2100 to 2600 of a tile's 5300 cycles).  Only pages that some
-//     row sees are computed, and 64 scores leave registers for the masks.
+//     softmax of a page meets the next one's scores ready (with one buffer of 128,
+//     and one issuing warp for both Q tiles, it waited for 2100 to 2600 of a tile's
+//     5300 cycles).  Only pages that some row sees are computed, and 64 scores leave
+//     registers for the masks.
 //   * Each Q tile has its own MMA warp: an issuing warp stands still while its
 //     MMAs wait for the pipe, and one for both tiles left the pipe idle for half
 //     of a page.  What these warps compute per page is held to a few uniform
@@ -24,8 +30,8 @@
 //   * The CTAs are persistent, one per SM: the next item's Q and pages come in
 //     while this one's last scores are taken, and its first scores are computed
 //     while the output goes out, by TMA through shared memory.  (Reading O out by
-//     warps of their own costs the softmax its registers: 231 and 246 us against
-//     231; stores of 32 bytes a lane instead of TMA: 238.)
+//     warps of their own gains nothing, 231 us against 231 with the softmax at 128
+//     registers and 246 with more; stores of 32 bytes a lane instead of TMA: 238.)
 //   * Tokens that no query of the pair sees (past L_r, or before the window and no
 //     sink) may hold anything: a warp of its own zeroes their V rows once the page
 //     has landed (0 * NaN would reach O) and passes every page on.
