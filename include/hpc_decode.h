@@ -78,6 +78,7 @@ typedef enum { HPC_KV_BF16 = 0, HPC_KV_FP8_E4M3 = 1, HPC_KV_E4M3_BLOCK = 2 } hpc
 #define HPC_FLAG_DESC_OVERFLOW 2u /* the plan needed more than cap_desc descriptors */
 #define HPC_FLAG_BAD_PAGE 4u     /* a block-table entry outside [0, num_pages); page 0 read instead */
 #define HPC_FLAG_TIMEOUT 8u      /* a pipeline wait hit its time limit; output invalid */
+#define HPC_FLAG_NO_PAGES 16u    /* a pool has fewer free pages than a call asked for; none taken */
 
 #define HPC_HEAD_DIM 128
 #define HPC_PAGE_SIZE 64
@@ -777,6 +778,105 @@ hpc_status hpc_kv_read_block(const void *d_k_cache, const void *d_v_cache,
                              int32_t Hkv, int32_t head_dim, void *d_k_out, void *d_v_out,
                              int32_t out_num_pages, const int32_t *d_out_block_table,
                              int32_t out_max_pages_per_req, int32_t *d_flags,
+                             hpc_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The pages of a cache as a pool: rows of a block table take pages, share the
+ * pages of a common beginning, give them back and are brought together, on the
+ * device and in stream order, so that a captured step may do it.
+ *
+ * A row holds its pages at entries 0 .. n - 1 and -1 behind them.
+ * The pool's arrays are the caller's (device memory):
+ *   refs       [num_pages] how many entries of the table name each page
+ *   free_list  [num_pages] a stack of the pages that none names:
+ *              free_list[state[0] - 1] is the next one to be handed out
+ *   state      [4] {pages on the stack, HPC_FLAG_* bits (OR-ed), 0, 0}
+ *   marks      [num_pages] scratch of the calls, INT32_MAX in every element
+ *              before the first call and after each
+ * An empty pool has refs 0, free_list num_pages - 1 .. 0 and state {num_pages,
+ * 0, 0, 0}.  Calls on one pool run one after the other (one stream, or ordered by
+ * events).  B, n <= HPC_MAX_BATCH; n * max_pages_per_req and 64 *
+ * max_pages_per_req are below 2^30.  Results do not depend on timing: pages are
+ * handed out and given back in the order of the call's list and, within a row, of
+ * the entries.  Rows outside [0, B) and lengths outside [0, 64 *
+ * max_pages_per_req] raise HPC_FLAG_BAD_SEQLEN and are passed over; pages outside
+ * [0, num_pages) and pages that no entry holds raise HPC_FLAG_BAD_PAGE.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+    int32_t *refs;
+    int32_t *free_list;
+    int32_t *state;
+    int32_t *marks;
+    int32_t num_pages;
+} hpc_page_pool;
+
+/*
+ * Rows d_rows[i] (NULL: row i), i < n, give back the pages behind their first
+ * d_keep[i] tokens (NULL: all): their entries from ceil(keep / 64) on become -1,
+ * and a page that no entry names any more goes on the stack.  Of the pages given
+ * back by a call the first one listed comes to lie on top (a fork or an extension
+ * of the same rows gets the same pages).  A row that is named twice gives its
+ * pages back once (with two different d_keep, those behind the smaller); which
+ * of its places counts for the order is left open.
+ */
+hpc_status hpc_kv_free(const hpc_page_pool *pool, int32_t *d_block_table, int32_t B,
+                       int32_t max_pages_per_req, const int32_t *d_rows, const int32_t *d_keep,
+                       int32_t n, hpc_stream_t stream);
+
+/*
+ * Rows d_rows[i] (NULL: row i), i < n, get pages for d_lens[i] tokens: each of
+ * their entries below ceil(d_lens[i] / 64) that names no page (-1) takes one from the
+ * stack.  With fewer on the stack than all of them need, none is taken and
+ * HPC_FLAG_NO_PAGES is raised.  A row that is named twice is served once.
+ */
+hpc_status hpc_kv_extend(const hpc_page_pool *pool, int32_t *d_block_table, int32_t B,
+                         int32_t max_pages_per_req, const int32_t *d_rows, const int32_t *d_lens,
+                         int32_t n, hpc_stream_t stream);
+
+/*
+ * Row d_dst[i] becomes a fork of the first d_lens[i] tokens of row d_src[i], i <
+ * n: it shares the pages that these tokens fill and gets a page of its own for
+ * the rest of them, which d_copies says to copy from (hpc_kv_copy_pages, for the
+ * caches of every layer).  What is appended to either row is then not seen by the
+ * other.  The rows d_dst[i] are empty before the call (their entries below
+ * ceil(d_lens[i] / 64) are -1) and no row d_src[k]; a child whose row is not,
+ * or whose source has not the pages, raises a flag and is left out, as is all but
+ * the first of children of one row.  With fewer pages on the stack than the
+ * children need, nothing changes and HPC_FLAG_NO_PAGES is raised.
+ *   d_copies    int32 [1 + cap_copies][2]: {count, 0}, then {from, to} in the
+ *               order of the children; cap_copies >= n (HPC_ERR_WORKSPACE)
+ */
+hpc_status hpc_kv_fork(const hpc_page_pool *pool, int32_t *d_block_table, int32_t B,
+                       int32_t max_pages_per_req, const int32_t *d_src, const int32_t *d_dst,
+                       const int32_t *d_lens, int32_t n, int32_t *d_copies, int32_t cap_copies,
+                       hpc_stream_t stream);
+
+/*
+ * Brings the L pages that are held into places 0 .. L - 1: those behind move, in
+ * order, into the holes.  Writes the table and the pool as they are afterwards
+ * (the stack holds the pages L .. num_pages - 1, L on top) and the moves to
+ * d_copies as hpc_kv_fork does (cap_copies >= num_pages / 2); the caches of every
+ * layer follow by hpc_kv_copy_pages before anything reads them through the new
+ * table.  All entries of the table's B rows are rewritten; other tables on the
+ * pool keep their old places.  d_block_table_out and pool_out may be d_block_table
+ * and pool (all of its arrays) or memory of their own; the marks used are pool's.
+ */
+hpc_status hpc_kv_compact(const hpc_page_pool *pool, const int32_t *d_block_table, int32_t B,
+                          int32_t max_pages_per_req, int32_t *d_copies, int32_t cap_copies,
+                          int32_t *d_block_table_out, const hpc_page_pool *pool_out,
+                          hpc_stream_t stream);
+
+/*
+ * Copies the pages that d_copies lists ({count, 0}, then {from, to}) within one
+ * layer's caches: K, V and, for HPC_KV_E4M3_BLOCK, the scales d_kv_scale (else
+ * NULL).  No page is copied to that another copy reads or writes.  At most
+ * cap_copies are made.  A pair outside [0, num_pages) raises HPC_FLAG_BAD_PAGE in
+ * d_flags (device int32 or NULL) and is passed over.  Caches are 32-byte aligned,
+ * scales 16-byte.
+ */
+hpc_status hpc_kv_copy_pages(const int32_t *d_copies, int32_t cap_copies, void *d_k_cache,
+                             void *d_v_cache, float *d_kv_scale, hpc_kv_dtype kv_dtype,
+                             int32_t num_pages, int32_t Hkv, int32_t head_dim, int32_t *d_flags,
                              hpc_stream_t stream);
 
 /*

@@ -18,6 +18,7 @@ from . import _build
 HPC_OK, HPC_ERR_ARG, HPC_ERR_UNSUPPORTED, HPC_ERR_WORKSPACE, HPC_ERR_CUDA = 0, -1, -2, -3, -4
 HPC_KV_BF16, HPC_KV_FP8_E4M3, HPC_KV_E4M3_BLOCK = 0, 1, 2
 HPC_FLAG_BAD_SEQLEN, HPC_FLAG_DESC_OVERFLOW, HPC_FLAG_BAD_PAGE, HPC_FLAG_TIMEOUT = 1, 2, 4, 8
+HPC_FLAG_NO_PAGES = 16
 HEAD_DIM, PAGE_SIZE, MAX_GROUP, MAX_QUERY_ROWS = 128, 64, 16, 16
 SCALE_BLOCK = 16
 HPC_ROPE_HALVES, HPC_ROPE_INTERLEAVED = 0, 1
@@ -34,6 +35,7 @@ EXPORTS = (
     "hpc_decode_packed_layout", "hpc_decode_step_host_packed",
     "hpc_decode_plan_win", "hpc_decode_attn_win", "hpc_decode_step_win", "hpc_prefill_attn_win",
     "hpc_rope_norm_block", "hpc_kv_read_block",
+    "hpc_kv_free", "hpc_kv_extend", "hpc_kv_fork", "hpc_kv_compact", "hpc_kv_copy_pages",
 )
 
 
@@ -62,6 +64,12 @@ class hpc_rope_norm_params(ctypes.Structure):
                 ("freq", ctypes.c_void_p)]
 
 
+class hpc_page_pool(ctypes.Structure):
+    _fields_ = [("refs", ctypes.c_void_p), ("free_list", ctypes.c_void_p),
+                ("state", ctypes.c_void_p), ("marks", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32)]
+
+
 _LIB = None
 
 
@@ -82,7 +90,7 @@ def lib():
                            "(python -c 'import __graft_entry__ as g; g.build()')")
     L = ctypes.CDLL(path)
     vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
-    tm = ctypes.POINTER(hpc_task_map)
+    tm, pool = ctypes.POINTER(hpc_task_map), ctypes.POINTER(hpc_page_pool)
     sig = {
         "hpc_decode_version": (ctypes.c_char_p, []),
         "hpc_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -148,6 +156,12 @@ def lib():
                                                ctypes.POINTER(hpc_rope_norm_params), vp]),
         "hpc_kv_read_block": (ctypes.c_int, [vp, vp, vp, i32, vp, i32, vp, vp, i32, i32, i32, vp,
                                              vp, i32, vp, i32, vp, vp]),
+        "hpc_kv_free": (ctypes.c_int, [pool, vp, i32, i32, vp, vp, i32, vp]),
+        "hpc_kv_extend": (ctypes.c_int, [pool, vp, i32, i32, vp, vp, i32, vp]),
+        "hpc_kv_fork": (ctypes.c_int, [pool, vp, i32, i32, vp, vp, vp, i32, vp, i32, vp]),
+        "hpc_kv_compact": (ctypes.c_int, [pool, vp, i32, i32, vp, i32, vp, pool, vp]),
+        "hpc_kv_copy_pages": (ctypes.c_int, [vp, i32, vp, vp, vp, ctypes.c_int, i32, i32, i32, vp,
+                                             vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -723,6 +737,151 @@ def hpc_kv_read_block(k_cache, v_cache, kv_scale, block_table, starts, seqlens, 
         shape[8][1], fl_, _raw_stream(dev, stream))
     if status != HPC_OK:
         _check(fn, status)
+
+
+class PagePool:
+    """The pages of a cache: how many table entries name each (refs), a stack of those that
+    none names (free_list) and the state {pages on the stack, flags, 0, 0}."""
+
+    def __init__(self, num_pages: int, device="cuda"):
+        dev = torch.device(device)
+        self._of(torch.zeros(num_pages, dtype=torch.int32, device=dev),
+                 torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=dev),
+                 torch.tensor([num_pages, 0, 0, 0], dtype=torch.int32, device=dev))
+
+    @classmethod
+    def of(cls, refs, free_list, state):
+        """A pool on arrays that say which pages are held already."""
+        self = cls.__new__(cls)
+        self._of(refs, free_list, state)
+        return self
+
+    def _of(self, refs, free_list, state):
+        self.num_pages = int(refs.numel())
+        if any(t.dtype is not _I32 or not t.is_contiguous() or t.device != refs.device
+               for t in (refs, free_list, state)) or free_list.numel() != self.num_pages or \
+                state.numel() != 4:
+            raise ValueError("PagePool: refs, free_list [num_pages] and state [4] are int32 "
+                             "arrays of one device")
+        self.refs, self.free_list, self.state = refs, free_list, state
+        self.marks = torch.full_like(refs, 2 ** 31 - 1)
+        self.c = hpc_page_pool(_ptr(refs), _ptr(free_list), _ptr(state), _ptr(self.marks),
+                               self.num_pages)
+
+    @property
+    def free_pages(self) -> int:
+        """Pages on the stack (synchronises)."""
+        return int(self.state[0])
+
+    @property
+    def flags(self) -> int:
+        """HPC_FLAG_* bits raised so far (synchronises)."""
+        return int(self.state[1])
+
+
+def _pool_args(fn, dev, pool, names, *tensors):
+    """The checks of the pool's calls: (addresses, shapes, element counts) of int32 arrays."""
+    if not isinstance(pool, PagePool) or pool.refs.get_device() != dev:
+        raise ValueError(f"{fn}: no PagePool on the current device")
+    got = _arrays(fn, dev, names, (_I32,) * len(tensors), *tensors)
+    if len(got[1][0]) != 2:
+        raise ValueError(f"{fn}: block_table is no matrix")
+    return got
+
+
+def _listed(fn, n, **counts):
+    for name, c in counts.items():
+        if c is not None and c != n:
+            raise ValueError(f"{fn}: {name} has not {n} entries")
+
+
+def hpc_kv_free(pool: PagePool, block_table, rows=None, keep=None, stream=None):
+    """The rows (None: all) give back the pages behind their first keep[i] tokens (None: all)."""
+    fn, dev = "hpc_kv_free", _current_device()
+    (bt_, rows_, keep_), shape, count = _pool_args(fn, dev, pool, "block_table rows keep",
+                                                   block_table, rows, keep)
+    B, cols = shape[0]
+    n = B if rows is None else count[1]
+    _listed(fn, n, keep=count[2])
+    _check(fn, lib().hpc_kv_free(ctypes.byref(pool.c), bt_, B, cols, rows_, keep_, n,
+                                 _raw_stream(dev, stream)))
+
+
+def hpc_kv_extend(pool: PagePool, block_table, rows, lens, stream=None):
+    """The rows (None: all) get the pages that lens[i] tokens need and they have not."""
+    fn, dev = "hpc_kv_extend", _current_device()
+    (bt_, rows_, lens_), shape, count = _pool_args(fn, dev, pool, "block_table rows lens",
+                                                   block_table, rows, lens)
+    B, cols = shape[0]
+    n = B if rows is None else count[1]
+    _listed(fn, n, lens=count[2] or 0)
+    _check(fn, lib().hpc_kv_extend(ctypes.byref(pool.c), bt_, B, cols, rows_, lens_, n,
+                                   _raw_stream(dev, stream)))
+
+
+def hpc_kv_fork(pool: PagePool, block_table, src, dst, lens, copies, stream=None):
+    """Row dst[i] becomes a fork of the first lens[i] tokens of row src[i]; copies [1 + cap, 2]
+    gets the pages to copy ({count, 0}, then {from, to})."""
+    fn, dev = "hpc_kv_fork", _current_device()
+    (bt_, src_, dst_, lens_, cp_), shape, count = _pool_args(
+        fn, dev, pool, "block_table src dst lens copies", block_table, src, dst, lens, copies)
+    if any(t is None for t in (src, dst, lens, copies)):
+        raise ValueError(f"{fn}: src, dst, lens and copies are needed")
+    B, cols = shape[0]
+    n = count[1]
+    _listed(fn, n, dst=count[2], lens=count[3])
+    _check(fn, lib().hpc_kv_fork(ctypes.byref(pool.c), bt_, B, cols, src_, dst_, lens_, n, cp_,
+                                 _cap(fn, shape[4]), _raw_stream(dev, stream)))
+
+
+def _cap(fn, shape):
+    if len(shape) != 2 or shape[0] < 1 or shape[1] != 2:
+        raise ValueError(f"{fn}: copies is {shape}, not [1 + capacity, 2]")
+    return shape[0] - 1
+
+
+def hpc_kv_compact(pool: PagePool, block_table, copies, out_table=None, out_pool=None,
+                   stream=None):
+    """The pages that are held move into the first places; copies [1 + cap, 2] gets the moves.
+    out_table, out_pool: where the table and the pool are written (None: in place)."""
+    fn, dev = "hpc_kv_compact", _current_device()
+    if out_table is None:
+        out_table = block_table
+    out_pool = pool if out_pool is None else out_pool
+    (bt_, cp_, ot_), shape, _ = _pool_args(fn, dev, pool, "block_table copies out_table",
+                                           block_table, copies, out_table)
+    if copies is None or not isinstance(out_pool, PagePool) or \
+            out_pool.refs.get_device() != dev:
+        raise ValueError(f"{fn}: copies, or no PagePool on the current device")
+    _shape(fn, "out_table", shape[2], shape[0])
+    _check(fn, lib().hpc_kv_compact(ctypes.byref(pool.c), bt_, shape[0][0], shape[0][1], cp_,
+                                    _cap(fn, shape[1]), ot_, ctypes.byref(out_pool.c),
+                                    _raw_stream(dev, stream)))
+
+
+_PAGE_TYPES = [(_I32, t, t, _F32, _I32) for t in (_BF16, _E4M3)]
+
+
+def hpc_kv_copy_pages(copies, k_cache, v_cache, kv_scale=None, flags=None, stream=None):
+    """The copies that hpc_kv_fork or hpc_kv_compact listed, in one layer's caches (and the
+    block scales [num_pages, Hkv, 2, 4] of a block-scaled one)."""
+    fn, dev = "hpc_kv_copy_pages", _current_device()
+    (cp_, k_, v_, sc_, fl_), shape, _ = _arrays(
+        fn, dev, "copies k_cache v_cache kv_scale flags",
+        _PAGE_TYPES[k_cache.dtype is _E4M3], copies, k_cache, v_cache, kv_scale, flags)
+    if copies is None or len(shape[1]) != 4:
+        raise ValueError(f"{fn}: copies, or a cache [num_pages, 64, Hkv, 128]")
+    pages, _, Hkv, _ = shape[1]
+    want = (pages, PAGE_SIZE, Hkv, HEAD_DIM)
+    _shape(fn, "k_cache", shape[1], want)
+    _shape(fn, "v_cache", shape[2], want)
+    if kv_scale is not None:
+        if k_cache.dtype is not _E4M3:
+            raise ValueError(f"{fn}: kv_scale belongs to E4M3 pages")
+        _shape(fn, "kv_scale", shape[3], (pages, Hkv, 2, PAGE_SIZE // SCALE_BLOCK))
+    kv = HPC_KV_E4M3_BLOCK if kv_scale is not None else kv_dtype_of(k_cache)
+    _check(fn, lib().hpc_kv_copy_pages(cp_, _cap(fn, shape[0]), k_, v_, sc_, kv, pages, Hkv,
+                                       HEAD_DIM, fl_, _raw_stream(dev, stream)))
 
 
 class Workspace:
