@@ -781,6 +781,98 @@ hpc_status hpc_kv_read_block(const void *d_k_cache, const void *d_v_cache,
                              hpc_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Decode attention over shared prefixes.  A batch's requests form groups of
+ * neighbours: group g is requests d_group_starts[g] .. d_group_starts[g + 1] - 1
+ * (the starts do not fall; requests outside all groups are ordinary ones), and the
+ * first d_prefix_pages[g] block-table entries of its requests name the same pages
+ * (those of hpc_kv_fork's children do).  The attention over these pages is computed
+ * for all of the group's queries at once, each page being read once for up to 256
+ * query rows of a KV head instead of once per request.
+ *
+ * The result is that of hpc_decode_step_mq (hpc_decode_step_win without a window)
+ * on the same batch: prefixes only say what may be computed together.  A request of
+ * a group whose queries do not all see all of the shared pages (L_r - q_len + 1 <
+ * 64 * d_prefix_pages[g], an empty one among them) is computed by itself, as are
+ * the requests of a group in which fewer than two others are left; the group's
+ * pages are then looked up in the row of its first request that shares them, so
+ * the rows of those that do not may hold other pages.
+ * ---------------------------------------------------------------------- */
+#define HPC_MAX_SHARED_BATCH 8192
+#define HPC_MAX_SHARED_GROUPS 4096
+
+/*
+ * The plan of such a step: a task map for the tails (what each request has behind
+ * its group's pages), which only the calls below take, and buffers for the heads
+ * (the shared pages).  All of it is caller-owned device memory.
+ *   tail       cap_desc, cap_bins >= num_ctas + 1, cap_units >= B * Hkv; its meta
+ *              is the step's ({tail tiles, budget, descriptors, flags})
+ *   head       [cap_head] int32, 16-byte aligned
+ *   head_o     [cap_slots, 128, 128] fp32, 32-byte aligned; head_lse [cap_slots,
+ *              128] fp32: the heads' partials
+ * cap_desc, cap_head and cap_slots as hpc_decode_shared_capacity says.  Hq,
+ * num_groups and kv_dtype are written by the planner.
+ */
+typedef struct {
+    hpc_task_map tail;
+    int32_t *head;
+    float *head_o;
+    float *head_lse;
+    int64_t cap_head, cap_slots;
+    int32_t Hq, num_groups, kv_dtype;
+} hpc_shared_map;
+
+/* sizes[3] = {cap_desc, cap_head, cap_slots} that always suffice. */
+hpc_status hpc_decode_shared_capacity(int32_t B, int32_t Hq, int32_t Hkv, int32_t q_len,
+                                      int32_t num_groups, int32_t num_ctas, int64_t sizes[3]);
+
+/*
+ * Plans a step, once for all layers: who shares, the CTAs for heads and tails, and
+ * the descriptors of both.
+ *   d_group_starts  device int32 [num_groups + 1], not falling, in [0, B]; otherwise
+ *                   HPC_FLAG_BAD_SEQLEN is raised and nothing is shared
+ *   d_prefix_pages  device int32 [num_groups], in [0, max_pages_per_req] (else
+ *                   flagged, and nothing is shared in that group)
+ *   num_ctas        2 .. 65536 (hpc_decode_num_ctas)
+ * B <= HPC_MAX_SHARED_BATCH, num_groups <= HPC_MAX_SHARED_GROUPS, B *
+ * max_pages_per_req * Hkv < 2^28.  Other arguments as in hpc_decode_plan_win.
+ */
+hpc_status hpc_decode_plan_shared(const int32_t *d_seqlens, int32_t B, int32_t Hq, int32_t Hkv,
+                                  int32_t max_pages_per_req, const int32_t *d_group_starts,
+                                  const int32_t *d_prefix_pages, int32_t num_groups,
+                                  int32_t num_ctas, int32_t min_tiles_per_cta,
+                                  hpc_kv_dtype kv_dtype, int32_t q_len, hpc_shared_map *map,
+                                  hpc_stream_t stream);
+
+/*
+ * The attention and the join of its partials (two launches) on a planned map; the
+ * lengths and table are those of the plan.  Arguments and layouts as in
+ * hpc_decode_attn_win without a window; d_out is always written, zeros for queries
+ * that see no token.  sm_scale * log2(e) * k_scale is finite.
+ *   d_part_o   [map->tail.cap_desc, q_len * G, 128] fp32, d_part_lse
+ *              [map->tail.cap_desc, q_len * G] fp32: the tails' partials
+ */
+hpc_status hpc_decode_attn_shared(const void *d_q, const float *d_q_scale, const void *d_k_cache,
+                                  const void *d_v_cache, int32_t num_pages, float k_scale,
+                                  float v_scale, const float *d_kv_scale, hpc_kv_dtype kv_dtype,
+                                  const int32_t *d_block_table, int32_t max_pages_per_req,
+                                  const int32_t *d_seqlens, int32_t B, int32_t Hq, int32_t Hkv,
+                                  int32_t head_dim, int32_t q_len, float sm_scale,
+                                  const hpc_shared_map *map, float *d_part_o, float *d_part_lse,
+                                  void *d_out, hpc_stream_t stream);
+
+/* Both, for a single layer. */
+hpc_status hpc_decode_step_shared(const void *d_q, const float *d_q_scale, const void *d_k_cache,
+                                  const void *d_v_cache, int32_t num_pages, float k_scale,
+                                  float v_scale, const float *d_kv_scale, hpc_kv_dtype kv_dtype,
+                                  const int32_t *d_block_table, int32_t max_pages_per_req,
+                                  const int32_t *d_seqlens, const int32_t *d_group_starts,
+                                  const int32_t *d_prefix_pages, int32_t num_groups, int32_t B,
+                                  int32_t Hq, int32_t Hkv, int32_t head_dim, int32_t q_len,
+                                  float sm_scale, int32_t num_ctas, int32_t min_tiles_per_cta,
+                                  hpc_shared_map *map, float *d_part_o, float *d_part_lse,
+                                  void *d_out, hpc_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * The pages of a cache as a pool: rows of a block table take pages, share the
  * pages of a common beginning, give them back and are brought together, on the
  * device and in stream order, so that a captured step may do it.

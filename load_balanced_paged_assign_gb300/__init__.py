@@ -13,7 +13,9 @@ holds the build step, the ctypes binding and the seeded workload generators.
 """
 
 from .binding import (EXPORTS, HPC_KV_BF16, HPC_KV_E4M3_BLOCK, HPC_KV_FP8_E4M3, HPC_ROPE_HALVES,
-                      HPC_ROPE_INTERLEAVED, HpcError, PagePool, TaskMap, Workspace, hpc_decode_attn,
+                      HPC_ROPE_INTERLEAVED, HpcError, PagePool, SharedWorkspace, TaskMap, Workspace,
+                      hpc_decode_attn, hpc_decode_attn_shared, hpc_decode_plan_shared,
+                      hpc_decode_step_shared,
                       hpc_decode_attn_combine, hpc_decode_attn_combine_mq, hpc_decode_attn_mq,
                       hpc_decode_attn_win,
                       hpc_decode_combine, hpc_decode_combine_mq, hpc_decode_desc_capacity,
@@ -31,7 +33,7 @@ from .binding import (EXPORTS, HPC_KV_BF16, HPC_KV_E4M3_BLOCK, HPC_KV_FP8_E4M3, 
 
 __all__ = [
     "EXPORTS", "HPC_KV_BF16", "HPC_KV_E4M3_BLOCK", "HPC_KV_FP8_E4M3", "HPC_ROPE_HALVES", "HPC_ROPE_INTERLEAVED",
-    "HpcError", "PagePool", "TaskMap", "Workspace", "hpc_decode_attn", "hpc_decode_attn_combine",
+    "HpcError", "PagePool", "SharedWorkspace", "TaskMap", "Workspace", "hpc_decode_attn", "hpc_decode_attn_combine",
     "hpc_decode_attn_combine_mq", "hpc_decode_attn_mq", "hpc_decode_combine",
     "hpc_decode_combine_mq", "hpc_decode_desc_capacity", "hpc_decode_num_ctas",
     "hpc_decode_plan", "hpc_decode_plan_static", "hpc_decode_read_meta",
@@ -42,5 +44,6 @@ __all__ = [
     "hpc_decode_version", "hpc_prefill_attn", "hpc_rope_frequencies", "hpc_rope_norm", "hpc_router_gemm",
     "hpc_router_plan", "hpc_router_split", "hpc_router_workspace_bytes", "hpc_selftest_wait_timeout",
     "hpc_kv_compact", "hpc_kv_copy_pages", "hpc_kv_extend", "hpc_kv_fork", "hpc_kv_free",
+    "hpc_decode_attn_shared", "hpc_decode_plan_shared", "hpc_decode_step_shared",
     "kv_dtype_of", "lib",
 ]

@@ -36,6 +36,8 @@ EXPORTS = (
     "hpc_decode_plan_win", "hpc_decode_attn_win", "hpc_decode_step_win", "hpc_prefill_attn_win",
     "hpc_rope_norm_block", "hpc_kv_read_block",
     "hpc_kv_free", "hpc_kv_extend", "hpc_kv_fork", "hpc_kv_compact", "hpc_kv_copy_pages",
+    "hpc_decode_shared_capacity", "hpc_decode_plan_shared", "hpc_decode_attn_shared",
+    "hpc_decode_step_shared",
 )
 
 
@@ -70,6 +72,13 @@ class hpc_page_pool(ctypes.Structure):
                 ("num_pages", ctypes.c_int32)]
 
 
+class hpc_shared_map(ctypes.Structure):
+    _fields_ = [("tail", hpc_task_map), ("head", ctypes.c_void_p), ("head_o", ctypes.c_void_p),
+                ("head_lse", ctypes.c_void_p), ("cap_head", ctypes.c_int64),
+                ("cap_slots", ctypes.c_int64), ("Hq", ctypes.c_int32),
+                ("num_groups", ctypes.c_int32), ("kv_dtype", ctypes.c_int32)]
+
+
 _LIB = None
 
 
@@ -91,6 +100,7 @@ def lib():
     L = ctypes.CDLL(path)
     vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
     tm, pool = ctypes.POINTER(hpc_task_map), ctypes.POINTER(hpc_page_pool)
+    sm = ctypes.POINTER(hpc_shared_map)
     sig = {
         "hpc_decode_version": (ctypes.c_char_p, []),
         "hpc_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -156,6 +166,16 @@ def lib():
                                                ctypes.POINTER(hpc_rope_norm_params), vp]),
         "hpc_kv_read_block": (ctypes.c_int, [vp, vp, vp, i32, vp, i32, vp, vp, i32, i32, i32, vp,
                                              vp, i32, vp, i32, vp, vp]),
+        "hpc_decode_shared_capacity": (ctypes.c_int, [i32, i32, i32, i32, i32, i32,
+                                                      ctypes.POINTER(i64)]),
+        "hpc_decode_plan_shared": (ctypes.c_int, [vp, i32, i32, i32, i32, vp, vp, i32, i32, i32,
+                                                  ctypes.c_int, i32, sm, vp]),
+        "hpc_decode_attn_shared": (ctypes.c_int, [vp, vp, vp, vp, i32, f32, f32, vp, ctypes.c_int,
+                                                  vp, i32, vp, i32, i32, i32, i32, i32, f32, sm,
+                                                  vp, vp, vp, vp]),
+        "hpc_decode_step_shared": (ctypes.c_int, [vp, vp, vp, vp, i32, f32, f32, vp, ctypes.c_int,
+                                                  vp, i32, vp, vp, vp, i32, i32, i32, i32, i32,
+                                                  i32, f32, i32, i32, sm, vp, vp, vp, vp]),
         "hpc_kv_free": (ctypes.c_int, [pool, vp, i32, i32, vp, vp, i32, vp]),
         "hpc_kv_extend": (ctypes.c_int, [pool, vp, i32, i32, vp, vp, i32, vp]),
         "hpc_kv_fork": (ctypes.c_int, [pool, vp, i32, i32, vp, vp, vp, i32, vp, i32, vp]),
@@ -735,6 +755,115 @@ def hpc_kv_read_block(k_cache, v_cache, kv_scale, block_table, starts, seqlens, 
     status = lib().hpc_kv_read_block(
         k_, v_, sc_, pages, bt_, shape[3][1], st_, sl_, B, Hkv, HEAD_DIM, ko_, vo_, out_pages, ot_,
         shape[8][1], fl_, _raw_stream(dev, stream))
+    if status != HPC_OK:
+        _check(fn, status)
+
+
+class SharedWorkspace:
+    """The plan and the split buffers of decode steps over shared prefixes, for batches of up
+    to num_groups groups of one shape."""
+
+    def __init__(self, B: int, Hq: int, Hkv: int, num_groups: int, *, num_ctas: int = 0,
+                 device="cuda", kv_dtype: int = HPC_KV_BF16, q_len: int = 1):
+        dev = torch.device(device)
+        if num_ctas <= 0:
+            num_ctas = hpc_decode_num_ctas(dev.index or 0, kv_dtype)
+        sizes = (ctypes.c_int64 * 3)()
+        _check("hpc_decode_shared_capacity", lib().hpc_decode_shared_capacity(
+            int(B), int(Hq), int(Hkv), int(q_len), int(num_groups), num_ctas, sizes))
+        cap, ints, slots = (int(n) for n in sizes)
+        self.B, self.Hq, self.Hkv, self.q_len = int(B), int(Hq), int(Hkv), int(q_len)
+        self.num_groups, self.num_ctas, self.kv_dtype = int(num_groups), num_ctas, int(kv_dtype)
+        self.device = dev
+        self.tmap = TaskMap(B, Hkv, cap, num_ctas + 1, dev)
+        self.head = torch.zeros(ints, dtype=torch.int32, device=dev)
+        rows = q_len * (Hq // Hkv)
+        f32 = dict(dtype=torch.float32, device=dev)
+        self.part_o = torch.empty((cap, rows, HEAD_DIM), **f32)
+        self.part_lse = torch.empty((cap, rows), **f32)
+        self.head_o = torch.empty((slots, 128, HEAD_DIM), **f32)
+        self.head_lse = torch.empty((slots, 128), **f32)
+        self.c = hpc_shared_map(self.tmap.c, _ptr(self.head), _ptr(self.head_o),
+                                _ptr(self.head_lse), ints, slots)
+        self.tmap.c = self.c.tail  # the planner writes to this one
+
+    @property
+    def flags(self) -> int:
+        """HPC_FLAG_* bits of the last step (synchronises)."""
+        return int(self.tmap.meta[3])
+
+    def head_ctas(self) -> int:
+        """CTAs that the last plan gave to the shared pages (synchronises)."""
+        return int(self.head[0])
+
+
+def _groups_arg(fn, starts, groups_shape, ws):
+    """The number of groups, checked against the workspace."""
+    n = starts[0] - 1 if starts else 0
+    if len(starts) != 1 or n < 0 or groups_shape != (n,):
+        raise ValueError(f"{fn}: group_starts is no list of one more than prefix_pages")
+    if n > ws.num_groups:
+        raise ValueError(f"{fn}: {n} groups, but the workspace has room for {ws.num_groups}")
+    return n
+
+
+def hpc_decode_plan_shared(seqlens, group_starts, prefix_pages, Hq, Hkv, q_len, max_pages_per_req,
+                           min_tiles_per_cta, ws: SharedWorkspace, stream=None):
+    """Plans decode steps of a batch whose groups share their first pages: group g is requests
+    group_starts[g] .. group_starts[g + 1] - 1, its pages the first prefix_pages[g]."""
+    fn, dev = "hpc_decode_plan_shared", _current_device()
+    (sl_, gs_, pp_), shape, count = _arrays(fn, dev, "seqlens group_starts prefix_pages",
+                                            (_I32, _I32, _I32), seqlens, group_starts,
+                                            prefix_pages)
+    n = _groups_arg(fn, shape[1], shape[2], ws)
+    _on(fn, ws, dev)
+    _check(fn, lib().hpc_decode_plan_shared(
+        sl_, count[0], int(Hq), int(Hkv), int(max_pages_per_req), gs_, pp_, n, ws.num_ctas,
+        int(min_tiles_per_cta), ws.kv_dtype, int(q_len), ctypes.byref(ws.c),
+        _raw_stream(dev, stream)))
+
+
+def _on(fn, ws, dev):
+    if not isinstance(ws, SharedWorkspace) or ws.head.get_device() != dev:
+        raise ValueError(f"{fn}: no SharedWorkspace on the current device")
+
+
+def hpc_decode_attn_shared(q, q_scale, k_cache, v_cache, k_scale, v_scale, kv_scale, block_table,
+                           seqlens, Hq, Hkv, q_len, sm_scale, ws: SharedWorkspace, out,
+                           stream=None):
+    """Attention of a batch that hpc_decode_plan_shared planned, as hpc_decode_step_mq
+    computes it.  kv_scale: the block scales of a block-scaled cache, else None."""
+    fn = "hpc_decode_attn_shared"
+    Hq, Hkv, q_len = int(Hq), int(Hkv), int(q_len)
+    kv, dev, B, pages, cols, (q_, k_, v_, qs_, sc_, bt_, sl_, po_, pl_, _, out_) = _win_args(
+        fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, Hq, Hkv, q_len,
+        ws.part_o, ws.part_lse, out, None, ws.tmap.cap_desc)
+    _on(fn, ws, dev)
+    status = lib().hpc_decode_attn_shared(
+        q_, qs_, k_, v_, pages, float(k_scale), float(v_scale), sc_, kv, bt_, cols, sl_, B, Hq,
+        Hkv, HEAD_DIM, q_len, float(sm_scale), ctypes.byref(ws.c), po_, pl_, out_,
+        _raw_stream(dev, stream))
+    if status != HPC_OK:
+        _check(fn, status)
+
+
+def hpc_decode_step_shared(q, q_scale, k_cache, v_cache, k_scale, v_scale, kv_scale, block_table,
+                           seqlens, group_starts, prefix_pages, Hq, Hkv, q_len, sm_scale,
+                           min_tiles_per_cta, ws: SharedWorkspace, out, stream=None):
+    """hpc_decode_plan_shared and hpc_decode_attn_shared in one call."""
+    fn = "hpc_decode_step_shared"
+    Hq, Hkv, q_len = int(Hq), int(Hkv), int(q_len)
+    kv, dev, B, pages, cols, (q_, k_, v_, qs_, sc_, bt_, sl_, po_, pl_, _, out_) = _win_args(
+        fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, Hq, Hkv, q_len,
+        ws.part_o, ws.part_lse, out, None, ws.tmap.cap_desc)
+    _on(fn, ws, dev)
+    (gs_, pp_), shape, _ = _arrays(fn, dev, "group_starts prefix_pages", (_I32, _I32),
+                                   group_starts, prefix_pages)
+    n = _groups_arg(fn, shape[0], shape[1], ws)
+    status = lib().hpc_decode_step_shared(
+        q_, qs_, k_, v_, pages, float(k_scale), float(v_scale), sc_, kv, bt_, cols, sl_, gs_, pp_,
+        n, B, Hq, Hkv, HEAD_DIM, q_len, float(sm_scale), ws.num_ctas, int(min_tiles_per_cta),
+        ctypes.byref(ws.c), po_, pl_, out_, _raw_stream(dev, stream))
     if status != HPC_OK:
         _check(fn, status)
 

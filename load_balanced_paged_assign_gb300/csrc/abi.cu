@@ -350,6 +350,7 @@ hpc_status combine_impl(const float *d_part_o, const float *d_part_lse, const hp
     if (st != HPC_OK) return st;
     if (map->B != B || map->Hkv != Hkv || (int64_t)B * Hkv > map->cap_units) return HPC_ERR_ARG;
     if (map->window > 0 && map->q_len != q_len) return HPC_ERR_ARG;
+    if (map->persistent & 4) return HPC_ERR_ARG;  // the tails of shared prefixes
     // descriptors of head pairs: half as many units with twice the rows
     const int heads = 1 + ((map->persistent >> 1) & 1);
     return cuda_status(launch_combine(d_part_o, d_part_lse, *map, B, Hq, Hkv / heads, q_len, d_out,
@@ -418,6 +419,10 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return encoder(); }
 hpc_status cache_tensor_map(CUtensorMap *m, const void *base, int32_t num_pages, int32_t Hkv,
                             bool fp8) {
     return make_cache_map(m, base, num_pages, Hkv, fp8);
+}
+hpc_status heads_tensor_map(CUtensorMap *m, const void *base, int32_t num_pages, int32_t Hkv,
+                            int heads) {
+    return make_heads_map(m, base, num_pages, Hkv, heads);
 }
 }  // namespace hpc
 

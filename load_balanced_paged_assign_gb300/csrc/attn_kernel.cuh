@@ -1285,10 +1285,11 @@ __device__ __forceinline__ bool attn_consumer(const AttnParams &p, uint8_t *smem
 }
 
 // ------------------------------------------------------------------ kernel
+// What a CTA of the grid does (threads past the kernel's own, in a grid of larger
+// CTAs, only set up with the others).
 template <bool FP8, int STAGES, int TPS, int NB, bool WIN = false>
-__global__ void __launch_bounds__(AttnTraits<FP8, STAGES, TPS, NB, WIN>::kThreads, 1)
-    attn_kernel(const __grid_constant__ CUtensorMap tmap_k,
-                const __grid_constant__ CUtensorMap tmap_v, const AttnParams p) {
+__device__ __forceinline__ void attn_cta(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
+                                         const AttnParams &p) {
     using Tr = AttnTraits<FP8, STAGES, TPS, NB, WIN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -1330,6 +1331,7 @@ __global__ void __launch_bounds__(AttnTraits<FP8, STAGES, TPS, NB, WIN>::kThread
     // waits for the assign kernel right before it first needs the map.
     grid_launch_dependents();
     __syncthreads();
+    if (threadIdx.x >= Tr::kThreads) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) {
         attn_producer<FP8, STAGES, TPS, NB, WIN>(&tmap_k, &tmap_v, p, smem, abort);
@@ -1395,6 +1397,13 @@ __global__ void __launch_bounds__(AttnTraits<FP8, STAGES, TPS, NB, WIN>::kThread
         for (int item = w; item < items; item += nw)
             merge_unit_head<NB == 1 ? 16 : 8>(p, last[1 + item / p.R].di, item % p.R);
     }
+}
+
+template <bool FP8, int STAGES, int TPS, int NB, bool WIN = false>
+__global__ void __launch_bounds__(AttnTraits<FP8, STAGES, TPS, NB, WIN>::kThreads, 1)
+    attn_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                const __grid_constant__ CUtensorMap tmap_v, const AttnParams p) {
+    attn_cta<FP8, STAGES, TPS, NB, WIN>(tmap_k, tmap_v, p);
 }
 
 // Launches one instantiation as a programmatic dependent of the previous

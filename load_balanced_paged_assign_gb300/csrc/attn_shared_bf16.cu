@@ -1,0 +1,30 @@
+// Decode attention over shared prefixes, BF16 pages.
+#include "attn_shared.cuh"
+
+namespace hpc {
+namespace {
+
+// (the plain form's pipeline: one tile per stage, four stages)
+template <int NB>
+struct Tail {
+    using Tr = AttnTraits<false, 4, 1, NB>;
+    static constexpr int kThreads = Tr::kThreads, kSmemBytes = Tr::kSmemBytes;
+    static __device__ __forceinline__ void run(const CUtensorMap &tk, const CUtensorMap &tv,
+                                               const AttnParams &t) {
+        attn_cta<false, 4, 1, NB>(tk, tv, t);
+    }
+};
+
+using One = SharedVariant<HPC_KV_BF16, Tail<1>>;  // up to 8 query rows per KV head and request
+using Two = SharedVariant<HPC_KV_BF16, Tail<2>>;  // up to 16
+
+}  // namespace
+
+AttnConfig shared_config_bf16(int nb) { return nb == 2 ? Two::config() : One::config(); }
+
+cudaError_t launch_shared_bf16(int nb, const SharedMaps &m, const AttnParams &t, const HeadArgs &h,
+                               int grid, cudaStream_t s) {
+    return nb == 2 ? Two::launch(m, t, h, grid, s) : One::launch(m, t, h, grid, s);
+}
+
+}  // namespace hpc

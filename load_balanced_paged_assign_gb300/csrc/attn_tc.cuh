@@ -1030,9 +1030,8 @@ __device__ __forceinline__ bool tc_join(const AttnParams &p, uint8_t *smem, uint
 
 // ------------------------------------------------------------------ kernel
 template <int RB, int HEADS, bool BLK>
-__global__ void __launch_bounds__(kTcThreads, 1)
-    attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
-                   const __grid_constant__ CUtensorMap tmap_v, const AttnParams p) {
+__device__ __forceinline__ void attn_tc_cta(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
+                                            const AttnParams &p) {
     using Tr = TcTraits<RB, HEADS, BLK>;
     constexpr int STAGES = Tr::STAGES;
     extern __shared__ uint8_t smem_raw[];
@@ -1151,6 +1150,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int k = 0; k < 2 && item + k < items; ++k) merge_unit_head<8>(p, dd[k], rr[k]);
         }
     }
+}
+
+template <int RB, int HEADS, bool BLK>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    attn_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                   const __grid_constant__ CUtensorMap tmap_v, const AttnParams p) {
+    attn_tc_cta<RB, HEADS, BLK>(tmap_k, tmap_v, p);
 }
 
 template <int RB, int HEADS, bool BLK>

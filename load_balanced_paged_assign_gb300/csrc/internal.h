@@ -120,6 +120,10 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 hpc_status cache_tensor_map(CUtensorMap *m, const void *base, int32_t num_pages, int32_t Hkv,
                             bool fp8);
 
+// Tensor map over one 8-bit cache that brings `heads` neighbouring heads of a page at once.
+hpc_status heads_tensor_map(CUtensorMap *m, const void *base, int32_t num_pages, int32_t Hkv,
+                            int heads);
+
 cudaError_t launch_combine(const float *part_o, const float *part_lse, const hpc_task_map &map,
                            int B, int Hq, int Hkv, int q_len, void *out, cudaStream_t s);
 

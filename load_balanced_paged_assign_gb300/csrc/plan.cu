@@ -12,40 +12,12 @@
 // units' chunk counts places the descriptors, and each bin's CSR offset is
 // found by locating the unit that owns the bin's first tile.
 
+#include "block_scan.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
 namespace hpc {
 namespace {
-
-constexpr unsigned kFull = 0xffffffffu;
-
-// Inclusive block-wide prefix sum over blockDim.x (a multiple of 32) values;
-// also returns the block total.  Uses `scratch` (32 ints) and synchronises.
-__device__ int block_inclusive_scan(int v, int *scratch, int &total) {
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        int y = __shfl_up_sync(kFull, v, o);
-        if (lane >= o) v += y;
-    }
-    if (lane == 31) scratch[wid] = v;
-    __syncthreads();
-    if (wid == 0) {
-        int w = lane < nwarps ? scratch[lane] : 0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            int y = __shfl_up_sync(kFull, w, o);
-            if (lane >= o) w += y;
-        }
-        scratch[lane] = w;
-    }
-    __syncthreads();
-    if (wid > 0) v += scratch[wid - 1];
-    total = scratch[nwarps - 1];
-    __syncthreads();
-    return v;
-}
 
 __device__ __forceinline__ int tiles_of(int L) { return (L + kTile - 1) / kTile; }
 
