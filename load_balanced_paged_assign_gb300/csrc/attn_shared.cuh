@@ -7,12 +7,14 @@
 // and the softmax; the tail by HBM.  So the plan gives each CTAs of its own, and both
 // run at the same time.
 //
-// A head's CTA holds two row tiles of 128 queries (or one, the last of an odd number).
-// S = Q_x K^T of a page into TMEM, one softmax thread per row (online in fp32, with a
-// reference that moves when a score passes it by 2^8; P in 16 bits over the scores),
-// O_x += P V with P read from TMEM; two score buffers for each tile, an issuing warp
-// for each, and scores two pages ahead of the products.  Every row sees every token
-// of every page here, so there are no masks.
+// A head's CTA has two halves, each with its softmax warps, its issuing warp and its
+// accumulator: S = Q_x K^T of a page into TMEM, one softmax thread per row (online in
+// fp32, with a reference that moves when a score passes it by 2^8; P in 16 bits over the
+// scores), O_x += P V with P read from TMEM; two score buffers for each half, and its
+// scores two of its pages ahead of the products.  Every row sees every token of every
+// page here, so there are no masks.  The halves take a row tile of 128 queries each, and
+// every page; where a row tile is alone (the last of an odd number) they take every
+// other page of it, and leave a partial each.
 //
 // 8-bit pages: scores on E4M3 MMAs from the codes as they land; V is widened by warps
 // of its own into a second ring, to f16 where one scale holds for the cache (weights as
@@ -48,23 +50,26 @@ struct HeadTraits {
     static constexpr int kQBytes = kHeadRows * kRow;       // of a row tile
     static constexpr int kPageBytes = kTile * kRow;        // of K or V
     static constexpr int kWideBytes = kTile * 256;
-    static constexpr int S = k8 ? 6 : 5;                   // pages of K and V in the ring
-    static constexpr int W = k8 ? 4 : 0;                   // widened pages of V
+    // Pages in the first ring (K; 8-bit: and V's codes) and in the second (V as the
+    // products take it).  Even numbers: a page's place says which half takes it where
+    // they alternate.
+    static constexpr int S = k8 ? 6 : 4;
+    static constexpr int W = k8 ? 4 : 6;
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = kOffQ + 2 * kQBytes;
-    static constexpr int kOffV = kOffK + S * kPageBytes;
-    static constexpr int kOffWide = kOffV + S * kPageBytes;
-    static constexpr int kOffScale = kOffWide + W * kWideBytes;
+    static constexpr int kOffCodes = kOffK + S * kPageBytes;
+    static constexpr int kOffV = kOffCodes + (k8 ? S * kPageBytes : 0);
+    static constexpr int kOffScale = kOffV + W * kWideBytes;
     static constexpr int kOffBar = kOffScale + (kBlk ? kScaleRing * kPageScales * 4 : 0);
-    // q_full, q_free, full[S], empty[S], wide_full[W], wide_free[W], s_full[2][2],
+    // q_full, q_free, full[S], empty[S], v_full[W], v_free[W], s_full[2][2],
     // p_full[2][2], o_done[2][2], o_free[2], mma_done, end
     static constexpr int kNumBars = 2 + 2 * S + 2 * W + 12 + 2 + 2;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // TMEM address, abort word
     static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
-    // the scores' buffers hold a page's softmax back by at most two pages of its tile,
-    // so a page's scales have been read when S + 2 later ones are on their way
-    static_assert(kScaleRing >= S + 3, "block scales");
+    // a half's scores are at most two of its pages ahead of its softmax, so where the
+    // halves alternate a page's scales have been read when S + 5 later ones are on their way
+    static_assert(kScaleRing >= S + 6 && S % 2 == 0 && W % 2 == 0, "rings");
 };
 
 struct HeadItem {
@@ -79,6 +84,20 @@ __device__ __forceinline__ HeadItem head_item(const HeadPlan &p, int d) {
     return {x.x, x.y, x.z, x.w, y.x, y.y, y.z != 0, 2 * d};
 }
 
+// The pages of an item that half x takes, in the CTA's count of pages (`kt` before the
+// item): all, or every other one, by the place they have in the rings.
+struct HeadPages {
+    uint32_t at, step;
+    int n;
+};
+
+__device__ __forceinline__ HeadPages head_pages(const HeadItem &it, uint32_t kt, int x) {
+    const int n = it.hi - it.lo;
+    if (it.two) return {kt, 1, n};
+    const int skip = (int)(kt ^ (uint32_t)x) & 1;
+    return {kt + skip, 2, (n - skip + 1) >> 1};
+}
+
 __device__ __forceinline__ float head_max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -88,9 +107,6 @@ __device__ __forceinline__ float head_max3(float a, float b, float c) {
 // acc += a BF16 value, without widening it first.
 __device__ __forceinline__ void head_add_bf16(float &acc, uint16_t x) {
     asm("add.f32.bf16 %0, %1, %0;" : "+f"(acc) : "h"(x));
-}
-__device__ __forceinline__ void head_add_f16(float &acc, uint16_t x) {
-    asm("add.f32.f16 %0, %1, %0;" : "+f"(acc) : "h"(x));
 }
 
 __device__ __forceinline__ void store_f32x8(float *p, const float *v) {
@@ -122,12 +138,11 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Tr::kOffBar);
     uint64_t *q_full = bars, *q_free = bars + 1;
-    uint64_t *full = bars + 2;            // [stage]: a page has landed
-    uint64_t *empty = full + S;           // [stage]: its products are done (8-bit: its scores,
-                                          // and V is widened)
-    uint64_t *wide_full = empty + S;      // [slot]: V widened
-    uint64_t *wide_free = wide_full + W;  // [slot]: its products are done
-    uint64_t *s_full = wide_free + W;     // [x][b]: the scores of an even or odd page
+    uint64_t *full = bars + 2;         // [stage]: K of a page has landed (8-bit: and V's codes)
+    uint64_t *empty = full + S;        // [stage]: its scores are done (and V is widened)
+    uint64_t *v_full = empty + S;      // [slot]: V is there
+    uint64_t *v_free = v_full + W;     // [slot]: its products are done
+    uint64_t *s_full = v_free + W;     // [x][b]: the scores of an even or odd page of x
     uint64_t *p_full = s_full + 4;        // [x][b]: its P written (four warps)
     uint64_t *o_done = p_full + 4;        // [x][b]: O_x += P V of that page complete
     uint64_t *o_free = o_done + 4;        // [x]: O_x read out (four warps)
@@ -139,12 +154,13 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
         for (int b = 0; b < Tr::kNumBars; ++b) {
             uint64_t *bar = &bars[b];
             int n = 1;
-            // both row tiles' last scores (and all of V widened: the wide ring's phases
-            // are met in order by a tile that sat out an item)
+            // Both halves' last scores, and all of V widened.  So when the next item's Q
+            // lands, all pages of this one have, and V of each is or has been in place: a
+            // half that left a page to the other meets no phase of its barriers early.
             if (bar == q_free) n = 2 + Tr::kWideners;
             if (bar >= empty && bar < empty + S) n = 2 + Tr::kWideners;
-            if (bar >= wide_full && bar < wide_full + W) n = Tr::kWideners;
-            if (bar >= wide_free && bar < wide_free + W) n = 2;
+            if (bar >= v_full && bar < v_full + W) n = Tr::k8 ? Tr::kWideners : 1;
+            if (bar >= v_free && bar < v_free + W) n = 2;
             // (block scales: beside the scores' commit, the word of a thread that has seen
             // the page land)
             if (Tr::kBlk && bar >= s_full && bar < p_full) n = 2;
@@ -175,7 +191,7 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
         uint64_t keep;  // the pages are read by the other row tiles' CTAs too
         asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
         const uint32_t q_tile = (uint32_t)(tpb * a.G * Tr::kRow);
-        uint32_t kt = 0, items = 0;
+        uint32_t kt = 0, items = 0, v_pages = 0;
         for (int d = first; ok && d < last; ++d) {
             const HeadItem it = head_item(a.plan, d);
             if (items > 0 && !mbar_wait_warp(q_free, (items - 1) & 1u, abort)) {
@@ -200,39 +216,50 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
             const int32_t *bt = a.block_table + (size_t)it.req * a.max_pages;
             int pg = 0;
             for (int j = it.lo; j < it.hi; ++j, ++kt) {
-                const int k = (j - it.lo) & 31;
-                if (k == 0) {  // the entries of 32 pages, one per lane
+                const int e = (j - it.lo) & 31;
+                if (e == 0) {  // the entries of 32 pages, one per lane
                     pg = j + lane < it.hi ? __ldg(bt + j + lane) : 0;
                     if (pg < 0 || pg >= a.num_pages) {
                         atomicOr(a.meta + 3, (int)HPC_FLAG_BAD_PAGE);
                         pg = 0;
                     }
                 }
-                const int page = __shfl_sync(kFullMask, pg, k);
-                const int s = (int)(kt % S);
+                const int page = __shfl_sync(kFullMask, pg, e);
+                const int s = (int)(kt % S), v = (int)(kt % W);
+                // V before K: who sees K land knows that V's place was free
+                if (!Tr::k8) {
+                    ok = mbar_wait_warp(&v_free[v], ((kt / W) & 1u) ^ 1u, abort);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        if (!it.two) mbar_arrive(&v_free[v]);  // for the half that leaves it
+                        mbar_arrive_expect_tx(&v_full[v], Tr::kPageBytes);
+                        for (int hf = 0; hf < 2; ++hf)
+                            tma_load_5d(smem + Tr::kOffV + v * Tr::kPageBytes + hf * (kTile * 128),
+                                        &m.v, &v_full[v], 0, hf, it.h, 0, page, keep);
+                    }
+                    ++v_pages;
+                }
                 ok = mbar_wait_warp(&empty[s], ((kt / S) & 1u) ^ 1u, abort);
                 if (!ok) break;
                 if (lane == 0) {
-                    if (!it.two) mbar_arrive(&empty[s]);  // for the tile that there is not
-                    mbar_arrive_expect_tx(
-                        &full[s], 2 * Tr::kPageBytes + (Tr::kBlk ? kPageScales * 4 : 0));
-                    uint8_t *k8 = smem + Tr::kOffK + s * Tr::kPageBytes;
-                    uint8_t *v8 = smem + Tr::kOffV + s * Tr::kPageBytes;
+                    if (!it.two) mbar_arrive(&empty[s]);
+                    uint8_t *k = smem + Tr::kOffK + s * Tr::kPageBytes;
                     if (Tr::k8) {
-                        tma_load_4d(k8, &m.k, &full[s], 0, it.h, 0, page, keep);
-                        tma_load_4d(v8, &m.v, &full[s], 0, it.h, 0, page, keep);
+                        mbar_arrive_expect_tx(
+                            &full[s], 2 * Tr::kPageBytes + (Tr::kBlk ? kPageScales * 4 : 0));
+                        tma_load_4d(k, &m.k, &full[s], 0, it.h, 0, page, keep);
+                        tma_load_4d(smem + Tr::kOffCodes + s * Tr::kPageBytes, &m.v, &full[s], 0,
+                                    it.h, 0, page, keep);
+                        if (Tr::kBlk)
+                            bulk_load(smem + Tr::kOffScale + (kt % kScaleRing) * kPageScales * 4,
+                                      a.kv_scale + ((size_t)page * a.Hkv + it.h) * kPageScales,
+                                      kPageScales * 4, &full[s]);
                     } else {
+                        mbar_arrive_expect_tx(&full[s], Tr::kPageBytes);
                         for (int hf = 0; hf < 2; ++hf)
-                            tma_load_5d(k8 + hf * (kTile * 128), &m.k, &full[s], 0, hf, it.h, 0,
-                                        page, keep);
-                        for (int hf = 0; hf < 2; ++hf)
-                            tma_load_5d(v8 + hf * (kTile * 128), &m.v, &full[s], 0, hf, it.h, 0,
+                            tma_load_5d(k + hf * (kTile * 128), &m.k, &full[s], 0, hf, it.h, 0,
                                         page, keep);
                     }
-                    if (Tr::kBlk)
-                        bulk_load(smem + Tr::kOffScale + (kt % kScaleRing) * kPageScales * 4,
-                                  a.kv_scale + ((size_t)page * a.Hkv + it.h) * kPageScales,
-                                  kPageScales * 4, &full[s]);
                 }
             }
         }
@@ -244,20 +271,21 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
             if (items > 0) mbar_wait(q_full, (items - 1) & 1u, &no_abort);
             for (uint32_t t = kt > S ? kt - S : 0; t < kt; ++t)
                 mbar_wait(&full[t % S], (t / S) & 1u, &no_abort);
+            for (uint32_t t = v_pages > W ? v_pages - W : 0; t < v_pages; ++t)
+                mbar_wait(&v_full[t % W], (t / W) & 1u, &no_abort);
             __syncwarp();
         }
     } else if (warp == kHeadMma || warp == kHeadMma + 1) {
-        const int x = warp - kHeadMma;  // the row tile
+        const int x = warp - kHeadMma;  // the half
         constexpr uint32_t id_s = Tr::k8 ? idesc_e4m3_f32(kHeadRows, kTile, false, false)
                                          : idesc_bf16_f32(kHeadRows, kTile);
         // (E4M3: f16 weights and values, the type bits of both zero)
         constexpr uint32_t id_o = idesc_bf16_f32_bmn(kHeadRows, kHeadDim) &
                                   (KV == HPC_KV_FP8_E4M3 ? ~((1u << 7) | (1u << 10)) : ~0u);
-        const uint64_t dq = smem_desc_k128(smem_u32(smem + Tr::kOffQ + x * Tr::kQBytes));
+        const uint64_t dq0 = smem_desc_k128(smem_u32(smem + Tr::kOffQ));
         const uint64_t dk0 = smem_desc_k128(smem_u32(smem + Tr::kOffK));
-        const uint64_t dv0 = smem_desc_mn128(
-            smem_u32(smem + (Tr::k8 ? Tr::kOffWide : Tr::kOffV)), kTile * 128);
-        auto issue_s = [&](uint32_t b, uint32_t page) {
+        const uint64_t dv0 = smem_desc_mn128(smem_u32(smem + Tr::kOffV), kTile * 128);
+        auto issue_s = [&](uint32_t b, uint64_t dq, uint32_t page) {
             const uint32_t s = page % S;
             const uint64_t dk = dk0 + (uint64_t)((s * Tr::kPageBytes) >> 4);
             if (Tr::k8) {
@@ -275,41 +303,40 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
             }
             if (Tr::kBlk) mbar_arrive(&s_full[2 * x + b]);
             umma_commit(&s_full[2 * x + b]);
-            if (Tr::k8) umma_commit(&empty[s]);
+            umma_commit(&empty[s]);
         };
         auto issue_pv = [&](uint32_t b, uint32_t page, bool acc) {
-            const uint32_t s = Tr::k8 ? page % (W + !W) : page % S;
+            const uint32_t s = page % W;
             const uint64_t dv = dv0 + (uint64_t)((s * Tr::kWideBytes) >> 4);
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
                 umma_bf16_ts(tmem + kHeadOCol + 128 * x, tmem + 128 * x + 64 * b + 8 * k,
                              dv + (uint64_t)((k * 16 * 128) >> 4), id_o, acc || k > 0);
             umma_commit(&o_done[2 * x + b]);
-            umma_commit(Tr::k8 ? &wide_free[s] : &empty[s]);
+            umma_commit(&v_free[s]);
         };
         uint32_t kt = 0, items = 0;
         uint32_t sp = 0, pp = 0;  // score pages issued, P pages taken
         uint32_t outs = 0;        // items whose O_x has been claimed
         for (int d = first; ok && d < last; ++d) {
             const HeadItem it = head_item(a.plan, d);
-            const int n = it.hi - it.lo;
             ok = mbar_wait_warp(q_full, items & 1u, abort);
             ++items;
             if (!ok) break;
-            if (x == 1 && !it.two) {
+            const HeadPages pg = head_pages(it, kt, x);
+            const uint64_t dq = dq0 + (uint64_t)((it.two ? x * Tr::kQBytes : 0) >> 4);
+            if (pg.n == 0) {
                 if (elect_one()) mbar_arrive(q_free);
                 __syncwarp();
-                kt += n;
-                continue;
             }
-            for (int c = -2; c < n; ++c) {
-                const bool next = c + 2 < n;
-                const uint32_t ks = kt + c + 2, vs = kt + c;
+            for (int c = -2; c < pg.n; ++c) {
+                const bool next = c + 2 < pg.n;
+                const uint32_t ks = pg.at + (uint32_t)(c + 2) * pg.step;
+                const uint32_t vs = pg.at + (uint32_t)c * pg.step;
                 if (next) ok = mbar_wait_warp(&full[ks % S], (ks / S) & 1u, abort);
                 if (ok && c >= 0) {
-                    ok = mbar_wait_warp(&p_full[2 * x + (pp & 1u)], (pp >> 1) & 1u, abort);
-                    if (ok && Tr::k8)
-                        ok = mbar_wait_warp(&wide_full[vs % (W + !W)], (vs / (W + !W)) & 1u, abort);
+                    ok = mbar_wait_warp(&p_full[2 * x + (pp & 1u)], (pp >> 1) & 1u, abort) &&
+                         mbar_wait_warp(&v_full[vs % W], (vs / W) & 1u, abort);
                     if (ok && c == 0 && outs++ > 0)  // O_x of the item before is out
                         ok = mbar_wait_warp(&o_free[x], (outs - 2) & 1u, abort);
                 }
@@ -317,15 +344,15 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
                 tc_fence_after();
                 if (elect_one()) {
                     if (c >= 0) issue_pv(pp & 1u, vs, c > 0);
-                    if (next) issue_s(sp & 1u, ks);
+                    if (next) issue_s(sp & 1u, dq, ks);
                     // the item's last scores
-                    if (c + 3 == n || (c == -2 && n < 2)) umma_commit(q_free);
+                    if (c + 3 == pg.n) umma_commit(q_free);
                 }
                 __syncwarp();
                 if (c >= 0) ++pp;
                 if (next) ++sp;
             }
-            kt += n;
+            kt += it.hi - it.lo;
         }
         // arrives once every MMA issued has completed (TMEM is freed after it)
         if (elect_one()) umma_commit(mma_done);
@@ -333,18 +360,18 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
     } else if (Tr::k8 && warp >= kHeadWiden) {
         // V of a page, as it landed (rows of 128 codes, 16-byte groups swizzled), into
         // the two halves of 64 dims that the products take
-        constexpr int NW = Tr::kWideners > 0 ? Tr::kWideners : 1, WW = W + !W;
+        constexpr int NW = Tr::kWideners > 0 ? Tr::kWideners : 1;
         const int w = warp - kHeadWiden;
         uint32_t kt = 0;
         for (int d = first; ok && d < last; ++d) {
             const HeadItem it = head_item(a.plan, d);
             for (int j = it.lo; j < it.hi; ++j, ++kt) {
-                const uint32_t s = kt % S, t = kt % WW;
+                const uint32_t s = kt % S, t = kt % W;
                 ok = mbar_wait_warp(&full[s], (kt / S) & 1u, abort) &&
-                     mbar_wait_warp(&wide_free[t], ((kt / WW) & 1u) ^ 1u, abort);
+                     mbar_wait_warp(&v_free[t], ((kt / W) & 1u) ^ 1u, abort);
                 if (!ok) break;
-                const uint32_t src = smem_u32(smem + Tr::kOffV + s * Tr::kPageBytes);
-                const uint32_t dst = smem_u32(smem + Tr::kOffWide + t * Tr::kWideBytes);
+                const uint32_t src = smem_u32(smem + Tr::kOffCodes + s * Tr::kPageBytes);
+                const uint32_t dst = smem_u32(smem + Tr::kOffV + t * Tr::kWideBytes);
                 for (int e = 32 * w + lane; e < kTile * 8; e += 32 * NW) {
                     const int row = e >> 3, c = e & 7;  // token, 16 dims
                     const uint4 v = lds128(src + row * 128 + ((c ^ (row & 7)) << 4));
@@ -368,16 +395,15 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&wide_full[t]);
+                    mbar_arrive(&v_full[t]);
                     mbar_arrive(&empty[s]);
-                    if (!it.two && w == 0) mbar_arrive(&wide_free[t]);
+                    if (!it.two && w == 0) mbar_arrive(&v_free[t]);  // for the half that leaves it
                 }
             }
             if (ok && lane == 0) mbar_arrive(q_free);
         }
     } else if (warp < kHeadSoftmax) {
-        // softmax of row tile x: thread = one query row, warp w reads TMEM lanes
-        // 32 (w mod 4) ..
+        // softmax of half x: thread = one query row, warp w reads TMEM lanes 32 (w mod 4) ..
         const int x = warp >> 2, q4 = warp & 3;
         const int rho = 32 * q4 + lane;
         const uint32_t row = tmem + ((uint32_t)(32 * q4) << 16);
@@ -389,12 +415,8 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
         uint32_t kt = 0;
         for (int d = first; ok && d < last; ++d) {
             const HeadItem it = head_item(a.plan, d);
-            const int n = it.hi - it.lo;
-            if (x == 1 && !it.two) {
-                kt += n;
-                continue;
-            }
-            const int tok = it.tok + x * tpb + tok_in;
+            const HeadPages pg = head_pages(it, kt, x);
+            const int tok = it.tok + (it.two ? x * tpb : 0) + tok_in;
             const bool valid = tok_in < tpb && tok < it.end;
             float sc = a.score_scale;
             if (Tr::k8 && valid) sc *= __ldg(a.q_scale + (size_t)tok * a.Hq + it.h * a.G + g);
@@ -402,7 +424,7 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
             // a negative factor turns the maximum round: then the scores are scaled first
             const bool turned = __any_sync(kFullMask, sc < 0.f);
             float m_ref = -INFINITY, l = 0.f;
-            for (int c = 0; c < n; ++c, ++kt) {
+            for (int c = 0; c < pg.n; ++c) {
                 const uint32_t b = ns & 1u;
                 if (!mbar_wait_warp(&s_full[2 * x + b], (ns >> 1) & 1u, abort)) {
                     ok = false;
@@ -413,7 +435,8 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
                 tmem_ld32_nowait(scol + 64 * b, ra);
                 tmem_ld32_nowait(scol + 64 * b + 32, rb);
                 const float *scales = reinterpret_cast<const float *>(
-                    smem + Tr::kOffScale + (kt % kScaleRing) * kPageScales * 4);
+                    smem + Tr::kOffScale +
+                    ((pg.at + (uint32_t)c * pg.step) % kScaleRing) * kPageScales * 4);
                 tmem_wait_ld32x2(ra, rb);
                 float s[kTile];
 #pragma unroll
@@ -440,35 +463,31 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
                 uint32_t pk[32];  // P as packed pairs, over the first half of the scores
                 const float2 f2 = make_float2(f, f), nb2 = make_float2(-base, -base);
                 float ps[8] = {};
+                float2 *ps2 = reinterpret_cast<float2 *>(ps);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     const float2 e = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), f2, nb2);
                     const float w0 = ex2(e.x), w1 = ex2(e.y);
                     if (KV == HPC_KV_FP8_E4M3) {
                         pk[i] = pack_f16x2(w0, w1);
+                        ps2[i & 3] = __fadd2_rn(ps2[i & 3], make_float2(w0, w1));
                     } else if (Tr::kBlk) {
                         const float vs = scales[kTile / kScaleBlock + 2 * i / kScaleBlock];
                         pk[i] = pack_bf16x2(w0 * vs, w1 * vs);
-                        ps[2 * (i & 3)] += w0;
-                        ps[2 * (i & 3) + 1] += w1;
+                        ps2[i & 3] = __fadd2_rn(ps2[i & 3], make_float2(w0, w1));
                     } else {
                         pk[i] = pack_bf16x2(w0, w1);
                     }
                 }
                 tmem_st32_nowait(scol + 64 * b, pk);
-                // the sum takes the weights as they were rounded: the heaviest one's
-                // rounding then cancels against its own in the product (not so with
-                // block scales, which are rounded with them)
-                if (!Tr::kBlk) {
+                // BF16: the sum takes the weights as they were rounded: the heaviest one's
+                // rounding then cancels against its own in the product.  (f16 weights are
+                // rounded to 2^-11, and block scales are rounded with theirs.)
+                if (KV == HPC_KV_BF16) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        if (KV == HPC_KV_BF16) {
-                            head_add_bf16(ps[2 * (i & 3)], (uint16_t)pk[i]);
-                            head_add_bf16(ps[2 * (i & 3) + 1], (uint16_t)(pk[i] >> 16));
-                        } else {
-                            head_add_f16(ps[2 * (i & 3)], (uint16_t)pk[i]);
-                            head_add_f16(ps[2 * (i & 3) + 1], (uint16_t)(pk[i] >> 16));
-                        }
+                        head_add_bf16(ps[2 * (i & 3)], (uint16_t)pk[i]);
+                        head_add_bf16(ps[2 * (i & 3) + 1], (uint16_t)(pk[i] >> 16));
                     }
                 }
                 l = l * factor + (((ps[0] + ps[1]) + (ps[2] + ps[3])) +
@@ -499,13 +518,16 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
                 ++ns;
             }
             if (!ok) break;
+            kt += it.hi - it.lo;
+            const size_t at = (size_t)(it.slot + x) * kHeadRows + rho;
+            if (valid) a.part_lse[at] = l > 0.f ? (m_ref - kUp + lg2(l)) * kLn2 : -INFINITY;
+            if (pg.n == 0) continue;  // (a partial of no weight: its values are not read)
             if (!mbar_wait_warp(&o_done[2 * x + ((ns - 1) & 1u)], ((ns - 1) >> 1) & 1u, abort)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
             const float inv = l > 0.f ? (KV == HPC_KV_FP8_E4M3 ? a.v_scale : 1.f) / l : 0.f;
-            const size_t at = (size_t)(it.slot + x) * kHeadRows + rho;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 float o[64];
@@ -523,8 +545,6 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
                         store_f32x8(a.part_o + at * kHeadDim + 64 * hf + i, o + i);
                 }
             }
-            if (valid)
-                a.part_lse[at] = l > 0.f ? (m_ref - kUp + lg2(l)) * kLn2 : -INFINITY;
         }
         tc_fence_before();
         __syncwarp();

@@ -4,14 +4,17 @@
 namespace hpc {
 namespace {
 
-// (the plain form's pipeline: one tile per stage, four stages)
+#ifndef HPC_SHARED_STAGES
+#define HPC_SHARED_STAGES 4
+#define HPC_SHARED_TPS 1
+#endif
 template <int NB>
 struct Tail {
-    using Tr = AttnTraits<false, 4, 1, NB>;
+    using Tr = AttnTraits<false, HPC_SHARED_STAGES, HPC_SHARED_TPS, NB>;
     static constexpr int kThreads = Tr::kThreads, kSmemBytes = Tr::kSmemBytes;
     static __device__ __forceinline__ void run(const CUtensorMap &tk, const CUtensorMap &tv,
                                                const AttnParams &t) {
-        attn_cta<false, 4, 1, NB>(tk, tv, t);
+        attn_cta<false, HPC_SHARED_STAGES, HPC_SHARED_TPS, NB>(tk, tv, t);
     }
 };
 

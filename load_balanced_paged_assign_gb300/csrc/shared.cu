@@ -13,16 +13,16 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 
-// What the plan takes the work to cost, in nanoseconds: a page against one row tile of
-// the head, a tail tile of a CTA that has HBM to itself, and (picoseconds) where all
-// CTAs stream.
+// What the plan takes the work to cost (see SharedPlan).
 struct Cost {
-    int head_ns, tail_ns, tail_ps;
+    float head_us, tail_us, stream_us;
+    int head_start, tail_start;
 };
 
-Cost cost_of(hpc_kv_dtype dt, int heads) {
-    if (dt == HPC_KV_BF16) return {375, 450, 4960};
-    return {420, 250 * heads, 2480 * heads};
+// (nb blocks of 8 query rows per KV head and request)
+Cost cost_of(hpc_kv_dtype dt, int heads, int nb) {
+    if (dt == HPC_KV_BF16) return {0.118f, nb == 1 ? 0.62f : 0.80f, 4.96e-3f, 32, 2};
+    return {0.100f, 0.36f * heads, 2.48e-3f * heads, 32, 2};
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -42,8 +42,9 @@ hpc_status check_shape(int32_t B, int32_t Hq, int32_t Hkv, int32_t q_len, int32_
         return HPC_ERR_UNSUPPORTED;
     if (B > HPC_MAX_SHARED_BATCH || groups > HPC_MAX_SHARED_GROUPS || num_ctas > 1 << 16)
         return HPC_ERR_UNSUPPORTED;
-    // costs, tile counts and token indices stay in int32
+    // costs, tile counts, query rows and token indices stay in int32
     if ((int64_t)B * max_pages * Hkv >= (int64_t)1 << 28 ||
+        (int64_t)B * q_len * Hq >= (int64_t)1 << 30 ||
         (int64_t)max_pages * HPC_PAGE_SIZE >= (int64_t)1 << 30)
         return HPC_ERR_UNSUPPORTED;
     return HPC_OK;
@@ -120,10 +121,12 @@ hpc_status plan_shared(const int32_t *d_seqlens, int32_t B, int32_t Hq, int32_t 
     p.q_len = q_len;
     p.num_ctas = num_ctas;
     p.floor = min_tiles;
-    const Cost c = cost_of(dt, heads);
-    p.head_ns = c.head_ns;
-    p.tail_ns = c.tail_ns;
-    p.tail_ps = c.tail_ps;
+    const Cost c = cost_of(dt, heads, q_len * G > 8 ? 2 : 1);
+    p.head_us = c.head_us;
+    p.tail_us = c.tail_us;
+    p.stream_us = c.stream_us;
+    p.head_start = c.head_start;
+    p.tail_start = c.tail_start;
     p.desc = reinterpret_cast<int4 *>(map->tail.desc);
     p.bin_ptr = map->tail.bin_ptr;
     p.chunk_count = map->tail.chunk_count;

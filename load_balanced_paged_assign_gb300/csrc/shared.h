@@ -24,7 +24,7 @@ constexpr int kHeadRows = 128;  // query rows of a tile
 //         the request whose table row is read}, {first tile, end, 1: two row tiles, 0}
 // A unit is a KV head of a group and a pair of its row tiles (or the last one alone).
 // Descriptor d leaves the partials of its first row tile in slot 2 d, the second's in
-// slot 2 d + 1.
+// slot 2 d + 1; a row tile that is alone leaves two, of every other page.
 struct HeadPlan {
     int32_t *hdr;
     int4 *req;
@@ -65,9 +65,10 @@ inline HeadPlan head_plan(int32_t *at, int64_t B, int64_t units, int64_t num_cta
 struct SharedPlan {
     const int32_t *seqlens, *starts, *prefix;
     int B, groups, Hkv, heads, G, max_pages, q_len, num_ctas, floor;
-    int head_ns;  // time of a page against one row tile
-    int tail_ns;  // of a tail descriptor's tile in a CTA that has HBM to itself
-    int tail_ps;  // and of a tile where HBM is what all CTAs wait for
+    float head_us;    // of one unit of the head's cost (an eighth of a page of two row tiles)
+    float tail_us;    // of a tail descriptor's tile in a CTA
+    float stream_us;  // of a tail tile where HBM is what all CTAs wait for
+    int head_start, tail_start;  // what a unit costs beside its pages
     int4 *desc;
     int32_t *bin_ptr, *chunk_count, *chunk_off, *meta;
     HeadPlan head;

@@ -22,54 +22,87 @@ __device__ __forceinline__ int clamp_live(const SharedPlan &p, int L) {
     return min(max(L, 0), p.max_pages * kTile);
 }
 
-// Cost of a page: 2 against a pair of row tiles, 1 against a single one.  A unit's
-// cost is even, so that bins of even budgets begin at tiles.
-__device__ __forceinline__ int pair_cost(int np) { return 2 * np; }
-__device__ __forceinline__ int single_cost(int np) { return (np + 1) & ~1; }
+// The head's cost of a page: against a pair of row tiles, and against one that is alone.
+// Measured 0.80 and 0.50 us.
+constexpr int kPairCost = 8, kAloneCost = 5;
+
+// Costs are positions on a line that bins of one budget cut: a unit of n pages of cost w
+// begins with `start` positions for what it costs beside them (Q, its partials), and a
+// page belongs to the bin in which it begins.  A bin is longer than `start` + w, so that
+// some page begins in each.
+
+// a / b for quotients below 2^20, with `inv` = 1 / b: off by one at most before the
+// correction.  (One reciprocal for all quotients of a divisor: a division is 100 cycles of
+// latency, and this kernel is a chain of them.)
+__device__ __forceinline__ int quotient(int a, int b, float inv) {
+    const int q = (int)((float)a * inv), r = a - q * b;
+    return q + (r >= b) - (r < 0);
+}
+
+// Descriptors of a unit that spans several bins: a thread writes the first kOwn of its
+// own unit, its warp the others (a long prefix of few requests is one unit of as many
+// descriptors as there are CTAs).  The cooperative way costs 300 cycles a unit, a
+// thread's own 60 a descriptor.
+constexpr int kOwn = 16;
+
+template <class Write>
+__device__ __forceinline__ void write_chunks(int cnt, Write write) {
+    const int lane = threadIdx.x & 31;
+    for (int i = 0; i < min(cnt, kOwn); ++i) write(lane, i, false);
+    for (unsigned many = __ballot_sync(kFull, cnt > kOwn); many; many &= many - 1) {
+        const int of = __ffs(many) - 1, n = __shfl_sync(kFull, cnt, of);
+        for (int i0 = kOwn; i0 < n; i0 += 32) write(of, i0 + lane, true);
+    }
+}
 
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedPlan p) {
-    // [B] tail tiles of the requests up to each; of each group: shared pages, first
+    // of each request: its length, then the tail tiles of the requests up to it; its
+    // group where it shares, else -1; the tails up to it.  Of each group: first request, shared pages, first
     // sharing request, row tiles, units and cost of the groups before it
     extern __shared__ int s_mem[];
-    int *s_end = s_mem;
-    int *g_np = s_end + p.B, *g_lead = g_np + p.groups, *g_nb = g_lead + p.groups;
-    int *g_unit = g_nb + p.groups, *g_cost = g_unit + p.groups + 1;
-    __shared__ int s_scan[32];
+    int *s_end = s_mem, *s_of = s_end + p.B, *s_tail = s_of + p.B;
+    int *g_start = s_tail + p.B, *g_np = g_start + p.groups + 1, *g_lead = g_np + p.groups;
+    int *g_nb = g_lead + p.groups, *g_unit = g_nb + p.groups, *g_cost = g_unit + p.groups;
+    __shared__ int s_scan[4 * 32];
     __shared__ unsigned s_flags;
-    __shared__ int s_bad, s_np;
+    __shared__ int s_bad, s_last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    if (tid == 0) s_flags = 0, s_bad = 0, s_last = -1;
+    // the arguments' lines of the constant bank, cold, while the kernel before still runs
+    asm volatile("" ::"l"(p.seqlens), "r"(p.floor), "f"(p.head_us), "r"(p.tail_start), "l"(p.desc),
+                 "l"(p.meta), "l"(p.head.hdr), "l"(p.head.desc));
     grid_dependency_wait();
     grid_launch_dependents();
-    if (tid == 0) s_flags = 0, s_bad = 0;
-    __syncthreads();
     unsigned flags = 0;
-
-    // lengths into shared memory, flagged where out of range; the groups' bounds
-    for (int r = tid; r < p.B; r += blockDim.x) {
-        const int L = p.seqlens[r];
-        if (L < 0 || L > p.max_pages * kTile) flags |= HPC_FLAG_BAD_SEQLEN;
-        s_end[r] = clamp_live(p, L);
-        p.head.req[r] = make_int4(0, 0, 0, 0);
-    }
-    for (int g = tid; g < p.groups; g += blockDim.x) {
-        const int a = p.starts[g], b = p.starts[g + 1];
-        if (a < 0 || b < a || b > p.B) s_bad = 1;
-        const int np = p.prefix[g];
-        if (np < 0 || np > p.max_pages) flags |= HPC_FLAG_BAD_SEQLEN;
+    for (int i = tid; i < p.B || i <= p.groups; i += blockDim.x) {
+        // (the three loads in flight together)
+        const int L = i < p.B ? p.seqlens[i] : 0;
+        const int start = p.groups > 0 && i <= p.groups ? p.starts[i] : 0;
+        const int np = i < p.groups ? p.prefix[i] : 0;
+        const bool bad_len = L < 0 || L > p.max_pages * kTile, bad_np = np < 0 || np > p.max_pages;
+        if (bad_len || bad_np) flags |= HPC_FLAG_BAD_SEQLEN;
+        if (i < p.B) {
+            s_end[i] = clamp_live(p, L);
+            s_of[i] = -1;
+        }
+        if (i <= p.groups) g_start[i] = start;
+        if (i < p.groups) g_np[i] = bad_np ? 0 : np;
     }
     __syncthreads();
-    const bool bad = s_bad != 0;
+    for (int g = tid; g < p.groups; g += blockDim.x)
+        if (g_start[g] < 0 || g_start[g + 1] < g_start[g] || g_start[g + 1] > p.B) s_bad = 1;
+    if (p.groups > 0) __syncthreads();
+    const bool bad = s_bad != 0;  // (not read before the barrier where it may be written)
     if (bad) flags |= HPC_FLAG_BAD_SEQLEN;
 
     // who shares: a warp per group
     const int tpb = head_tokens(p.G);
     for (int g = warp; g < p.groups; g += warps) {
-        const int a = bad ? 0 : p.starts[g], b = bad ? 0 : p.starts[g + 1];
-        int np = p.prefix[g];
-        if (np < 0 || np > p.max_pages) np = 0;
+        const int a = bad ? 0 : g_start[g], b = bad ? 0 : g_start[g + 1], np = g_np[g];
+        const int need = np * kTile + p.q_len - 1;
         int count = 0, lead = p.B, last = -1;
-        for (int r = a + lane; r < b; r += 32)
-            if (np > 0 && s_end[r] - p.q_len + 1 >= np * kTile) {
+        for (int r = a + lane; r < b && np > 0; r += 32)
+            if (s_end[r] >= need) {
                 ++count;
                 lead = min(lead, r);
                 last = r;
@@ -77,152 +110,170 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
         count = __reduce_add_sync(kFull, count);
         lead = __reduce_min_sync(kFull, lead);
         last = __reduce_max_sync(kFull, last);
+        if (count >= 2)
+            for (int r = a + lane; r < b; r += 32)
+                if (s_end[r] >= need) {
+                    s_of[r] = g;
+                    s_end[r] -= np * kTile;  // the tail's tokens
+                }
+        __syncwarp();
         if (lane == 0) {
-            g_np[g] = count >= 2 ? np : 0;
             g_lead[g] = lead;
             g_nb[g] = count >= 2 ? ((last - lead + 1) * p.q_len + tpb - 1) / tpb : 0;
+            if (count < 2) g_np[g] = 0;
         }
     }
     __syncthreads();
 
-    // units and costs of the groups
-    int units = 0, cost = 0;
-    for (int base = 0; base < p.groups; base += blockDim.x) {
-        const int g = base + tid;
-        int u = 0, c = 0;
-        if (g < p.groups && g_np[g] > 0) {
-            const int np = g_np[g], nb = g_nb[g];
-            u = p.Hkv * ((nb + 1) / 2);
-            c = p.Hkv * ((nb / 2) * pair_cost(np) + (nb & 1) * single_cost(np));
+    // units, pages' costs of the groups, tail tiles and tails of the requests, and their
+    // running sums
+    int units = 0, pages = 0, tiles = 0, tails = 0;
+    for (int base = 0; base < max(p.B, p.groups); base += blockDim.x) {
+        const int i = base + tid;
+        int v[4] = {0, 0, 0, 0}, total[4];
+        if (i < p.groups && g_np[i] > 0) {
+            const int np = g_np[i], nb = g_nb[i];
+            v[0] = p.Hkv * ((nb + 1) / 2);
+            v[1] = p.Hkv * np * ((nb / 2) * kPairCost + (nb & 1) * kAloneCost);
         }
-        int tu, tc;
-        const int iu = block_inclusive_scan(u, s_scan, tu);
-        const int ic = block_inclusive_scan(c, s_scan, tc);
-        if (g < p.groups) {
-            g_unit[g] = units + iu - u;
-            g_cost[g] = cost + ic - c;
+        if (i < p.B) v[2] = (s_end[i] + kTile - 1) / kTile;
+        v[3] = v[2] > 0;
+        const int u = v[0], c = v[1];
+        block_inclusive_scans(v, s_scan, total);
+        if (i < p.groups) {
+            g_unit[i] = units + v[0] - u;
+            g_cost[i] = pages + v[1] - c;
+            if (u > 0) atomicMax(&s_last, i);  // the last group with units
         }
-        units += tu;
-        cost += tc;
-    }
-    if (tid == 0) g_unit[p.groups] = units, g_cost[p.groups] = cost;
-    __syncthreads();
-
-    // the requests' part in it
-    for (int g = warp; g < p.groups; g += warps) {
-        const int np = g_np[g];
-        if (np == 0) continue;
-        const int lead = g_lead[g], nb = g_nb[g], u0 = g_unit[g];
-        for (int r = p.starts[g] + lane; r < p.starts[g + 1]; r += 32) {
-            if (s_end[r] - p.q_len + 1 < np * kTile) continue;
-            p.head.req[r] = make_int4(np, u0, lead * p.q_len, nb);
-            s_end[r] -= np * kTile;  // the tail's tokens
+        if (i < p.B) {
+            s_end[i] = tiles + v[2];
+            s_tail[i] = tails + v[3];
         }
+        units += total[0];
+        pages += total[1];
+        tiles += total[2];
+        tails += total[3];
     }
-    __syncthreads();
-
-    // tail tiles per request and their running sum
-    int N = 0;
-    for (int base = 0; base < p.B; base += blockDim.x) {
-        const int r = base + tid;
-        const int n = r < p.B ? (s_end[r] + kTile - 1) / kTile : 0;
-        int total;
-        const int incl = block_inclusive_scan(n, s_scan, total);
-        if (r < p.B) s_end[r] = N + incl;
-        N += total;
-    }
+    __syncthreads();  // the sums are complete
     const int tail_units = p.Hkv / p.heads;  // per request
-    const int T = tail_units * N;
 
+    // What a unit costs beside its pages counts where a CTA has several microseconds of
+    // work; with less, the floor alone says how finely units are cut.
+    const float head_us = (float)pages * p.head_us, tail_us = (float)(tail_units * tiles) * p.tail_us;
+    const bool busy = head_us + tail_us > 2.f * p.num_ctas;
+    const int start = busy ? p.head_start : 0, tail_start = busy ? p.tail_start : 0;
+    const int cost = pages + units * start;
+    const int N = tiles + tails * tail_start, T = tail_units * N;
     // CTAs: where the tail's HBM time is what everything takes, no more for it than
     // that needs; else in proportion to the times
-    if (tid == 0) {
-        const long long C = p.num_ctas;
-        const long long head = (long long)cost * p.head_ns, tail = (long long)T * p.tail_ns;
-        const long long even = (head + tail + C - 1) / C;
-        const long long stream = (long long)T * p.tail_ps / 1000;
-        const long long time = max(max(even, stream), 1LL);
-        long long n = (head + time - 1) / time;
-        n = max(min(n, T > 0 ? C - 1 : C), cost > 0 ? 1LL : 0LL);
-        s_np = (int)n;
-    }
-    __syncthreads();
-    const int want = s_np;
-    const int budget = want > 0 ? (max((cost + want - 1) / want, 2 * max(p.floor, 1)) + 1) & ~1 : 2;
-    const int np_ctas = (cost + budget - 1) / budget;
+    const float head = (float)cost * p.head_us, tail = (float)T * p.tail_us;
+    const float time = fmaxf((head + tail) / p.num_ctas, (float)(tail_units * tiles) * p.stream_us);
+    const int most = T > 0 ? p.num_ctas - 1 : p.num_ctas;
+    const int want = cost > 0 ? max((int)fminf(ceilf(head / time), (float)most), 1) : 0;
+    const int budget = max(want > 0 ? (cost + want - 1) / want : 0,
+                           start + kPairCost * max(p.floor, 1));
+    // up to the bin in which the last page begins
+    const int np_ctas =
+        units > 0 ? (cost - (g_nb[s_last] & 1 ? kAloneCost : kPairCost)) / budget + 1 : 0;
+    const int tail_ctas = max(p.num_ctas - np_ctas, 1);
+    const int tail_budget = max((T + tail_ctas - 1) / tail_ctas, tail_start + max(p.floor, 1));
+    const float budget_inv = 1.f / (float)budget, tail_inv = 1.f / (float)tail_budget;
+    const float B_inv = 1.f / (float)max(p.B, 1);
 
-    // the head's descriptors
-    int num_head = 0;
-    for (int base = 0; base < units; base += blockDim.x) {
+    for (int r = tid; r < p.B; r += blockDim.x) {
+        const int g = s_of[r];
+        p.head.req[r] = g < 0 ? make_int4(0, 0, 0, 0)
+                              : make_int4(g_np[g], g_unit[g], g_lead[g] * p.q_len, g_nb[g]);
+    }
+    auto group_of = [&](int u) {  // the last group with g_unit <= u: it has units
+        int lo = 0, hi = p.groups;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (g_unit[mid] <= u) lo = mid;
+            else hi = mid;
+        }
+        return lo;
+    };
+    // the descriptors of the head and, behind its CTAs, of the tail
+    int num_head = 0, num_desc = 0;
+    for (int base = 0; base < max(units, tail_units * p.B); base += blockDim.x) {
         const int u = base + tid;
-        int cnt = 0, S = 0, g = 0, h = 0, pair = 0, n = 0, w = 1;
+        int hc = 0, hS = 0, hbin = 0, hh = 0, first = 0, end = 0, lead = 0, n = 0, w = 1,
+            prev = 0;
         if (u < units) {
-            int lo = 0, hi = p.groups;  // the last group with g_unit <= u that has units
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (g_unit[mid] <= u) lo = mid;
-                else hi = mid;
+            const int lo = group_of(u);
+            const int nb = g_nb[lo], pairs = (nb + 1) / 2, i = u - g_unit[lo];
+            n = g_np[lo];
+            hh = quotient(i, pairs, 1.f / (float)pairs);
+            const int pair = i - hh * pairs;
+            w = 2 * pair + 1 < nb ? kPairCost : kAloneCost;
+            hS = g_cost[lo] + u * start +
+                 hh * n * ((nb / 2) * kPairCost + (nb & 1) * kAloneCost) + pair * n * kPairCost +
+                 start;  // of its first page
+            // what a page of the unit before costs
+            if (pair == 0 && hh == 0 && u > 0) {
+                prev = g_nb[group_of(u - 1)] & 1;
+            } else {
+                prev = pair == 0 ? nb & 1 : 0;
             }
-            g = lo;
-            const int nb = g_nb[g], pairs = (nb + 1) / 2, i = u - g_unit[g];
-            n = g_np[g];
-            h = i / pairs;
-            pair = i - h * pairs;
-            w = 2 * pair + 1 < nb ? 2 : 1;
-            const int per_head = (nb / 2) * pair_cost(n) + (nb & 1) * single_cost(n);
-            S = g_cost[g] + h * per_head + pair * pair_cost(n);
-            cnt = (S + w * (n - 1)) / budget - S / budget + 1;
+            prev = prev ? kAloneCost : kPairCost;
+            hbin = quotient(hS, budget, budget_inv);
+            hc = quotient(hS + w * (n - 1), budget, budget_inv) - hbin + 1;
+            lead = g_lead[lo];
+            first = lead * p.q_len + 2 * pair * tpb;
+            end = min(lead * p.q_len + nb * tpb, g_start[lo + 1] * p.q_len);
         }
-        int total;
-        const int incl = block_inclusive_scan(cnt, s_scan, total);
-        if (u < units) {
-            const int off = num_head + incl - cnt, bin0 = S / budget;
-            p.head.unit[u] = make_int2(off, cnt);
-            const int lead = g_lead[g] * p.q_len, first = lead + 2 * pair * tpb;
-            // (row tiles of the group are counted from its first sharing request to its last)
-            const int end = min(lead + g_nb[g] * tpb, p.starts[g + 1] * p.q_len);
-            for (int i = 0; i < cnt; ++i) {
-                const int lo = i == 0 ? 0 : ((bin0 + i) * budget - S + w - 1) / w;
-                const int hi = i == cnt - 1 ? n : ((bin0 + i + 1) * budget - S + w - 1) / w;
-                p.head.desc[2 * (off + i)] = make_int4(h, first, end, g_lead[g]);
-                p.head.desc[2 * (off + i) + 1] = make_int4(lo, hi, w - 1, 0);
-                if (i > 0 || S == bin0 * budget) p.head.bin[bin0 + i] = off + i;
-            }
+        int tc = 0, th = 0, r = 0, tn = 0, tS = 0, tbin = 0, skip = 0;
+        if (u < tail_units * p.B) {
+            th = quotient(u, p.B, B_inv);
+            r = u - th * p.B;
+            tn = s_end[r] - (r ? s_end[r - 1] : 0);
+            // of its first tile
+            tS = th * N + s_end[r] - tn + s_tail[r] * tail_start;
+            tbin = quotient(tS, tail_budget, tail_inv);
+            tc = tn ? quotient(tS + tn - 1, tail_budget, tail_inv) - tbin + 1 : 0;
+            if (s_of[r] >= 0) skip = g_np[s_of[r]];
         }
-        num_head += total;
+        int v[2] = {hc, tc}, total[2];
+        block_inclusive_scans(v, s_scan, total);
+        const int hoff = num_head + v[0] - hc, toff = num_desc + v[1] - tc;
+        num_head += total[0];
+        num_desc += total[1];
+        if (u < units) p.head.unit[u] = make_int2(hoff, hc);
+        if (u < tail_units * p.B) {
+            p.chunk_count[u] = tc;
+            p.chunk_off[u] = toff;
+        }
+        write_chunks(hc, [&](int of, int i, bool all) {
+            auto get = [&](int x) { return all ? __shfl_sync(kFull, x, of) : x; };
+            const int S = get(hS), cnt = get(hc), n_ = get(n), w_ = get(w), off = get(hoff);
+            const int prev_ = get(prev);
+            const int4 a = make_int4(get(hh), get(first), get(end), get(lead));
+            const int bin = get(hbin) + i;
+            if (i >= cnt) return;
+            const bool two = w_ == kPairCost;
+            auto page_at = [&](int x) {
+                return two ? (x + kPairCost - 1) / kPairCost : (x + kAloneCost - 1) / kAloneCost;
+            };
+            const int lo = i == 0 ? 0 : page_at(bin * budget - S);
+            const int hi = i == cnt - 1 ? n_ : page_at((bin + 1) * budget - S);
+            p.head.desc[2 * (off + i)] = a;
+            p.head.desc[2 * (off + i) + 1] = make_int4(lo, hi, two, 0);
+            // the first that begins in its bin: the unit before has its last page earlier
+            if (i > 0 || S - start - prev_ < bin * budget) p.head.bin[bin] = off + i;
+        });
+        write_chunks(tc, [&](int of, int i, bool all) {
+            auto get = [&](int x) { return all ? __shfl_sync(kFull, x, of) : x; };
+            const int S = get(tS), cnt = get(tc), n_ = get(tn), off = get(toff);
+            const int h_ = get(th), r_ = get(r), sk = get(skip);
+            const int bin = get(tbin) + i, bin_lo = bin * tail_budget;
+            if (i >= cnt) return;
+            const int lo = max(S, bin_lo), hi = min(S + n_ - bin_lo, tail_budget) + bin_lo;
+            p.desc[off + i] = make_int4(h_, r_, sk + lo - S, sk + hi - S);
+            if (S - tail_start <= bin_lo) p.bin_ptr[np_ctas + bin] = off + i;
+        });
     }
     for (int b = np_ctas + tid; b <= p.num_ctas; b += blockDim.x) p.head.bin[b] = num_head;
-
-    // the tail's, behind the head's CTAs
-    const int tail_ctas = max(p.num_ctas - np_ctas, 1);
-    const int tail_budget = max((T + tail_ctas - 1) / tail_ctas, max(p.floor, 1));
-    int num_desc = 0;
-    for (int base = 0; base < tail_units * p.B; base += blockDim.x) {
-        const int u = base + tid;
-        int cnt = 0, h = 0, r = 0, n = 0, S = 0;
-        if (u < tail_units * p.B) {
-            h = u / p.B;
-            r = u - h * p.B;
-            n = s_end[r] - (r ? s_end[r - 1] : 0);
-            S = h * N + s_end[r] - n;
-            cnt = n ? (S + n - 1) / tail_budget - S / tail_budget + 1 : 0;
-        }
-        int total;
-        const int incl = block_inclusive_scan(cnt, s_scan, total);
-        if (u < tail_units * p.B) {
-            const int off = num_desc + incl - cnt, skip = p.head.req[r].x;
-            p.chunk_count[u] = cnt;
-            p.chunk_off[u] = off;
-            for (int i = 0; i < cnt; ++i) {
-                const int bin = S / tail_budget + i;
-                const int bin_lo = bin * tail_budget;
-                const int lo = max(S, bin_lo), hi = (int)min((long long)(S + n), (long long)bin_lo + tail_budget);
-                p.desc[off + i] = make_int4(h, r, skip + lo - S, skip + hi - S);
-                if (lo == bin_lo) p.bin_ptr[np_ctas + bin] = off + i;
-            }
-        }
-        num_desc += total;
-    }
     const int used = np_ctas + (T + tail_budget - 1) / tail_budget;
     for (int b = used + tid; b <= p.num_ctas; b += blockDim.x) p.bin_ptr[b] = num_desc;
     for (int b = tid; b < np_ctas; b += blockDim.x) p.bin_ptr[b] = 0;
@@ -230,13 +281,10 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     if (flags && lane == 0) atomicOr(&s_flags, flags);
     __syncthreads();
     if (tid == 0) {
-        p.head.hdr[0] = np_ctas;
-        p.head.hdr[1] = num_head;
-        p.head.hdr[2] = budget;
-        p.head.hdr[3] = cost;
-        p.head.hdr[4] = units;
-        p.head.hdr[5] = p.head.hdr[6] = p.head.hdr[7] = 0;
-        p.meta[0] = T;
+        int4 *hdr = reinterpret_cast<int4 *>(p.head.hdr);
+        hdr[0] = make_int4(np_ctas, num_head, budget, cost);
+        hdr[1] = make_int4(units, 0, 0, 0);
+        p.meta[0] = tail_units * tiles;
         p.meta[1] = tail_budget;
         p.meta[2] = num_desc;
         p.meta[3] = (int)s_flags;
@@ -260,62 +308,79 @@ struct JoinArgs {
 // w_c = exp(lse_c - max), over the row's partials of the tail and of the head.
 __global__ void __launch_bounds__(32 * kJoinWarps)
     shared_join_kernel(const JoinArgs a, __nv_bfloat16 *__restrict__ out) {
-    grid_dependency_wait();
     const int lane = threadIdx.x & 31;
     const int row = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);  // (r * q_len + i) * Hq + hq
-    if (row >= a.B * a.q_len * a.Hq) return;
-    const int ri = row / a.Hq, hq = row - ri * a.Hq;
-    const int r = ri / a.q_len, i = ri - r * a.q_len;
-    const int Gt = a.tail_heads * a.G, ht = hq / Gt;
-    const int R = a.q_len * Gt, g = i * Gt + (hq - ht * Gt);
-    const int n_tail = a.chunk_count[ht * a.B + r], off = a.chunk_off[ht * a.B + r];
-    const int4 req = a.plan.req[r];
-    int n_head = 0, slot0 = 0, step = 1, rho = 0;
-    if (req.x > 0) {
-        const int h = hq / a.G, tpb = head_tokens(a.G);
-        const int tok = ri - req.z, tile = tok / tpb;
-        const int2 un = a.plan.unit[req.y + h * ((req.w + 1) / 2) + tile / 2];
-        n_head = un.y;
-        slot0 = 2 * un.x + (tile & 1);
-        step = 2;
-        rho = (tok - tile * tpb) * a.G + (hq - h * a.G);
+    const bool any = row < a.B * a.q_len * a.Hq;
+    // The plan is read ahead of the attention's end: its kernel had finished before the
+    // attention's let this one start.
+    int n_tail = 0, off = 0, n_head = 0, slot0 = 0, step = 1, rho = 0, R = 1, g = 0;
+    if (any) {
+        const int ri = row / a.Hq, hq = row - ri * a.Hq;
+        const int r = ri / a.q_len, i = ri - r * a.q_len;
+        const int Gt = a.tail_heads * a.G, ht = hq / Gt;
+        R = a.q_len * Gt;
+        g = i * Gt + (hq - ht * Gt);
+        n_tail = a.chunk_count[ht * a.B + r];
+        off = a.chunk_off[ht * a.B + r];
+        const int4 req = a.plan.req[r];
+        if (req.x > 0) {
+            const int h = hq / a.G, tpb = head_tokens(a.G);
+            const int tok = ri - req.z, tile = tok / tpb;
+            const int2 un = a.plan.unit[req.y + h * ((req.w + 1) / 2) + tile / 2];
+            const bool alone = tile + 1 == req.w && (tile & 1) == 0;
+            n_head = alone ? 2 * un.y : un.y;
+            slot0 = 2 * un.x + (tile & 1);
+            step = alone ? 1 : 2;
+            rho = (tok - tile * tpb) * a.G + (hq - h * a.G);
+        }
     }
+    grid_dependency_wait();
+    if (!any) return;
     const int n = n_tail + n_head;
     auto at = [&](int c, const float *tail, const float *head, int width) {
         return c < n_tail ? tail + ((size_t)(off + c) * R + g) * width
                           : head + ((size_t)(slot0 + step * (c - n_tail)) * kHeadRows + rho) * width;
     };
-    float m = -INFINITY;
-    for (int c = lane; c < n; c += 32) m = fmaxf(m, *at(c, a.tail_lse, a.head_lse, 1));
+    // the first rows on their way with the log-sum-exps (nothing is read twice but the
+    // latter of rows with more than 32 partials)
+    constexpr int kAhead = 8;
+    float4 x[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+        x[j] = j < n ? reinterpret_cast<const float4 *>(at(j, a.tail_o, a.head_o, kHeadDim))[lane]
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float own = lane < n ? *at(lane, a.tail_lse, a.head_lse, 1) : -INFINITY;
+    float m = own;
+    for (int c = 32 + lane; c < n; c += 32) m = fmaxf(m, *at(c, a.tail_lse, a.head_lse, 1));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float wsum = 0.f;
     for (int base = 0; base < n; base += 32) {
         const int cnt = min(32, n - base);
-        const float wl =
-            lane < cnt ? ex2((*at(base + lane, a.tail_lse, a.head_lse, 1) - m) * kJoinLog2e) : 0.f;
+        float wl = 0.f;
+        if (lane < cnt)
+            wl = ex2(((base ? *at(base + lane, a.tail_lse, a.head_lse, 1) : own) - m) * kJoinLog2e);
         float ws = wl;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(kFull, ws, o);
         wsum += ws;
-        for (int k = 0; k < cnt; k += 4) {
-            float4 x[4];
-            float w[4];
+        for (int k = 0; k < cnt; k += kAhead) {
+            if (base | k) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                w[j] = __shfl_sync(kFull, wl, (k + j) & 31);
-                x[j] = k + j < cnt
-                           ? reinterpret_cast<const float4 *>(
-                                 at(base + k + j, a.tail_o, a.head_o, kHeadDim))[lane]
-                           : make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int j = 0; j < kAhead; ++j)
+                    if (k + j < cnt)
+                        x[j] = reinterpret_cast<const float4 *>(
+                            at(base + k + j, a.tail_o, a.head_o, kHeadDim))[lane];
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                acc.x += w[j] * x[j].x;
-                acc.y += w[j] * x[j].y;
-                acc.z += w[j] * x[j].z;
-                acc.w += w[j] * x[j].w;
+            for (int j = 0; j < kAhead; ++j) {
+                const float w = __shfl_sync(kFull, wl, (k + j) & 31);
+                if (k + j >= cnt || !(w > 0.f)) continue;  // (no values where no weight is)
+                acc.x += w * x[j].x;
+                acc.y += w * x[j].y;
+                acc.z += w * x[j].z;
+                acc.w += w * x[j].w;
             }
         }
     }
@@ -346,7 +411,7 @@ cudaError_t launch_dependent(void (*kernel)(P...), int grid, int threads, size_t
 }  // namespace
 
 cudaError_t launch_shared_plan(const SharedPlan &p, cudaStream_t s) {
-    const size_t smem = ((size_t)p.B + 5 * (size_t)p.groups + 2) * sizeof(int);
+    const size_t smem = (3 * (size_t)p.B + 6 * (size_t)p.groups + 1) * sizeof(int);
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(
             shared_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

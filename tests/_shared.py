@@ -77,7 +77,9 @@ class Shared(Case):
         assert bins[0] == 0 and bins[ctas:] == [num] * (C + 1 - ctas)
         assert all(a < b for a, b in zip(bins[:ctas], bins[1:ctas + 1]))
         for c in range(ctas):
-            assert sum((d[5] - d[4]) * (1 + d[6]) for d in desc[bins[c]:bins[c + 1]]) <= budget
+            # (8 a page of two row tiles, 5 one of a tile alone; the last may reach over)
+            cost = [(d[5] - d[4], 8 if d[6] else 5) for d in desc[bins[c]:bins[c + 1]]]
+            assert sum(n * w for n, w in cost) < budget + cost[-1][1]
         seen = [0] * num
         tail = ws.tmap.to_host()
         two = 2 if self.kv != "bf16" and Hkv % 2 == 0 else 1
