@@ -963,8 +963,8 @@ hpc_status hpc_kv_compact(const hpc_page_pool *pool, const int32_t *d_block_tabl
  * layer's caches: K, V and, for HPC_KV_E4M3_BLOCK, the scales d_kv_scale (else
  * NULL).  No page is copied to that another copy reads or writes.  At most
  * cap_copies are made.  A pair outside [0, num_pages) raises HPC_FLAG_BAD_PAGE in
- * d_flags (device int32 or NULL) and is passed over.  Caches are 32-byte aligned,
- * scales 16-byte.
+ * d_flags (device int32 or NULL) and is passed over; HPC_FLAG_TIMEOUT if a wait
+ * timed out.  All pointers but d_copies and d_flags are 16-byte aligned.
  */
 hpc_status hpc_kv_copy_pages(const int32_t *d_copies, int32_t cap_copies, void *d_k_cache,
                              void *d_v_cache, float *d_kv_scale, hpc_kv_dtype kv_dtype,

@@ -74,7 +74,7 @@ def test_refusals_of_copies():
 
     assert call(cap=0) == E.HPC_OK
     assert call(copies=None) == ARG and call(k=None) == ARG and call(v=None) == ARG
-    assert call(k=FAKE + 16) == ARG and call(v=FAKE + 16) == ARG
+    assert call(k=FAKE + 8) == ARG and call(v=FAKE + 8) == ARG
     assert call(sc=FAKE) == ARG  # scales of a cache that has none
     assert call(dtype=2) == ARG and call(dtype=2, sc=FAKE + 8) == ARG and call(dtype=3) == ARG
     assert call(D=64) == UNS and call(Hkv=1 << 20) == UNS
