@@ -815,8 +815,8 @@ def hpc_decode_plan_shared(seqlens, group_starts, prefix_pages, Hq, Hkv, q_len, 
     (sl_, gs_, pp_), shape, count = _arrays(fn, dev, "seqlens group_starts prefix_pages",
                                             (_I32, _I32, _I32), seqlens, group_starts,
                                             prefix_pages)
-    n = _groups_arg(fn, shape[1], shape[2], ws)
     _on(fn, ws, dev)
+    n = _groups_arg(fn, shape[1], shape[2], ws)
     _check(fn, lib().hpc_decode_plan_shared(
         sl_, count[0], int(Hq), int(Hkv), int(max_pages_per_req), gs_, pp_, n, ws.num_ctas,
         int(min_tiles_per_cta), ws.kv_dtype, int(q_len), ctypes.byref(ws.c),
@@ -834,11 +834,11 @@ def hpc_decode_attn_shared(q, q_scale, k_cache, v_cache, k_scale, v_scale, kv_sc
     """Attention of a batch that hpc_decode_plan_shared planned, as hpc_decode_step_mq
     computes it.  kv_scale: the block scales of a block-scaled cache, else None."""
     fn = "hpc_decode_attn_shared"
+    _on(fn, ws, _current_device())
     Hq, Hkv, q_len = int(Hq), int(Hkv), int(q_len)
     kv, dev, B, pages, cols, (q_, k_, v_, qs_, sc_, bt_, sl_, po_, pl_, _, out_) = _win_args(
         fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, Hq, Hkv, q_len,
         ws.part_o, ws.part_lse, out, None, ws.tmap.cap_desc)
-    _on(fn, ws, dev)
     status = lib().hpc_decode_attn_shared(
         q_, qs_, k_, v_, pages, float(k_scale), float(v_scale), sc_, kv, bt_, cols, sl_, B, Hq,
         Hkv, HEAD_DIM, q_len, float(sm_scale), ctypes.byref(ws.c), po_, pl_, out_,
@@ -852,11 +852,11 @@ def hpc_decode_step_shared(q, q_scale, k_cache, v_cache, k_scale, v_scale, kv_sc
                            min_tiles_per_cta, ws: SharedWorkspace, out, stream=None):
     """hpc_decode_plan_shared and hpc_decode_attn_shared in one call."""
     fn = "hpc_decode_step_shared"
+    _on(fn, ws, _current_device())
     Hq, Hkv, q_len = int(Hq), int(Hkv), int(q_len)
     kv, dev, B, pages, cols, (q_, k_, v_, qs_, sc_, bt_, sl_, po_, pl_, _, out_) = _win_args(
         fn, q, q_scale, k_cache, v_cache, kv_scale, block_table, seqlens, Hq, Hkv, q_len,
         ws.part_o, ws.part_lse, out, None, ws.tmap.cap_desc)
-    _on(fn, ws, dev)
     (gs_, pp_), shape, _ = _arrays(fn, dev, "group_starts prefix_pages", (_I32, _I32),
                                    group_starts, prefix_pages)
     n = _groups_arg(fn, shape[0], shape[1], ws)
@@ -896,6 +896,7 @@ class PagePool:
         self.marks = torch.full_like(refs, 2 ** 31 - 1)
         self.c = hpc_page_pool(_ptr(refs), _ptr(free_list), _ptr(state), _ptr(self.marks),
                                self.num_pages)
+        self.ref, self.dev = ctypes.byref(self.c), refs.get_device()
 
     @property
     def free_pages(self) -> int:
@@ -908,65 +909,72 @@ class PagePool:
         return int(self.state[1])
 
 
-def _pool_args(fn, dev, pool, names, *tensors):
-    """The checks of the pool's calls: (addresses, shapes, element counts) of int32 arrays."""
-    if not isinstance(pool, PagePool) or pool.refs.get_device() != dev:
+_I32S = [(_I32,) * n for n in range(6)]
+
+
+def _pool_table(fn, dev, pool, shape):
+    """The table's rows and columns; raises for a pool of another device or no pool."""
+    if type(pool) is not PagePool or pool.dev != dev:
         raise ValueError(f"{fn}: no PagePool on the current device")
-    got = _arrays(fn, dev, names, (_I32,) * len(tensors), *tensors)
-    if len(got[1][0]) != 2:
+    if len(shape) != 2:
         raise ValueError(f"{fn}: block_table is no matrix")
-    return got
+    return shape
 
 
-def _listed(fn, n, **counts):
-    for name, c in counts.items():
-        if c is not None and c != n:
-            raise ValueError(f"{fn}: {name} has not {n} entries")
-
-
-def hpc_kv_free(pool: PagePool, block_table, rows=None, keep=None, stream=None):
-    """The rows (None: all) give back the pages behind their first keep[i] tokens (None: all)."""
-    fn, dev = "hpc_kv_free", _current_device()
-    (bt_, rows_, keep_), shape, count = _pool_args(fn, dev, pool, "block_table rows keep",
-                                                   block_table, rows, keep)
-    B, cols = shape[0]
-    n = B if rows is None else count[1]
-    _listed(fn, n, keep=count[2])
-    _check(fn, lib().hpc_kv_free(ctypes.byref(pool.c), bt_, B, cols, rows_, keep_, n,
-                                 _raw_stream(dev, stream)))
-
-
-def hpc_kv_extend(pool: PagePool, block_table, rows, lens, stream=None):
-    """The rows (None: all) get the pages that lens[i] tokens need and they have not."""
-    fn, dev = "hpc_kv_extend", _current_device()
-    (bt_, rows_, lens_), shape, count = _pool_args(fn, dev, pool, "block_table rows lens",
-                                                   block_table, rows, lens)
-    B, cols = shape[0]
-    n = B if rows is None else count[1]
-    _listed(fn, n, lens=count[2] or 0)
-    _check(fn, lib().hpc_kv_extend(ctypes.byref(pool.c), bt_, B, cols, rows_, lens_, n,
-                                   _raw_stream(dev, stream)))
-
-
-def hpc_kv_fork(pool: PagePool, block_table, src, dst, lens, copies, stream=None):
-    """Row dst[i] becomes a fork of the first lens[i] tokens of row src[i]; copies [1 + cap, 2]
-    gets the pages to copy ({count, 0}, then {from, to})."""
-    fn, dev = "hpc_kv_fork", _current_device()
-    (bt_, src_, dst_, lens_, cp_), shape, count = _pool_args(
-        fn, dev, pool, "block_table src dst lens copies", block_table, src, dst, lens, copies)
-    if any(t is None for t in (src, dst, lens, copies)):
-        raise ValueError(f"{fn}: src, dst, lens and copies are needed")
-    B, cols = shape[0]
-    n = count[1]
-    _listed(fn, n, dst=count[2], lens=count[3])
-    _check(fn, lib().hpc_kv_fork(ctypes.byref(pool.c), bt_, B, cols, src_, dst_, lens_, n, cp_,
-                                 _cap(fn, shape[4]), _raw_stream(dev, stream)))
+def _listed(fn, name, n):
+    raise ValueError(f"{fn}: {name} has not {n} entries")
 
 
 def _cap(fn, shape):
     if len(shape) != 2 or shape[0] < 1 or shape[1] != 2:
         raise ValueError(f"{fn}: copies is {shape}, not [1 + capacity, 2]")
     return shape[0] - 1
+
+
+def hpc_kv_free(pool: PagePool, block_table, rows=None, keep=None, stream=None):
+    """The rows (None: all) give back the pages behind their first keep[i] tokens (None: all)."""
+    fn, dev = "hpc_kv_free", _current_device()
+    adr, shape, count = _arrays(fn, dev, "block_table rows keep", _I32S[3], block_table, rows, keep)
+    B, cols = _pool_table(fn, dev, pool, shape[0])
+    n = B if rows is None else count[1]
+    if keep is not None and count[2] != n:
+        _listed(fn, "keep", n)
+    status = lib().hpc_kv_free(pool.ref, adr[0], B, cols, adr[1], adr[2], n,
+                               _raw_stream(dev, stream))
+    if status != HPC_OK:
+        _check(fn, status)
+
+
+def hpc_kv_extend(pool: PagePool, block_table, rows, lens, stream=None):
+    """The rows (None: all) get the pages that lens[i] tokens need and they have not."""
+    fn, dev = "hpc_kv_extend", _current_device()
+    adr, shape, count = _arrays(fn, dev, "block_table rows lens", _I32S[3], block_table, rows, lens)
+    B, cols = _pool_table(fn, dev, pool, shape[0])
+    n = B if rows is None else count[1]
+    if count[2] != n:
+        _listed(fn, "lens", n)
+    status = lib().hpc_kv_extend(pool.ref, adr[0], B, cols, adr[1], adr[2], n,
+                                 _raw_stream(dev, stream))
+    if status != HPC_OK:
+        _check(fn, status)
+
+
+def hpc_kv_fork(pool: PagePool, block_table, src, dst, lens, copies, stream=None):
+    """Row dst[i] becomes a fork of the first lens[i] tokens of row src[i]; copies [1 + cap, 2]
+    gets the pages to copy ({count, 0}, then {from, to})."""
+    fn, dev = "hpc_kv_fork", _current_device()
+    adr, shape, count = _arrays(fn, dev, "block_table src dst lens copies", _I32S[5], block_table,
+                                src, dst, lens, copies)
+    B, cols = _pool_table(fn, dev, pool, shape[0])
+    if None in count:
+        raise ValueError(f"{fn}: src, dst, lens and copies are needed")
+    n = count[1]
+    if count[2] != n or count[3] != n:
+        _listed(fn, "dst" if count[2] != n else "lens", n)
+    status = lib().hpc_kv_fork(pool.ref, adr[0], B, cols, adr[1], adr[2], adr[3], n, adr[4],
+                               _cap(fn, shape[4]), _raw_stream(dev, stream))
+    if status != HPC_OK:
+        _check(fn, status)
 
 
 def hpc_kv_compact(pool: PagePool, block_table, copies, out_table=None, out_pool=None,
@@ -976,16 +984,20 @@ def hpc_kv_compact(pool: PagePool, block_table, copies, out_table=None, out_pool
     fn, dev = "hpc_kv_compact", _current_device()
     if out_table is None:
         out_table = block_table
-    out_pool = pool if out_pool is None else out_pool
-    (bt_, cp_, ot_), shape, _ = _pool_args(fn, dev, pool, "block_table copies out_table",
-                                           block_table, copies, out_table)
-    if copies is None or not isinstance(out_pool, PagePool) or \
-            out_pool.refs.get_device() != dev:
-        raise ValueError(f"{fn}: copies, or no PagePool on the current device")
-    _shape(fn, "out_table", shape[2], shape[0])
-    _check(fn, lib().hpc_kv_compact(ctypes.byref(pool.c), bt_, shape[0][0], shape[0][1], cp_,
-                                    _cap(fn, shape[1]), ot_, ctypes.byref(out_pool.c),
-                                    _raw_stream(dev, stream)))
+    if out_pool is None:
+        out_pool = pool
+    adr, shape, count = _arrays(fn, dev, "block_table copies out_table", _I32S[3], block_table,
+                                copies, out_table)
+    B, cols = _pool_table(fn, dev, pool, shape[0])
+    _pool_table(fn, dev, out_pool, shape[0])
+    if copies is None:
+        raise ValueError(f"{fn}: copies is needed")
+    if shape[2] != shape[0]:
+        _shape(fn, "out_table", shape[2], shape[0])
+    status = lib().hpc_kv_compact(pool.ref, adr[0], B, cols, adr[1], _cap(fn, shape[1]), adr[2],
+                                  out_pool.ref, _raw_stream(dev, stream))
+    if status != HPC_OK:
+        _check(fn, status)
 
 
 _PAGE_TYPES = [(_I32, t, t, _F32, _I32) for t in (_BF16, _E4M3)]
@@ -995,22 +1007,27 @@ def hpc_kv_copy_pages(copies, k_cache, v_cache, kv_scale=None, flags=None, strea
     """The copies that hpc_kv_fork or hpc_kv_compact listed, in one layer's caches (and the
     block scales [num_pages, Hkv, 2, 4] of a block-scaled one)."""
     fn, dev = "hpc_kv_copy_pages", _current_device()
-    (cp_, k_, v_, sc_, fl_), shape, _ = _arrays(
-        fn, dev, "copies k_cache v_cache kv_scale flags",
-        _PAGE_TYPES[k_cache.dtype is _E4M3], copies, k_cache, v_cache, kv_scale, flags)
-    if copies is None or len(shape[1]) != 4:
+    e4m3 = k_cache.dtype is _E4M3
+    adr, shape, _ = _arrays(fn, dev, "copies k_cache v_cache kv_scale flags", _PAGE_TYPES[e4m3],
+                            copies, k_cache, v_cache, kv_scale, flags)
+    cache = shape[1]
+    if copies is None or len(cache) != 4:
         raise ValueError(f"{fn}: copies, or a cache [num_pages, 64, Hkv, 128]")
-    pages, _, Hkv, _ = shape[1]
-    want = (pages, PAGE_SIZE, Hkv, HEAD_DIM)
-    _shape(fn, "k_cache", shape[1], want)
-    _shape(fn, "v_cache", shape[2], want)
+    pages, Hkv = cache[0], cache[2]
+    if cache[1] != PAGE_SIZE or cache[3] != HEAD_DIM:
+        _shape(fn, "k_cache", cache, (pages, PAGE_SIZE, Hkv, HEAD_DIM))
+    if shape[2] != cache:
+        _shape(fn, "v_cache", shape[2], cache)
+    kv = HPC_KV_FP8_E4M3 if e4m3 else HPC_KV_BF16
     if kv_scale is not None:
-        if k_cache.dtype is not _E4M3:
+        if not e4m3:
             raise ValueError(f"{fn}: kv_scale belongs to E4M3 pages")
         _shape(fn, "kv_scale", shape[3], (pages, Hkv, 2, PAGE_SIZE // SCALE_BLOCK))
-    kv = HPC_KV_E4M3_BLOCK if kv_scale is not None else kv_dtype_of(k_cache)
-    _check(fn, lib().hpc_kv_copy_pages(cp_, _cap(fn, shape[0]), k_, v_, sc_, kv, pages, Hkv,
-                                       HEAD_DIM, fl_, _raw_stream(dev, stream)))
+        kv = HPC_KV_E4M3_BLOCK
+    status = lib().hpc_kv_copy_pages(adr[0], _cap(fn, shape[0]), adr[1], adr[2], adr[3], kv, pages,
+                                     Hkv, HEAD_DIM, adr[4], _raw_stream(dev, stream))
+    if status != HPC_OK:
+        _check(fn, status)
 
 
 class Workspace:
