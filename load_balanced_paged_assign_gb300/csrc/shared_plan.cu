@@ -18,10 +18,6 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 
-__device__ __forceinline__ int clamp_live(const SharedPlan &p, int L) {
-    return min(max(L, 0), p.max_pages * kTile);
-}
-
 // The head's cost of a page: against a pair of row tiles, and against one that is alone.
 // Measured 0.80 and 0.50 us.
 constexpr int kPairCost = 8, kAloneCost = 5;
@@ -39,111 +35,177 @@ __device__ __forceinline__ int quotient(int a, int b, float inv) {
     return q + (r >= b) - (r < 0);
 }
 
-// Descriptors of a unit that spans several bins: a thread writes the first kOwn of its
-// own unit, its warp the others (a long prefix of few requests is one unit of as many
-// descriptors as there are CTAs).  The cooperative way costs 300 cycles a unit, a
-// thread's own 60 a descriptor.
+// The kernel is one chain of dependent steps over code that runs once, 5 us of 10,000
+// cycles at first.  So the head's units and the tail's are warps of their own, requests
+// find their groups for themselves, and loops are not unrolled.
+constexpr int kHeadThreads = 64;
+
+// A unit of either kind, by the thread that owns it: its first page's position, pages, their
+// cost, bins, descriptors.
+struct Unit {
+    int S = 0, n = 0, w = 1, bin = 0, count = 0;
+};
+
+__device__ __forceinline__ Unit unit_of(int S, int n, int w, int budget, float inv) {
+    Unit u;
+    u.S = S;
+    u.n = n;
+    u.w = w;
+    if (n == 0) return u;
+    u.bin = quotient(S, budget, inv);
+    u.count = quotient(S + w * (n - 1), budget, inv) - u.bin + 1;
+    return u;
+}
+
+// Descriptors of a unit that spans several bins: put(owner's lane or -1 for one's own, i,
+// first page, end) for each.  A thread writes the first kOwn of its own unit, its warp the
+// others (a long prefix of few requests is one unit of as many descriptors as there are
+// CTAs).
 constexpr int kOwn = 16;
 
-template <class Write>
-__device__ __forceinline__ void write_chunks(int cnt, Write write) {
+__device__ __forceinline__ int page_from(int x, int w) {  // the first that begins at x or later
+    return w == kPairCost    ? (x + kPairCost - 1) / kPairCost
+           : w == kAloneCost ? (x + kAloneCost - 1) / kAloneCost
+                             : x;
+}
+
+template <class Put>
+__device__ __forceinline__ void write_chunks(const Unit &u, int budget, Put put) {
     const int lane = threadIdx.x & 31;
-    for (int i = 0; i < min(cnt, kOwn); ++i) write(lane, i, false);
-    for (unsigned many = __ballot_sync(kFull, cnt > kOwn); many; many &= many - 1) {
-        const int of = __ffs(many) - 1, n = __shfl_sync(kFull, cnt, of);
-        for (int i0 = kOwn; i0 < n; i0 += 32) write(of, i0 + lane, true);
+    int lo = 0;
+#pragma unroll 1
+    for (int i = 0; i < min(u.count, kOwn); ++i) {
+        const int hi = i == u.count - 1 ? u.n : page_from((u.bin + i + 1) * budget - u.S, u.w);
+        put(-1, i, lo, hi);
+        lo = hi;
     }
+#pragma unroll 1
+    for (unsigned many = __ballot_sync(kFull, u.count > kOwn); many; many &= many - 1) {
+        const int of = __ffs(many) - 1, count = __shfl_sync(kFull, u.count, of);
+        const int S = __shfl_sync(kFull, u.S, of), n = __shfl_sync(kFull, u.n, of);
+        const int w = __shfl_sync(kFull, u.w, of), bin = __shfl_sync(kFull, u.bin, of);
+#pragma unroll 1
+        for (int i0 = kOwn; i0 < count; i0 += 32) {
+            const int i = i0 + lane;
+            put(of, i < count ? i : -1, page_from((bin + i) * budget - S, w),
+                i == count - 1 ? n : page_from((bin + i + 1) * budget - S, w));
+        }
+    }
+}
+
+// The last group whose entry in `first` is not behind i.
+__device__ __forceinline__ int last_from(const int *first, int groups, int i) {
+    int lo = 0, hi = groups;
+#pragma unroll 1
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first[mid] <= i) lo = mid;
+        else hi = mid;
+    }
+    return lo;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedPlan p) {
     // of each request: its length, then the tail tiles of the requests up to it; its
-    // group where it shares, else -1; the tails up to it.  Of each group: first request, shared pages, first
-    // sharing request, row tiles, units and cost of the groups before it
+    // group where it shares, else -1; the tails up to it.  Of each group: first request,
+    // shared pages, sharing requests, the first and last of them, units and cost of the
+    // groups before it
     extern __shared__ int s_mem[];
     int *s_end = s_mem, *s_of = s_end + p.B, *s_tail = s_of + p.B;
-    int *g_start = s_tail + p.B, *g_np = g_start + p.groups + 1, *g_lead = g_np + p.groups;
-    int *g_nb = g_lead + p.groups, *g_unit = g_nb + p.groups, *g_cost = g_unit + p.groups;
+    int *g_start = s_tail + p.B, *g_np = g_start + p.groups + 1, *g_count = g_np + p.groups;
+    int *g_lead = g_count + p.groups, *g_last = g_lead + p.groups;
+    int *g_unit = g_last + p.groups, *g_cost = g_unit + p.groups;
     __shared__ int s_scan[4 * 32];
     __shared__ unsigned s_flags;
     __shared__ int s_bad, s_last;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, threads = blockDim.x;
     if (tid == 0) s_flags = 0, s_bad = 0, s_last = -1;
-    // the arguments' lines of the constant bank, cold, while the kernel before still runs
-    asm volatile("" ::"l"(p.seqlens), "r"(p.floor), "f"(p.head_us), "r"(p.tail_start), "l"(p.desc),
-                 "l"(p.meta), "l"(p.head.hdr), "l"(p.head.desc));
+    __syncthreads();
     grid_dependency_wait();
     grid_launch_dependents();
     unsigned flags = 0;
-    for (int i = tid; i < p.B || i <= p.groups; i += blockDim.x) {
-        // (the three loads in flight together)
+#pragma unroll 1
+    for (int i = tid; i < p.B || i <= p.groups; i += threads) {
+        // (the loads in flight together)
         const int L = i < p.B ? p.seqlens[i] : 0;
         const int start = p.groups > 0 && i <= p.groups ? p.starts[i] : 0;
+        const int next = i < p.groups ? p.starts[i + 1] : start;
         const int np = i < p.groups ? p.prefix[i] : 0;
         const bool bad_len = L < 0 || L > p.max_pages * kTile, bad_np = np < 0 || np > p.max_pages;
+        if (start < 0 || next < start || next > p.B) s_bad = 1;
         if (bad_len || bad_np) flags |= HPC_FLAG_BAD_SEQLEN;
-        if (i < p.B) {
-            s_end[i] = clamp_live(p, L);
-            s_of[i] = -1;
-        }
+        if (i < p.B) s_end[i] = min(max(L, 0), p.max_pages * kTile);
         if (i <= p.groups) g_start[i] = start;
-        if (i < p.groups) g_np[i] = bad_np ? 0 : np;
+        if (i < p.groups) {
+            g_np[i] = bad_np ? 0 : np;
+            g_count[i] = 0;
+            g_lead[i] = p.B;
+            g_last[i] = -1;
+        }
     }
     __syncthreads();
-    for (int g = tid; g < p.groups; g += blockDim.x)
-        if (g_start[g] < 0 || g_start[g + 1] < g_start[g] || g_start[g + 1] > p.B) s_bad = 1;
-    if (p.groups > 0) __syncthreads();
-    const bool bad = s_bad != 0;  // (not read before the barrier where it may be written)
+    const bool bad = s_bad != 0;
     if (bad) flags |= HPC_FLAG_BAD_SEQLEN;
 
-    // who shares: a warp per group
+    // who shares: a request all of whose queries see all of its group's pages, with another
+    // one that does
     const int tpb = head_tokens(p.G);
-    for (int g = warp; g < p.groups; g += warps) {
-        const int a = bad ? 0 : g_start[g], b = bad ? 0 : g_start[g + 1], np = g_np[g];
-        const int need = np * kTile + p.q_len - 1;
-        int count = 0, lead = p.B, last = -1;
-        for (int r = a + lane; r < b && np > 0; r += 32)
-            if (s_end[r] >= need) {
-                ++count;
-                lead = min(lead, r);
-                last = r;
+#pragma unroll 1
+    for (int r0 = tid - lane; r0 < p.B; r0 += threads) {
+        const int r = r0 + lane;
+        int g = -1;
+        if (r < p.B && !bad && p.groups > 0 && r >= g_start[0] && r < g_start[p.groups]) {
+            const int lo = last_from(g_start, p.groups, r);
+            if (g_np[lo] > 0 && s_end[r] >= g_np[lo] * kTile + p.q_len - 1) g = lo;
+        }
+        if (r < p.B) s_of[r] = g;
+        // (one set of atomics for a warp whose requests share one group, as most do)
+        const int top = __reduce_max_sync(kFull, g);
+        const unsigned same = __ballot_sync(kFull, g == top), any = __ballot_sync(kFull, g >= 0);
+        if (any == 0) continue;
+        if ((any & ~same) == 0) {
+            if (lane == __ffs(any) - 1) {
+                atomicAdd(g_count + g, __popc(any));
+                atomicMin(g_lead + g, r);
+                atomicMax(g_last + g, r0 + 31 - __clz(any));
             }
-        count = __reduce_add_sync(kFull, count);
-        lead = __reduce_min_sync(kFull, lead);
-        last = __reduce_max_sync(kFull, last);
-        if (count >= 2)
-            for (int r = a + lane; r < b; r += 32)
-                if (s_end[r] >= need) {
-                    s_of[r] = g;
-                    s_end[r] -= np * kTile;  // the tail's tokens
-                }
-        __syncwarp();
-        if (lane == 0) {
-            g_lead[g] = lead;
-            g_nb[g] = count >= 2 ? ((last - lead + 1) * p.q_len + tpb - 1) / tpb : 0;
-            if (count < 2) g_np[g] = 0;
+        } else if (g >= 0) {
+            atomicAdd(g_count + g, 1);
+            atomicMin(g_lead + g, r);
+            atomicMax(g_last + g, r);
         }
     }
     __syncthreads();
 
-    // units, pages' costs of the groups, tail tiles and tails of the requests, and their
-    // running sums
+    // units and pages' costs of the groups, tail tiles and tails of the requests, and
+    // their running sums
+    auto row_tiles = [&](int g) {
+        return ((g_last[g] - g_lead[g] + 1) * p.q_len + tpb - 1) / tpb;
+    };
     int units = 0, pages = 0, tiles = 0, tails = 0;
-    for (int base = 0; base < max(p.B, p.groups); base += blockDim.x) {
+#pragma unroll 1
+    for (int base = 0; base < max(p.B, p.groups); base += threads) {
         const int i = base + tid;
         int v[4] = {0, 0, 0, 0}, total[4];
-        if (i < p.groups && g_np[i] > 0) {
-            const int np = g_np[i], nb = g_nb[i];
+        if (i < p.groups && g_count[i] >= 2) {
+            const int nb = row_tiles(i);
             v[0] = p.Hkv * ((nb + 1) / 2);
-            v[1] = p.Hkv * np * ((nb / 2) * kPairCost + (nb & 1) * kAloneCost);
+            v[1] = p.Hkv * g_np[i] * ((nb / 2) * kPairCost + (nb & 1) * kAloneCost);
+            atomicMax(&s_last, i);  // the last group with units
         }
-        if (i < p.B) v[2] = (s_end[i] + kTile - 1) / kTile;
-        v[3] = v[2] > 0;
+        if (i < p.B) {
+            int L = s_end[i];
+            const int g = s_of[i];
+            if (g >= 0 && g_count[g] >= 2) L -= g_np[g] * kTile;
+            else s_of[i] = -1;
+            v[2] = (L + kTile - 1) / kTile;
+            v[3] = v[2] > 0;
+        }
         const int u = v[0], c = v[1];
         block_inclusive_scans(v, s_scan, total);
         if (i < p.groups) {
             g_unit[i] = units + v[0] - u;
             g_cost[i] = pages + v[1] - c;
-            if (u > 0) atomicMax(&s_last, i);  // the last group with units
         }
         if (i < p.B) {
             s_end[i] = tiles + v[2];
@@ -154,7 +216,6 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
         tiles += total[2];
         tails += total[3];
     }
-    __syncthreads();  // the sums are complete
     const int tail_units = p.Hkv / p.heads;  // per request
 
     // What a unit costs beside its pages counts where a CTA has several microseconds of
@@ -172,111 +233,106 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     const int want = cost > 0 ? max((int)fminf(ceilf(head / time), (float)most), 1) : 0;
     const int budget = max(want > 0 ? (cost + want - 1) / want : 0,
                            start + kPairCost * max(p.floor, 1));
+    __syncthreads();  // the sums are complete
     // up to the bin in which the last page begins
     const int np_ctas =
-        units > 0 ? (cost - (g_nb[s_last] & 1 ? kAloneCost : kPairCost)) / budget + 1 : 0;
+        units > 0 ? (cost - (row_tiles(s_last) & 1 ? kAloneCost : kPairCost)) / budget + 1 : 0;
     const int tail_ctas = max(p.num_ctas - np_ctas, 1);
     const int tail_budget = max((T + tail_ctas - 1) / tail_ctas, tail_start + max(p.floor, 1));
-    const float budget_inv = 1.f / (float)budget, tail_inv = 1.f / (float)tail_budget;
-    const float B_inv = 1.f / (float)max(p.B, 1);
 
-    for (int r = tid; r < p.B; r += blockDim.x) {
-        const int g = s_of[r];
-        p.head.req[r] = g < 0 ? make_int4(0, 0, 0, 0)
-                              : make_int4(g_np[g], g_unit[g], g_lead[g] * p.q_len, g_nb[g]);
-    }
-    auto group_of = [&](int u) {  // the last group with g_unit <= u: it has units
-        int lo = 0, hi = p.groups;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (g_unit[mid] <= u) lo = mid;
-            else hi = mid;
-        }
-        return lo;
-    };
-    // the descriptors of the head and, behind its CTAs, of the tail
+    // the descriptors of the head, by the last warps, and of the tail, by the others
+    const bool for_head = p.groups > 0 && tid >= threads - kHeadThreads;
+    const int own_threads = for_head ? kHeadThreads : threads - (p.groups > 0 ? kHeadThreads : 0);
+    const int own = for_head ? tid - (threads - kHeadThreads) : tid;
+    const int line = for_head ? budget : tail_budget;
+    const float line_inv = 1.f / (float)line, B_inv = 1.f / (float)max(p.B, 1);
     int num_head = 0, num_desc = 0;
-    for (int base = 0; base < max(units, tail_units * p.B); base += blockDim.x) {
-        const int u = base + tid;
-        int hc = 0, hS = 0, hbin = 0, hh = 0, first = 0, end = 0, lead = 0, n = 0, w = 1,
-            prev = 0;
-        if (u < units) {
-            const int lo = group_of(u);
-            const int nb = g_nb[lo], pairs = (nb + 1) / 2, i = u - g_unit[lo];
-            n = g_np[lo];
-            hh = quotient(i, pairs, 1.f / (float)pairs);
-            const int pair = i - hh * pairs;
-            w = 2 * pair + 1 < nb ? kPairCost : kAloneCost;
-            hS = g_cost[lo] + u * start +
-                 hh * n * ((nb / 2) * kPairCost + (nb & 1) * kAloneCost) + pair * n * kPairCost +
-                 start;  // of its first page
+#pragma unroll 1
+    for (int k = 0;; ++k) {
+        const int u = k * own_threads + own;
+        Unit un;
+        int h = 0, x = 0, y = 0, z = 0, prev = 0;  // head: group's numbers; tail: request, pages before
+        if (for_head && u < units) {
+            // (the last group with g_unit <= u has units)
+            const int g = last_from(g_unit, p.groups, u), nb = row_tiles(g), pairs = (nb + 1) / 2, i = u - g_unit[g];
+            h = quotient(i, pairs, 1.f / (float)pairs);
+            const int pair = i - h * pairs, n = g_np[g];
+            // of its first page
+            const int S = g_cost[g] + u * start + start + pair * n * kPairCost +
+                          h * n * ((nb / 2) * kPairCost + (nb & 1) * kAloneCost);
+            un = unit_of(S, n, 2 * pair + 1 < nb ? kPairCost : kAloneCost, line, line_inv);
             // what a page of the unit before costs
-            if (pair == 0 && hh == 0 && u > 0) {
-                prev = g_nb[group_of(u - 1)] & 1;
-            } else {
-                prev = pair == 0 ? nb & 1 : 0;
-            }
+            prev = pair > 0            ? 0
+                   : h > 0 || u == 0 ? nb & 1
+                                     : row_tiles(last_from(g_unit, p.groups, u - 1)) & 1;
             prev = prev ? kAloneCost : kPairCost;
-            hbin = quotient(hS, budget, budget_inv);
-            hc = quotient(hS + w * (n - 1), budget, budget_inv) - hbin + 1;
-            lead = g_lead[lo];
-            first = lead * p.q_len + 2 * pair * tpb;
-            end = min(lead * p.q_len + nb * tpb, g_start[lo + 1] * p.q_len);
-        }
-        int tc = 0, th = 0, r = 0, tn = 0, tS = 0, tbin = 0, skip = 0;
-        if (u < tail_units * p.B) {
-            th = quotient(u, p.B, B_inv);
-            r = u - th * p.B;
-            tn = s_end[r] - (r ? s_end[r - 1] : 0);
+            z = g_lead[g];
+            x = z * p.q_len + 2 * pair * tpb;
+            y = min(z * p.q_len + nb * tpb, g_start[g + 1] * p.q_len);
+        } else if (!for_head && u < tail_units * p.B) {
+            h = quotient(u, p.B, B_inv);
+            x = u - h * p.B;
+            const int n = s_end[x] - (x ? s_end[x - 1] : 0);
+            if (s_of[x] >= 0) y = g_np[s_of[x]];
             // of its first tile
-            tS = th * N + s_end[r] - tn + s_tail[r] * tail_start;
-            tbin = quotient(tS, tail_budget, tail_inv);
-            tc = tn ? quotient(tS + tn - 1, tail_budget, tail_inv) - tbin + 1 : 0;
-            if (s_of[r] >= 0) skip = g_np[s_of[r]];
+            un = unit_of(h * N + s_end[x] - n + s_tail[x] * tail_start, n, 1, line, line_inv);
         }
-        int v[2] = {hc, tc}, total[2];
+        int v[2] = {for_head ? un.count : 0, for_head ? 0 : un.count}, total[2];
         block_inclusive_scans(v, s_scan, total);
-        const int hoff = num_head + v[0] - hc, toff = num_desc + v[1] - tc;
+        const int off = (for_head ? num_head + v[0] : num_desc + v[1]) - un.count;
         num_head += total[0];
         num_desc += total[1];
-        if (u < units) p.head.unit[u] = make_int2(hoff, hc);
-        if (u < tail_units * p.B) {
-            p.chunk_count[u] = tc;
-            p.chunk_off[u] = toff;
+        if (for_head && u < units) p.head.unit[u] = make_int2(off, un.count);
+        if (!for_head && u < tail_units * p.B) {
+            p.chunk_count[u] = un.count;
+            p.chunk_off[u] = off;
         }
-        write_chunks(hc, [&](int of, int i, bool all) {
-            auto get = [&](int x) { return all ? __shfl_sync(kFull, x, of) : x; };
-            const int S = get(hS), cnt = get(hc), n_ = get(n), w_ = get(w), off = get(hoff);
-            const int prev_ = get(prev);
-            const int4 a = make_int4(get(hh), get(first), get(end), get(lead));
-            const int bin = get(hbin) + i;
-            if (i >= cnt) return;
-            const bool two = w_ == kPairCost;
-            auto page_at = [&](int x) {
-                return two ? (x + kPairCost - 1) / kPairCost : (x + kAloneCost - 1) / kAloneCost;
-            };
-            const int lo = i == 0 ? 0 : page_at(bin * budget - S);
-            const int hi = i == cnt - 1 ? n_ : page_at((bin + 1) * budget - S);
-            p.head.desc[2 * (off + i)] = a;
-            p.head.desc[2 * (off + i) + 1] = make_int4(lo, hi, two, 0);
-            // the first that begins in its bin: the unit before has its last page earlier
-            if (i > 0 || S - start - prev_ < bin * budget) p.head.bin[bin] = off + i;
-        });
-        write_chunks(tc, [&](int of, int i, bool all) {
-            auto get = [&](int x) { return all ? __shfl_sync(kFull, x, of) : x; };
-            const int S = get(tS), cnt = get(tc), n_ = get(tn), off = get(toff);
-            const int h_ = get(th), r_ = get(r), sk = get(skip);
-            const int bin = get(tbin) + i, bin_lo = bin * tail_budget;
-            if (i >= cnt) return;
-            const int lo = max(S, bin_lo), hi = min(S + n_ - bin_lo, tail_budget) + bin_lo;
-            p.desc[off + i] = make_int4(h_, r_, sk + lo - S, sk + hi - S);
-            if (S - tail_start <= bin_lo) p.bin_ptr[np_ctas + bin] = off + i;
-        });
+        if (for_head) {
+            write_chunks(un, line, [&](int of, int i, int lo, int hi) {
+                int a = h, b = x, c = y, d = z, at = off, bin = un.bin, w = un.w;
+                if (of >= 0) {
+                    a = __shfl_sync(kFull, h, of), b = __shfl_sync(kFull, x, of);
+                    c = __shfl_sync(kFull, y, of), d = __shfl_sync(kFull, z, of);
+                    at = __shfl_sync(kFull, off, of), bin = __shfl_sync(kFull, un.bin, of);
+                    w = __shfl_sync(kFull, un.w, of);
+                    if (i < 0) return;
+                }
+                p.head.desc[2 * (at + i)] = make_int4(a, b, c, d);
+                p.head.desc[2 * (at + i) + 1] = make_int4(lo, hi, w == kPairCost, 0);
+                // the first that begins in its bin: the unit before has its last page earlier
+                if (i > 0 || un.S - start - prev < bin * line) p.head.bin[bin + i] = at + i;
+            });
+        } else {
+            write_chunks(un, line, [&](int of, int i, int lo, int hi) {
+                int a = h, b = x, c = y, at = off, bin = un.bin;
+                if (of >= 0) {
+                    a = __shfl_sync(kFull, h, of), b = __shfl_sync(kFull, x, of);
+                    c = __shfl_sync(kFull, y, of), at = __shfl_sync(kFull, off, of);
+                    bin = __shfl_sync(kFull, un.bin, of);
+                    if (i < 0) return;
+                }
+                p.desc[at + i] = make_int4(a, b, c + lo, c + hi);
+                if (i > 0 || un.S - tail_start <= bin * line) p.bin_ptr[np_ctas + bin + i] = at + i;
+            });
+        }
+        // (the same number of rounds for all threads)
+        if ((k + 1) * kHeadThreads >= units &&
+            (k + 1) * (threads - (p.groups > 0 ? kHeadThreads : 0)) >= tail_units * p.B)
+            break;
     }
-    for (int b = np_ctas + tid; b <= p.num_ctas; b += blockDim.x) p.head.bin[b] = num_head;
+#pragma unroll 1
+    for (int r = tid; r < p.B; r += threads) {
+        const int g = s_of[r];
+        p.head.req[r] = g < 0 ? make_int4(0, 0, 0, 0)
+                              : make_int4(g_np[g], g_unit[g], g_lead[g] * p.q_len, row_tiles(g));
+    }
     const int used = np_ctas + (T + tail_budget - 1) / tail_budget;
-    for (int b = used + tid; b <= p.num_ctas; b += blockDim.x) p.bin_ptr[b] = num_desc;
-    for (int b = tid; b < np_ctas; b += blockDim.x) p.bin_ptr[b] = 0;
+#pragma unroll 1
+    for (int b = tid; b <= p.num_ctas; b += threads) {
+        if (b >= np_ctas) p.head.bin[b] = num_head;
+        if (b >= used) p.bin_ptr[b] = num_desc;
+        if (b < np_ctas) p.bin_ptr[b] = 0;
+    }
     flags = __reduce_or_sync(kFull, flags);
     if (flags && lane == 0) atomicOr(&s_flags, flags);
     __syncthreads();
@@ -411,15 +467,16 @@ cudaError_t launch_dependent(void (*kernel)(P...), int grid, int threads, size_t
 }  // namespace
 
 cudaError_t launch_shared_plan(const SharedPlan &p, cudaStream_t s) {
-    const size_t smem = (3 * (size_t)p.B + 6 * (size_t)p.groups + 1) * sizeof(int);
+    const size_t smem = (3 * (size_t)p.B + 7 * (size_t)p.groups + 1) * sizeof(int);
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(
             shared_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    const long long work = max(max((long long)p.B * (p.Hkv / p.heads), (long long)p.num_ctas + 1),
-                               32LL * p.groups);
-    const int threads = (int)min(max((work + 31) / 32 * 32, 64LL), (long long)kPlanThreads);
+    const long long work = max((long long)p.B * (p.Hkv / p.heads), (long long)p.groups + 1);
+    const int own = p.groups > 0 ? kHeadThreads : 0;
+    const int threads =
+        own + (int)min(max((work + 31) / 32 * 32, 64LL), (long long)(kPlanThreads - own));
     return launch_dependent(shared_plan_kernel, 1, threads, smem, s, p);
 }
 
