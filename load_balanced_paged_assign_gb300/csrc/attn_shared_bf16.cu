@@ -6,15 +6,21 @@ namespace {
 
 #ifndef HPC_SHARED_STAGES
 #define HPC_SHARED_STAGES 4
+#endif
+#ifndef HPC_SHARED_TPS
 #define HPC_SHARED_TPS 1
+#endif
+#ifndef HPC_SHARED_STAGES_MQ
+#define HPC_SHARED_STAGES_MQ 4
 #endif
 template <int NB>
 struct Tail {
-    using Tr = AttnTraits<false, HPC_SHARED_STAGES, HPC_SHARED_TPS, NB>;
+    static constexpr int kStages = NB == 1 ? HPC_SHARED_STAGES : HPC_SHARED_STAGES_MQ;
+    using Tr = AttnTraits<false, kStages, HPC_SHARED_TPS, NB>;
     static constexpr int kThreads = Tr::kThreads, kSmemBytes = Tr::kSmemBytes;
     static __device__ __forceinline__ void run(const CUtensorMap &tk, const CUtensorMap &tv,
                                                const AttnParams &t) {
-        attn_cta<false, HPC_SHARED_STAGES, HPC_SHARED_TPS, NB>(tk, tv, t);
+        attn_cta<false, kStages, HPC_SHARED_TPS, NB>(tk, tv, t);
     }
 };
 

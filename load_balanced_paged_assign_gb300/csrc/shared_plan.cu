@@ -349,7 +349,10 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
 }
 
 // ------------------------------------------------------------------ join
-constexpr int kJoinWarps = 4;
+// CTAs of an SM: as many rows in flight as there are (a kernel that spills costs 3 us more
+// than its time: its launch waits for local memory).
+constexpr int kJoinWarps = 4, kJoinCtas = 7;
+constexpr int kJoinAhead = 6;  // partials of a row on their way together
 constexpr float kJoinLog2e = 1.4426950408889634f;
 
 struct JoinArgs {
@@ -362,86 +365,78 @@ struct JoinArgs {
 
 // One warp per query row, lane i dims 4 i .. 4 i + 3: out = sum_c w_c o_c / sum_c w_c with
 // w_c = exp(lse_c - max), over the row's partials of the tail and of the head.
-__global__ void __launch_bounds__(32 * kJoinWarps)
+__global__ void __launch_bounds__(32 * kJoinWarps, kJoinCtas)
     shared_join_kernel(const JoinArgs a, __nv_bfloat16 *__restrict__ out) {
     const int lane = threadIdx.x & 31;
     const int row = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);  // (r * q_len + i) * Hq + hq
     const bool any = row < a.B * a.q_len * a.Hq;
     // The plan is read ahead of the attention's end: its kernel had finished before the
     // attention's let this one start.
-    int n_tail = 0, off = 0, n_head = 0, slot0 = 0, step = 1, rho = 0, R = 1, g = 0;
+    int n_tail = 0, n = 0;
+    size_t tail = 0, head = 0;  // the row's first partial, in rows
+    uint32_t tail_step = 0, head_step = 0;
     if (any) {
         const int ri = row / a.Hq, hq = row - ri * a.Hq;
         const int r = ri / a.q_len, i = ri - r * a.q_len;
         const int Gt = a.tail_heads * a.G, ht = hq / Gt;
-        R = a.q_len * Gt;
-        g = i * Gt + (hq - ht * Gt);
-        n_tail = a.chunk_count[ht * a.B + r];
-        off = a.chunk_off[ht * a.B + r];
+        n_tail = n = a.chunk_count[ht * a.B + r];
+        tail_step = a.q_len * Gt;
+        tail = (size_t)a.chunk_off[ht * a.B + r] * tail_step + i * Gt + (hq - ht * Gt);
         const int4 req = a.plan.req[r];
         if (req.x > 0) {
             const int h = hq / a.G, tpb = head_tokens(a.G);
             const int tok = ri - req.z, tile = tok / tpb;
             const int2 un = a.plan.unit[req.y + h * ((req.w + 1) / 2) + tile / 2];
             const bool alone = tile + 1 == req.w && (tile & 1) == 0;
-            n_head = alone ? 2 * un.y : un.y;
-            slot0 = 2 * un.x + (tile & 1);
-            step = alone ? 1 : 2;
-            rho = (tok - tile * tpb) * a.G + (hq - h * a.G);
+            n += alone ? 2 * un.y : un.y;
+            head_step = (alone ? 1 : 2) * kHeadRows;
+            head = (size_t)(2 * un.x + (tile & 1)) * kHeadRows + (tok - tile * tpb) * a.G +
+                   (hq - h * a.G);
         }
     }
     grid_dependency_wait();
     if (!any) return;
-    const int n = n_tail + n_head;
-    auto at = [&](int c, const float *tail, const float *head, int width) {
-        return c < n_tail ? tail + ((size_t)(off + c) * R + g) * width
-                          : head + ((size_t)(slot0 + step * (c - n_tail)) * kHeadRows + rho) * width;
+    auto lse = [&](int c) {
+        return c < n_tail ? a.tail_lse[tail + (size_t)c * tail_step]
+                          : a.head_lse[head + (size_t)(c - n_tail) * head_step];
     };
-    // the first rows on their way with the log-sum-exps (nothing is read twice but the
-    // latter of rows with more than 32 partials)
-    constexpr int kAhead = 8;
-    float4 x[kAhead];
+    float4 x[kJoinAhead];
+    auto load = [&](int k) {  // partials k .. (none past the last)
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-        x[j] = j < n ? reinterpret_cast<const float4 *>(at(j, a.tail_o, a.head_o, kHeadDim))[lane]
-                     : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float own = lane < n ? *at(lane, a.tail_lse, a.head_lse, 1) : -INFINITY;
+        for (int j = 0; j < kJoinAhead; ++j) {
+            const int c = k + j;
+            if (c >= n) break;
+            const float *p = c < n_tail
+                                 ? a.tail_o + (tail + (size_t)c * tail_step) * kHeadDim
+                                 : a.head_o + (head + (size_t)(c - n_tail) * head_step) * kHeadDim;
+            x[j] = reinterpret_cast<const float4 *>(p)[lane];
+        }
+    };
+    load(0);  // (on their way with the log-sum-exps)
+    const float own = lane < n ? lse(lane) : -INFINITY;
     float m = own;
-    for (int c = 32 + lane; c < n; c += 32) m = fmaxf(m, *at(c, a.tail_lse, a.head_lse, 1));
+    for (int c = 32 + lane; c < n; c += 32) m = fmaxf(m, lse(c));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float wsum = 0.f;
-    for (int base = 0; base < n; base += 32) {
-        const int cnt = min(32, n - base);
-        float wl = 0.f;
-        if (lane < cnt)
-            wl = ex2(((base ? *at(base + lane, a.tail_lse, a.head_lse, 1) : own) - m) * kJoinLog2e);
-        float ws = wl;
+    float wsum = 0.f, w32 = 0.f;  // w32: the weights of 32 partials, one per lane
+#pragma unroll 1
+    for (int k = 0; k < n; k += kJoinAhead) {
+        if ((k & 31) == 0)
+            w32 = k + lane < n ? ex2(((k == 0 ? own : lse(k + lane)) - m) * kJoinLog2e) : 0.f;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(kFull, ws, o);
-        wsum += ws;
-        for (int k = 0; k < cnt; k += kAhead) {
-            if (base | k) {
-#pragma unroll
-                for (int j = 0; j < kAhead; ++j)
-                    if (k + j < cnt)
-                        x[j] = reinterpret_cast<const float4 *>(
-                            at(base + k + j, a.tail_o, a.head_o, kHeadDim))[lane];
-            }
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                const float w = __shfl_sync(kFull, wl, (k + j) & 31);
-                if (k + j >= cnt || !(w > 0.f)) continue;  // (no values where no weight is)
-                acc.x += w * x[j].x;
-                acc.y += w * x[j].y;
-                acc.z += w * x[j].z;
-                acc.w += w * x[j].w;
-            }
+        for (int j = 0; j < kJoinAhead; ++j) {
+            const float w = __shfl_sync(kFull, w32, (k + j) & 31);
+            if (k + j >= n || !(w > 0.f)) continue;  // (no values where no weight is)
+            wsum += w;
+            acc.x += w * x[j].x;
+            acc.y += w * x[j].y;
+            acc.z += w * x[j].z;
+            acc.w += w * x[j].w;
         }
+        load(k + kJoinAhead);
     }
-    const float inv = n > 0 && m != -INFINITY ? 1.f / wsum : 0.f;
-    if (inv == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
     uint2 packed;
     packed.x = pack_bf16x2(acc.x * inv, acc.y * inv);
     packed.y = pack_bf16x2(acc.z * inv, acc.w * inv);
