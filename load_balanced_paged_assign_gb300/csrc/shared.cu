@@ -22,7 +22,9 @@ struct Cost {
 // (nb blocks of 8 query rows per KV head and request)
 Cost cost_of(hpc_kv_dtype dt, int heads, int nb) {
     if (dt == HPC_KV_BF16) return {0.118f, nb == 1 ? 0.62f : 0.80f, 4.96e-3f, 32, 2};
-    return {0.100f, 0.36f * heads, 2.48e-3f * heads, 32, 2};
+    const float tile = (nb == 1 ? 0.36f : 0.40f) * heads, stream = 2.48e-3f * heads;
+    if (dt == HPC_KV_FP8_E4M3) return {0.108f, tile, stream, 32, nb == 1 ? 2 : 3};
+    return {0.115f, tile, stream, 32, nb == 1 ? 2 : 3};
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

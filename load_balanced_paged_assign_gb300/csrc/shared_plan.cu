@@ -117,9 +117,9 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     int *g_unit = g_last + p.groups, *g_cost = g_unit + p.groups;
     __shared__ int s_scan[4 * 32];
     __shared__ unsigned s_flags;
-    __shared__ int s_bad, s_last;
+    __shared__ int s_bad, s_first, s_last;
     const int tid = threadIdx.x, lane = tid & 31, threads = blockDim.x;
-    if (tid == 0) s_flags = 0, s_bad = 0, s_last = -1;
+    if (tid == 0) s_flags = 0, s_bad = 0, s_first = p.groups, s_last = -1;
     __syncthreads();
     grid_dependency_wait();
     grid_launch_dependents();
@@ -191,7 +191,8 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
             const int nb = row_tiles(i);
             v[0] = p.Hkv * ((nb + 1) / 2);
             v[1] = p.Hkv * g_np[i] * ((nb / 2) * kPairCost + (nb & 1) * kAloneCost);
-            atomicMax(&s_last, i);  // the last group with units
+            atomicMin(&s_first, i);  // the first and the last group with units
+            atomicMax(&s_last, i);
         }
         if (i < p.B) {
             int L = s_end[i];
@@ -222,21 +223,43 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     // work; with less, the floor alone says how finely units are cut.
     const float head_us = (float)pages * p.head_us, tail_us = (float)(tail_units * tiles) * p.tail_us;
     const bool busy = head_us + tail_us > 2.f * p.num_ctas;
-    const int start = busy ? p.head_start : 0, tail_start = busy ? p.tail_start : 0;
-    const int cost = pages + units * start;
+    int start = busy ? p.head_start : 0;
+    const int tail_start = busy ? p.tail_start : 0;
+    int cost = pages + units * start;
     const int N = tiles + tails * tail_start, T = tail_units * N;
     // CTAs: where the tail's HBM time is what everything takes, no more for it than
     // that needs; else in proportion to the times
     const float head = (float)cost * p.head_us, tail = (float)T * p.tail_us;
-    const float time = fmaxf((head + tail) / p.num_ctas, (float)(tail_units * tiles) * p.stream_us);
+    const float stream = (float)(tail_units * tiles) * p.stream_us;
+    const float time = fmaxf((head + tail) / p.num_ctas, stream);
     const int most = T > 0 ? p.num_ctas - 1 : p.num_ctas;
     const int want = cost > 0 ? max((int)fminf(ceilf(head / time), (float)most), 1) : 0;
-    const int budget = max(want > 0 ? (cost + want - 1) / want : 0,
-                           start + kPairCost * max(p.floor, 1));
+    int budget = max(want > 0 ? (cost + want - 1) / want : 0,
+                     start + kPairCost * max(p.floor, 1));
     __syncthreads();  // the sums are complete
+    const int last_nb = units > 0 ? row_tiles(s_last) : 0;
+    int last_w = last_nb & 1 ? kAloneCost : kPairCost;
+    if (busy && s_first == s_last && (last_nb == 1 || !(last_nb & 1))) {
+        // Units alike (one group's, all of pairs or all alone): the same number of CTAs for
+        // each, and bins that end with the units, so that no CTA has parts of two: a second
+        // descriptor costs as much as `start`, and the slowest CTA is waited for.
+        const int pages_cost = last_w * g_np[s_last];
+        float best = time + p.head_start * p.head_us;
+        for (int k = max(want / units, 1), i = 0; i < 2; ++i, ++k) {
+            const int ctas = units * k, b = (pages_cost + k - 1) / k;
+            if (ctas > most || b < k + kPairCost * max(p.floor, 1)) break;
+            const float t = fmaxf((b + p.head_start) * p.head_us,
+                                  fmaxf(T > 0 ? tail / (p.num_ctas - ctas) : 0.f, stream));
+            if (t < best) {
+                best = t;
+                budget = b;
+                start = k * b - pages_cost;  // (below k: what fills the unit's last bin)
+            }
+        }
+        cost = pages + units * start;
+    }
     // up to the bin in which the last page begins
-    const int np_ctas =
-        units > 0 ? (cost - (row_tiles(s_last) & 1 ? kAloneCost : kPairCost)) / budget + 1 : 0;
+    const int np_ctas = units > 0 ? (cost - last_w) / budget + 1 : 0;
     const int tail_ctas = max(p.num_ctas - np_ctas, 1);
     const int tail_budget = max((T + tail_ctas - 1) / tail_ctas, tail_start + max(p.floor, 1));
 
@@ -419,14 +442,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinCtas)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float wsum = 0.f, w32 = 0.f;  // w32: the weights of 32 partials, one per lane
+    float wsum = 0.f, ws = 0.f;  // ws: the weights of kRound partials, one per lane
+    constexpr int kRound = 32 / kJoinAhead * kJoinAhead;
+    int in = kRound;  // the round's partials before k
 #pragma unroll 1
-    for (int k = 0; k < n; k += kJoinAhead) {
-        if ((k & 31) == 0)
-            w32 = k + lane < n ? ex2(((k == 0 ? own : lse(k + lane)) - m) * kJoinLog2e) : 0.f;
+    for (int k = 0; k < n; k += kJoinAhead, in += kJoinAhead) {
+        if (in == kRound) {
+            in = 0;
+            ws = k + lane < n ? ex2(((k == 0 ? own : lse(k + lane)) - m) * kJoinLog2e) : 0.f;
+        }
 #pragma unroll
         for (int j = 0; j < kJoinAhead; ++j) {
-            const float w = __shfl_sync(kFull, w32, (k + j) & 31);
+            const float w = __shfl_sync(kFull, ws, in + j);
             if (k + j >= n || !(w > 0.f)) continue;  // (no values where no weight is)
             wsum += w;
             acc.x += w * x[j].x;
