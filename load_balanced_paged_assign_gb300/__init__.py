@@ -8,7 +8,8 @@ partials, and the combine kernel merges them into BF16 output.  Beside the
 decode path: extend / prefill attention on tcgen05 tensor cores and the
 router GEMM with a BF16 hi/lo split of FP32 weights; an 8-bit cache with a
 scale for each 16 tokens and head (written, read back, attended over) and
-attention with a sliding window and sinks.  This package
+attention with a sliding window and sinks; decode over shared prefixes, and
+the pages of a cache as a pool (extended, forked, freed, compacted).  This package
 holds the build step, the ctypes binding and the seeded workload generators.
 """
 
