@@ -520,14 +520,15 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
             if (!ok) break;
             kt += it.hi - it.lo;
             const size_t at = (size_t)(it.slot + x) * kHeadRows + rho;
-            if (valid) a.part_lse[at] = l > 0.f ? (m_ref - kUp + lg2(l)) * kLn2 : -INFINITY;
+            // (l is NaN where a score is: so is the sum's logarithm, and the row)
+            if (valid) a.part_lse[at] = l == 0.f ? -INFINITY : (m_ref - kUp + lg2(l)) * kLn2;
             if (pg.n == 0) continue;  // (a partial of no weight: its values are not read)
             if (!mbar_wait_warp(&o_done[2 * x + ((ns - 1) & 1u)], ((ns - 1) >> 1) & 1u, abort)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const float inv = l > 0.f ? (KV == HPC_KV_FP8_E4M3 ? a.v_scale : 1.f) / l : 0.f;
+            const float inv = l == 0.f ? 0.f : (KV == HPC_KV_FP8_E4M3 ? a.v_scale : 1.f) / l;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 float o[64];

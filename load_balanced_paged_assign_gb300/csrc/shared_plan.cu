@@ -19,7 +19,12 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 
 // The head's cost of a page: against a pair of row tiles, and against one that is alone.
-// Measured 0.80 and 0.50 us.
+// Long prefixes alone on the GPU take 0.73 to 0.82 us a page and 0.73 (BF16, whose lone tiles
+// wait for HBM), 0.72 and 0.55 (E4M3), 0.87 and 0.61 (block scales); beside tails a lone
+// tile's pages cost less.  Steps with 5, 6 and 7: 12 requests of 64 heads on 8 behind 8K
+// tokens, E4M3, 24.5, 27.1 and 27.2 us; 37 in five groups 26.2, 27.0 and 27.5; 48 in six,
+// block scales, 36.7, 37.3 and 37.9; 40 behind 12.5K tokens (a pair and a lone tile), BF16,
+// 48.2, 45.2 and 46.5.
 constexpr int kPairCost = 8, kAloneCost = 5;
 
 // Costs are positions on a line that bins of one budget cut: a unit of n pages of cost w
@@ -387,7 +392,8 @@ struct JoinArgs {
 };
 
 // One warp per query row, lane i dims 4 i .. 4 i + 3: out = sum_c w_c o_c / sum_c w_c with
-// w_c = exp(lse_c - max), over the row's partials of the tail and of the head.
+// w_c = exp(lse_c - max), over the row's partials of the tail and of the head.  A partial
+// that is NaN, or whose lse is, makes the row NaN.
 __global__ void __launch_bounds__(32 * kJoinWarps, kJoinCtas)
     shared_join_kernel(const JoinArgs a, __nv_bfloat16 *__restrict__ out) {
     const int lane = threadIdx.x & 31;
@@ -449,12 +455,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinCtas)
     for (int k = 0; k < n; k += kJoinAhead, in += kJoinAhead) {
         if (in == kRound) {
             in = 0;
-            ws = k + lane < n ? ex2(((k == 0 ? own : lse(k + lane)) - m) * kJoinLog2e) : 0.f;
+            const float l = k == 0 ? own : k + lane < n ? lse(k + lane) : -INFINITY;
+            ws = l == -INFINITY ? 0.f : ex2((l - m) * kJoinLog2e);
         }
 #pragma unroll
         for (int j = 0; j < kJoinAhead; ++j) {
             const float w = __shfl_sync(kFull, ws, in + j);
-            if (k + j >= n || !(w > 0.f)) continue;  // (no values where no weight is)
+            // (a head's partial of no weight may have no values, a tail's always has)
+            if (k + j >= n || (w == 0.f && k + j >= n_tail)) continue;
             wsum += w;
             acc.x += w * x[j].x;
             acc.y += w * x[j].y;
@@ -463,7 +471,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinCtas)
         }
         load(k + kJoinAhead);
     }
-    const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
     uint2 packed;
     packed.x = pack_bf16x2(acc.x * inv, acc.y * inv);
     packed.y = pack_bf16x2(acc.z * inv, acc.w * inv);

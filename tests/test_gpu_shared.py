@@ -266,3 +266,65 @@ def test_results_repeat_bit_for_bit():
         for _ in range(3):
             again, _ = c.step(ws=ws)
             assert torch.equal(first, again)
+
+
+@pytest.mark.parametrize("kv", KINDS)
+def test_not_a_number_reaches_the_rows_that_see_it_and_no_others(kv):
+    """NaN in a key of a shared page: all that the group's sharing rows get of that KV head is
+    NaN, whatever the other partials are; all other rows keep their bits."""
+    lens = wide(20, 40, 1, 11) + wide(9, 3, 1, 12) + [200]
+    c = Shared(kv, lens, [0, 20, 29], [40, 3], 16, 2, 1, seed=17).to_gpu()
+    clean, ws = c.step()
+    page = c.table[0, 17]
+    if kv == "bf16":
+        c.k[page, 5, 1, 7] = float("nan")
+    else:
+        c.k.view(torch.uint8)[page, 5, 1, 7] = 0x7F
+    got, _ = c.step(ws=ws)
+    hit = torch.zeros(len(lens), 1, 16, dtype=torch.bool)
+    for r, (g, _) in c.lead.items():
+        hit[r, :, 8:] |= g == 0
+    nan = got.isnan().cpu()
+    assert torch.equal(nan.all(-1), hit) and torch.equal(nan.any(-1), hit)
+    assert torch.equal(got.cpu()[~hit], clean.cpu()[~hit])
+
+
+def test_the_largest_batch():
+    """8192 requests in 4096 groups of two; a batch smaller than its workspace; as many
+    CTAs as a plan may have, many more than the GPU has SMs."""
+    B = 8192
+    lens = [64 + (7 * r) % 90 for r in range(B)]
+    c = Shared("bf16", lens, list(range(0, B + 1, 2)), [1] * (B // 2), 1, 1, 1, seed=18).to_gpu()
+    got, ws = c.step()
+    c.check_plan(ws)
+    c.check(got)
+    small = Shared("bf16", wide(20, 3, 1, 13), [0, 20], [3], 1, 1, 1, seed=19).to_gpu()
+    small.n = 1
+    got, _ = small.step(ws=ws)
+    small.check_plan(ws)
+    small.check(got)
+    for kv in KINDS:
+        many = Shared(kv, wide(30, 50, 1, 14), [0, 30], [50], 8, 2, 1, seed=20).to_gpu()
+        for ctas in (500, 65536):
+            got, ws = many.step(ctas=ctas, floor=1)
+            many.check_plan(ws)
+            many.check(got)
+
+
+def test_two_streams_at_once():
+    """Steps on two streams, each with a workspace of its own."""
+    cases = [Shared(kv, wide(24, 30, 1, 15 + i), [0, 24], [30], 16, 2, 1, seed=21 + i).to_gpu()
+             for i, kv in enumerate(("bf16", "e4m3"))]
+    for c in cases:
+        c.ws, c.o, c.dev = c.workspace(), [c.out() for _ in range(20)], c.groups()
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for c, s in zip(cases, streams):
+            hd.hpc_decode_step_shared(c.q, c.qs, c.k, c.v, c.ks, c.vs, None, c.bt, c.sl, *c.dev, 16, 2,
+                                      1, c.sm, 2, c.ws, c.o[i], stream=s)
+    torch.cuda.synchronize()
+    for c in cases:
+        assert c.ws.flags == 0
+        c.check(c.o[0])
+        assert all(torch.equal(o, c.o[0]) for o in c.o)
