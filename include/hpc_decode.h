@@ -909,7 +909,10 @@ typedef struct {
  * back by a call the first one listed comes to lie on top (a fork or an extension
  * of the same rows gets the same pages).  A row that is named twice gives its
  * pages back once (with two different d_keep, those behind the smaller); which
- * of its places counts for the order is left open.
+ * of its places counts for the order is left open.  Where d_keep ends inside a page
+ * that other entries name too, the row keeps a share of it: what is then appended
+ * there is seen by all of them.  To go back to such a token and write, fork the row's
+ * first d_keep[i] tokens (hpc_kv_fork copies that page) and free the row.
  */
 hpc_status hpc_kv_free(const hpc_page_pool *pool, int32_t *d_block_table, int32_t B,
                        int32_t max_pages_per_req, const int32_t *d_rows, const int32_t *d_keep,

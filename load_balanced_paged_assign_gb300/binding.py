@@ -932,7 +932,8 @@ def _cap(fn, shape):
 
 
 def hpc_kv_free(pool: PagePool, block_table, rows=None, keep=None, stream=None):
-    """The rows (None: all) give back the pages behind their first keep[i] tokens (None: all)."""
+    """The rows (None: all) give back the pages behind their first keep[i] tokens (None: all).
+    A shared page that keep ends inside stays shared: to write there, fork and free the row."""
     fn, dev = "hpc_kv_free", _current_device()
     adr, shape, count = _arrays(fn, dev, "block_table rows keep", _I32S[3], block_table, rows, keep)
     B, cols = _pool_table(fn, dev, pool, shape[0])
@@ -1007,11 +1008,11 @@ def hpc_kv_copy_pages(copies, k_cache, v_cache, kv_scale=None, flags=None, strea
     """The copies that hpc_kv_fork or hpc_kv_compact listed, in one layer's caches (and the
     block scales [num_pages, Hkv, 2, 4] of a block-scaled one)."""
     fn, dev = "hpc_kv_copy_pages", _current_device()
-    e4m3 = k_cache.dtype is _E4M3
+    e4m3 = k_cache is not None and k_cache.dtype is _E4M3
     adr, shape, _ = _arrays(fn, dev, "copies k_cache v_cache kv_scale flags", _PAGE_TYPES[e4m3],
                             copies, k_cache, v_cache, kv_scale, flags)
     cache = shape[1]
-    if copies is None or len(cache) != 4:
+    if copies is None or cache is None or len(cache) != 4:
         raise ValueError(f"{fn}: copies, or a cache [num_pages, 64, Hkv, 128]")
     pages, Hkv = cache[0], cache[2]
     if cache[1] != PAGE_SIZE or cache[3] != HEAD_DIM:

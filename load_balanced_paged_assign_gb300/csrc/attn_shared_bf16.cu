@@ -4,23 +4,16 @@
 namespace hpc {
 namespace {
 
-#ifndef HPC_SHARED_STAGES
-#define HPC_SHARED_STAGES 4
-#endif
-#ifndef HPC_SHARED_TPS
-#define HPC_SHARED_TPS 1
-#endif
-#ifndef HPC_SHARED_STAGES_MQ
-#define HPC_SHARED_STAGES_MQ 4
-#endif
+// The decode kernel with rings of four stages of one tile, for one and for two blocks of
+// query rows (five stages: the same times; two of two tiles: the same or slower).
 template <int NB>
 struct Tail {
-    static constexpr int kStages = NB == 1 ? HPC_SHARED_STAGES : HPC_SHARED_STAGES_MQ;
-    using Tr = AttnTraits<false, kStages, HPC_SHARED_TPS, NB>;
+    static constexpr int kStages = 4, kTps = 1;
+    using Tr = AttnTraits<false, kStages, kTps, NB>;
     static constexpr int kThreads = Tr::kThreads, kSmemBytes = Tr::kSmemBytes;
     static __device__ __forceinline__ void run(const CUtensorMap &tk, const CUtensorMap &tv,
                                                const AttnParams &t) {
-        attn_cta<false, kStages, HPC_SHARED_TPS, NB>(tk, tv, t);
+        attn_cta<false, kStages, kTps, NB>(tk, tv, t);
     }
 };
 

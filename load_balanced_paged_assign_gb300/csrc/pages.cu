@@ -36,9 +36,11 @@ namespace {
 constexpr int kPoolThreads = 1024;
 constexpr int kPoolWarps = kPoolThreads / 32;
 constexpr int kPoolCtas = 16;  // of a cluster, at most
-// List entries of a thread in a round: one where the cluster then holds the list (code that
-// runs once is fetched once: 3.6 us a call, 6.0 with eight unrolled), else eight (15 us a
-// call over 102,400 entries, 30 with two).
+// List entries of a thread in a round: one where the cluster then holds the list, else eight.
+// Code that runs once is fetched once: two calls over 4 rows 6.3 us with one entry, 12.0
+// with eight; over 102,400 entries 60 us with two, 30 with eight.  And no more CTAs than
+// hold the list: two calls over 4 rows 11.9 us on 16, 6.9 on one; over 102,400 entries 30 us
+// on 16, 58 on eight, 265 on one.
 constexpr int kFew = 1, kMany = 8;
 constexpr int kUnroll = 2;  // of the other loops
 constexpr int kForkPages = 128;  // of a child, for one warp at a time

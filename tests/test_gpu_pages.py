@@ -267,3 +267,27 @@ def test_captured_on_a_stream_of_its_own():
     want = op.fork(b.want, [1, 0, 0], [7, 3, 9], [130, 0, 449])
     graph.replay()
     b.check(copies=want)
+
+
+def test_lists_of_several_rounds():
+    """More list entries than a cluster holds at once (131,072)."""
+    play(Both(600, 501, 60000), random.Random(11), 8)
+
+
+def test_a_rollback_into_a_shared_page_by_a_fork():
+    """A child that goes back to a token inside a page that others hold: a fork of its
+    first tokens gets a copy to write to, and the row itself then goes."""
+    both = Both(3, 4, 20)
+    hd.hpc_kv_extend(both.pool, both.table, ints([0]), ints([256]))
+    op.extend(both.want, [0], [256])
+    hd.hpc_kv_fork(both.pool, both.table, ints([0]), ints([1]), ints([256]), both.copies)
+    both.check(copies=op.fork(both.want, [0], [1], [256]))
+    hd.hpc_kv_fork(both.pool, both.table, ints([1]), ints([2]), ints([200]), both.copies)
+    copies = op.fork(both.want, [1], [2], [200])
+    both.check(copies=copies)
+    assert copies == [(both.want["table"][0][3], both.want["table"][2][3])]
+    hd.hpc_kv_free(both.pool, both.table, ints([1]))
+    op.free(both.want, [1], [0])
+    both.check()
+    assert both.table[2, :3].tolist() == both.table[0, :3].tolist()
+    assert both.table[2, 3] != both.table[0, 3]
