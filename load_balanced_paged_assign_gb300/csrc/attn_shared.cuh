@@ -17,10 +17,13 @@
 // other page of it, and leave a partial each.
 //
 // 8-bit pages: scores on E4M3 MMAs from the codes as they land; V is widened by warps
-// of its own into a second ring, to f16 where one scale holds for the cache (weights as
-// f16, times 2^6 so that the smallest keep their bits: at most 2^14), to BF16 where the
-// blocks' scales multiply the weights (their range is BF16's).  All E4M3 values are
-// exact in either.
+// of its own into a second ring, to f16, in which all E4M3 values are exact.  Weights are
+// f16 (rounded to 2^-11), times 2^6 so that the smallest keep their bits: at most 2^14.
+// Block scales of V multiply the weights, and the reference follows score + log2(scale),
+// as the decode kernel's does (attn_tc.cuh), so that this bound holds whatever the scales
+// and a sum of products stays below 2^23 a token.  (Weights in BF16, whose range holds the
+// scales, with a reference that follows the scores alone: sums over 2400 tokens of scale
+// 2^100 pass 2^128, and the error of a step is 0.0018 to 0.0021 of its norm, not 0.0017.)
 //
 // Every wait is bounded; on a timeout the CTA raises the flag, waits (bounded) for its
 // copies and MMAs in flight, frees TMEM and leaves.
@@ -279,9 +282,9 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
         const int x = warp - kHeadMma;  // the half
         constexpr uint32_t id_s = Tr::k8 ? idesc_e4m3_f32(kHeadRows, kTile, false, false)
                                          : idesc_bf16_f32(kHeadRows, kTile);
-        // (E4M3: f16 weights and values, the type bits of both zero)
+        // (8-bit pages: f16 weights and values, the type bits of both zero)
         constexpr uint32_t id_o = idesc_bf16_f32_bmn(kHeadRows, kHeadDim) &
-                                  (KV == HPC_KV_FP8_E4M3 ? ~((1u << 7) | (1u << 10)) : ~0u);
+                                  (Tr::k8 ? ~((1u << 7) | (1u << 10)) : ~0u);
         const uint64_t dq0 = smem_desc_k128(smem_u32(smem + Tr::kOffQ));
         const uint64_t dk0 = smem_desc_k128(smem_u32(smem + Tr::kOffK));
         const uint64_t dv0 = smem_desc_mn128(smem_u32(smem + Tr::kOffV), kTile * 128);
@@ -380,13 +383,6 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
                     e4m3x4_to_f16x2x2(v.y, o[2], o[3]);
                     e4m3x4_to_f16x2x2(v.z, o[4], o[5]);
                     e4m3x4_to_f16x2x2(v.w, o[6], o[7]);
-                    if (Tr::kBlk) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float2 f = f16x2_to_f32x2(o[i]);
-                            o[i] = pack_bf16x2(f.x, f.y);
-                        }
-                    }
                     const uint32_t to = dst + (c >> 2) * (kTile * 128) + row * 128;
                     const int g = 2 * (c & 3);
                     sts128(to + ((g ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
@@ -409,8 +405,12 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
         const uint32_t row = tmem + ((uint32_t)(32 * q4) << 16);
         const uint32_t scol = row + 128 * x, ocol = row + kHeadOCol + 128 * x;
         const int tok_in = rho / a.G, g = rho - tok_in * a.G;
-        // E4M3: weights times 2^6 (see above)
-        constexpr float kUp = KV == HPC_KV_FP8_E4M3 ? 6.f : 0.f;
+        // 8-bit pages: weights times 2^6 (see above)
+        constexpr float kUp = Tr::k8 ? 6.f : 0.f;
+        // Block scales: a term of the weights' sum is up to 2^88 times its weight (of a V
+        // scale that counts as 2^-88 in the reference), so the sum is kept times 2^-8: below
+        // 2^124 for the 2^30 tokens that a request may have.
+        constexpr float kUnit = Tr::kBlk ? kSumUnit : 1.f;
         uint32_t ns = 0;  // score pages taken
         uint32_t kt = 0;
         for (int d = first; ok && d < last; ++d) {
@@ -445,6 +445,15 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
                     s[32 + i] = __uint_as_float(rb[i]);
                 }
                 float f = sc;
+                float lv[kPageScales / 2], vf[kPageScales / 2];  // V's scales, and their logarithms
+                if (Tr::kBlk) {
+#pragma unroll
+                    for (int i = 0; i < kPageScales / 2; ++i) {
+                        const float v = scales[kPageScales / 2 + i];
+                        lv[i] = lg2(fmaxf(v, kMinVRef));
+                        vf[i] = v < kMinVScale ? 0.f : v;
+                    }
+                }
                 if (Tr::kBlk || turned) {
 #pragma unroll
                     for (int i = 0; i < kTile; ++i)
@@ -453,12 +462,21 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
                 }
                 float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int i = 0; i < kTile / 2; ++i)
-                    mx4[i & 3] = head_max3(mx4[i & 3], s[2 * i], s[2 * i + 1]);
+                for (int i = 0; i < kTile / 2; ++i) {
+                    const int to = Tr::kBlk ? 2 * i / kScaleBlock : i & 3;
+                    mx4[to] = head_max3(mx4[to], s[2 * i], s[2 * i + 1]);
+                }
+                if (Tr::kBlk) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mx4[i] += lv[i];
+                }
                 const float m_tile = head_max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]) * f;
                 const bool need = m_tile > m_ref + kHeadLazy;
                 const float new_ref = need ? m_tile : m_ref;
-                const float factor = need ? ex2(m_ref - new_ref) : 1.f;
+                // (in two steps: with block scales the reference may move by more than the
+                // 126 that one holds, and the sum has terms that much larger than O's)
+                const float step = need ? ex2((m_ref - new_ref) * (Tr::kBlk ? 0.5f : 1.f)) : 1.f;
+                const float factor = Tr::kBlk ? step * step : step;
                 const float base = (new_ref == -INFINITY ? 0.f : new_ref) - kUp;
                 uint32_t pk[32];  // P as packed pairs, over the first half of the scores
                 const float2 f2 = make_float2(f, f), nb2 = make_float2(-base, -base);
@@ -468,12 +486,13 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
                 for (int i = 0; i < 32; ++i) {
                     const float2 e = __ffma2_rn(make_float2(s[2 * i], s[2 * i + 1]), f2, nb2);
                     const float w0 = ex2(e.x), w1 = ex2(e.y);
-                    if (KV == HPC_KV_FP8_E4M3) {
+                    if (Tr::kBlk) {
+                        const float v = vf[2 * i / kScaleBlock];
+                        pk[i] = pack_f16x2(w0 * v, w1 * v);
+                        ps2[i & 3] = __ffma2_rn(make_float2(w0, w1), make_float2(kUnit, kUnit),
+                                                ps2[i & 3]);
+                    } else if (Tr::k8) {
                         pk[i] = pack_f16x2(w0, w1);
-                        ps2[i & 3] = __fadd2_rn(ps2[i & 3], make_float2(w0, w1));
-                    } else if (Tr::kBlk) {
-                        const float vs = scales[kTile / kScaleBlock + 2 * i / kScaleBlock];
-                        pk[i] = pack_bf16x2(w0 * vs, w1 * vs);
                         ps2[i & 3] = __fadd2_rn(ps2[i & 3], make_float2(w0, w1));
                     } else {
                         pk[i] = pack_bf16x2(w0, w1);
@@ -482,7 +501,7 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
                 tmem_st32_nowait(scol + 64 * b, pk);
                 // BF16: the sum takes the weights as they were rounded: the heaviest one's
                 // rounding then cancels against its own in the product.  (f16 weights are
-                // rounded to 2^-11, and block scales are rounded with theirs.)
+                // rounded to 2^-11.)
                 if (KV == HPC_KV_BF16) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
@@ -490,7 +509,8 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
                         head_add_bf16(ps[2 * (i & 3) + 1], (uint16_t)(pk[i] >> 16));
                     }
                 }
-                l = l * factor + (((ps[0] + ps[1]) + (ps[2] + ps[3])) +
+                if (Tr::kBlk) l *= step;
+                l = l * step + (((ps[0] + ps[1]) + (ps[2] + ps[3])) +
                                   ((ps[4] + ps[5]) + (ps[6] + ps[7])));
                 if (c > 0 && __any_sync(kFullMask, need)) {
                     // O_x is settled once its last product is done (the product two
@@ -521,14 +541,15 @@ __device__ __forceinline__ void head_cta(const SharedMaps &m, const HeadArgs &a,
             kt += it.hi - it.lo;
             const size_t at = (size_t)(it.slot + x) * kHeadRows + rho;
             // (l is NaN where a score is: so is the sum's logarithm, and the row)
-            if (valid) a.part_lse[at] = l == 0.f ? -INFINITY : (m_ref - kUp + lg2(l)) * kLn2;
+            constexpr float kLow = kUp + (Tr::kBlk ? kSumLog2 : 0.f);
+            if (valid) a.part_lse[at] = l == 0.f ? -INFINITY : (m_ref - kLow + lg2(l)) * kLn2;
             if (pg.n == 0) continue;  // (a partial of no weight: its values are not read)
             if (!mbar_wait_warp(&o_done[2 * x + ((ns - 1) & 1u)], ((ns - 1) >> 1) & 1u, abort)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const float inv = l == 0.f ? 0.f : (KV == HPC_KV_FP8_E4M3 ? a.v_scale : 1.f) / l;
+            const float inv = l == 0.f ? 0.f : (KV == HPC_KV_FP8_E4M3 ? a.v_scale : kUnit) / l;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 float o[64];

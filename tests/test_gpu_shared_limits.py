@@ -1,0 +1,111 @@
+"""Decode attention over shared prefixes at the ends of its inputs' ranges: V scales, values
+that are not finite, bad table entries.  What can be is checked against the fp64 oracle."""
+
+import numpy as np
+import pytest
+import torch
+
+from _blocks import Case
+from _shared import Shared, check_shared
+from oracle import block_cache as bc
+
+pytestmark = pytest.mark.gpu
+
+E4M3 = torch.float8_e4m3fn
+
+
+def set_keys(c, value_of_page, other):
+    """Keys and queries of which only dim 0 is not zero: the score of a token is 8 times its
+    page's value (table entry t of the shared pages: value_of_page[t], the other pages: other),
+    times sm_scale."""
+    x = torch.full((c.k.shape[0],), float(other))
+    for t, v in enumerate(value_of_page):
+        x[int(c.table[0, t])] = v
+    k = torch.zeros(c.k.shape, dtype=torch.float32)
+    k[..., 0] = x[:, None, None]
+    q = torch.zeros(c.q.shape, dtype=torch.float32)
+    q[..., 0] = 8.0
+    if c.kv == "bf16":
+        c.k, c.q = k.bfloat16(), q.bfloat16()
+        c.kf, c.qf = c.k.double().numpy(), c.q.double().numpy()
+        return
+    c.k, c.q, c.ks = k.to(E4M3), q.to(E4M3), 1.0
+    c.qs = torch.ones(c.qs.shape)
+    c.kf, c.qf = c.k.float().double().numpy(), c.q.float().double().numpy()
+    if c.scale is not None:
+        c.scale[:, :, 0] = 1.0
+
+
+def set_v_scales(c, scales):
+    """V scales [pages, Hkv, 4] of a block-scaled cache; below 2^-100 they count as zero."""
+    c.scale[:, :, 1] = scales
+    counted = c.scale.numpy().copy()
+    v = counted[:, :, 1]
+    v[v < 2.0 ** -100] = 0.0
+    c.vf = bc.values(c.v.view(torch.uint8).numpy(), counted, 1)
+
+
+def check_scaled(c, got, log2):
+    """check_shared of the output and the reference times 2^log2 (exact): small values count."""
+    ref, mass = c.reference()
+    f = 2.0 ** log2
+    check_shared(got.double() * f, ref * f, mass * f, c.kv)
+
+
+@pytest.mark.parametrize("B", [9, 20])
+@pytest.mark.parametrize("log2", [100, -100])
+def test_v_scales_at_both_ends_of_their_range(B, log2):
+    """Scales of 2^100 and 2^-100, codes of 448 in half of the dims: over the 150 pages of one
+    descriptor (or 75 of a half) their sums with weights of up to 2^8 pass 2^128.  The first
+    page's scores stand 8 (log2) below the others: the softmax's reference is the first page's,
+    or was when it was used."""
+    lens = [64 * 150 + 1 + 5 * r for r in range(B)]
+    c = Shared("block", lens, [0, B], [150], 8, 1, 1, seed=30 + B, poison=False)
+    set_keys(c, [0.0] + [7.9 / 8 / 1.4426950408889634 * 128 ** 0.5] * 149, 7.5)
+    step = float(c.k[int(c.table[0, 1]), 0, 0, 0].float())  # (as E4M3 holds it)
+    assert 7.0 < 8 * step * c.sm * 1.4426950408889634 < 8.0
+    c.v.view(torch.uint8)[..., ::2] = 0x7E  # 448
+    set_v_scales(c, 2.0 ** log2)
+    c.to_gpu()
+    for ctas in (2, 0):
+        got, _ = c.step(ctas=ctas)
+        check_scaled(c, got, -log2)
+
+
+def test_a_v_scale_below_its_range_counts_as_zero():
+    """In the shared pages as in a request's own."""
+    lens = [64 * 40 + 70 * r for r in range(12)]
+    c = Shared("block", lens, [0, 12], [40], 8, 2, 1, seed=40, poison=False)
+    set_v_scales(c, 2.0 ** -101)
+    c.to_gpu()
+    got, _ = c.step()
+    assert not torch.count_nonzero(got)
+    # where only some do, the others' values are as large as ever, the weights' sum too
+    rng = np.random.default_rng(1)
+    scales = torch.from_numpy(np.where(rng.random((c.k.shape[0], 2, 4)) < 0.5, 2.0 ** -101, 0.25))
+    c.scale = c.scale.cpu()
+    c.v = c.v.cpu()
+    set_v_scales(c, scales.float())
+    c.to_gpu()
+    got, _ = c.step()
+    c.check(got)
+
+
+@pytest.mark.parametrize("heads", [(8, 1, 1), (16, 2, 1), (12, 2, 2), (64, 8, 1)])
+def test_the_error_over_block_scales_is_that_of_the_unshared_step(heads):
+    """In the Euclidean norm.  Both round their output to BF16 (2^-8 at most, 2^-8 / sqrt 3 of a
+    value's step in the mean); the unshared step's weights are off by up to 2^-9 + 2^-11, the
+    heads' by 2^-11 (f16), so the shared step's error is not larger but for chance: over at least
+    20,000 outputs 1 / sqrt(2 n) = 0.5%; four times that is allowed."""
+    hq, hkv, n = heads
+    rng = np.random.default_rng(3)
+    lens = [64 * 30 + n + int(t) for t in rng.integers(0, 300, 24)]
+    c = Shared("block", lens, [0, 24], [30], hq, hkv, n, seed=41).to_gpu()
+    ref, _ = c.reference()
+
+    def error(got):
+        return np.linalg.norm(got.double().cpu().numpy().reshape(ref.shape) - ref)
+
+    assert ref.size >= 20000
+    shared, unshared = error(c.step()[0]), error(Case.step(c, ws=Case.workspace(c))[0])
+    assert shared <= 1.02 * unshared, (shared / np.linalg.norm(ref), unshared / np.linalg.norm(ref))
