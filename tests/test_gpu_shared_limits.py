@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from _blocks import Case
+from _blocks import Case, check_attention
 from _shared import Shared, check_shared
 from oracle import block_cache as bc
 
@@ -109,3 +109,27 @@ def test_the_error_over_block_scales_is_that_of_the_unshared_step(heads):
     assert ref.size >= 20000
     shared, unshared = error(c.step()[0]), error(Case.step(c, ws=Case.workspace(c))[0])
     assert shared <= 1.02 * unshared, (shared / np.linalg.norm(ref), unshared / np.linalg.norm(ref))
+
+
+@pytest.mark.parametrize("heads", [(8, 1, 1), (16, 1, 1), (16, 2, 1), (24, 2, 1)])
+@pytest.mark.parametrize("down", [False, True])
+def test_v_scales_that_change_by_more_than_a_float_holds(heads, down):
+    """Pages of V scale 2^-90 and pages of 2^90 behind one another (either way round), all
+    scores alike: the first kind is in the sum of the weights, so the result is the second
+    kind's mean times its share."""
+    hq, hkv, n = heads
+    lens = [64 * 44 + 3 * r for r in range(10)]
+    c = Shared("block", lens, [0, 10], [40], hq, hkv, n, seed=42, poison=False)
+    c.k = torch.zeros(c.k.shape).to(E4M3)
+    c.kf = np.zeros(c.kf.shape)
+    low = torch.zeros(c.k.shape[0], dtype=torch.bool)
+    for row in c.table:  # of each request's entries the first 20, or those behind
+        low[[int(p) for p in (row[20:] if down else row[:20]) if p >= 0]] = True
+    set_v_scales(c, torch.where(low, 2.0 ** -90, 2.0 ** 90)[:, None, None])
+    c.to_gpu()
+    for ctas in (2, 0):
+        got, _ = c.step(ctas=ctas)  # over shared pages
+        check_scaled(c, got, -90)
+        got, _ = Case.step(c, ws=Case.workspace(c, ctas))  # each request by itself
+        ref, mass = c.reference()
+        check_attention(got.double() * 2.0 ** -90, ref * 2.0 ** -90, mass * 2.0 ** -90, "block")
