@@ -448,7 +448,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinCtas)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float wsum = 0.f, ws = 0.f;  // ws: the weights of kRound partials, one per lane
+    // ws: the weights of kRound partials, one per lane; -1: no values are there (a head's
+    // partial that saw no page, whose lse says so).  A weight that is zero because the lse lies
+    // far below the others' counts: NaN times zero is NaN.
+    float wsum = 0.f, ws = -1.f;
     constexpr int kRound = 32 / kJoinAhead * kJoinAhead;
     int in = kRound;  // the round's partials before k
 #pragma unroll 1
@@ -456,13 +459,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kJoinCtas)
         if (in == kRound) {
             in = 0;
             const float l = k == 0 ? own : k + lane < n ? lse(k + lane) : -INFINITY;
-            ws = l == -INFINITY ? 0.f : ex2((l - m) * kJoinLog2e);
+            ws = l != -INFINITY ? ex2((l - m) * kJoinLog2e) : k + lane < n_tail ? 0.f : -1.f;
         }
 #pragma unroll
         for (int j = 0; j < kJoinAhead; ++j) {
             const float w = __shfl_sync(kFull, ws, in + j);
-            // (a head's partial of no weight may have no values, a tail's always has)
-            if (k + j >= n || (w == 0.f && k + j >= n_tail)) continue;
+            if (k + j >= n || w < 0.f) continue;
             wsum += w;
             acc.x += w * x[j].x;
             acc.y += w * x[j].y;

@@ -11,6 +11,7 @@ from oracle import block_cache as bc
 
 pytestmark = pytest.mark.gpu
 
+KINDS = ["bf16", "e4m3", "block"]
 E4M3 = torch.float8_e4m3fn
 
 
@@ -133,3 +134,28 @@ def test_v_scales_that_change_by_more_than_a_float_holds(heads, down):
         got, _ = Case.step(c, ws=Case.workspace(c, ctas))  # each request by itself
         ref, mass = c.reference()
         check_attention(got.double() * 2.0 ** -90, ref * 2.0 ** -90, mass * 2.0 ** -90, "block")
+
+
+@pytest.mark.parametrize("kv", KINDS)
+@pytest.mark.parametrize("B", [9, 20])
+def test_not_a_number_in_a_value_that_weighs_nothing(kv, B):
+    """NaN in V of a shared page whose scores lie so far below the tails' that the heads'
+    partials weigh 2^-200: times zero it is NaN still, in that dim of the rows that see it.
+    The other dims are what they are."""
+    lens = [64 * 3 + 1 + 11 * r for r in range(B)] + [150]
+    c = Shared(kv, lens, [0, B], [3], 16, 2, 1, seed=50 + B, poison=False)
+    set_keys(c, [0.0] * 3, 208.0)
+    assert 8 * 208 * c.sm * 1.44 > 200
+    c.to_gpu()
+    clean, ws = c.step()
+    c.check(clean)
+    page = c.table[0, 2]
+    if kv == "bf16":
+        c.v[page, 5, 1, 7] = float("nan")
+    else:
+        c.v.view(torch.uint8)[page, 5, 1, 7] = 0x7F
+    got, _ = c.step(ws=ws)
+    hit = torch.zeros(got.shape, dtype=torch.bool)
+    hit[:B, :, 8:, 7] = True
+    assert torch.equal(got.isnan().cpu(), hit)
+    assert torch.equal(got.cpu()[~hit], clean.cpu()[~hit])
