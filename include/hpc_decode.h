@@ -891,8 +891,9 @@ hpc_status hpc_decode_step_shared(const void *d_q, const float *d_q_scale, const
  * max_pages_per_req are below 2^30.  Results do not depend on timing: pages are
  * handed out and given back in the order of the call's list and, within a row, of
  * the entries.  Rows outside [0, B) and lengths outside [0, 64 *
- * max_pages_per_req] raise HPC_FLAG_BAD_SEQLEN and are passed over; pages outside
- * [0, num_pages) and pages that no entry holds raise HPC_FLAG_BAD_PAGE.
+ * max_pages_per_req] raise HPC_FLAG_BAD_SEQLEN and are passed over; where a call gives
+ * back, shares or moves an entry's page, a page outside [0, num_pages) or one that no
+ * entry holds raises HPC_FLAG_BAD_PAGE.
  * ---------------------------------------------------------------------- */
 typedef struct {
     int32_t *refs;
@@ -952,9 +953,10 @@ hpc_status hpc_kv_fork(const hpc_page_pool *pool, int32_t *d_block_table, int32_
  * (the stack holds the pages L .. num_pages - 1, L on top) and the moves to
  * d_copies as hpc_kv_fork does (cap_copies >= num_pages / 2); the caches of every
  * layer follow by hpc_kv_copy_pages before anything reads them through the new
- * table.  All entries of the table's B rows are rewritten; other tables on the
- * pool keep their old places.  d_block_table_out and pool_out may be d_block_table
- * and pool (all of its arrays) or memory of their own; the marks used are pool's.
+ * table.  All entries of the table's B rows are rewritten, and one that names no held
+ * page becomes -1 (HPC_FLAG_BAD_PAGE, in pool_out's state); other tables on the pool
+ * keep their old places.  d_block_table_out and pool_out may be d_block_table and pool
+ * (all of its arrays) or memory of their own; the marks used are pool's.
  */
 hpc_status hpc_kv_compact(const hpc_page_pool *pool, const int32_t *d_block_table, int32_t B,
                           int32_t max_pages_per_req, int32_t *d_copies, int32_t cap_copies,

@@ -45,6 +45,7 @@ constexpr int kFew = 1, kMany = 8;
 constexpr int kUnroll = 2;  // of the other loops
 constexpr int kForkPages = 128;  // of a child, for one warp at a time
 constexpr int kIdle = INT_MAX;        // marks[p] between calls
+constexpr int kUnheld = -1;           // marks[p] in a compaction, of a page that none holds
 // Numbers below -2^30 in the table are the calls' own, and gone when they end: the list's
 // place that claims an empty entry (the smaller wins).
 constexpr int kCodes = 1 << 30;
@@ -460,9 +461,10 @@ __global__ void __launch_bounds__(kPoolThreads) fork_kernel(const Pool pool, con
 
 // ------------------------------------------------------------------ compact
 // The live pages behind the first L places (L live ones in all) move, in order,
-// into the holes among those; marks[p] holds a moved page's new place meanwhile.  A
-// page's number and the live ones before it say both its ranks, so one sum over the
-// pages (and the live ones below L) places everything.
+// into the holes among those; marks[p] holds a moved page's new place meanwhile, and
+// kUnheld for a page that none holds: an entry that names one all the same becomes -1, as
+// the page will be another's.  A page's number and the live ones before it say both its
+// ranks, so one sum over the pages (and the live ones below L) places everything.
 __global__ void __launch_bounds__(kPoolThreads)
     compact_kernel(const Pool in, const Pool out, const int32_t *table, int32_t *table_out,
                    int64_t entries, int32_t *copies) {
@@ -504,6 +506,7 @@ __global__ void __launch_bounds__(kPoolThreads)
     const int moves = L - kept;
     over(hi, [&](int p, int refs, int before) {
         before += base;
+        if (refs <= 0) in.marks[p] = kUnheld;
         if (p < L && refs <= 0) copies[2 * (p - before + 1) + 1] = p;   // hole number p - before
         if (p >= L && refs > 0) copies[2 * (before - kept + 1)] = p;
     });
@@ -514,6 +517,7 @@ __global__ void __launch_bounds__(kPoolThreads)
         out.refs[dst] = __ldcg(in.refs + src);
     }
     sync_all();
+    unsigned flags = 0;
     for (int64_t e0 = first; e0 < entries; e0 += (int64_t)threads * kUnroll) {
         int p[kUnroll], m[kUnroll];
 #pragma unroll
@@ -521,11 +525,15 @@ __global__ void __launch_bounds__(kPoolThreads)
             p[k] = e0 + (int64_t)k * threads < entries ? __ldcg(table + e0 + (int64_t)k * threads) : -1;
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k)
-            m[k] = p[k] >= 0 && p[k] < in.num_pages ? __ldcg(in.marks + p[k]) : kIdle;
+            m[k] = p[k] < 0               ? kIdle
+                   : p[k] >= in.num_pages ? kUnheld
+                                          : __ldcg(in.marks + p[k]);
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k)
+        for (int k = 0; k < kUnroll; ++k) {
+            if (m[k] == kUnheld) flags |= HPC_FLAG_BAD_PAGE;
             if (e0 + (int64_t)k * threads < entries)
                 table_out[e0 + (int64_t)k * threads] = m[k] != kIdle ? m[k] : p[k];
+        }
     }
     for (int p = first; p < in.num_pages; p += threads) {
         if (p >= L) {
@@ -543,7 +551,9 @@ __global__ void __launch_bounds__(kPoolThreads)
         out.state[0] = in.num_pages - L;
     }
     sync_all();
-    for (int k = first; k < moves; k += threads) in.marks[__ldcg(copies + 2 * (k + 1))] = kIdle;
+    for (int p = first; p < in.num_pages; p += threads) in.marks[p] = kIdle;
+    flags = __reduce_or_sync(kAll, flags);
+    if (flags && lane == 0) atomicOr(out.state + 1, (int)flags);
 }
 
 // ------------------------------------------------------------------ copy
