@@ -226,8 +226,10 @@ cudaError_t launch_assign(const int32_t *seqlens, int B, int Hkv, int max_pages,
     if (smem > 48 * 1024) {
         const void *kernel = plain ? reinterpret_cast<const void *>(&assign_kernel)
                                    : reinterpret_cast<const void *>(&assign_window_kernel);
+        // (always the largest size: the attribute is the process's, and one that followed the
+        // calls could be lowered by another thread between here and the launch)
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             smem);
+                                             assign_smem_bytes(HPC_MAX_BATCH));
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};

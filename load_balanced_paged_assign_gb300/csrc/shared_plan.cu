@@ -499,10 +499,14 @@ cudaError_t launch_dependent(void (*kernel)(P...), int grid, int threads, size_t
 }  // namespace
 
 cudaError_t launch_shared_plan(const SharedPlan &p, cudaStream_t s) {
-    const size_t smem = (3 * (size_t)p.B + 7 * (size_t)p.groups + 1) * sizeof(int);
+    auto smem_bytes = [](size_t B, size_t groups) { return (3 * B + 7 * groups + 1) * sizeof(int); };
+    const size_t smem = smem_bytes(p.B, p.groups);
     if (smem > 48 * 1024) {
+        // always the largest size: the attribute is the process's, and one that followed the
+        // calls could be lowered by another thread between here and the launch
         const cudaError_t e = cudaFuncSetAttribute(
-            shared_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            shared_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            (int)smem_bytes(HPC_MAX_SHARED_BATCH, HPC_MAX_SHARED_GROUPS));
         if (e != cudaSuccess) return e;
     }
     const long long work = max((long long)p.B * (p.Hkv / p.heads), (long long)p.groups + 1);
