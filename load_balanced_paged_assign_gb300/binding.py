@@ -4,6 +4,12 @@ Every function here has the name of the C entry point it forwards to and does
 nothing but turn torch tensors into pointers and sizes, call the library and
 raise on a non-zero status.  All compute happens in libhpcdecode.so; there is
 no fallback path: if the library is missing, every call raises.
+
+A call is queued on `stream` (None: the current one) and runs behind what is queued
+there, not behind other streams: tensors that are filled on another stream, or whose
+memory the allocator took from work on another one, have to be waited for first, and
+all of a call's tensors have to live until it has run.  The workspaces, task maps and
+pools of this module are ready for any stream when their constructors return.
 """
 
 from __future__ import annotations
@@ -286,8 +292,18 @@ def _raw_stream(dev: int, stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _ready(dev: torch.device):
+    """Waits for the current stream, on which new tensors are filled, and by which alone the
+    allocator orders their memory's earlier use: then any stream may use them.  Part of a
+    graph while one is captured (they belong to that graph)."""
+    if dev.type == "cuda" and not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(dev).synchronize()
+
+
 class TaskMap:
-    """Caller-owned device buffers of one task map and the C struct describing them."""
+    """Caller-owned device buffers of one task map and the C struct describing them.  It is
+    ready for calls on any stream when it is made, as workspaces and pools are; like them it
+    has to outlive the work that uses it."""
 
     def __init__(self, B: int, Hkv: int, cap_desc: int, cap_bins: int, device="cuda"):
         dev = torch.device(device)
@@ -299,6 +315,7 @@ class TaskMap:
         self.meta = torch.zeros(8, dtype=torch.int32, device=dev)
         self.c = hpc_task_map(_ptr(self.desc), _ptr(self.bin_ptr), _ptr(self.chunk_count),
                               _ptr(self.chunk_off), _ptr(self.meta), cap_desc, cap_bins, units)
+        _ready(dev)
 
     @classmethod
     def dynamic(cls, B: int, Hkv: int, num_ctas: int, device="cuda"):
@@ -786,6 +803,7 @@ class SharedWorkspace:
         self.c = hpc_shared_map(self.tmap.c, _ptr(self.head), _ptr(self.head_o),
                                 _ptr(self.head_lse), ints, slots)
         self.tmap.c = self.c.tail  # the planner writes to this one
+        _ready(dev)
 
     @property
     def flags(self) -> int:
@@ -897,6 +915,7 @@ class PagePool:
         self.c = hpc_page_pool(_ptr(refs), _ptr(free_list), _ptr(state), _ptr(self.marks),
                                self.num_pages)
         self.ref, self.dev = ctypes.byref(self.c), refs.get_device()
+        _ready(refs.device)
 
     @property
     def free_pages(self) -> int:
@@ -1058,3 +1077,4 @@ class Workspace:
         self.out = torch.empty(out_shape, dtype=torch.bfloat16, device=dev)
         # chunk counters of the fused combine: zero once, left zero by every launch
         self.unit_done = torch.zeros(max(B * Hkv, 1), dtype=torch.int32, device=dev)
+        _ready(dev)
