@@ -159,3 +159,25 @@ def test_not_a_number_in_a_value_that_weighs_nothing(kv, B):
     hit[:B, :, 8:, 7] = True
     assert torch.equal(got.isnan().cpu(), hit)
     assert torch.equal(got.cpu()[~hit], clean.cpu()[~hit])
+
+
+@pytest.mark.parametrize("kv", KINDS)
+@pytest.mark.parametrize("where", ["tail", "shared"])
+@pytest.mark.parametrize("entry", [-3, 10 ** 6])
+def test_a_bad_entry_is_page_0_and_other_rows_keep_their_bits(kv, where, entry):
+    """An entry out of range in request 7's own pages, or in the row that the group's shared
+    pages are looked up in (request 0's): page 0 is read in its place."""
+    lens = [64 * 3 + 40 * r for r in range(9)] + [64 * 3 - 1, 0, 250]
+    c = Shared(kv, lens, [0, 11], [3], 16, 2, 1, seed=60, poison=False).to_gpu()
+    clean, ws = c.step()
+    r, t, rows = (7, 3, [7]) if where == "tail" else (0, 1, list(range(9)))
+    good = c.bt[r, t].item()
+    c.bt[r, t] = entry
+    got, _ = c.step(ws=ws, flags=4)
+    c.table[rows, t] = 0
+    c.check(got)
+    others = [b for b in range(len(lens)) if b not in rows]
+    assert torch.equal(got[others], clean[others])
+    c.bt[r, t] = good
+    again, _ = c.step(ws=ws)
+    assert torch.equal(again, clean)
