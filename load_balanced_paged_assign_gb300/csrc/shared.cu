@@ -25,13 +25,14 @@ struct Cost {
     float head_us, tail_us, stream_us;
     int head_start, tail_start;
 };
+constexpr int kHeadStart = 32;
 
 // (nb blocks of 8 query rows per KV head and request)
 Cost cost_of(hpc_kv_dtype dt, int heads, int nb) {
-    if (dt == HPC_KV_BF16) return {0.118f, nb == 1 ? 0.62f : 0.80f, 4.96e-3f, 32, 2};
+    if (dt == HPC_KV_BF16) return {0.118f, nb == 1 ? 0.62f : 0.80f, 4.96e-3f, kHeadStart, 2};
     const float tile = (nb == 1 ? 0.36f : 0.40f) * heads, stream = 2.48e-3f * heads;
-    if (dt == HPC_KV_FP8_E4M3) return {0.108f, tile, stream, 32, nb == 1 ? 2 : 3};
-    return {0.115f, tile, stream, 32, nb == 1 ? 2 : 3};
+    if (dt == HPC_KV_FP8_E4M3) return {0.108f, tile, stream, kHeadStart, nb == 1 ? 2 : 3};
+    return {0.115f, tile, stream, kHeadStart, nb == 1 ? 2 : 3};
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -51,10 +52,14 @@ hpc_status check_shape(int32_t B, int32_t Hq, int32_t Hkv, int32_t q_len, int32_
         return HPC_ERR_UNSUPPORTED;
     if (B > HPC_MAX_SHARED_BATCH || groups > HPC_MAX_SHARED_GROUPS || num_ctas > 1 << 16)
         return HPC_ERR_UNSUPPORTED;
-    // costs, tile counts, query rows and token indices stay in int32
+    // Costs, tile counts, query rows and token indices stay in int32.  A page costs 4 a row
+    // tile and 1 more for an odd number of them, of which n requests (two at least) have n / 8
+    // + 1 at most: 3 n, below 3 2^28 in all; the units' starts are below 2^30.  The plan's
+    // quotients, KV heads among them, are exact below 2^20.
     if ((int64_t)B * max_pages * Hkv >= (int64_t)1 << 28 ||
         (int64_t)B * q_len * Hq >= (int64_t)1 << 30 ||
-        (int64_t)max_pages * HPC_PAGE_SIZE >= (int64_t)1 << 30)
+        (int64_t)max_pages * HPC_PAGE_SIZE >= (int64_t)1 << 30 || Hkv >= 1 << 20 ||
+        head_units(B, Hq / Hkv, Hkv, q_len, groups) * kHeadStart >= (int64_t)1 << 30)
         return HPC_ERR_UNSUPPORTED;
     return HPC_OK;
 }

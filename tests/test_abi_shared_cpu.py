@@ -144,3 +144,16 @@ def test_refusals_of_the_binding():
         hd.hpc_decode_plan_shared(lens, starts, pages, 8, 1, 1, 3, 2, hd.Workspace)
     with pytest.raises(hd.HpcError):  # more requests than the workspace holds
         hd.hpc_decode_plan_shared(torch.ones(64, **i32), starts, pages, 8, 1, 1, 3, 2, ws)
+
+
+def test_shapes_whose_costs_leave_32_bits():
+    """32 a unit: 16,384 KV heads times 4096 pairs of requests and more; and KV heads that the
+    plan's quotients do not hold."""
+    assert capacity(B=8192, Hq=16384, Hkv=16384, groups=4096) == UNS
+    assert type(capacity(B=8192, Hq=4096, Hkv=4096, groups=4096)) is list
+    assert type(capacity(B=8192, Hq=16384, Hkv=16384, groups=0)) is list
+    assert capacity(B=1, Hq=1 << 20, Hkv=1 << 20) == UNS
+    assert type(capacity(B=1, Hq=(1 << 20) - 1, Hkv=(1 << 20) - 1)) is list
+    assert plan(shared_map(cap_desc=1 << 40, cap_head=1 << 40, cap_slots=1 << 40,
+                           cap_units=1 << 30), B=8192, Hq=16384, Hkv=16384, max_pages=1,
+                groups=4096) == UNS
