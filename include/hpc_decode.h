@@ -792,10 +792,15 @@ hpc_status hpc_kv_read_block(const void *d_k_cache, const void *d_v_cache,
  * The result is that of hpc_decode_step_mq (hpc_decode_step_win without a window)
  * on the same batch: prefixes only say what may be computed together.  A request of
  * a group whose queries do not all see all of the shared pages (L_r - q_len + 1 <
- * 64 * d_prefix_pages[g], an empty one among them) is computed by itself, as are
- * the requests of a group in which fewer than two others are left; the group's
- * pages are then looked up in the row of its first request that shares them, so
- * the rows of those that do not may hold other pages.
+ * 64 * d_prefix_pages[g], an empty one among them) is computed by itself, as is a
+ * request that would be the only one of its group to share; the group's pages are
+ * then looked up in the row of its first request that shares them, so the rows of
+ * those that do not may hold other pages.
+ *
+ * Sharing has a longer plan and a join behind the attention, some 3 us of a step,
+ * and the plan does not weigh them against the bytes that are saved: for few
+ * requests, or prefixes that are short beside the rest of the context,
+ * hpc_decode_step_win is the faster call.
  * ---------------------------------------------------------------------- */
 #define HPC_MAX_SHARED_BATCH 8192
 #define HPC_MAX_SHARED_GROUPS 4096
@@ -935,7 +940,8 @@ hpc_status hpc_kv_extend(const hpc_page_pool *pool, int32_t *d_block_table, int3
  * the rest of them, which d_copies says to copy from (hpc_kv_copy_pages, for the
  * caches of every layer).  What is appended to either row is then not seen by the
  * other.  The rows d_dst[i] are empty before the call (their entries below
- * ceil(d_lens[i] / 64) are -1) and no row d_src[k]; a child whose row is not,
+ * ceil(d_lens[i] / 64) are -1) and no row d_src[k] (so a step that reorders beams
+ * forks into a second set of rows, and frees the first); a child whose row is not,
  * or whose source has not the pages, raises a flag and is left out, as is all but
  * the first of children of one row.  With fewer pages on the stack than the
  * children need, nothing changes and HPC_FLAG_NO_PAGES is raised.

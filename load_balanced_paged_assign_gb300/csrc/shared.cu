@@ -16,11 +16,29 @@ constexpr int kMaxDevices = 64;
 // What the plan takes the work to cost (see SharedPlan), in us of one CTA: head_us an
 // eighth of a page against two row tiles, with what a CTA's work has around it; tail_us a
 // tile and stream_us its share of HBM's time; the starts what a unit costs beside its
-// pages, in the same units.  Measured as whole steps, each constant on both sides.  64
-// requests behind 8K tokens, BF16 (51.2 us): head_us 0.11, 0.128 56.1, 52.5; 37 requests in
-// five groups, three tokens each, BF16: tail_us 0.62 instead of 0.80 31 us for 26.6; no
-// starts 34.9, 8 and 2 26.4; 128 behind 32K, E4M3 (45.8): head_us 0.09, 0.128 46.5, 44.7, no
-// starts 53.9; 48 in six groups, block scales: tail_start 2, 3, 4 38.0, 37.6, 40.5.
+// pages, in the same units.  One number serves all batches of a type, and most batches have
+// a better one.  Steps in us, each number with one to either side of it.
+//   BF16: 64 requests of 64 heads behind 8K tokens, tails 0.1 to 2K (53.7 as it is); 40 behind
+//   12.5K (52.2); 37 in five groups of 15 heads, three tokens (28.5, two row blocks)
+//     head_us 0.100, 0.140       53.5, 56.7;  55.0, 50.0;  29.2, 28.9
+//     tail_us 0.50, 0.75         57.5, 53.8;  49.4, 54.0;  (0.66, 0.96)  28.6, 29.6
+//     head_start 16, 48          53.8, 53.9;  51.9, 50.9;  28.8, 28.4
+//     tail_start 0, 4            57.3, 55.3;  50.1, 54.7;  37.3, 29.1
+//   E4M3: 128 of 16 heads behind 32K, tails 16 to 4K (47.5); 64 of 64 behind 8K (42.6); 48 in
+//   three groups behind 4K, two tokens (42.2, two row blocks)
+//     head_us 0.090, 0.128       48.7, 50.0;  40.9, 41.5;  40.5, 41.6
+//     tail_us 0.30, 0.43         50.0, 48.6;  41.6, 40.8;  (0.33, 0.48)  41.6, 40.5
+//     head_start 16, 48          50.4, 47.5;  43.4, 41.5;  41.4, 41.9
+//     tail_start 0, 4            53.8, 48.3;  43.9, 40.5;  51.4, 40.8
+//   block scales: 128 behind 32K (51.3); 64 behind 8K (44.4); 48 in six groups, two tokens
+//   (40.6, two row blocks)
+//     head_us 0.100, 0.130       51.4, 52.5;  44.0, 42.4;  40.9, 41.9
+//     tail_us 0.30, 0.43         51.4, 53.2;  42.3, 43.9;  (0.33, 0.48)  41.6, 40.5
+//     head_start 16, 48          54.6, 51.4;  46.3, 42.3;  41.5, 41.4
+//     tail_start 0, 4            59.4, 51.2;  44.8, 43.4;  49.5, 41.6
+//   stream_us times 1/2 and 2 (it counts where tails are nearly all of the work): 64 of 64
+//   heads behind 1K, tails of 2K to 6K, BF16 158.6 and 155.5 (155.7), E4M3 89.1 and 88.9
+//   (89.1); 32 pairs behind a page, BF16 60.3 and 61.0 (60.2); times 4 70.8
 struct Cost {
     float head_us, tail_us, stream_us;
     int head_start, tail_start;

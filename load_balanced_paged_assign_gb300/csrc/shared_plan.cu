@@ -5,8 +5,11 @@
 // a KV head, pairs of them) times the shared pages are the head's work, the requests'
 // tiles behind them the tail's; each has CTAs of its own, as many as its part of the
 // time is.  Both are then cut as the plain plan cuts its tiles: units in a fixed order,
-// bins of one budget, in closed form.  All integers: the map depends on the lengths
-// alone.
+// bins of one budget, in closed form, all in integers.  How the CTAs are shared out and
+// which budgets that gives is reckoned in fp32 from measured costs (shared.cu), which
+// depend on the cache type, the rows of a request and KV head and the heads of a
+// descriptor.  So the map is a function of the lengths, the groups, the shape, the number
+// of CTAs and the floor.
 #include <cuda_bf16.h>
 
 #include "block_scan.cuh"
@@ -19,12 +22,13 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 
 // The head's cost of a page: against a pair of row tiles, and against one that is alone.
-// Long prefixes alone on the GPU take 0.73 to 0.82 us a page and 0.73 (BF16, whose lone tiles
-// wait for HBM), 0.72 and 0.55 (E4M3), 0.87 and 0.61 (block scales); beside tails a lone
-// tile's pages cost less.  Steps with 5, 6 and 7: 12 requests of 64 heads on 8 behind 8K
-// tokens, E4M3, 24.5, 27.1 and 27.2 us; 37 in five groups 26.2, 27.0 and 27.5; 48 in six,
-// block scales, 36.7, 37.3 and 37.9; 40 behind 12.5K tokens (a pair and a lone tile), BF16,
-// 48.2, 45.2 and 46.5.
+// What a page more of a long prefix takes a CTA, with no tails (64 and 16 requests of 64 heads
+// on 8, 16K to 128K tokens): 0.72 us and 0.80 (BF16, whose lone tiles wait for HBM), 0.89 and
+// 0.62 (E4M3), 0.86 and 0.64 (block scales); beside tails a lone tile's pages cost less.
+// Steps with 5, 6 and 7: 12 requests of 64 heads on 8 behind 8K tokens, E4M3, 27.4, 29.6 and
+// 29.6 us, block scales 28.0, 30.3 and 32.6; 48 in six groups, block scales, 40.6, 41.8 and
+// 42.1; 37 in five groups, BF16, 28.4, 28.4 and 29.6, and 40 behind 12.5K tokens (a pair and a
+// lone tile) 52.2, 49.8 and 48.2: one number for all types, of which 6 would suit BF16 better.
 constexpr int kPairCost = 8, kAloneCost = 5;
 
 // Costs are positions on a line that bins of one budget cut: a unit of n pages of cost w
@@ -225,7 +229,11 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
     const int tail_units = p.Hkv / p.heads;  // per request
 
     // What a unit costs beside its pages counts where a CTA has several microseconds of
-    // work; with less, the floor alone says how finely units are cut.
+    // work; with less, the floor alone says how finely units are cut.  (Steps with thresholds of
+    // 0, 1, 2 and 8 us: 4 requests behind 960 tokens, BF16, 14.1, 13.2, 13.2 and 13.3 us; 8
+    // behind 2K, 64 heads, E4M3, 17.8, 17.8, 21.5 and 21.5; 16 behind 4K, 16 heads, 21.4, 26.5,
+    // 26.5 and 26.5; 12 behind 8K, 64 heads, 27.4, 27.4, 27.4 and 30.4: a lower one would suit
+    // the batches between better.)
     const float head_us = (float)pages * p.head_us, tail_us = (float)(tail_units * tiles) * p.tail_us;
     const bool busy = head_us + tail_us > 2.f * p.num_ctas;
     int start = busy ? p.head_start : 0;
@@ -377,8 +385,8 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedP
 }
 
 // ------------------------------------------------------------------ join
-// CTAs of an SM: as many rows in flight as there are (a kernel that spills costs 3 us more
-// than its time: its launch waits for local memory).
+// CTAs of an SM: as many rows in flight as there are registers for (with eight the kernel
+// spilled and took 3.5 us longer).
 constexpr int kJoinWarps = 4, kJoinCtas = 7;
 constexpr int kJoinAhead = 6;  // partials of a row on their way together
 constexpr float kJoinLog2e = 1.4426950408889634f;
