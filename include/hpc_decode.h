@@ -838,8 +838,9 @@ hpc_status hpc_decode_shared_capacity(int32_t B, int32_t Hq, int32_t Hkv, int32_
  *   d_prefix_pages  device int32 [num_groups], in [0, max_pages_per_req] (else
  *                   flagged, and nothing is shared in that group)
  *   num_ctas        2 .. 65536 (hpc_decode_num_ctas)
- * B <= HPC_MAX_SHARED_BATCH, num_groups <= HPC_MAX_SHARED_GROUPS, B *
- * max_pages_per_req * Hkv < 2^28.  Other arguments as in hpc_decode_plan_win.
+ * B <= HPC_MAX_SHARED_BATCH, num_groups <= HPC_MAX_SHARED_GROUPS, Hkv < 2^20, B *
+ * max_pages_per_req * Hkv < 2^28, cap_slots as hpc_decode_shared_capacity says
+ * below 2^26 (4 TB; HPC_ERR_UNSUPPORTED).  Other arguments as in hpc_decode_plan_win.
  */
 hpc_status hpc_decode_plan_shared(const int32_t *d_seqlens, int32_t B, int32_t Hq, int32_t Hkv,
                                   int32_t max_pages_per_req, const int32_t *d_group_starts,

@@ -811,7 +811,8 @@ __device__ __forceinline__ bool tc_softmax(const AttnParams &p, uint8_t *smem, u
                 m[r] = mn;
                 // Block scales: the reference may move by 200, and the sum's terms are that
                 // much larger than O's, but one factor holds 2^-126 at the least.  So in two
-                // steps, or by the sum's logarithm: 123.1 and 125.8 us with 8 rows (64
+                // steps, or by the sum's logarithm (off by 2^-22 of itself, 2e-5 of the sum at
+                // the most): 123.1 and 125.8 us with 8 rows (64
                 // requests of 64 heads, 8K to 10K tokens; 123.1 without either), 49.1 and 48.6
                 // with 16 (48 requests of 48 heads, two tokens each; 48.0).
                 if (!BLK) {
